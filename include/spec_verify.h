@@ -56,7 +56,8 @@ typedef enum {
 
 typedef enum {
     SPEC_DTYPE_F32 = 0, /* IEEE float32 logits */
-    SPEC_DTYPE_BF16 = 1 /* bfloat16 logits */
+    SPEC_DTYPE_BF16 = 1, /* bfloat16 logits */
+    SPEC_DTYPE_F16 = 2   /* float16: key/value caches only (spec_cache.h) */
 } spec_dtype_t;
 
 /* Device status bits (OR-ed into *dev_status when dev_status != NULL). */

@@ -9,13 +9,18 @@ raises.
 
     out_tokens, accept_len = verify(target, draft, tokens, verify_len, temperature, seed)
     verify_len = schedule_len(draft_maxprob, threshold)
+
+The paged key/value cache and the tree attention that precede the step are in
+cache.py.
 """
 import ctypes
 import os
 
 import torch
 
-from . import _build
+from . import _build, cache
+from .cache import (DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_NO_PAGES, DTYPE_F16, PagedCache,  # noqa: F401
+                    cache_append, cache_commit, cache_copy, cache_fork, cache_resize, tree_attention)
 
 SPEC_OK = 0
 DTYPE_F32, DTYPE_BF16 = 0, 1
@@ -104,6 +109,7 @@ def load_library():
     L.spec_debug_force_wait_timeout.restype = ctypes.c_int
     L.spec_status_str.argtypes = [ctypes.c_int]
     L.spec_status_str.restype = ctypes.c_char_p
+    cache.declare(L)
     _lib = L
     return L
 
@@ -117,7 +123,7 @@ def exported_symbols():
             "spec_schedule_len", "spec_verify_noalloc", "spec_verify_from_host",
             "spec_verify_scheduled_from_host",
             "spec_profile_events", "spec_debug_force_wait_timeout",
-            "spec_verify_kernel_count", "spec_status_str"]
+            "spec_verify_kernel_count", "spec_status_str"] + cache.EXPORTED
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -1,0 +1,298 @@
+"""Tree attention over a paged cache against the definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import cache_helpers as ch
+
+pytestmark = pytest.mark.gpu
+
+
+def _sv():
+    import speculative_decoding_verification_69_gb300 as sv
+    return sv
+
+
+def _case(seed, lens, N, hq, hkv, D, page, dtype, *, tree=True, hnd=False, qscale=2.0, spare=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B = len(lens)
+    P = max(-(-(n + N) // page) for n in lens) + 1
+    pages = sum(-(-(n + N) // page) for n in lens) + spare
+    table, count, ref, cl = ch.make_table(g, lens, N, page, P, pages)
+    k = ch.make_pool(g, pages, page, hkv, D, dtype, hnd=hnd)
+    v = ch.make_pool(g, pages, page, hkv, D, dtype, hnd=hnd)
+    q = (torch.randn((B, N, hq, D), generator=g, device="cuda") * qscale).to(dtype)
+    parent = ch.random_parents(g, B, N) if tree else None
+    return dict(q=q, k=k, v=v, table=table, len=cl, parent=parent)
+
+
+def _run(c, **kw):
+    sv = _sv()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, l = sv.tree_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"], return_lse=True,
+                             dev_status=st, **kw)
+    torch.cuda.synchronize()
+    return o, l, int(st.item())
+
+
+def _check(c, status=0, **kw):
+    o, l, st = _run(c, **kw)
+    assert st == status
+    ref = ch.ref_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"], **kw)
+    ch.check_attention(o, l, ref, c["q"].dtype, c["q"].shape[-1])
+    return o, l
+
+
+LENS = [0, 1, 7, 8, 63, 64, 127, 128, 129, 200, 255, 256, 257, 511, 640]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,hq,hkv,D,page,hnd", [
+    (1, 8, 8, 64, 16, False),      # single tokens, a key head each
+    (1, 8, 1, 128, 8, True),       # one key head for all
+    (2, 4, 4, 8, 8, False),        # the smallest head
+    (9, 8, 2, 128, 16, False),     # linear-draft size
+    (16, 14, 2, 128, 32, True),    # a group of 7
+    (33, 4, 1, 96, 64, False),     # 132 rows of one key head: just past 128
+    (64, 4, 2, 64, 128, False),    # 128 rows exactly
+    (64, 8, 2, 128, 256, True),    # 256 rows, pages longer than a tile of keys
+    (63, 10, 2, 72, 16, False),    # 315 rows, a head of 72
+    (64, 64, 1, 40, 8, False),     # 4096 rows of one key head
+])
+def test_lengths_heads_layouts(N, hq, hkv, D, page, hnd, dtype):
+    lens = LENS if hq < 64 else [0, 5, 130, 300]
+    _check(_case(N * 131 + D, lens, N, hq, hkv, D, page, dtype, hnd=hnd))
+
+
+@pytest.mark.parametrize("N", [1, 9, 33])
+def test_chain_is_causal(N):
+    c = _case(7, [0, 3, 100, 700], N, 8, 2, 128, 16, torch.bfloat16, tree=False)
+    o, l = _check(c)
+    c["parent"] = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(4, 1)
+    o2, l2, _ = _run(c)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 4), (17, 0), (64, 3), (128, 130), (129, 128),
+                                          (300, 1), (5000, 4), (700, 0)])
+@pytest.mark.parametrize("N,hq,hkv,D,page", [(1, 8, 1, 64, 16), (12, 8, 2, 64, 16), (40, 8, 2, 128, 64)])
+def test_window_and_sinks(N, hq, hkv, D, page, window, sinks):
+    _check(_case(window * 7 + N, [0, 1, 5, 127, 128, 300, 513, 1000], N, hq, hkv, D, page, torch.bfloat16),
+           window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("window", [0, 100])
+def test_unseen_positions_hold_anything(window, dtype):
+    """Stale pages: every position of the pool that no node sees is NaN or
+    infinite, and the table's entries for pages that no node sees are rubbish."""
+    page, N, lens = 16, 11, [0, 4, 37, 250, 260, 385]
+    c = _case(91, lens, N, 8, 2, 64, page, dtype)
+    cnt = torch.tensor([11, 3, 11, 0, 7, 10], dtype=torch.int32, device="cuda")
+    sinks = 3 if window else 0
+    seen = torch.zeros(c["k"].shape[:2], dtype=torch.bool)
+    P = c["table"].shape[1]
+    for b, n0 in enumerate(lens):
+        used = set()
+        for p in ch.paths(c["parent"][b].tolist(), int(cnt[b])):
+            used |= set(ch.seen_positions(n0, p, window, sinks))
+        row = c["table"][b].tolist()
+        for j in used:
+            seen[row[j // page], j % page] = True
+        for i in range(P):
+            if not any(j // page == i for j in used):
+                c["table"][b, i] = [-1, 2 ** 31 - 1, -2 ** 31][i % 3]
+    bad = ~seen.cuda().unsqueeze(-1).unsqueeze(-1).expand_as(c["k"])
+    fill = torch.tensor([float("nan"), float("inf"), float("-inf")], device="cuda", dtype=dtype)
+    noise = fill[torch.randint(0, 3, c["k"].shape, device="cuda")]
+    c["k"] = torch.where(bad, noise, c["k"])
+    c["v"] = torch.where(bad, noise, c["v"])
+    o, l = _check(c, node_count=cnt, window=window, sinks=sinks)
+    for b in range(len(lens)):  # rows past the count see nothing
+        assert (o[b, int(cnt[b]):] == 0).all() and torch.isneginf(l[b, int(cnt[b]):]).all()
+
+
+@pytest.mark.parametrize("N,hq,hkv,D,ctx", [(1, 8, 1, 128, 70001), (16, 8, 2, 128, 20000), (64, 8, 2, 64, 9999),
+                                            (5, 4, 4, 64, 33333)])
+def test_long_contexts(N, hq, hkv, D, ctx):
+    _check(_case(ctx, [ctx], N, hq, hkv, D, 64, torch.bfloat16))
+
+
+def test_many_requests_of_mixed_lengths():
+    g = torch.Generator().manual_seed(5)
+    lens = [int(x) for x in (torch.rand(300, generator=g) ** 3 * 900).tolist()] + [4000, 0, 0, 0]
+    _check(_case(17, lens, 5, 8, 4, 64, 16, torch.bfloat16))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(seed):
+    import random
+    r = random.Random(1000 + seed)
+    hkv, G = r.choice([1, 2, 3, 8]), r.choice([1, 2, 3, 5, 8, 16])
+    N, D = r.randint(1, 64), 8 * r.randint(1, 16)
+    page = r.choice([8, 16, 32, 64, 128, 256])
+    B = r.randint(1, 6)
+    lens = [r.choice([0, r.randint(0, 40), r.randint(0, 1500)]) for _ in range(B)]
+    window = r.choice([0, 0, r.randint(1, 600)])
+    c = _case(seed, lens, N, hkv * G, hkv, D, page, r.choice([torch.bfloat16, torch.float16]),
+              hnd=r.random() < 0.5, tree=r.random() < 0.7)
+    cnt = torch.tensor([r.randint(0, N) for _ in range(B)], dtype=torch.int32, device="cuda")
+    _check(c, node_count=cnt, window=window, sinks=r.choice([0, 2, 200]) if window else 0,
+           scale=r.choice([None, 0.05]))
+
+
+def test_large_scores():
+    """Sharp distributions whose maximum grows along the keys (the running
+    maximum moves many times) and falls (it never moves again)."""
+    for sign in (1.0, -1.0):
+        c = _case(3, [1500, 900], 4, 4, 1, 64, 64, torch.bfloat16, qscale=1.0)
+        kk, page = c["k"], 64
+        for b, n0 in enumerate([1500, 900]):
+            j = torch.arange(n0 + 4, device="cuda")
+            pg = c["table"][b].long()[j // page]
+            ramp = (sign * (j.float() / 100 - 5)).view(-1, 1, 1)
+            kk[pg, j % page] = (kk[pg, j % page].float() * 0.5 + ramp).bfloat16()
+        c["q"] = c["q"].abs() * 4 + 1
+        _check(c)
+
+
+def test_strided_queries_and_single_extents():
+    """Queries that are a slice of a fused projection, batches of one, and
+    dimensions of one element with odd strides."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    c = _case(2, [77], 9, 8, 2, 64, 16, torch.bfloat16)
+    qkv = torch.randn((1, 9, 12, 64), generator=g, device="cuda").bfloat16()
+    c["q"] = qkv[:, :, 2:10]
+    _check(c)
+    c["q"] = torch.as_strided(qkv, (1, 9, 8, 64), (3, 12 * 64, 64, 1))
+    _check(c)
+
+
+def test_pool_past_32_bit_offsets():
+    """A pool of more than 2^31 elements: pages at both of its ends."""
+    page, hkv, D, N = 64, 8, 128, 4
+    pages = (1 << 31) // (page * hkv * D) + 40
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.empty((pages, page, hkv, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    ids = [pages - 1, 0, pages - 7, pages - 30, 5]
+    for p in ids:
+        k[p].normal_(generator=g)
+        v[p].normal_(generator=g)
+    table = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, N, 16, D), generator=g, device="cuda").bfloat16()
+    _check(dict(q=q, k=k, v=v, table=table, len=torch.tensor([300], dtype=torch.int32, device="cuda"),
+                parent=ch.random_parents(g, 1, N)))
+
+
+def test_bad_data_is_reported_and_survived():
+    sv = _sv()
+    c = _case(4, [40, 100], 6, 4, 2, 64, 16, torch.bfloat16)
+    c["parent"][1] = torch.tensor([-1, 0, 5, -3, 2 ** 31 - 1, 4], device="cuda")
+    _check(c, status=sv.DEV_BAD_TREE)
+    c = _case(4, [40, 100], 6, 4, 2, 64, 16, torch.bfloat16)
+    c["table"][0, 1] = 10 ** 6
+    o, l, st = _run(c)
+    assert st == sv.DEV_BAD_PAGE
+    ref = ch.ref_attention(c["q"][1:], c["k"], c["v"], c["table"][1:], c["len"][1:], c["parent"][1:])
+    ch.check_attention(o[1:], l[1:], ref, torch.bfloat16, 64)
+    c = _case(4, [40, 100], 6, 4, 2, 64, 16, torch.bfloat16)
+    P = c["table"].shape[1]
+    for bad in (-5, P * 16 + 1, 2 ** 31 - 1):
+        c["len"][0] = bad
+        o, l, st = _run(c)
+        assert st & sv.DEV_BAD_LEN
+        ref = ch.ref_attention(c["q"][1:], c["k"], c["v"], c["table"][1:], c["len"][1:], c["parent"][1:])
+        ch.check_attention(o[1:], l[1:], ref, torch.bfloat16, 64)
+
+
+def test_length_up_to_the_last_place_of_the_table():
+    """The tree fills the row of the table to its end; one token more is cut."""
+    sv = _sv()
+    page, N = 16, 8
+    c = _case(6, [page * 5 - N], N, 4, 2, 64, page, torch.bfloat16, tree=False)
+    c["table"] = c["table"][:, :5].contiguous()
+    o, l = _check(c)
+    c["len"] += 1
+    o2, l2, st = _run(c)
+    assert st == sv.DEV_BAD_LEN
+    ref = ch.ref_attention(c["q"], c["k"], c["v"], c["table"], c["len"], None, node_count=[N - 1])
+    ch.check_attention(o2, l2, ref, torch.bfloat16, 64)
+
+
+def test_same_inputs_same_bits_on_any_stream():
+    c = _case(8, [1000, 3, 5000], 16, 8, 2, 128, 32, torch.bfloat16)
+    o, l, _ = _run(c)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    sv = _sv()
+    for _ in range(3):
+        o2, l2 = sv.tree_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"], return_lse=True, stream=s)
+        s.synchronize()
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+def test_captured_in_a_graph():
+    """One captured call follows the lengths and the data of later replays."""
+    c = _case(9, [600, 30], 7, 8, 2, 64, 16, torch.bfloat16)
+    sv = _sv()
+    out = torch.empty_like(c["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def call():
+        sv.tree_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"], out=out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    c["len"][0] = 333
+    c["q"].mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    ref = ch.ref_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"])
+    ch.check_attention(out, None, ref, torch.bfloat16, 64)
+
+
+def test_refusals():
+    sv = _sv()
+    c = _case(1, [20, 30], 4, 4, 2, 64, 16, torch.bfloat16)
+
+    def call(**kw):
+        x = dict(c, **{a: b for a, b in kw.items() if a in c})
+        opt = {a: b for a, b in kw.items() if a not in c}
+        return sv.tree_attention(x["q"], x["k"], x["v"], x["table"], x["len"], x["parent"], **opt)
+
+    with pytest.raises(ValueError):
+        call(q=c["q"].half())
+    with pytest.raises(ValueError):
+        call(q=c["q"][..., :32])
+    with pytest.raises(ValueError):
+        call(q=c["q"].cpu())
+    with pytest.raises(ValueError):
+        call(v=c["v"][:-1])
+    with pytest.raises(ValueError):
+        call(v=c["v"].transpose(1, 2).contiguous().transpose(1, 2))    # other strides than k
+    with pytest.raises(ValueError):
+        call(table=c["table"].long())
+    with pytest.raises(ValueError):
+        call(len=c["len"][:1])
+    with pytest.raises(ValueError):
+        call(parent=c["parent"][:, :3])
+    with pytest.raises(ValueError):
+        call(out=torch.empty_like(c["q"]).half())
+    for kw in (dict(window=-1), dict(sinks=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
+               dict(scale=math.inf)):
+        with pytest.raises(sv.SpecVerifyError):
+            call(**kw)
+    with pytest.raises(sv.SpecVerifyError):                             # 3 query heads on 2 key heads
+        call(q=c["q"][:, :, :3])
+    with pytest.raises(sv.SpecVerifyError):                             # float32 caches
+        call(q=c["q"].float(), k=c["k"].float(), v=c["v"].float())
+    with pytest.raises(sv.SpecVerifyError):                             # a misaligned pool
+        flat = torch.zeros(c["k"].numel() + 8, dtype=torch.bfloat16, device="cuda")
+        x = flat[1:1 + c["k"].numel()].view(c["k"].shape)
+        call(k=x, v=x)
+    with pytest.raises(sv.SpecVerifyError):
+        call(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
