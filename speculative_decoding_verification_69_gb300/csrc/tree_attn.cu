@@ -1,120 +1,933 @@
-// tree_attn.cu -- attention of drafted trees over a paged key/value cache.
+// tree_attn.cu -- attention of drafted trees over a paged key/value cache on the
+// sm_103a tensor cores.
+//
+// Mathematics.  For one request and one key head all N nodes' query heads of
+// the group (G = Hq / heads) read the same keys and values, so the N * G rows
+// form one matrix: S = Q K^T, softmax over the keys each row sees, O = P V.
+// One pass over the keys keeps per row a reference m (near the running maximum
+// of the scaled scores, base 2), l = sum 2^(s - m) and O = sum 2^(s - m) v:
+// a later, larger maximum rescales l and O by 2^(m - m').  O is rescaled only
+// when the maximum has grown by more than 2^8: until then the weights are
+// merely larger than 1, exactly representable in scale, and O stays untouched
+// in the tensor memory.  Partial results over disjoint keys join the same way.
+//
+// Split.  The work is a list of units, one per (request, key head, row tile,
+// 128-key tile) that somebody sees, in that order, cut into equal runs, one per
+// CTA of a grid of one CTA per SM.  So one long request spreads over the GPU and
+// thousands of short ones balance whatever their lengths; the lengths are
+// read on the device.  A (request, head, row tile) that a cut falls into
+// leaves float32 partials in the workspace, joined by tree_attn_join.
+//
+// One CTA: a TMA warp, an MMA thread and two streams of softmax, four warps
+// each (thread = row).  Up to 128 rows: the streams take the key tiles in
+// turn, each with its own m, l and O, joined at the end (SPLIT_ROWS false).
+// More rows: the streams take 128 rows each of the same key tile (SPLIT_ROWS
+// true), so a row tile is 256 rows for one read of K and V.  Either way one
+// stream's exponentials run while the tensor cores work for the other.
+//
+// What bounds it: up to about 200 rows per key head the bytes of K and V
+// (4 D bytes per key at 2 D flops per row and key), above that the tensor
+// cores and the exponentials together.
+#include <cuda.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
+#include "lm_gemm.cuh"
 #include "spec_cache.h"
 #include "sv_cache.cuh"
+#include "tmem.cuh"
 
 namespace sv {
 
-template <int DT> __device__ __forceinline__ float to_float(uint16_t x);
-template <> __device__ __forceinline__ float to_float<SPEC_DTYPE_BF16>(uint16_t x) {
-    return __uint_as_float((uint32_t)x << 16);
-}
-template <> __device__ __forceinline__ float to_float<SPEC_DTYPE_F16>(uint16_t x) {
-    return __half2float(__ushort_as_half(x));
-}
-template <int DT> __device__ __forceinline__ uint16_t from_float(float x);
-template <> __device__ __forceinline__ uint16_t from_float<SPEC_DTYPE_BF16>(float x) {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-template <> __device__ __forceinline__ uint16_t from_float<SPEC_DTYPE_F16>(float x) {
-    return __half_as_ushort(__float2half_rn(x));
-}
+constexpr int kTaKeys = 128;        // keys of a tile (MMA N of S, MMA K of O)
+constexpr int kTaRows = 128;        // rows of a stream (MMA M, TMEM lanes)
+constexpr int kTaThreads = 320;     // 8 softmax warps, the TMA warp, the MMA warp
+constexpr int kTaMaxCtas = 160;     // CTAs the workspace has room for
+constexpr int kTaChunks = 128;      // entries of the running sum over requests
+constexpr unsigned long long kTaWaitNs = 2000000000ull;  // 2 s
+constexpr float kTaGrow = 8.f;      // growth of a row's maximum that rescales its O
 
-struct AttnArgs {
-    const uint16_t *q;
-    long long qb, qn, qh;
-    Pool P;  // strides in elements here
+struct TaArgs {
     const int *table, *len, *parent, *node_count;
-    int B, N, Hq, D, max_pages, window, sinks;
+    int B, N, Hq, H, G, D, max_pages, num_pages, page, page_shift;
+    int window, sinks;
+    int np;              // nodes of one stream's rows
+    int box;             // tokens of a TMA box
     float scale_log2;
     uint16_t *out;
     float *lse;
+    float *part_o;       // [cta][2][rows][D]
+    float2 *part_ml;     // [cta][2][rows]: m (base 2), l
+    int4 *joins;         // [cta][2]: the item a cut falls into, see tree_attn_join
     uint32_t *status;
 };
 
-// One warp per (request, node, query head): lanes share the head dimension, the
-// keys one after another with the running maximum and sum of a softmax.
-template <int DT>
-__global__ void __launch_bounds__(32) sv_tree_attn(AttnArgs A) {
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x;
-    const int h = blockIdx.x % A.Hq, n = blockIdx.x / A.Hq, b = blockIdx.y;
-    const int G = A.Hq / (A.P.cols / A.P.vecs), hk = h / G;
-    const int cap = (int)min((long long)A.max_pages << A.P.page_shift, 0x7FFFFFFFll);
-    int cnt = A.node_count ? max(0, min(A.node_count[b], A.N)) : A.N;
-    int c = A.len[b];
-    if (c < 0 || c > cap - cnt) {
-        if (lane == 0) flag(A.status, SPEC_DEV_BAD_LEN);
-        c = max(0, min(c, cap));
-        cnt = min(cnt, cap - c);
+template <int DP, bool SPLIT_ROWS> struct TaCfg {
+    static constexpr int kStreamQ = kTaRows * DP * 2;            // bytes of one stream's Q
+    static constexpr int kQ = kStreamQ * (SPLIT_ROWS ? 2 : 1);
+    static constexpr int kStage = kTaKeys * DP * 2;              // one K or V tile
+    // as many tiles in flight as the shared memory holds beside Q
+    static constexpr int kStages = DP == 128 ? 5 : 11;
+    static constexpr int kRowsCta = kTaRows * (SPLIT_ROWS ? 2 : 1);
+};
+
+template <int DP, bool SPLIT_ROWS> struct TaShared {
+    using C = TaCfg<DP, SPLIT_ROWS>;
+    uint8_t q[C::kQ];
+    uint8_t kv[C::kStages][C::kStage];
+    long long incl[kTaChunks];  // units of the requests up to the end of each chunk of them
+    uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, ml_full, done;
+    uint32_t tmem_base;
+    int abort;
+    float2 ml[SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : kTaRows];  // [segment parity][stream][row]
+};
+
+// What one request's tiles cover: positions [0, min(sinks, ...)) in its first
+// `st` tiles and [wlo, end) in the tiles from wt0 on.
+struct Geo {
+    int c, cnt, end;   // committed positions, nodes, positions
+    int wlo;           // first position inside the root's window
+    int st, wt0, nt;   // sink tiles, first window tile, tiles
+    __device__ __forceinline__ int tile(int i) const { return i < st ? i : wt0 + (i - st); }
+};
+
+__device__ __forceinline__ Geo ta_geo(const TaArgs &A, int b) {
+    Geo g;
+    const int cap = (int)min((long long)A.max_pages << A.page_shift, 0x7FFFFFFFll);
+    g.cnt = A.node_count ? max(0, min(__ldcg(A.node_count + b), A.N)) : A.N;
+    g.c = __ldcg(A.len + b);
+    if (g.c < 0 || g.c > cap - g.cnt) {
+        flag(A.status, SPEC_DEV_BAD_LEN);
+        g.c = max(0, min(g.c, cap));
+        g.cnt = min(g.cnt, cap - g.c);
     }
-    uint16_t *o = A.out + (((long long)b * A.N + n) * A.Hq + h) * A.D;
-    float *l_out = A.lse ? A.lse + ((long long)b * A.N + n) * A.Hq + h : nullptr;
-    if (n >= cnt) {
-        for (int d = lane; d < A.D; d += 32) o[d] = 0;
-        if (lane == 0 && l_out) *l_out = -INFINITY;
+    g.end = g.c + g.cnt;
+    g.wlo = A.window ? max(0, g.c - A.window + 1) : 0;
+    g.wt0 = g.wlo / kTaKeys;
+    g.st = A.window && A.sinks > 0 ? min((A.sinks - 1) / kTaKeys + 1, g.wt0) : 0;
+    g.nt = g.cnt > 0 ? g.st + (g.end - 1) / kTaKeys + 1 - g.wt0 : 0;
+    return g;
+}
+
+// A run of key tiles of one (request, key head, row tile).
+struct Seg {
+    Geo g;
+    int b, hk, node0;   // node0: first node of the row tile
+    int i0, n;          // tiles [i0, i0 + n) of the g.nt
+    long long start;    // unit of tile 0
+};
+
+template <bool SPLIT_ROWS> __device__ __forceinline__ int ta_nodes(const TaArgs &A) {
+    return A.np * (SPLIT_ROWS ? 2 : 1);
+}
+template <bool SPLIT_ROWS> __device__ __forceinline__ long long ta_units(const TaArgs &A, const Geo &g) {
+    const int npt = ta_nodes<SPLIT_ROWS>(A);
+    return (long long)g.nt * A.H * ((g.cnt + npt - 1) / npt);
+}
+
+// The segment that unit u begins, at most up to unit u1.  Called by whole warps.
+template <bool SPLIT_ROWS>
+__device__ __forceinline__ Seg ta_segment(const TaArgs &A, const long long *incl, long long u, long long u1) {
+    const int lane = threadIdx.x & 31;
+    int chunk = 0;
+#pragma unroll
+    for (int i = 0; i < kTaChunks; i += 32)
+        chunk += __popc(__ballot_sync(0xFFFFFFFFu, incl[i + lane] <= u));
+    long long base = chunk > 0 ? incl[chunk - 1] : 0;
+    const int per = (A.B + kTaChunks - 1) / kTaChunks;
+    int b = chunk * per;
+    if (per > 1) {
+        const int b1 = min(A.B, b + per);
+        for (int b0 = b; b0 < b1; b0 += 32) {
+            long long x = b0 + lane < b1 ? ta_units<SPLIT_ROWS>(A, ta_geo(A, b0 + lane)) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int k = __popc(__ballot_sync(0xFFFFFFFFu, base + x <= u));
+            if (k > 0) {
+                const long long skip = __shfl_sync(0xFFFFFFFFu, x, k - 1);
+                b = b0 + k;
+                base += skip;
+                if (k == 32) continue;
+            } else {
+                b = b0;
+            }
+            break;
+        }
+        b = min(b, A.B - 1);
+    }
+    Seg s;
+    s.b = b;
+    s.g = ta_geo(A, b);
+    const long long off = u - base;
+    const int nt = max(s.g.nt, 1);
+    const int item = (int)(off / nt);
+    const int npt = ta_nodes<SPLIT_ROWS>(A);
+    const int rts = max((s.g.cnt + npt - 1) / npt, 1);
+    s.hk = item / rts;
+    s.node0 = (item - s.hk * rts) * npt;
+    s.i0 = (int)(off - (long long)item * nt);
+    s.n = (int)min((long long)(nt - s.i0), u1 - u);
+    s.start = base + (long long)item * nt;
+    return s;
+}
+
+// Position of a tile in the order in which a segment of n tiles loads and uses
+// them.  SPLIT_ROWS: K0 V0 K1 V1 ...; else K0 K1 V0 K2 V1 K3 ... (both streams'
+// scores first).
+template <bool SPLIT_ROWS> __device__ __forceinline__ uint32_t k_index(int t) {
+    return SPLIT_ROWS ? 2u * t : (t < 2 ? (uint32_t)t : 2u * t - 1u);
+}
+template <bool SPLIT_ROWS> __device__ __forceinline__ uint32_t v_index(int t, int n) {
+    return SPLIT_ROWS ? 2u * t + 1u : (t + 1 < n ? 2u * t + 2u : 2u * t + 1u);
+}
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, int x, int y, int z, int w,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// D (TMEM) (+)= A (shared) B (shared)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D (TMEM) (+)= A (TMEM, two 16-bit elements per column) B (shared)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of a V tile as the B operand of O += P V: keys are
+// the K dimension, the head dimension is contiguous (MN-major).  128-byte
+// swizzle atoms of 8 keys x 64 elements: the next 8 keys 1024 bytes on (stride
+// byte offset), the next 64 elements kTaKeys * 128 bytes on (leading byte
+// offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((uint32_t)(kTaKeys * 128) >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// Instruction descriptor of kind::f16: float32 accumulator, A and B of the
+// cache's dtype, M = 128; b_mn: B is MN-major.
+template <int DT> __device__ __forceinline__ constexpr uint32_t ta_idesc(int n, bool b_mn) {
+    const uint32_t f = DT == SPEC_DTYPE_BF16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kTaRows >> 4) << 24);
+}
+
+template <int DT> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<SPEC_DTYPE_BF16>(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+template <> __device__ __forceinline__ uint32_t pack2<SPEC_DTYPE_F16>(float lo, float hi) {
+    const __half2 x = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+// Bits of a 32-position word starting at j0 for the positions [lo, hi).
+__device__ __forceinline__ uint32_t range_bits(long long lo, long long hi, long long j0) {
+    const int a = (int)max(0ll, min(32ll, lo - j0)), b = (int)max(0ll, min(32ll, hi - j0));
+    if (b <= a) return 0u;
+    const uint32_t up = b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
+    return up & ~((1u << a) - 1u);
+}
+
+// The nodes on the path to every node, as bits, for nodes `lane` and `lane +
+// 32` of the warp: the links are followed by doubling (6 rounds reach 64).
+__device__ __forceinline__ void ta_paths(const TaArgs &A, int b, int cnt, unsigned long long (&anc)[2]) {
+    const int lane = threadIdx.x & 31;
+    if (!A.parent) {
+        anc[0] = (2ull << lane) - 1ull;
+        anc[1] = lane == 31 ? ~0ull : (2ull << (lane + 32)) - 1ull;
         return;
     }
-    // the path, as a mask of nodes and their depths
-    const int *par = A.parent ? A.parent + (long long)b * A.N : nullptr;
-    auto up = [&](int m) -> int {
-        const int p = par ? par[m] : m - 1;
-        if (m > 0 && (unsigned)p >= (unsigned)m) {
-            flag(A.status, SPEC_DEV_BAD_TREE);
-            return -1;
-        }
-        return m > 0 ? p : -1;
-    };
-    unsigned long long anc = 0;
-    int depth = -1;
-    for (int m = n; m >= 0; m = up(m)) {
-        anc |= 1ull << m;
-        ++depth;
-    }
-    float q[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint16_t *qp = A.q + b * A.qb + n * A.qn + h * A.qh;
+    int up[2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) q[u] = lane + 32 * u < A.D ? to_float<DT>(qp[lane + 32 * u]) : 0.f;
-    const uint16_t *kp = reinterpret_cast<const uint16_t *>(A.P.k), *vp = reinterpret_cast<const uint16_t *>(A.P.v);
-    float m_run = -INFINITY, l_run = 0.f;
-    const int tip = c + depth;
-    const int low = A.window ? max(0, tip - A.window + 1) : 0;
-    int up_depth = depth;
-    (void)up_depth;
-    for (int j = 0; j < c + cnt; ++j) {
-        int place = j;
-        if (j >= c) {
-            if (!((anc >> (j - c)) & 1ull)) continue;
-            place = c + __popcll(anc & ((2ull << (j - c)) - 1ull)) - 1;
+    for (int k = 0; k < 2; ++k) {
+        const int n = lane + 32 * k;
+        anc[k] = 1ull << n;
+        up[k] = -1;
+        if (n > 0 && n < cnt) {
+            up[k] = __ldcg(A.parent + (long long)b * A.N + n);
+            if ((unsigned)up[k] >= (unsigned)n) {
+                flag(A.status, SPEC_DEV_BAD_TREE);
+                up[k] = -1;
+            }
         }
-        if (place < low && place >= A.sinks) {
-            if (j < c) j = min(low, c) - 1;
-            continue;
-        }
-        int p = A.table[(long long)b * A.max_pages + (j >> A.P.page_shift)];
-        if ((unsigned)p >= (unsigned)A.P.num_pages) {
-            if (lane == 0) flag(A.status, SPEC_DEV_BAD_PAGE);
-            p = 0;
-        }
-        const long long at = p * A.P.page_st + (j & (A.P.page - 1)) * A.P.token + hk * A.P.head;
-        float s = 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (lane + 32 * u < A.D) s = fmaf(q[u], to_float<DT>(kp[at + lane + 32 * u]), s);
-        s = warp_sum(s) * A.scale_log2;
-        const float m_new = fmaxf(m_run, s), corr = exp2f(m_run - m_new), e = exp2f(s - m_new);
-        m_run = m_new;
-        l_run = fmaf(l_run, corr, e);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (lane + 32 * u < A.D) acc[u] = fmaf(acc[u], corr, e * to_float<DT>(vp[at + lane + 32 * u]));
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-        if (lane + 32 * u < A.D) o[lane + 32 * u] = from_float<DT>(acc[u] / l_run);
-    if (lane == 0 && l_out) *l_out = 0.69314718056f * (m_run + log2f(l_run));
+    for (int r = 0; r < 6; ++r) {
+        unsigned long long na[2];
+        int nu[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int p = up[k] & 31;
+            const unsigned long long a0 = __shfl_sync(0xFFFFFFFFu, anc[0], p), a1 = __shfl_sync(0xFFFFFFFFu, anc[1], p);
+            const int u0 = __shfl_sync(0xFFFFFFFFu, up[0], p), u1 = __shfl_sync(0xFFFFFFFFu, up[1], p);
+            na[k] = up[k] < 0 ? anc[k] : anc[k] | (up[k] < 32 ? a0 : a1);
+            nu[k] = up[k] < 0 ? -1 : (up[k] < 32 ? u0 : u1);
+        }
+        anc[0] = na[0], anc[1] = na[1];
+        up[0] = nu[0], up[1] = nu[1];
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int DT, int DP, bool SPLIT_ROWS>
+__global__ void __launch_bounds__(kTaThreads, 1)
+    tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v, TaArgs A) {
+    using C = TaCfg<DP, SPLIT_ROWS>;
+    using Sh = TaShared<DP, SPLIT_ROWS>;
+    extern __shared__ uint8_t ta_raw[];
+    Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(ta_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kSt = C::kStages;
+    constexpr int kHalves = DP / 64;
+    // P is scaled up to 2^15 in float16, so that weights 2^-29 below the
+    // maximum are still normal numbers; bfloat16 has float32's range
+    constexpr float kLift = DT == SPEC_DTYPE_F16 ? 7.f : 0.f;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSt; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.pv_done[i], 1);
+        }
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_free, 1);
+        mbar_init(&sh.o_free, 8);
+        mbar_init(&sh.ml_full, 8);
+        mbar_init(&sh.done, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&tm_q);
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+    }
+    if (warp == 9) {
+        tmem_alloc(&sh.tmem_base, 512);
+        tmem_relinquish();
+    }
+    pdl_trigger();
+    pdl_wait();
+    // the units of all requests, summed up to the end of each chunk of them
+    if (threadIdx.x < kTaChunks) {
+        const int per = (A.B + kTaChunks - 1) / kTaChunks;
+        const int b0 = threadIdx.x * per, b1 = min(A.B, b0 + per);
+        long long x = 0;
+        for (int b = b0; b < b1; ++b) x += ta_units<SPLIT_ROWS>(A, ta_geo(A, b));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        sh.incl[threadIdx.x] = x;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x < kTaChunks && warp > 0) {  // add the sums of the warps before
+        long long before = 0;
+        for (int w = 0; w < warp; ++w) before += sh.incl[w * 32 + 31];
+        __syncwarp();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        sh.incl[threadIdx.x] += before;
+    } else if (warp == 0) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    __syncthreads();
+    const uint32_t tmem = sh.tmem_base;
+    volatile int *abort = &sh.abort;
+    const long long total = sh.incl[kTaChunks - 1];
+    const long long run = (total + gridDim.x - 1) / gridDim.x;
+    const long long u_first = min(total, (long long)blockIdx.x * run), u_last = min(total, u_first + run);
+
+    if (warp == 8) {  // ------------------------------------------------ TMA
+        uint32_t it = 0;  // tiles loaded so far
+        int seg_no = 0;
+        const int nb = kTaKeys / A.box;             // boxes of a tile
+        const int ahead = 32 / nb;                  // tiles whose pages one load of the warp fetches
+        bool ok = true;
+        for (long long u = u_first; u < u_last && ok; ++seg_no) {
+            const Seg s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
+            u += s.n;
+            const int *row = A.table + (long long)s.b * A.max_pages;
+            // is any position of the box of this lane in tile i seen by some node
+            auto box_pos = [&](int i, int box) -> long long { return (long long)s.g.tile(i) * kTaKeys + box * A.box; };
+            auto box_seen = [&](long long j) -> bool {
+                return j < s.g.end && (j + A.box > s.g.wlo || j < A.sinks);
+            };
+            auto fetch = [&](int i0) -> int {  // page of this lane's box in tile i0 + lane / nb
+                const int i = i0 + lane / nb;
+                if (i >= s.i0 + s.n) return 0;
+                const long long j = box_pos(i, lane % nb);
+                if (!box_seen(j)) return 0;
+                int p = __ldcg(row + (j >> A.page_shift));
+                if ((unsigned)p >= (unsigned)A.num_pages) {
+                    flag(A.status, SPEC_DEV_BAD_PAGE);
+                    p = 0;
+                }
+                return p;
+            };
+            // Q of this segment once the scores of the last one are done
+            if (lane == 0) {
+                ok = seg_no == 0 || lm_wait(&sh.q_free, (seg_no - 1) & 1, abort, kTaWaitNs);
+                if (ok) {
+                    constexpr int kQs = SPLIT_ROWS ? 2 : 1;
+                    mbar_expect_tx(&sh.q_full, (uint32_t)(kQs * kHalves * A.np * A.G * 128));
+                    for (int q = 0; q < kQs; ++q)
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_4d(sh.q + q * C::kStreamQ + h * kTaRows * 128, &tm_q, h * 64, s.hk * A.G,
+                                        s.node0 + q * A.np, s.b, &sh.q_full);
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            // two windows of page numbers: K runs ahead of V by at most two tiles
+            int base = s.i0, cur = fetch(base), nxt = fetch(base + ahead);
+            int prev = 0;
+            const int loads = 2 * s.n;
+            int kt = 0, vt = 0;  // next K and V tile
+            for (int x = 0; x < loads && ok; ++x, ++it) {
+                bool is_k;
+                if (SPLIT_ROWS) is_k = (x & 1) == 0;
+                else is_k = kt < s.n && (uint32_t)x == k_index<false>(kt);
+                const int t = is_k ? kt++ : vt++;
+                const int i = s.i0 + t;
+                while (i >= base + ahead) {
+                    prev = cur;
+                    cur = nxt;
+                    base += ahead;
+                    nxt = fetch(base + ahead);
+                }
+                const int box = lane % nb;
+                const bool mine = lane < nb && box_seen(box_pos(i, box));
+                const int at = (i >= base ? i - base : i - base + ahead) * nb + box;
+                const int pc = __shfl_sync(0xFFFFFFFFu, cur, at & 31), pp = __shfl_sync(0xFFFFFFFFu, prev, at & 31);
+                const int page = i >= base ? pc : pp;
+                const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+                const int stage = (int)(it % kSt);
+                const uint32_t fill = it / kSt;
+                if (lane == 0) {
+                    ok = fill == 0 || lm_wait(&sh.empty[stage], (fill - 1) & 1u, abort, kTaWaitNs);
+                    if (ok) mbar_expect_tx(&sh.full[stage], (uint32_t)(boxes * kHalves * A.box * 128));
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+                if (!ok) break;
+                if (mine) {
+                    const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
+                    const int tok = (int)(box_pos(i, box) & (A.page - 1));
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_4d(sh.kv[stage] + h * kTaKeys * 128 + box * A.box * 128, tm, h * 64, tok, s.hk, page,
+                                    &sh.full[stage]);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {  // every copy has landed before the CTA may exit
+            for (int s = 0; s < kSt; ++s) {
+                const uint32_t n = it / kSt + ((uint32_t)s < it % kSt ? 1u : 0u);
+                if (n > 0) mbar_wait_bounded(&sh.full[s], (n - 1) & 1u, kTaWaitNs);
+            }
+            if (seg_no > 0) mbar_wait_bounded(&sh.q_full, (seg_no - 1) & 1, kTaWaitNs);
+        }
+    } else if (warp == 9) {  // ----------------------------------------- MMA
+        uint32_t base = 0;                 // tiles used by earlier segments
+        uint32_t pv[2] = {0, 0};           // O products issued per stream
+        int seg_no = 0;
+        bool ok = true;
+        const int ks = (A.D + 15) / 16;    // k steps of S
+        constexpr uint32_t kIdS = ta_idesc<DT>(kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
+        for (long long u = u_first; u < u_last && ok; ++seg_no) {
+            const Seg s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
+            u += s.n;
+            if (lane == 0) {
+                auto stage_of = [&](uint32_t idx) { return (int)((base + idx) % kSt); };
+                auto wait_full = [&](uint32_t idx) {
+                    return lm_wait(&sh.full[stage_of(idx)], ((base + idx) / kSt) & 1u, abort, kTaWaitNs);
+                };
+                // scores of stream i against the K tile at load idx; the stream's
+                // last weights have been consumed (they share the columns)
+                auto scores = [&](int i, uint32_t idx, bool release, bool last) -> bool {
+                    if (pv[i] > 0 && !lm_wait(&sh.pv_done[i], (pv[i] - 1) & 1u, abort, kTaWaitNs)) return false;
+                    if (!wait_full(idx)) return false;
+                    tc_fence_after();
+                    const int st = stage_of(idx);
+                    const uint64_t qd = umma_desc_sw128(smem_u32(sh.q + (SPLIT_ROWS ? i : 0) * C::kStreamQ));
+                    const uint64_t kd = umma_desc_sw128(smem_u32(sh.kv[st]));
+                    for (int k = 0; k < ks; ++k) {
+                        const uint64_t off = (uint64_t)((k >> 2) * (kTaRows * 128 / 16) + (k & 3) * 2);
+                        mma_ss(tmem + (uint32_t)(i * kTaKeys), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&sh.s_full[i]);
+                    if (release) umma_commit(&sh.empty[st]);
+                    if (last) umma_commit(&sh.q_free);
+                    return true;
+                };
+                bool o_ready = seg_no == 0;
+                auto values = [&](int i, uint32_t idx, uint32_t p_use, bool first, bool release) -> bool {
+                    if (!lm_wait(&sh.p_full[i], p_use & 1u, abort, kTaWaitNs)) return false;
+                    if (!wait_full(idx)) return false;
+                    if (!o_ready) {  // the epilogue of the segment before has read O
+                        if (!lm_wait(&sh.o_free, (seg_no - 1) & 1, abort, kTaWaitNs)) return false;
+                        o_ready = true;
+                    }
+                    tc_fence_after();
+                    const int st = stage_of(idx);
+                    const uint64_t vd = v_desc(smem_u32(sh.kv[st]));
+#pragma unroll
+                    for (int k = 0; k < kTaKeys / 16; ++k)
+                        mma_ts(tmem + 256u + (uint32_t)(i * DP), tmem + (uint32_t)(i * kTaKeys + k * 8),
+                               vd + (uint64_t)(k * 2048 / 16), kIdO, first && k == 0 ? 0u : 1u);
+                    umma_commit(&sh.pv_done[i]);
+                    if (release) umma_commit(&sh.empty[st]);
+                    ++pv[i];
+                    return true;
+                };
+                ok = lm_wait(&sh.q_full, seg_no & 1, abort, kTaWaitNs);
+                if (ok) {
+                    if (SPLIT_ROWS) {
+                        ok = scores(0, 0, false, false) && scores(1, 0, true, s.n == 1);
+                        for (int t = 0; t < s.n && ok; ++t) {
+                            const bool more = t + 1 < s.n;
+                            ok = values(0, v_index<true>(t, s.n), pv[0], t == 0, false);
+                            if (ok && more) ok = scores(0, k_index<true>(t + 1), false, false);
+                            if (ok) ok = values(1, v_index<true>(t, s.n), pv[1], t == 0, true);
+                            if (ok && more) ok = scores(1, k_index<true>(t + 1), true, t + 2 == s.n);
+                        }
+                    } else {
+                        ok = scores(0, 0, true, s.n == 1);
+                        if (ok && s.n > 1) ok = scores(1, 1, true, s.n == 2);
+                        for (int t = 0; t < s.n && ok; ++t) {
+                            ok = values(t & 1, v_index<false>(t, s.n), pv[t & 1], t < 2, true);
+                            if (ok && t + 2 < s.n) ok = scores(t & 1, k_index<false>(t + 2), true, t + 3 == s.n);
+                        }
+                    }
+                }
+                base += 2u * (uint32_t)s.n;
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            __syncwarp();
+        }
+        if (lane == 0) {  // every MMA has finished before the TMEM is freed
+            umma_commit(&sh.done);
+            mbar_wait_bounded(&sh.done, 0u, kTaWaitNs);
+        }
+        __syncwarp();
+    } else {  // ---------------------------------------------------- softmax
+        const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S, then P
+        const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);        // O
+        const int rows_used = A.np * A.G;
+        uint32_t base = 0, tiles[2] = {0, 0};  // loads before this segment, tiles done per stream
+        int seg_no = 0;
+        bool ok = true, joins = false;
+        for (long long u = u_first; u < u_last && ok; ++seg_no) {
+            const Seg s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
+            u += s.n;
+            const Geo &g = s.g;
+            const int local = row / A.G, node = s.node0 + (SPLIT_ROWS ? stream * A.np : 0) + local;
+            const bool valid = row < rows_used && node < g.cnt;
+            unsigned long long anc[2];
+            ta_paths(A, s.b, g.cnt, anc);
+            const unsigned long long a0 = __shfl_sync(0xFFFFFFFFu, anc[0], node & 31),
+                                     a1 = __shfl_sync(0xFFFFFFFFu, anc[1], node & 31);
+            unsigned long long path = valid ? (node < 32 ? a0 : a1) : 0ull;
+            const int tip = g.c + __popcll(path) - 1;  // the node's place
+            int low = 0;                               // first committed position in its window
+            if (A.window) {
+                low = max(0, tip - A.window + 1);
+                unsigned long long left = path;
+                for (int place = g.c; left; ++place) {
+                    const unsigned long long bit = left & (0ull - left);
+                    if (place < low && place >= A.sinks) path &= ~bit;
+                    left ^= bit;
+                }
+            }
+            const bool warp_works = __any_sync(0xFFFFFFFFu, valid);
+            float m = -INFINITY;                       // reference of the weights, less the lift
+            float2 l2 = make_float2(0.f, 0.f);
+            const int t_step = SPLIT_ROWS ? 1 : 2;
+            bool first = true;
+            for (int t = SPLIT_ROWS ? 0 : stream; t < s.n && ok; t += t_step, first = false) {
+                const long long j0 = (long long)g.tile(s.i0 + t) * kTaKeys;
+                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.s_full[stream], tiles[stream] & 1u, abort, kTaWaitNs));
+                if (!ok) break;
+                tc_fence_after();
+                if (warp_works) {
+                    uint32_t x[kTaKeys];
+                    tmem_load(ts, x);
+                    const bool whole = j0 + kTaKeys <= g.c && (j0 >= low || j0 + kTaKeys <= A.sinks);
+                    if (!__all_sync(0xFFFFFFFFu, whole || !valid)) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const long long jw = j0 + 32 * w;
+                            uint32_t bits = 0;
+                            if (valid) {
+                                bits = range_bits(low, g.c, jw) | (A.window ? range_bits(0, min(A.sinks, g.c), jw) : 0u);
+                                const long long sft = jw - g.c;  // bit sft of the path is position jw
+                                if (sft >= 0 && sft < 64) bits |= (uint32_t)(path >> sft);
+                                else if (sft < 0 && sft > -32) bits |= (uint32_t)(path << -sft);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((bits >> i) & 1u)) x[32 * w + i] = 0xFF800000u;
+                        }
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kTaKeys; i += 8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
+                    if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kTaGrow))) {
+                        const float m_new = top > m + kLift ? top - kLift : m;
+                        const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);
+                        m = m_new;
+                        l2 = make_float2(l2.x * f, l2.y * f);
+                        if (!first) {
+                            ok = __all_sync(0xFFFFFFFFu,
+                                            lm_wait(&sh.pv_done[stream], (tiles[stream] - 1) & 1u, abort, kTaWaitNs));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int d = 0; d < DP; d += 32) {
+                                uint32_t o[32];
+                                tmem_load(to + d, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_store(to + d, o);
+                            }
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float2 c2 = make_float2(A.scale_log2, A.scale_log2), nm2 = make_float2(-mu, -mu);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 z = fma2(make_float2(__uint_as_float(x[32 * q + 2 * i]),
+                                                              __uint_as_float(x[32 * q + 2 * i + 1])), c2, nm2);
+                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                            sum[i & 1] = add2(sum[i & 1], e);
+                            p[i] = pack2<DT>(e.x, e.y);
+                        }
+                        tmem_store(ts + 16 * q, p);
+                    }
+                    l2 = add2(l2, add2(sum[0], sum[1]));
+                    tmem_wait_store();
+                }
+                // values that no node sees may be anything: they are cleared, so that
+                // their zero weights leave them out
+                if ((!SPLIT_ROWS || stream == 0) && (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks))) {
+                    const uint32_t idx = base + v_index<SPLIT_ROWS>(t, s.n);
+                    ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.full[idx % kSt], (idx / kSt) & 1u, abort, kTaWaitNs));
+                    if (!ok) break;
+                    const long long j = j0 + row;
+                    if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) {
+                            uint4 *z = reinterpret_cast<uint4 *>(sh.kv[idx % kSt] + h * kTaKeys * 128 + row * 128);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_proxy_async();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.p_full[stream]));
+                ++tiles[stream];
+            }
+            if (!ok) break;
+            base += 2u * (uint32_t)s.n;
+            float l = l2.x + l2.y;
+            if (!valid) l = 0.f, m = -INFINITY;
+
+            // ---- the segment's result
+            const int n_other = SPLIT_ROWS ? 0 : (stream == 0 ? s.n / 2 : (s.n + 1) / 2);
+            if (!SPLIT_ROWS) tiles[stream ^ 1] += (uint32_t)n_other;
+            const bool whole_item = s.n == g.nt;
+            // a cut item: its first part in this CTA's slot 1, any later one in slot 0
+            const long long slot = (long long)blockIdx.x * 2 + (s.i0 == 0 ? 1 : 0);
+            constexpr int kCols = SPLIT_ROWS ? DP : DP / 2;  // columns of O this thread writes
+            const int col0 = SPLIT_ROWS ? 0 : stream * kCols;
+            const bool two = !SPLIT_ROWS && s.n > 1;         // both streams hold a part
+            float w_a = 1.f, w_b = 0.f;                      // weights of stream 0's (this stream's) part and the other
+            if (!SPLIT_ROWS) {
+                sh.ml[seg_no & 1][stream][row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.ml_full));
+                ok = lm_wait(&sh.ml_full, seg_no & 1, abort, kTaWaitNs);
+                ok = ok && lm_wait(&sh.pv_done[0], (tiles[0] - 1) & 1u, abort, kTaWaitNs);
+                if (two) ok = ok && lm_wait(&sh.pv_done[1], (tiles[1] - 1) & 1u, abort, kTaWaitNs);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const float2 x = sh.ml[seg_no & 1][0][row], y = sh.ml[seg_no & 1][1][row];
+                m = fmaxf(x.x, y.x);
+                w_a = m == -INFINITY ? 0.f : ex2(x.x - m);
+                w_b = m == -INFINITY ? 0.f : ex2(y.x - m);
+                l = x.y * w_a + y.y * w_b;
+            } else {
+                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.pv_done[stream], (tiles[stream] - 1) & 1u, abort, kTaWaitNs));
+                if (!ok) break;
+            }
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const bool writes = row < rows_used && node < A.N;
+            const int head = s.hk * A.G + (row - local * A.G);
+            const long long orow = ((long long)s.b * A.N + node) * A.Hq + head;
+            const int prow = (SPLIT_ROWS ? stream * rows_used : 0) + row;
+            const int rows_cta = rows_used * (SPLIT_ROWS ? 2 : 1);
+            const bool any_write = __any_sync(0xFFFFFFFFu, writes);
+            if (any_write) {
+#pragma unroll
+                for (int d = 0; d < kCols; d += 32) {
+                    uint32_t o[32];
+                    const uint32_t oa = tmem + lanes + 256u + (uint32_t)((SPLIT_ROWS ? stream * DP : 0) + col0 + d);
+                    tmem_load(oa, o);
+                    if (!SPLIT_ROWS) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w_a);
+                        if (two) {
+                            uint32_t o2[32];
+                            tmem_load(oa + DP, o2);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), w_b, __uint_as_float(o[i])));
+                        }
+                    }
+                    if (!writes) {
+                    } else if (whole_item) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(A.out + orow * A.D + col0 + d);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            if (col0 + d + i < A.D) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = l > 0.f ? pack2<DT>(__uint_as_float(o[i + 2 * e]) * inv,
+                                                               __uint_as_float(o[i + 2 * e + 1]) * inv)
+                                                   : 0u;
+                                dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    } else if (valid) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(A.part_o + (slot * rows_cta + prow) * A.D + col0 + d);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            if (col0 + d + i < A.D) dst[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.o_free));
+            if (writes && col0 == 0) {
+                if (whole_item) {
+                    if (A.lse) A.lse[orow] = l > 0.f ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
+                } else {
+                    A.part_ml[slot * rows_cta + prow] = make_float2(m, l);
+                }
+            }
+            if (s.i0 > 0 && threadIdx.x == 0) {
+                // this CTA's first unit lies inside an item: if the item began in the
+                // CTA before, this is its first cut, where its parts are joined
+                const long long first_cta = s.start / run, last_cta = (s.start + g.nt - 1) / run;
+                if (first_cta == (long long)blockIdx.x - 1) {
+                    joins = true;
+                    A.joins[2 * blockIdx.x] = make_int4(s.b, s.hk, s.node0, 0);
+                    A.joins[2 * blockIdx.x + 1] = make_int4(1, (int)first_cta, (int)last_cta, 0);
+                }
+            }
+        }
+        if (threadIdx.x == 0 && !joins) A.joins[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        if (!ok) *abort = 1;
+    }
+
+    if (warp < 8) {  // the nodes past every row tile (past the counts) see nothing
+        const int npt = ta_nodes<SPLIT_ROWS>(A);
+        for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+            const Geo g = ta_geo(A, b);
+            const int n0 = min(A.N, (g.cnt + npt - 1) / npt * npt);
+            if (n0 >= A.N) continue;
+            const long long r0 = ((long long)b * A.N + n0) * A.Hq, r1 = ((long long)b * A.N + A.N) * A.Hq;
+            uint4 *o = reinterpret_cast<uint4 *>(A.out);
+            for (long long i = r0 * A.D / 8 + threadIdx.x; i < r1 * A.D / 8; i += 256) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (A.lse)
+                for (long long i = r0 + threadIdx.x; i < r1; i += 256) A.lse[i] = -INFINITY;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && sh.abort) flag(A.status, SPEC_DEV_TIMEOUT);
+}
+
+// The parts of an item that cuts fell into, joined: one warp per row.
+// joins[2 j + 1].x: the first cut of an item lies at CTA j's first unit; its parts
+// are slot 1 of the CTA where it begins and slot 0 of the CTAs after it.
+template <int DT>
+__global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta) {
+    pdl_trigger();
+    pdl_wait();
+    const int4 z = A.joins[2 * blockIdx.x + 1];
+    if (z.x == 0) return;
+    const int4 a = A.joins[2 * blockIdx.x];
+    const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (prow >= rows_cta) return;
+    const int stream = prow / rows_used, row = prow - stream * rows_used;
+    const int local = row / A.G, node = a.z + stream * A.np + local;
+    if (node >= A.N) return;
+    const int first = z.y, parts = z.z - z.y + 1;
+    auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * rows_cta + prow; };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, A.part_ml[slot(i)].x);
+    m = warp_max(m);
+    const long long orow = ((long long)a.x * A.N + node) * A.Hq + (long long)a.y * A.G + (row - local * A.G);
+    uint2 *dst = reinterpret_cast<uint2 *>(A.out + orow * A.D) + lane;
+    if (m == -INFINITY) {
+        if (4 * lane < A.D) *dst = make_uint2(0u, 0u);
+        if (lane == 0 && A.lse) A.lse[orow] = -INFINITY;
+        return;
+    }
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < parts) {
+            const float2 x = A.part_ml[slot(i0 + lane)];
+            w = ex2(x.x - m);
+            l = fmaf(x.y, w, l);
+        }
+        const int k = min(32, parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < k; ++i) {
+            const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
+            if (4 * lane < A.D) {
+                const float4 x = reinterpret_cast<const float4 *>(A.part_o + slot(i0 + i) * A.D)[lane];
+                o.x = fmaf(x.x, wi, o.x);
+                o.y = fmaf(x.y, wi, o.y);
+                o.z = fmaf(x.z, wi, o.z);
+                o.w = fmaf(x.w, wi, o.w);
+            }
+        }
+    }
+    l = warp_sum(l);
+    const float inv = 1.f / l;
+    if (4 * lane < A.D) *dst = make_uint2(pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv));
+    if (lane == 0 && A.lse) A.lse[orow] = 0.69314718056f * (m + log2f(l));
+}
+
+// ------------------------------------------------------------------ host
+
+// A 4D tensor map over 16-bit elements, 64 of them (128 bytes, the swizzle
+// span) wide; elements past an extent read as zero.
+static bool ta_tmap(CUtensorMap *tm, int dtype, const void *base, const cuuint64_t (&dims)[4],
+                    const cuuint64_t (&strides)[3], cuuint32_t box1, cuuint32_t box2) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    if (!encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return false;
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    const cuuint32_t box[4] = {64, box1, box2, 1}, estr[4] = {1, 1, 1, 1};
+    return encode(tm, dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a stream: whole nodes, at most 128 rows.  Up to one stream's worth
+// the streams share the rows and split the keys; more nodes are spread evenly
+// over the streams of as few row tiles as hold them.
+struct TaRows {
+    int np, used, cta;
+    bool split;
+};
+static TaRows ta_rows(int N, int G) {
+    TaRows r;
+    const int most = kTaRows / G;
+    r.split = N > most;
+    const int tiles = (N + 2 * most - 1) / (2 * most), nodes = (N + tiles - 1) / tiles;
+    r.np = r.split ? (nodes + 1) / 2 : N;
+    r.used = r.np * G;
+    r.cta = r.used * (r.split ? 2 : 1);
+    return r;
+}
+
+struct TaLayout {
+    size_t o, ml, joins, total;
+};
+static TaLayout ta_layout(int N, int Hq, int heads, int D) {
+    TaLayout L;
+    const size_t rows = (size_t)kTaMaxCtas * 2 * ta_rows(N, Hq / heads).cta;
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    L.o = 0;
+    L.ml = up(rows * (size_t)D * sizeof(float));
+    L.joins = up(L.ml + rows * sizeof(float2));
+    L.total = up(L.joins + (size_t)kTaMaxCtas * 2 * sizeof(int4));
+    return L;
+}
+
+template <int DT, int DP, bool SPLIT_ROWS>
+static spec_status_t ta_launch(const TaArgs &A, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                               const TaRows &r, int ctas, int dev, cudaStream_t s) {
+    constexpr size_t smem = sizeof(TaShared<DP, SPLIT_ROWS>) + 1024;
+    static_assert(smem <= 232448, "shared memory of a CTA");
+    static bool ready[64] = {};
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(tree_attn<DT, DP, SPLIT_ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem) != cudaSuccess)
+            return SPEC_ERR_CUDA;
+        ready[dev] = true;
+    }
+    const spec_status_t st =
+        launch_pdl(tree_attn<DT, DP, SPLIT_ROWS>, dim3((unsigned)ctas), dim3(kTaThreads), smem, s, q, k, v, A);
+    if (st != SPEC_OK) return st;
+    return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((r.cta + 7) / 8)), dim3(256), 0, s, A,
+                      r.used, r.cta);
 }
 
 } // namespace sv
@@ -125,7 +938,7 @@ size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int heads, int 
     if (B < 1 || B >= (1 << 16) || N < 1 || N > SPEC_MAX_TREE || heads < 1 || heads > 1024 || Hq < heads ||
         Hq % heads || Hq / heads > 64 || head_dim < 8 || head_dim % 8 || head_dim > SPEC_MAX_HEAD_DIM)
         return 0;
-    return 256;
+    return sv::ta_layout(N, Hq, heads, head_dim).total;
 }
 
 spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long q_stride_n,
@@ -135,24 +948,31 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
                                   int Hq, int max_pages, float scale, int window, int sinks,
                                   void *out, float *lse, void *workspace, size_t workspace_bytes,
                                   uint32_t *dev_status, void *stream) {
-    sv::AttnArgs A = {};
-    const spec_status_t st = sv::make_pool(pages, A.P);
+    sv::Pool P;
+    const spec_status_t st = sv::make_pool(pages, P);
     if (st != SPEC_OK) return st;
     if (pages->dtype != SPEC_DTYPE_BF16 && pages->dtype != SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
-    const size_t need = spec_tree_attention_workspace_bytes(B, N, Hq, pages->heads, pages->head_dim);
+    const int D = pages->head_dim, H = pages->heads;
+    const size_t need = spec_tree_attention_workspace_bytes(B, N, Hq, H, D);
     if (!q || !page_table || !cache_len || !out || need == 0 || pages->layers != 1 || max_pages < 1 ||
-        ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || q_stride_b < 0 || q_stride_n < 0 || q_stride_h < 0 ||
-        q_stride_b % 8 || q_stride_n % 8 || q_stride_h % 8 || window < 0 || sinks < 0 || !(scale > 0.f) ||
+        ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || window < 0 || sinks < 0 || !(scale > 0.f) ||
         !(scale < 3.0e38f))
         return SPEC_ERR_INVALID_ARG;
+    const long long qst[3] = {q_stride_h, q_stride_n, q_stride_b};
+    const int qext[3] = {Hq, N, B};
+    for (int i = 0; i < 3; ++i)
+        if (qst[i] % 8 || qst[i] < (qext[i] > 1 ? D : 0)) return SPEC_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need) return SPEC_ERR_WORKSPACE;
-    A.P.page_st = pages->page_stride;
-    A.P.token = pages->token_stride;
-    A.P.head = pages->head_stride;
-    A.q = static_cast<const uint16_t *>(q);
-    A.qb = q_stride_b;
-    A.qn = q_stride_n;
-    A.qh = q_stride_h;
+    int dev = 0;
+    static int sms[64] = {};
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    const int ctas = sms[dev] < sv::kTaMaxCtas ? sms[dev] : sv::kTaMaxCtas;
+
+    const sv::TaRows r = sv::ta_rows(N, Hq / H);
+    const sv::TaLayout L = sv::ta_layout(N, Hq, H, D);
+    sv::TaArgs A = {};
     A.table = page_table;
     A.len = cache_len;
     A.parent = parent;
@@ -160,17 +980,52 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     A.B = B;
     A.N = N;
     A.Hq = Hq;
-    A.D = pages->head_dim;
+    A.H = H;
+    A.G = Hq / H;
+    A.D = D;
     A.max_pages = max_pages;
+    A.num_pages = P.num_pages;
+    A.page = P.page;
+    A.page_shift = P.page_shift;
     A.window = window;
     A.sinks = sinks;
+    A.np = r.np;
+    A.box = P.page < sv::kTaKeys ? P.page : sv::kTaKeys;
     A.scale_log2 = scale * 1.44269504089f;
     A.out = static_cast<uint16_t *>(out);
     A.lse = lse;
+    char *ws = static_cast<char *>(workspace);
+    A.part_o = reinterpret_cast<float *>(ws + L.o);
+    A.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
+    A.joins = reinterpret_cast<int4 *>(ws + L.joins);
     A.status = dev_status;
-    return sv::launch_pdl(pages->dtype == SPEC_DTYPE_BF16 ? sv::sv_tree_attn<SPEC_DTYPE_BF16>
-                                                          : sv::sv_tree_attn<SPEC_DTYPE_F16>,
-                          dim3((unsigned)N * Hq, (unsigned)B), dim3(32), 0, static_cast<cudaStream_t>(stream), A);
+
+    CUtensorMap tq, tk, tv;
+    // an extent of one is never stepped over: any valid stride stands for it
+    auto bytes = [&](long long stride, int extent) { return (cuuint64_t)(extent > 1 ? stride : D) * 2; };
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)N, (cuuint64_t)B};
+    const cuuint64_t qs[3] = {bytes(q_stride_h, Hq), bytes(q_stride_n, N), bytes(q_stride_b, B)};
+    const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)P.page, (cuuint64_t)H, (cuuint64_t)P.num_pages};
+    const cuuint64_t ks[3] = {bytes(pages->token_stride, P.page), bytes(pages->head_stride, H),
+                              bytes(pages->page_stride, P.num_pages)};
+    if (!sv::ta_tmap(&tq, pages->dtype, q, qd, qs, (cuuint32_t)A.G, (cuuint32_t)r.np) ||
+        !sv::ta_tmap(&tk, pages->dtype, pages->k, kd, ks, (cuuint32_t)A.box, 1) ||
+        !sv::ta_tmap(&tv, pages->dtype, pages->v, kd, ks, (cuuint32_t)A.box, 1))
+        return SPEC_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf = pages->dtype == SPEC_DTYPE_BF16;
+    if (D <= 64) {
+        if (r.split)
+            return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 64, true>(A, tq, tk, tv, r, ctas, dev, s)
+                      : sv::ta_launch<SPEC_DTYPE_F16, 64, true>(A, tq, tk, tv, r, ctas, dev, s);
+        return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 64, false>(A, tq, tk, tv, r, ctas, dev, s)
+                  : sv::ta_launch<SPEC_DTYPE_F16, 64, false>(A, tq, tk, tv, r, ctas, dev, s);
+    }
+    if (r.split)
+        return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 128, true>(A, tq, tk, tv, r, ctas, dev, s)
+                  : sv::ta_launch<SPEC_DTYPE_F16, 128, true>(A, tq, tk, tv, r, ctas, dev, s);
+    return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 128, false>(A, tq, tk, tv, r, ctas, dev, s)
+              : sv::ta_launch<SPEC_DTYPE_F16, 128, false>(A, tq, tk, tv, r, ctas, dev, s);
 }
 
 } // extern "C"
