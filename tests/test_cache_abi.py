@@ -12,12 +12,16 @@ def lib():
     return sv.load_library()
 
 
+FIELDS = ("k", "v", "dtype", "layers", "num_pages", "page_size", "heads", "head_dim", "layer_stride", "page_stride",
+          "token_stride", "head_stride")
+
+
 def _pages(**kw):
     from speculative_decoding_verification_69_gb300 import cache
     d = dict(k=0x10000, v=0x10000, dtype=1, layers=1, num_pages=10, page_size=16, heads=2, head_dim=64,
              layer_stride=10 * 16 * 128, page_stride=16 * 128, token_stride=128, head_stride=64)
     d.update(kw)
-    return cache._Pages(*[d[n] for n, _ in cache._Pages._fields_])
+    return cache._PAGES.pack(*[d[n] or 0 for n in FIELDS])
 
 
 BAD_POOLS = [dict(k=None), dict(v=None), dict(layers=0), dict(num_pages=0), dict(page_size=4), dict(page_size=24),
@@ -37,8 +41,8 @@ def test_pools_are_checked(lib):
     ]
     for call in calls:
         for bad in BAD_POOLS:
-            assert call(ctypes.byref(_pages(**bad))) == 1, bad
-        assert call(ctypes.byref(_pages(dtype=7))) == 2
+            assert call(_pages(**bad)) == 1, bad
+        assert call(_pages(dtype=7)) == 2
         assert call(None) == 1
 
 
@@ -62,7 +66,7 @@ def test_fork_refusals(lib):
 
     def call(**kw):
         a = dict(base, **kw)
-        return lib.spec_cache_fork(ctypes.byref(p), a["t"], a["c"], a["r"], a["l"], a["s"], a["d"], a["F"], a["S"],
+        return lib.spec_cache_fork(p, a["t"], a["c"], a["r"], a["l"], a["s"], a["d"], a["F"], a["S"],
                                    a["P"], a["ws"], a["n"], None, None)
     for bad in (dict(t=None), dict(c=None), dict(r=None), dict(l=None), dict(s=None), dict(d=None), dict(F=0),
                 dict(F=8193), dict(S=0), dict(S=8193), dict(P=0)):
@@ -75,7 +79,7 @@ def test_append_and_commit_refusals(lib):
 
     def app(**kw):
         a = dict(base, **kw)
-        return lib.spec_cache_append(ctypes.byref(a["p"]), a["t"], a["l"], a["k"], a["v"], a["sb"], a["sn"], a["sh"],
+        return lib.spec_cache_append(a["p"], a["t"], a["l"], a["k"], a["v"], a["sb"], a["sn"], a["sh"],
                                      None, a["B"], a["N"], a["P"], None, None)
     for bad in (dict(t=None), dict(l=None), dict(k=None), dict(v=None), dict(k=ctypes.c_void_p(0x10008)), dict(sb=4),
                 dict(sn=-128), dict(sh=63), dict(B=0), dict(B=1 << 16), dict(N=0), dict(P=0),
@@ -83,7 +87,7 @@ def test_append_and_commit_refusals(lib):
         assert app(**bad) == 1, bad
 
     def com(t=FAKE, l=FAKE, a=FAKE, new=FAKE, B=2, N=4, P=8):
-        return lib.spec_cache_commit(ctypes.byref(_pages()), t, l, FAKE, a, new, B, N, P, None, None)
+        return lib.spec_cache_commit(_pages(), t, l, FAKE, a, new, B, N, P, None, None)
     for bad in (dict(t=None), dict(l=None), dict(a=None), dict(new=None), dict(B=0), dict(B=1 << 16), dict(N=0),
                 dict(N=65), dict(P=0)):
         assert com(**bad) == 1, bad
@@ -100,7 +104,7 @@ def test_attention_refusals(lib):
 
     def call(**kw):
         a = dict(base, **kw)
-        return lib.spec_tree_attention(a["q"], a["sb"], a["sn"], a["sh"], ctypes.byref(a["p"]), a["t"], a["l"], None,
+        return lib.spec_tree_attention(a["q"], a["sb"], a["sn"], a["sh"], a["p"], a["t"], a["l"], None,
                                        None, a["B"], a["N"], a["Hq"], a["P"], a["scale"], a["w"], a["s"], a["o"], None,
                                        a["ws"], a["n"], None, None)
     for bad in (dict(q=None), dict(t=None), dict(l=None), dict(o=None), dict(q=ctypes.c_void_p(0x10008)),
