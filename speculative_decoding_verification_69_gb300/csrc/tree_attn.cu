@@ -41,7 +41,8 @@ namespace sv {
 
 constexpr int kTaKeys = 128;        // keys of a tile (MMA N of S, MMA K of O)
 constexpr int kTaRows = 128;        // rows of a stream (MMA M, TMEM lanes)
-constexpr int kTaThreads = 320;     // 8 softmax warps, the TMA warp, the MMA warp
+constexpr int kTaThreads = 352;     // 8 softmax warps, the TMA, MMA and scheduling warps
+constexpr int kTaSlots = 4;         // segments the scheduler may be ahead
 constexpr int kTaMaxCtas = 160;     // CTAs the workspace has room for
 constexpr int kTaChunks = 128;      // entries of the running sum over requests
 constexpr unsigned long long kTaWaitNs = 2000000000ull;  // 2 s
@@ -67,20 +68,8 @@ template <int DP, bool SPLIT_ROWS> struct TaCfg {
     static constexpr int kQ = kStreamQ * (SPLIT_ROWS ? 2 : 1);
     static constexpr int kStage = kTaKeys * DP * 2;              // one K or V tile
     // as many tiles in flight as the shared memory holds beside Q
-    static constexpr int kStages = DP == 128 ? 5 : 11;
+    static constexpr int kStages = DP == 128 ? 4 : 10;
     static constexpr int kRowsCta = kTaRows * (SPLIT_ROWS ? 2 : 1);
-};
-
-template <int DP, bool SPLIT_ROWS> struct TaShared {
-    using C = TaCfg<DP, SPLIT_ROWS>;
-    uint8_t q[C::kQ];
-    uint8_t kv[C::kStages][C::kStage];
-    long long incl[kTaChunks];  // units of the requests up to the end of each chunk of them
-    uint64_t full[C::kStages], empty[C::kStages];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, ml_full, done;
-    uint32_t tmem_base;
-    int abort;
-    float2 ml[SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : kTaRows];  // [segment parity][stream][row]
 };
 
 // What one request's tiles cover: positions [0, min(sinks, ...)) in its first
@@ -116,6 +105,26 @@ struct Seg {
     int b, hk, node0;   // node0: first node of the row tile
     int i0, n;          // tiles [i0, i0 + n) of the g.nt
     long long start;    // unit of tile 0
+};
+
+// A segment as the scheduling warp hands it to the others; n = 0 ends the list.
+struct SegSlot {
+    Seg s;
+    unsigned long long path[SPEC_MAX_TREE];  // the nodes on the path to each node
+};
+
+template <int DP, bool SPLIT_ROWS> struct TaShared {
+    using C = TaCfg<DP, SPLIT_ROWS>;
+    uint8_t q[C::kQ];
+    uint8_t kv[C::kStages][C::kStage];
+    long long incl[kTaChunks];  // units of the requests up to the end of each chunk of them
+    SegSlot seg[kTaSlots];
+    uint64_t seg_full[kTaSlots], seg_free[kTaSlots];
+    uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, ml_full, done;
+    uint32_t tmem_base;
+    int abort;
+    float2 ml[SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : kTaRows];  // [segment parity][stream][row]
 };
 
 template <bool SPLIT_ROWS> __device__ __forceinline__ int ta_nodes(const TaArgs &A) {
@@ -321,6 +330,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.pv_done[i], 1);
         }
+        for (int i = 0; i < kTaSlots; ++i) {
+            mbar_init(&sh.seg_full[i], 1);
+            mbar_init(&sh.seg_free[i], 8 + 2);
+        }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_free, 1);
         mbar_init(&sh.o_free, 8);
@@ -370,15 +383,50 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const long long run = (total + gridDim.x - 1) / gridDim.x;
     const long long u_first = min(total, (long long)blockIdx.x * run), u_last = min(total, u_first + run);
 
-    if (warp == 8) {  // ------------------------------------------------ TMA
+    // segment k, or nothing when the wait for it ran out
+    auto take = [&](int k) -> const SegSlot * {
+        const bool ok = lm_wait(&sh.seg_full[k % kTaSlots], (k / kTaSlots) & 1, abort, kTaWaitNs);
+        return __all_sync(0xFFFFFFFFu, ok) ? &sh.seg[k % kTaSlots] : nullptr;
+    };
+    auto give = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_free[k % kTaSlots]));
+    };
+
+    if (warp == 10) {  // ----------------------------------------------- scheduling
+        int k = 0, b = -1;
+        bool ok = true;
+        unsigned long long anc[2] = {0, 0};
+        for (long long u = u_first; ok; ++k) {
+            Seg s = {};
+            if (u < u_last) {
+                s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
+                u += s.n;
+                if (s.b != b) ta_paths(A, b = s.b, s.g.cnt, anc);
+            }
+            if (k >= kTaSlots)
+                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort, kTaWaitNs));
+            if (!ok) break;
+            SegSlot &slot = sh.seg[k % kTaSlots];
+            if (lane == 0) slot.s = s;
+            slot.path[lane] = anc[0];
+            slot.path[lane + 32] = anc[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_full[k % kTaSlots]));
+            if (s.n == 0) break;
+        }
+        __syncwarp();
+    } else if (warp == 8) {  // ----------------------------------------- TMA
         uint32_t it = 0;  // tiles loaded so far
         int seg_no = 0;
         const int nb = kTaKeys / A.box;             // boxes of a tile
         const int ahead = 32 / nb;                  // tiles whose pages one load of the warp fetches
         bool ok = true;
-        for (long long u = u_first; u < u_last && ok; ++seg_no) {
-            const Seg s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
-            u += s.n;
+        for (;; ++seg_no) {
+            const SegSlot *sp = take(seg_no);
+            if (!sp || sp->s.n == 0) break;
+            const Seg s = sp->s;
+            give(seg_no);
             const int *row = A.table + (long long)s.b * A.max_pages;
             // is any position of the box of this lane in tile i seen by some node
             auto box_pos = [&](int i, int box) -> long long { return (long long)s.g.tile(i) * kTaKeys + box * A.box; };
@@ -410,6 +458,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 }
             }
             ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            if (!ok) break;
             // two windows of page numbers: K runs ahead of V by at most two tiles
             int base = s.i0, cur = fetch(base), nxt = fetch(base + ahead);
             int prev = 0;
@@ -451,6 +500,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 }
                 __syncwarp();
             }
+            if (!ok) {
+                ++seg_no;
+                break;
+            }
         }
         if (lane == 0) {  // every copy has landed before the CTA may exit
             for (int s = 0; s < kSt; ++s) {
@@ -466,9 +519,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         bool ok = true;
         const int ks = (A.D + 15) / 16;    // k steps of S
         constexpr uint32_t kIdS = ta_idesc<DT>(kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
-        for (long long u = u_first; u < u_last && ok; ++seg_no) {
-            const Seg s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
-            u += s.n;
+        for (; ok; ++seg_no) {
+            const SegSlot *sp = take(seg_no);
+            if (!sp || sp->s.n == 0) break;
+            const Seg s = sp->s;
+            give(seg_no);
             if (lane == 0) {
                 auto stage_of = [&](uint32_t idx) { return (int)((base + idx) % kSt); };
                 auto wait_full = [&](uint32_t idx) {
@@ -551,17 +606,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         uint32_t base = 0, tiles[2] = {0, 0};  // loads before this segment, tiles done per stream
         int seg_no = 0;
         bool ok = true, joins = false;
-        for (long long u = u_first; u < u_last && ok; ++seg_no) {
-            const Seg s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
-            u += s.n;
+        for (; ok; ++seg_no) {
+            const SegSlot *sp = take(seg_no);
+            if (!sp || sp->s.n == 0) break;
+            const Seg s = sp->s;
             const Geo &g = s.g;
             const int local = row / A.G, node = s.node0 + (SPLIT_ROWS ? stream * A.np : 0) + local;
             const bool valid = row < rows_used && node < g.cnt;
-            unsigned long long anc[2];
-            ta_paths(A, s.b, g.cnt, anc);
-            const unsigned long long a0 = __shfl_sync(0xFFFFFFFFu, anc[0], node & 31),
-                                     a1 = __shfl_sync(0xFFFFFFFFu, anc[1], node & 31);
-            unsigned long long path = valid ? (node < 32 ? a0 : a1) : 0ull;
+            unsigned long long path = valid ? sp->path[node] : 0ull;
+            give(seg_no);
             const int tip = g.c + __popcll(path) - 1;  // the node's place
             int low = 0;                               // first committed position in its window
             if (A.window) {
