@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     const uint64_t vd = v_desc(smem_u32(sh.kv[st]));
 #pragma unroll
                     for (int k = 0; k < kTaKeys / 16; ++k)
-                        mma_ts(tmem + 256u + (uint32_t)(i * DP), tmem + (uint32_t)(i * kTaKeys + k * 8),
+                        mma_ts(tmem + 256u + (uint32_t)(i * DP), tmem + (uint32_t)(i * kTaKeys + kTaKeys / 2 + k * 8),
                                vd + (uint64_t)(k * 2048 / 16), kIdO, first && k == 0 ? 0u : 1u);
                     umma_commit(&sh.pv_done[i]);
                     if (release) umma_commit(&sh.empty[st]);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     } else {  // ---------------------------------------------------- softmax
         const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S, then P
+        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S; P over its second half
         const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);        // O
         const int rows_used = A.np * A.G;
         uint32_t base = 0, tiles[2] = {0, 0};  // loads before this segment, tiles done per stream
@@ -637,12 +637,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_works) {
-                    uint32_t x[kTaKeys];
-                    tmem_load(ts, x);
+                    // 64 scores at a time in registers; the other half is read twice
+                    // rather than kept (128 of a thread's 168 registers would spill)
+                    uint32_t x[64], seen[kTaKeys / 32];
                     const bool whole = j0 + kTaKeys <= g.c && (j0 >= low || j0 + kTaKeys <= A.sinks);
-                    if (!__all_sync(0xFFFFFFFFu, whole || !valid)) {
+                    const bool masked = !__all_sync(0xFFFFFFFFu, whole || !valid);
+                    if (masked) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
+                        for (int w = 0; w < kTaKeys / 32; ++w) {
                             const long long jw = j0 + 32 * w;
                             uint32_t bits = 0;
                             if (valid) {
@@ -651,17 +653,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                                 if (sft >= 0 && sft < 64) bits |= (uint32_t)(path >> sft);
                                 else if (sft < 0 && sft > -32) bits |= (uint32_t)(path << -sft);
                             }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((bits >> i) & 1u)) x[32 * w + i] = 0xFF800000u;
+                            seen[w] = bits;
                         }
+                        __syncwarp();
                     }
+                    auto load = [&](int part) {
+                        tmem_load(ts + 64 * part, x);
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (!((seen[2 * part + (i >> 5)] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+                        }
+                    };
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < kTaKeys; i += 8) {
+                    for (int part = 0; part < 2; ++part) {
+                        load(part);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
+                        for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
+                        }
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
                     if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kTaGrow))) {
@@ -688,17 +701,21 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     const float2 c2 = make_float2(A.scale_log2, A.scale_log2), nm2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t p[16];
+                    for (int part = 1; part >= 0; --part) {  // the second half is still in registers
+                        if (part == 0) load(0);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 z = fma2(make_float2(__uint_as_float(x[32 * q + 2 * i]),
-                                                              __uint_as_float(x[32 * q + 2 * i + 1])), c2, nm2);
-                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                            sum[i & 1] = add2(sum[i & 1], e);
-                            p[i] = pack2<DT>(e.x, e.y);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 z = fma2(make_float2(__uint_as_float(x[32 * h + 2 * i]),
+                                                                  __uint_as_float(x[32 * h + 2 * i + 1])), c2, nm2);
+                                const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                                sum[i & 1] = add2(sum[i & 1], e);
+                                p[i] = pack2<DT>(e.x, e.y);
+                            }
+                            tmem_store(ts + kTaKeys / 2 + 32 * part + 16 * h, p);
                         }
-                        tmem_store(ts + 16 * q, p);
                     }
                     l2 = add2(l2, add2(sum[0], sum[1]));
                     tmem_wait_store();
