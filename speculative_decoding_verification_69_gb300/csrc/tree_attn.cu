@@ -41,7 +41,8 @@ namespace sv {
 
 constexpr int kTaKeys = 128;        // keys of a tile (MMA N of S, MMA K of O)
 constexpr int kTaRows = 128;        // rows of a stream (MMA M, TMEM lanes)
-constexpr int kTaThreads = 352;     // 8 softmax warps, the TMA, MMA and scheduling warps
+constexpr int kTaThreads = 384;     // 8 softmax warps, then K loads, products, scheduling and V loads
+constexpr int kTaWarpK = 8, kTaWarpMma = 9, kTaWarpPlan = 10, kTaWarpV = 11;
 constexpr int kTaSlots = 4;         // segments the scheduler may be ahead
 constexpr int kTaMaxCtas = 160;     // CTAs the workspace has room for
 constexpr int kTaChunks = 128;      // entries of the running sum over requests
@@ -68,8 +69,8 @@ template <int DP, bool SPLIT_ROWS> struct TaCfg {
     static constexpr int kQ = kStreamQ * (SPLIT_ROWS ? 2 : 1);
     static constexpr int kStage = kTaKeys * DP * 2;              // one K or V tile
     // as many tiles in flight as the shared memory holds beside Q
-    static constexpr int kStages = DP == 128 ? 4 : 10;
-    static constexpr int kRowsCta = kTaRows * (SPLIT_ROWS ? 2 : 1);
+    static constexpr int kStagesK = DP == 128 ? 2 : (SPLIT_ROWS ? 5 : 6);
+    static constexpr int kStagesV = DP == 128 ? (SPLIT_ROWS ? 2 : 3) : 6;
 };
 
 // What one request's tiles cover: positions [0, min(sinks, ...)) in its first
@@ -116,11 +117,11 @@ struct SegSlot {
 template <int DP, bool SPLIT_ROWS> struct TaShared {
     using C = TaCfg<DP, SPLIT_ROWS>;
     uint8_t q[C::kQ];
-    uint8_t kv[C::kStages][C::kStage];
+    uint8_t k[C::kStagesK][C::kStage], v[C::kStagesV][C::kStage];
     long long incl[kTaChunks];  // units of the requests up to the end of each chunk of them
     SegSlot seg[kTaSlots];
-    uint64_t seg_full[kTaSlots], seg_free[kTaSlots];
-    uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
+    uint64_t k_full[C::kStagesK], k_empty[C::kStagesK], v_full[C::kStagesV], v_empty[C::kStagesV];
     uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, ml_full, done;
     uint32_t tmem_base;
     int abort;
@@ -184,16 +185,6 @@ __device__ __forceinline__ Seg ta_segment(const TaArgs &A, const long long *incl
     return s;
 }
 
-// Position of a tile in the order in which a segment of n tiles loads and uses
-// them.  SPLIT_ROWS: K0 V0 K1 V1 ...; else K0 K1 V0 K2 V1 K3 ... (both streams'
-// scores first).
-template <bool SPLIT_ROWS> __device__ __forceinline__ uint32_t k_index(int t) {
-    return SPLIT_ROWS ? 2u * t : (t < 2 ? (uint32_t)t : 2u * t - 1u);
-}
-template <bool SPLIT_ROWS> __device__ __forceinline__ uint32_t v_index(int t, int n) {
-    return SPLIT_ROWS ? 2u * t + 1u : (t + 1 < n ? 2u * t + 2u : 2u * t + 1u);
-}
-
 // ------------------------------------------------------------------ PTX
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, int x, int y, int z, int w,
@@ -203,6 +194,26 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, in
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
+}
+
+// True in one lane of a converged warp.  Products and copies are issued under
+// this predicate, with operands that are the same in all lanes: the compiler
+// then knows them to be uniform and issues them back to back.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one)::"memory");
+    return one != 0;
+}
+
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // D (TMEM) (+)= A (shared) B (shared)
@@ -314,16 +325,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     extern __shared__ uint8_t ta_raw[];
     Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(ta_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kSt = C::kStages;
+    constexpr int kKS = C::kStagesK, kVS = C::kStagesV;
     constexpr int kHalves = DP / 64;
     // P is scaled up to 2^15 in float16, so that weights 2^-29 below the
     // maximum are still normal numbers; bfloat16 has float32's range
     constexpr float kLift = DT == SPEC_DTYPE_F16 ? 7.f : 0.f;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kSt; ++s) {
-            mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+        for (int s = 0; s < kKS; ++s) {
+            mbar_init(&sh.k_full[s], 1);
+            mbar_init(&sh.k_empty[s], 1);
+        }
+        for (int s = 0; s < kVS; ++s) {
+            mbar_init(&sh.v_full[s], 1);
+            mbar_init(&sh.v_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -332,7 +347,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         for (int i = 0; i < kTaSlots; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_free[i], 8 + 2);
+            mbar_init(&sh.path_full[i], 1);
+            mbar_init(&sh.seg_free[i], 8 + 3);
         }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_free, 1);
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
     }
-    if (warp == 9) {
+    if (warp == kTaWarpMma) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
     }
@@ -384,8 +400,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const long long u_first = min(total, (long long)blockIdx.x * run), u_last = min(total, u_first + run);
 
     // segment k, or nothing when the wait for it ran out
-    auto take = [&](int k) -> const SegSlot * {
-        const bool ok = lm_wait(&sh.seg_full[k % kTaSlots], (k / kTaSlots) & 1, abort, kTaWaitNs);
+    auto take = [&](uint64_t *bars, int k) -> const SegSlot * {
+        const bool ok = lm_wait(&bars[k % kTaSlots], (k / kTaSlots) & 1, abort, kTaWaitNs);
         return __all_sync(0xFFFFFFFFu, ok) ? &sh.seg[k % kTaSlots] : nullptr;
     };
     auto give = [&](int k) {
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_free[k % kTaSlots]));
     };
 
-    if (warp == 10) {  // ----------------------------------------------- scheduling
+    if (warp == kTaWarpPlan) {  // ----------------------------------------------- scheduling
         int k = 0, b = -1;
         bool ok = true;
         unsigned long long anc[2] = {0, 0};
@@ -402,41 +418,52 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (u < u_last) {
                 s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
                 u += s.n;
-                if (s.b != b) ta_paths(A, b = s.b, s.g.cnt, anc);
             }
             if (k >= kTaSlots)
                 ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort, kTaWaitNs));
             if (!ok) break;
             SegSlot &slot = sh.seg[k % kTaSlots];
-            if (lane == 0) slot.s = s;
+            if (lane == 0) {
+                slot.s = s;
+                mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_full[k % kTaSlots]));
+            }
+            // the loads and scores go ahead; the softmax warps need the paths too
+            if (s.n > 0 && s.b != b) ta_paths(A, b = s.b, s.g.cnt, anc);
             slot.path[lane] = anc[0];
             slot.path[lane + 32] = anc[1];
             __syncwarp();
-            if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_full[k % kTaSlots]));
+            if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.path_full[k % kTaSlots]));
             if (s.n == 0) break;
         }
         __syncwarp();
-    } else if (warp == 8) {  // ----------------------------------------- TMA
-        uint32_t it = 0;  // tiles loaded so far
-        int seg_no = 0;
+    } else if (warp == kTaWarpK || warp == kTaWarpV) {  // --------------- loads
+        const bool is_k = warp == kTaWarpK;
+        const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
+        uint8_t *tiles = is_k ? sh.k[0] : sh.v[0];
+        uint64_t *full = is_k ? sh.k_full : sh.v_full, *empty = is_k ? sh.k_empty : sh.v_empty;
+        const uint32_t stages = is_k ? kKS : kVS;
+        uint32_t stage = 0, fill = 0;               // next stage, and how often all have been filled
+        int seg_no = 0, q_loads = 0;
         const int nb = kTaKeys / A.box;             // boxes of a tile
         const int ahead = 32 / nb;                  // tiles whose pages one load of the warp fetches
+        const int box = lane % nb;
         bool ok = true;
-        for (;; ++seg_no) {
-            const SegSlot *sp = take(seg_no);
+        for (; ok; ++seg_no) {
+            const SegSlot *sp = take(sh.seg_full, seg_no);
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             give(seg_no);
             const int *row = A.table + (long long)s.b * A.max_pages;
-            // is any position of the box of this lane in tile i seen by some node
-            auto box_pos = [&](int i, int box) -> long long { return (long long)s.g.tile(i) * kTaKeys + box * A.box; };
+            const int i_end = s.i0 + s.n;
+            // first position of this lane's box in tile i, and whether some node sees any of it
+            auto box_pos = [&](int i) -> long long { return (long long)s.g.tile(i) * kTaKeys + box * A.box; };
             auto box_seen = [&](long long j) -> bool {
                 return j < s.g.end && (j + A.box > s.g.wlo || j < A.sinks);
             };
             auto fetch = [&](int i0) -> int {  // page of this lane's box in tile i0 + lane / nb
                 const int i = i0 + lane / nb;
-                if (i >= s.i0 + s.n) return 0;
-                const long long j = box_pos(i, lane % nb);
+                if (i >= i_end) return 0;
+                const long long j = box_pos(i);
                 if (!box_seen(j)) return 0;
                 int p = __ldcg(row + (j >> A.page_shift));
                 if ((unsigned)p >= (unsigned)A.num_pages) {
@@ -445,169 +472,170 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 }
                 return p;
             };
-            // Q of this segment once the scores of the last one are done
-            if (lane == 0) {
-                ok = seg_no == 0 || lm_wait(&sh.q_free, (seg_no - 1) & 1, abort, kTaWaitNs);
-                if (ok) {
-                    constexpr int kQs = SPLIT_ROWS ? 2 : 1;
+            int base = s.i0, cur = fetch(base), nxt = base + ahead < i_end ? fetch(base + ahead) : 0;
+            // Q of this segment once the scores of the last one are done: looked for
+            // before every load, so that the tiles need not wait for it
+            bool q_due = is_k;
+            auto issue_q = [&]() {
+                constexpr int kQs = SPLIT_ROWS ? 2 : 1;
+                if (elect_one()) {
                     mbar_expect_tx(&sh.q_full, (uint32_t)(kQs * kHalves * A.np * A.G * 128));
                     for (int q = 0; q < kQs; ++q)
                         for (int h = 0; h < kHalves; ++h)
                             tma_load_4d(sh.q + q * C::kStreamQ + h * kTaRows * 128, &tm_q, h * 64, s.hk * A.G,
                                         s.node0 + q * A.np, s.b, &sh.q_full);
                 }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-            if (!ok) break;
-            // two windows of page numbers: K runs ahead of V by at most two tiles
-            int base = s.i0, cur = fetch(base), nxt = fetch(base + ahead);
-            int prev = 0;
-            const int loads = 2 * s.n;
-            int kt = 0, vt = 0;  // next K and V tile
-            for (int x = 0; x < loads && ok; ++x, ++it) {
-                bool is_k;
-                if (SPLIT_ROWS) is_k = (x & 1) == 0;
-                else is_k = kt < s.n && (uint32_t)x == k_index<false>(kt);
-                const int t = is_k ? kt++ : vt++;
-                const int i = s.i0 + t;
-                while (i >= base + ahead) {
-                    prev = cur;
+                __syncwarp();
+                q_due = false;
+                ++q_loads;
+            };
+            auto look_q = [&]() {
+                if (q_due && __any_sync(0xFFFFFFFFu, seg_no == 0 || mbar_test_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u)))
+                    issue_q();
+            };
+            for (int i = s.i0; i < i_end && ok; ++i) {
+                if (i >= base + ahead) {
                     cur = nxt;
                     base += ahead;
-                    nxt = fetch(base + ahead);
+                    nxt = base + ahead < i_end ? fetch(base + ahead) : 0;
                 }
-                const int box = lane % nb;
-                const bool mine = lane < nb && box_seen(box_pos(i, box));
-                const int at = (i >= base ? i - base : i - base + ahead) * nb + box;
-                const int pc = __shfl_sync(0xFFFFFFFFu, cur, at & 31), pp = __shfl_sync(0xFFFFFFFFu, prev, at & 31);
-                const int page = i >= base ? pc : pp;
-                const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-                const int stage = (int)(it % kSt);
-                const uint32_t fill = it / kSt;
-                if (lane == 0) {
-                    ok = fill == 0 || lm_wait(&sh.empty[stage], (fill - 1) & 1u, abort, kTaWaitNs);
-                    if (ok) mbar_expect_tx(&sh.full[stage], (uint32_t)(boxes * kHalves * A.box * 128));
-                }
-                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-                if (!ok) break;
-                if (mine) {
-                    const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
-                    const int tok = (int)(box_pos(i, box) & (A.page - 1));
+                const uint32_t seen = __ballot_sync(0xFFFFFFFFu, lane < nb && box_seen(box_pos(i)));
+                const int page = __shfl_sync(0xFFFFFFFFu, cur, ((i - base) * nb + box) & 31);
+                const int tok = (int)(((long long)s.g.tile(i) * kTaKeys) & (A.page - 1));
+                int pages[16];  // of all boxes, in every lane
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        tma_load_4d(sh.kv[stage] + h * kTaKeys * 128 + box * A.box * 128, tm, h * 64, tok, s.hk, page,
-                                    &sh.full[stage]);
+                for (int x = 0; x < 16; ++x) pages[x] = __shfl_sync(0xFFFFFFFFu, page, x);
+                look_q();
+                if (fill > 0) {
+                    const unsigned long long t0 = global_ns();
+                    for (uint32_t tries = 1;; ++tries) {
+                        if (__any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u))) break;
+                        look_q();
+                        if ((tries & 63u) == 0 && __any_sync(0xFFFFFFFFu, *abort || global_ns() - t0 > kTaWaitNs)) {
+                            *abort = 1;
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!ok) break;
+                }
+                uint8_t *tile = tiles + stage * C::kStage;
+                if (elect_one()) {
+                    mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        if ((seen >> x) & 1u) {
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_load_4d(tile + h * kTaKeys * 128 + x * A.box * 128, tm, h * 64, tok, s.hk, pages[x],
+                                            &full[stage]);
+                        }
                 }
                 __syncwarp();
+                if (++stage == stages) stage = 0, ++fill;
             }
-            if (!ok) {
-                ++seg_no;
-                break;
+            if (ok && q_due) {
+                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u, abort, kTaWaitNs));
+                if (ok) issue_q();
             }
         }
-        if (lane == 0) {  // every copy has landed before the CTA may exit
-            for (int s = 0; s < kSt; ++s) {
-                const uint32_t n = it / kSt + ((uint32_t)s < it % kSt ? 1u : 0u);
-                if (n > 0) mbar_wait_bounded(&sh.full[s], (n - 1) & 1u, kTaWaitNs);
-            }
-            if (seg_no > 0) mbar_wait_bounded(&sh.q_full, (seg_no - 1) & 1, kTaWaitNs);
+        // every copy has landed before the CTA may exit
+        for (uint32_t x = 0; x < stages; ++x) {
+            const uint32_t n = fill + (x < stage ? 1u : 0u);
+            if (n > 0) mbar_wait_bounded(&full[x], (n - 1) & 1u, kTaWaitNs);
         }
-    } else if (warp == 9) {  // ----------------------------------------- MMA
-        uint32_t base = 0;                 // tiles used by earlier segments
+        if (q_loads > 0) mbar_wait_bounded(&sh.q_full, (uint32_t)(q_loads - 1) & 1u, kTaWaitNs);
+        __syncwarp();
+    } else if (warp == kTaWarpMma) {  // --------------------------------- products
+        uint32_t k_tile = 0, v_tile = 0;   // K and V tiles used
         uint32_t pv[2] = {0, 0};           // O products issued per stream
         int seg_no = 0;
         bool ok = true;
         const int ks = (A.D + 15) / 16;    // k steps of S
         constexpr uint32_t kIdS = ta_idesc<DT>(kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
-        for (; ok; ++seg_no) {
-            const SegSlot *sp = take(seg_no);
-            if (!sp || sp->s.n == 0) break;
-            const Seg s = sp->s;
-            give(seg_no);
-            if (lane == 0) {
-                auto stage_of = [&](uint32_t idx) { return (int)((base + idx) % kSt); };
-                auto wait_full = [&](uint32_t idx) {
-                    return lm_wait(&sh.full[stage_of(idx)], ((base + idx) / kSt) & 1u, abort, kTaWaitNs);
-                };
-                // scores of stream i against the K tile at load idx; the stream's
-                // last weights have been consumed (they share the columns)
-                auto scores = [&](int i, uint32_t idx, bool release, bool last) -> bool {
-                    if (pv[i] > 0 && !lm_wait(&sh.pv_done[i], (pv[i] - 1) & 1u, abort, kTaWaitNs)) return false;
-                    if (!wait_full(idx)) return false;
-                    tc_fence_after();
-                    const int st = stage_of(idx);
-                    const uint64_t qd = umma_desc_sw128(smem_u32(sh.q + (SPLIT_ROWS ? i : 0) * C::kStreamQ));
-                    const uint64_t kd = umma_desc_sw128(smem_u32(sh.kv[st]));
-                    for (int k = 0; k < ks; ++k) {
-                        const uint64_t off = (uint64_t)((k >> 2) * (kTaRows * 128 / 16) + (k & 3) * 2);
-                        mma_ss(tmem + (uint32_t)(i * kTaKeys), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&sh.s_full[i]);
-                    if (release) umma_commit(&sh.empty[st]);
-                    if (last) umma_commit(&sh.q_free);
-                    return true;
-                };
-                bool o_ready = seg_no == 0;
-                auto values = [&](int i, uint32_t idx, uint32_t p_use, bool first, bool release) -> bool {
-                    if (!lm_wait(&sh.p_full[i], p_use & 1u, abort, kTaWaitNs)) return false;
-                    if (!wait_full(idx)) return false;
-                    if (!o_ready) {  // the epilogue of the segment before has read O
-                        if (!lm_wait(&sh.o_free, (seg_no - 1) & 1, abort, kTaWaitNs)) return false;
-                        o_ready = true;
-                    }
-                    tc_fence_after();
-                    const int st = stage_of(idx);
-                    const uint64_t vd = v_desc(smem_u32(sh.kv[st]));
-#pragma unroll
-                    for (int k = 0; k < kTaKeys / 16; ++k)
-                        mma_ts(tmem + 256u + (uint32_t)(i * DP), tmem + (uint32_t)(i * kTaKeys + kTaKeys / 2 + k * 8),
-                               vd + (uint64_t)(k * 2048 / 16), kIdO, first && k == 0 ? 0u : 1u);
-                    umma_commit(&sh.pv_done[i]);
-                    if (release) umma_commit(&sh.empty[st]);
-                    ++pv[i];
-                    return true;
-                };
-                ok = lm_wait(&sh.q_full, seg_no & 1, abort, kTaWaitNs);
-                if (ok) {
-                    if (SPLIT_ROWS) {
-                        ok = scores(0, 0, false, false) && scores(1, 0, true, s.n == 1);
-                        for (int t = 0; t < s.n && ok; ++t) {
-                            const bool more = t + 1 < s.n;
-                            ok = values(0, v_index<true>(t, s.n), pv[0], t == 0, false);
-                            if (ok && more) ok = scores(0, k_index<true>(t + 1), false, false);
-                            if (ok) ok = values(1, v_index<true>(t, s.n), pv[1], t == 0, true);
-                            if (ok && more) ok = scores(1, k_index<true>(t + 1), true, t + 2 == s.n);
-                        }
-                    } else {
-                        ok = scores(0, 0, true, s.n == 1);
-                        if (ok && s.n > 1) ok = scores(1, 1, true, s.n == 2);
-                        for (int t = 0; t < s.n && ok; ++t) {
-                            ok = values(t & 1, v_index<false>(t, s.n), pv[t & 1], t < 2, true);
-                            if (ok && t + 2 < s.n) ok = scores(t & 1, k_index<false>(t + 2), true, t + 3 == s.n);
-                        }
-                    }
+        auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xFFFFFFFFu, lm_wait(bar, parity, abort, kTaWaitNs)) != 0;
+        };
+        // scores of stream i against the next K tile (release: its last use; last: of
+        // the segment).  They overwrite the columns of the stream's last weights: the
+        // products of a CTA's one issuing thread execute in the order of issue, so
+        // those have been consumed by then.
+        auto scores = [&](int i, bool release, bool last) -> bool {
+            const uint32_t st = k_tile % kKS;
+            if (!wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
+            tc_fence_after();
+            const uint64_t qd = umma_desc_sw128(smem_u32(sh.q + (SPLIT_ROWS ? i : 0) * C::kStreamQ));
+            const uint64_t kd = umma_desc_sw128(smem_u32(sh.k[st]));
+            if (elect_one()) {
+                for (int k = 0; k < ks; ++k) {
+                    const uint64_t off = (uint64_t)((k >> 2) * (kTaRows * 128 / 16) + (k & 3) * 2);
+                    mma_ss(tmem + (uint32_t)(i * kTaKeys), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
                 }
-                base += 2u * (uint32_t)s.n;
+                umma_commit(&sh.s_full[i]);
+                if (release) umma_commit(&sh.k_empty[st]);
+                if (last) umma_commit(&sh.q_free);
             }
-            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
             __syncwarp();
+            if (release) ++k_tile;
+            return true;
+        };
+        // O of stream i plus its weights times the next V tile (fresh: its first of the segment)
+        auto values = [&](int i, bool fresh, bool release) -> bool {
+            const uint32_t st = v_tile % kVS;
+            if (!wait(&sh.p_full[i], pv[i] & 1u) || !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
+            tc_fence_after();
+            const uint64_t vd = v_desc(smem_u32(sh.v[st]));
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kTaKeys / 16; ++k)
+                    mma_ts(tmem + 256u + (uint32_t)(i * DP), tmem + (uint32_t)(i * kTaKeys + kTaKeys / 2 + k * 8),
+                           vd + (uint64_t)(k * 2048 / 16), kIdO, fresh && k == 0 ? 0u : 1u);
+                umma_commit(&sh.pv_done[i]);
+                if (release) umma_commit(&sh.v_empty[st]);
+            }
+            __syncwarp();
+            if (release) ++v_tile;
+            ++pv[i];
+            return true;
+        };
+        for (; ok; ++seg_no) {
+            const SegSlot *sp = take(sh.seg_full, seg_no);
+            if (!sp || sp->s.n == 0) break;
+            const int n = sp->s.n;
+            give(seg_no);
+            ok = wait(&sh.q_full, (uint32_t)seg_no & 1u);
+            if (SPLIT_ROWS) {
+                ok = ok && scores(0, false, false) && scores(1, true, n == 1);
+                for (int t = 0; t < n && ok; ++t) {
+                    const bool more = t + 1 < n;
+                    // the results of the segment before have been read out of O
+                    if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
+                    ok = ok && values(0, t == 0, false) && (!more || scores(0, false, false)) &&
+                         values(1, t == 0, true) && (!more || scores(1, true, t + 2 == n));
+                }
+            } else {
+                ok = ok && scores(0, true, n == 1) && (n == 1 || scores(1, true, n == 2));
+                for (int t = 0; t < n && ok; ++t) {
+                    if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
+                    ok = ok && values(t & 1, t < 2, true) && (t + 2 >= n || scores(t & 1, true, t + 3 == n));
+                }
+            }
         }
-        if (lane == 0) {  // every MMA has finished before the TMEM is freed
-            umma_commit(&sh.done);
-            mbar_wait_bounded(&sh.done, 0u, kTaWaitNs);
-        }
+        // every MMA has finished before the TMEM is freed
+        if (elect_one()) umma_commit(&sh.done);
+        mbar_wait_bounded(&sh.done, 0u, kTaWaitNs);
         __syncwarp();
-    } else {  // ---------------------------------------------------- softmax
+    } else if (warp < 8) {  // ------------------------------------------- softmax
         const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S; P over its second half
         const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);        // O
         const int rows_used = A.np * A.G;
-        uint32_t base = 0, tiles[2] = {0, 0};  // loads before this segment, tiles done per stream
+        uint32_t base = 0, tiles[2] = {0, 0};  // tiles before this segment, tiles done per stream
         int seg_no = 0;
         bool ok = true, joins = false;
         for (; ok; ++seg_no) {
-            const SegSlot *sp = take(seg_no);
+            const SegSlot *sp = take(sh.path_full, seg_no);
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             const Geo &g = s.g;
@@ -723,14 +751,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 // values that no node sees may be anything: they are cleared, so that
                 // their zero weights leave them out
                 if ((!SPLIT_ROWS || stream == 0) && (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks))) {
-                    const uint32_t idx = base + v_index<SPLIT_ROWS>(t, s.n);
-                    ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.full[idx % kSt], (idx / kSt) & 1u, abort, kTaWaitNs));
+                    const uint32_t idx = base + (uint32_t)t;
+                    ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.v_full[idx % kVS], (idx / kVS) & 1u, abort, kTaWaitNs));
                     if (!ok) break;
                     const long long j = j0 + row;
                     if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
 #pragma unroll
                         for (int h = 0; h < kHalves; ++h) {
-                            uint4 *z = reinterpret_cast<uint4 *>(sh.kv[idx % kSt] + h * kTaKeys * 128 + row * 128);
+                            uint4 *z = reinterpret_cast<uint4 *>(sh.v[idx % kVS] + h * kTaKeys * 128 + row * 128);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -743,7 +771,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 ++tiles[stream];
             }
             if (!ok) break;
-            base += 2u * (uint32_t)s.n;
+            base += (uint32_t)s.n;
             float l = l2.x + l2.y;
             if (!valid) l = 0.f, m = -INFINITY;
 
@@ -864,7 +892,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kTaWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
