@@ -324,7 +324,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     using Sh = TaShared<DP, SPLIT_ROWS>;
     extern __shared__ uint8_t ta_raw[];
     Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(ta_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // through a shuffle, so that the compiler knows the roles' branches, and what is
+    // computed in them, to be the same in all lanes of a warp
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     constexpr int kKS = C::kStagesK, kVS = C::kStagesV;
     constexpr int kHalves = DP / 64;
     // P is scaled up to 2^15 in float16, so that weights 2^-29 below the
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         asm volatile("bar.sync 1, 128;" ::: "memory");
     }
     __syncthreads();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
     volatile int *abort = &sh.abort;
     const long long total = sh.incl[kTaChunks - 1];
     const long long run = (total + gridDim.x - 1) / gridDim.x;
@@ -551,7 +553,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         uint32_t pv[2] = {0, 0};           // O products issued per stream
         int seg_no = 0;
         bool ok = true;
-        const int ks = (A.D + 15) / 16;    // k steps of S
+        const uint64_t q_desc = umma_desc_sw128(smem_u32(sh.q)), k_desc = umma_desc_sw128(smem_u32(sh.k[0])),
+                       vt_desc = v_desc(smem_u32(sh.v[0]));
         constexpr uint32_t kIdS = ta_idesc<DT>(kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xFFFFFFFFu, lm_wait(bar, parity, abort, kTaWaitNs)) != 0;
@@ -564,10 +567,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const uint32_t st = k_tile % kKS;
             if (!wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
             tc_fence_after();
-            const uint64_t qd = umma_desc_sw128(smem_u32(sh.q + (SPLIT_ROWS ? i : 0) * C::kStreamQ));
-            const uint64_t kd = umma_desc_sw128(smem_u32(sh.k[st]));
+            const uint64_t qd = q_desc + (uint64_t)((SPLIT_ROWS ? i : 0) * (C::kStreamQ / 16));
+            const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16));
             if (elect_one()) {
-                for (int k = 0; k < ks; ++k) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {  // the columns past D hold zeros
                     const uint64_t off = (uint64_t)((k >> 2) * (kTaRows * 128 / 16) + (k & 3) * 2);
                     mma_ss(tmem + (uint32_t)(i * kTaKeys), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
                 }
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const uint32_t st = v_tile % kVS;
             if (!wait(&sh.p_full[i], pv[i] & 1u) || !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
             tc_fence_after();
-            const uint64_t vd = v_desc(smem_u32(sh.v[st]));
+            const uint64_t vd = vt_desc + (uint64_t)(st * (C::kStage / 16));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kTaKeys / 16; ++k)
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         for (; ok; ++seg_no) {
             const SegSlot *sp = take(sh.seg_full, seg_no);
             if (!sp || sp->s.n == 0) break;
-            const int n = sp->s.n;
+            const int n = __shfl_sync(0xFFFFFFFFu, sp->s.n, 0);
             give(seg_no);
             ok = wait(&sh.q_full, (uint32_t)seg_no & 1u);
             if (SPLIT_ROWS) {
