@@ -122,7 +122,8 @@ template <int DP, bool SPLIT_ROWS> struct TaShared {
     SegSlot seg[kTaSlots];
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
     uint64_t k_full[C::kStagesK], k_empty[C::kStagesK], v_full[C::kStagesV], v_empty[C::kStagesV];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, ml_full, done;
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half of a tile]
+    uint64_t q_full, q_free, o_free, ml_full, done;
     uint32_t tmem_base;
     int abort;
     float2 ml[SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : kTaRows];  // [segment parity][stream][row]
@@ -343,9 +344,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             mbar_init(&sh.v_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.pv_done[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sh.s_full[i][h], 1);
+                mbar_init(&sh.p_full[i][h], 4);
+                mbar_init(&sh.pv_done[i][h], 1);
+            }
         }
         for (int i = 0; i < kTaSlots; ++i) {
             mbar_init(&sh.seg_full[i], 1);
@@ -550,32 +553,33 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         __syncwarp();
     } else if (warp == kTaWarpMma) {  // --------------------------------- products
         uint32_t k_tile = 0, v_tile = 0;   // K and V tiles used
-        uint32_t pv[2] = {0, 0};           // O products issued per stream
+        uint32_t use[2] = {0, 0};          // tiles of each stream whose values are through
         int seg_no = 0;
         bool ok = true;
+        constexpr uint32_t kIdS = ta_idesc<DT>(SPLIT_ROWS ? kTaKeys / 2 : kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
         const uint64_t q_desc = umma_desc_sw128(smem_u32(sh.q)), k_desc = umma_desc_sw128(smem_u32(sh.k[0])),
                        vt_desc = v_desc(smem_u32(sh.v[0]));
-        constexpr uint32_t kIdS = ta_idesc<DT>(kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xFFFFFFFFu, lm_wait(bar, parity, abort, kTaWaitNs)) != 0;
         };
-        // scores of stream i against the next K tile (release: its last use; last: of
-        // the segment).  They overwrite the columns of the stream's last weights: the
-        // products of a CTA's one issuing thread execute in the order of issue, so
-        // those have been consumed by then.
-        auto scores = [&](int i, bool release, bool last) -> bool {
+        // Scores of stream i against the next K tile: its half h (SPLIT_ROWS), or both
+        // halves in one product (h = 0); release: the tile's last use, last: the
+        // segment's.  They overwrite the columns of the stream's last weights of that
+        // half: the products of a CTA's one issuing thread execute in the order of
+        // issue, so those have been consumed by then.
+        auto scores = [&](int i, int h, bool release, bool last) -> bool {
             const uint32_t st = k_tile % kKS;
-            if (!wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
+            if ((!SPLIT_ROWS || (i == 0 && h == 0)) && !wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
             tc_fence_after();
             const uint64_t qd = q_desc + (uint64_t)((SPLIT_ROWS ? i : 0) * (C::kStreamQ / 16));
-            const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16));
+            const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16) + h * (kTaKeys / 2 * 128 / 16));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {  // the columns past D hold zeros
                     const uint64_t off = (uint64_t)((k >> 2) * (kTaRows * 128 / 16) + (k & 3) * 2);
-                    mma_ss(tmem + (uint32_t)(i * kTaKeys), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
+                    mma_ss(tmem + (uint32_t)(i * kTaKeys + h * (kTaKeys / 2)), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
                 }
-                umma_commit(&sh.s_full[i]);
+                umma_commit(&sh.s_full[i][h]);
                 if (release) umma_commit(&sh.k_empty[st]);
                 if (last) umma_commit(&sh.q_free);
             }
@@ -583,23 +587,26 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (release) ++k_tile;
             return true;
         };
-        // O of stream i plus its weights times the next V tile (fresh: its first of the segment)
-        auto values = [&](int i, bool fresh, bool release) -> bool {
+        // O of stream i plus its weights of half h times that half of the next V tile
+        // (fresh: the first of the segment)
+        auto values = [&](int i, int h, bool fresh, bool release) -> bool {
             const uint32_t st = v_tile % kVS;
-            if (!wait(&sh.p_full[i], pv[i] & 1u) || !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
+            if (!wait(&sh.p_full[i][h], use[i] & 1u)) return false;
+            if (h == 0 && (!SPLIT_ROWS || i == 0) && !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
             tc_fence_after();
-            const uint64_t vd = vt_desc + (uint64_t)(st * (C::kStage / 16));
+            const uint64_t vd = vt_desc + (uint64_t)(st * (C::kStage / 16) + h * (kTaKeys / 2 * 128 / 16));
+            const uint32_t p = tmem + (uint32_t)(i * kTaKeys + h * (kTaKeys / 2) + kTaKeys / 4);
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kTaKeys / 16; ++k)
-                    mma_ts(tmem + 256u + (uint32_t)(i * DP), tmem + (uint32_t)(i * kTaKeys + kTaKeys / 2 + k * 8),
-                           vd + (uint64_t)(k * 2048 / 16), kIdO, fresh && k == 0 ? 0u : 1u);
-                umma_commit(&sh.pv_done[i]);
+                for (int k = 0; k < kTaKeys / 32; ++k)
+                    mma_ts(tmem + 256u + (uint32_t)(i * DP), p + (uint32_t)(k * 8), vd + (uint64_t)(k * 2048 / 16), kIdO,
+                           fresh && h == 0 && k == 0 ? 0u : 1u);
+                umma_commit(&sh.pv_done[i][h]);
                 if (release) umma_commit(&sh.v_empty[st]);
             }
             __syncwarp();
             if (release) ++v_tile;
-            ++pv[i];
+            if (h == 1) ++use[i];
             return true;
         };
         for (; ok; ++seg_no) {
@@ -609,19 +616,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             give(seg_no);
             ok = wait(&sh.q_full, (uint32_t)seg_no & 1u);
             if (SPLIT_ROWS) {
-                ok = ok && scores(0, false, false) && scores(1, true, n == 1);
+                ok = ok && scores(0, 0, false, false) && scores(1, 0, false, false) && scores(0, 1, false, false) &&
+                     scores(1, 1, true, n == 1);
                 for (int t = 0; t < n && ok; ++t) {
                     const bool more = t + 1 < n;
                     // the results of the segment before have been read out of O
                     if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
-                    ok = ok && values(0, t == 0, false) && (!more || scores(0, false, false)) &&
-                         values(1, t == 0, true) && (!more || scores(1, true, t + 2 == n));
+                    ok = ok && values(0, 0, t == 0, false) && (!more || scores(0, 0, false, false)) &&
+                         values(1, 0, t == 0, false) && (!more || scores(1, 0, false, false)) &&
+                         values(0, 1, false, false) && (!more || scores(0, 1, false, false)) &&
+                         values(1, 1, false, true) && (!more || scores(1, 1, true, t + 2 == n));
                 }
             } else {
-                ok = ok && scores(0, true, n == 1) && (n == 1 || scores(1, true, n == 2));
+                ok = ok && scores(0, 0, true, n == 1) && (n == 1 || scores(1, 0, true, n == 2));
                 for (int t = 0; t < n && ok; ++t) {
                     if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
-                    ok = ok && values(t & 1, t < 2, true) && (t + 2 >= n || scores(t & 1, true, t + 3 == n));
+                    ok = ok && values(t & 1, 0, t < 2, false) && values(t & 1, 1, false, true) &&
+                         (t + 2 >= n || scores(t & 1, 0, true, t + 3 == n));
                 }
             }
         }
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     } else if (warp < 8) {  // ------------------------------------------- softmax
         const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S; P over its second half
+        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S; P over the second half of each half
         const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);        // O
         const int rows_used = A.np * A.G;
         uint32_t base = 0, tiles[2] = {0, 0};  // tiles before this segment, tiles done per stream
@@ -665,113 +676,108 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             bool first = true;
             for (int t = SPLIT_ROWS ? 0 : stream; t < s.n && ok; t += t_step, first = false) {
                 const long long j0 = (long long)g.tile(s.i0 + t) * kTaKeys;
-                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.s_full[stream], tiles[stream] & 1u, abort, kTaWaitNs));
-                if (!ok) break;
-                tc_fence_after();
-                if (warp_works) {
-                    // 64 scores at a time in registers; the other half is read twice
-                    // rather than kept (128 of a thread's 168 registers would spill)
-                    uint32_t x[64], seen[kTaKeys / 32];
-                    const bool whole = j0 + kTaKeys <= g.c && (j0 >= low || j0 + kTaKeys <= A.sinks);
-                    const bool masked = !__all_sync(0xFFFFFFFFu, whole || !valid);
-                    if (masked) {
+                const uint32_t use = tiles[stream];
+                // a tile in two halves of 64 keys, each with its own scores, weights and product:
+                // one half's products run while the other half's weights are formed
 #pragma unroll
-                        for (int w = 0; w < kTaKeys / 32; ++w) {
-                            const long long jw = j0 + 32 * w;
-                            uint32_t bits = 0;
-                            if (valid) {
-                                bits = range_bits(low, g.c, jw) | (A.window ? range_bits(0, min(A.sinks, g.c), jw) : 0u);
-                                const long long sft = jw - g.c;  // bit sft of the path is position jw
-                                if (sft >= 0 && sft < 64) bits |= (uint32_t)(path >> sft);
-                                else if (sft < 0 && sft > -32) bits |= (uint32_t)(path << -sft);
-                            }
-                            seen[w] = bits;
-                        }
-                        __syncwarp();
+                for (int h = 0; h < 2; ++h) {
+                    const long long jh = j0 + h * (kTaKeys / 2);
+                    const uint32_t th = ts + (uint32_t)(h * (kTaKeys / 2));
+                    if (SPLIT_ROWS || h == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.s_full[stream][h], use & 1u, abort, kTaWaitNs));
+                        if (!ok) break;
+                        tc_fence_after();
                     }
-                    auto load = [&](int part) {
-                        tmem_load(ts + 64 * part, x);
-                        if (masked) {
+                    if (warp_works) {
+                        uint32_t x[64];
+                        tmem_load(th, x);
+                        const bool whole = jh + 64 <= g.c && (jh >= low || jh + 64 <= A.sinks);
+                        if (!__all_sync(0xFFFFFFFFu, whole || !valid)) {
 #pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (!((seen[2 * part + (i >> 5)] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+                            for (int w = 0; w < 2; ++w) {
+                                const long long jw = jh + 32 * w;
+                                uint32_t bits = 0;
+                                if (valid) {
+                                    bits = range_bits(low, g.c, jw) | (A.window ? range_bits(0, min(A.sinks, g.c), jw) : 0u);
+                                    const long long sft = jw - g.c;  // bit sft of the path is position jw
+                                    if (sft >= 0 && sft < 64) bits |= (uint32_t)(path >> sft);
+                                    else if (sft < 0 && sft > -32) bits |= (uint32_t)(path << -sft);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!((bits >> i) & 1u)) x[32 * w + i] = 0xFF800000u;
+                            }
+                            __syncwarp();
                         }
-                    };
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        load(part);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int i = 0; i < 64; i += 8) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
                         }
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
-                    if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kTaGrow))) {
-                        const float m_new = top > m + kLift ? top - kLift : m;
-                        const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);
-                        m = m_new;
-                        l2 = make_float2(l2.x * f, l2.y * f);
-                        if (!first) {
-                            ok = __all_sync(0xFFFFFFFFu,
-                                            lm_wait(&sh.pv_done[stream], (tiles[stream] - 1) & 1u, abort, kTaWaitNs));
-                            if (!ok) break;
-                            tc_fence_after();
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
+                        if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kTaGrow))) {
+                            const float m_new = top > m + kLift ? top - kLift : m;
+                            const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);
+                            m = m_new;
+                            l2 = make_float2(l2.x * f, l2.y * f);
+                            if (h > 0 || !first) {  // O holds the halves before this one
+                                uint64_t *done = h > 0 ? &sh.pv_done[stream][0] : &sh.pv_done[stream][1];
+                                ok = __all_sync(0xFFFFFFFFu, lm_wait(done, (h > 0 ? use : use - 1) & 1u, abort, kTaWaitNs));
+                                if (!ok) break;
+                                tc_fence_after();
 #pragma unroll 1
-                            for (int d = 0; d < DP; d += 32) {
-                                uint32_t o[32];
-                                tmem_load(to + d, o);
+                                for (int d = 0; d < DP; d += 32) {
+                                    uint32_t o[32];
+                                    tmem_load(to + d, o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_store(to + d, o);
+                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_store(to + d, o);
+                                }
                             }
                         }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const float2 c2 = make_float2(A.scale_log2, A.scale_log2), nm2 = make_float2(-mu, -mu);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        const float mu = m == -INFINITY ? 0.f : m;
+                        const float2 c2 = make_float2(A.scale_log2, A.scale_log2), nm2 = make_float2(-mu, -mu);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int part = 1; part >= 0; --part) {  // the second half is still in registers
-                        if (part == 0) load(0);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int q = 0; q < 2; ++q) {
                             uint32_t p[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const float2 z = fma2(make_float2(__uint_as_float(x[32 * h + 2 * i]),
-                                                                  __uint_as_float(x[32 * h + 2 * i + 1])), c2, nm2);
+                                const float2 z = fma2(make_float2(__uint_as_float(x[32 * q + 2 * i]),
+                                                                  __uint_as_float(x[32 * q + 2 * i + 1])), c2, nm2);
                                 const float2 e = make_float2(ex2(z.x), ex2(z.y));
                                 sum[i & 1] = add2(sum[i & 1], e);
                                 p[i] = pack2<DT>(e.x, e.y);
                             }
-                            tmem_store(ts + kTaKeys / 2 + 32 * part + 16 * h, p);
+                            tmem_store(th + kTaKeys / 4 + 16 * q, p);
                         }
+                        l2 = add2(l2, add2(sum[0], sum[1]));
+                        tmem_wait_store();
                     }
-                    l2 = add2(l2, add2(sum[0], sum[1]));
-                    tmem_wait_store();
-                }
-                // values that no node sees may be anything: they are cleared, so that
-                // their zero weights leave them out
-                if ((!SPLIT_ROWS || stream == 0) && (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks))) {
-                    const uint32_t idx = base + (uint32_t)t;
-                    ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.v_full[idx % kVS], (idx / kVS) & 1u, abort, kTaWaitNs));
-                    if (!ok) break;
-                    const long long j = j0 + row;
-                    if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
+                    // values that no node sees may be anything: they are cleared, so that their zero
+                    // weights leave them out (SPLIT_ROWS: stream 0's weights are used first)
+                    if (h == 0 && (!SPLIT_ROWS || stream == 0) &&
+                        (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks))) {
+                        const uint32_t idx = base + (uint32_t)t;
+                        ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.v_full[idx % kVS], (idx / kVS) & 1u, abort, kTaWaitNs));
+                        if (!ok) break;
+                        const long long j = j0 + row;
+                        if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
 #pragma unroll
-                        for (int h = 0; h < kHalves; ++h) {
-                            uint4 *z = reinterpret_cast<uint4 *>(sh.v[idx % kVS] + h * kTaKeys * 128 + row * 128);
+                            for (int d = 0; d < kHalves; ++d) {
+                                uint4 *z = reinterpret_cast<uint4 *>(sh.v[idx % kVS] + d * kTaKeys * 128 + row * 128);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
+                                for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
+                            }
                         }
+                        fence_proxy_async();
                     }
-                    fence_proxy_async();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.p_full[stream][h]));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.p_full[stream]));
                 ++tiles[stream];
             }
             if (!ok) break;
@@ -794,8 +800,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.ml_full));
                 ok = lm_wait(&sh.ml_full, seg_no & 1, abort, kTaWaitNs);
-                ok = ok && lm_wait(&sh.pv_done[0], (tiles[0] - 1) & 1u, abort, kTaWaitNs);
-                if (two) ok = ok && lm_wait(&sh.pv_done[1], (tiles[1] - 1) & 1u, abort, kTaWaitNs);
+                ok = ok && lm_wait(&sh.pv_done[0][1], (tiles[0] - 1) & 1u, abort, kTaWaitNs);
+                if (two) ok = ok && lm_wait(&sh.pv_done[1][1], (tiles[1] - 1) & 1u, abort, kTaWaitNs);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const float2 x = sh.ml[seg_no & 1][0][row], y = sh.ml[seg_no & 1][1][row];
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 w_b = m == -INFINITY ? 0.f : ex2(y.x - m);
                 l = x.y * w_a + y.y * w_b;
             } else {
-                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.pv_done[stream], (tiles[stream] - 1) & 1u, abort, kTaWaitNs));
+                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.pv_done[stream][1], (tiles[stream] - 1) & 1u, abort, kTaWaitNs));
                 if (!ok) break;
             }
             tc_fence_after();
