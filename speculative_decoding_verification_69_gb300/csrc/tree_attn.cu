@@ -111,7 +111,8 @@ struct Seg {
 // A segment as the scheduling warp hands it to the others; n = 0 ends the list.
 struct SegSlot {
     Seg s;
-    unsigned long long path[SPEC_MAX_TREE];  // the nodes on the path to each node
+    unsigned long long path[SPEC_MAX_TREE];  // the nodes that each node sees
+    int low[SPEC_MAX_TREE];                  // the first committed position in its window
 };
 
 template <int DP, bool SPLIT_ROWS> struct TaShared {
@@ -120,6 +121,7 @@ template <int DP, bool SPLIT_ROWS> struct TaShared {
     uint8_t k[C::kStagesK][C::kStage], v[C::kStagesV][C::kStage];
     long long incl[kTaChunks];  // units of the requests up to the end of each chunk of them
     SegSlot seg[kTaSlots];
+    int pages[2][32];           // K's and V's next pages
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
     uint64_t k_full[C::kStagesK], k_empty[C::kStagesK], v_full[C::kStagesV], v_empty[C::kStagesV];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half of a tile]
@@ -217,6 +219,24 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Waits for a phase, at most kTaWaitNs or until another role has given up.  The
+// timer is read on every 64th look only.
+__device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    unsigned long long t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 63u) == 0) {
+            const unsigned long long t = global_ns();
+            if (t0 == 0) t0 = t;
+            if (*abort) return false;
+            if (t - t0 > kTaWaitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
 // D (TMEM) (+)= A (shared) B (shared)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -267,12 +287,17 @@ template <> __device__ __forceinline__ uint32_t pack2<SPEC_DTYPE_F16>(float lo, 
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-// Bits of a 32-position word starting at j0 for the positions [lo, hi).
-__device__ __forceinline__ uint32_t range_bits(long long lo, long long hi, long long j0) {
-    const int a = (int)max(0ll, min(32ll, lo - j0)), b = (int)max(0ll, min(32ll, hi - j0));
-    if (b <= a) return 0u;
-    const uint32_t up = b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
-    return up & ~((1u << a) - 1u);
+// The positions [j, j + 64) that a row sees: committed ones from `low` on and the
+// first `sinks`, and the nodes of its path, which lie from position c on.
+__device__ __forceinline__ unsigned long long seen_bits(long long j, int c, int low, int sinks,
+                                                        unsigned long long path) {
+    auto below = [&](int end) -> unsigned long long {  // the positions before `end`
+        const long long n = end - j;
+        return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << (int)n) - 1ull;
+    };
+    const long long d = j - c;
+    const unsigned long long nodes = d >= 64 || d <= -64 ? 0ull : d >= 0 ? path >> (int)d : path << (int)-d;
+    return (below(c) & ~below(low)) | below(min(sinks, c)) | nodes;
 }
 
 // The nodes on the path to every node, as bits, for nodes `lane` and `lane +
@@ -406,7 +431,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
     // segment k, or nothing when the wait for it ran out
     auto take = [&](uint64_t *bars, int k) -> const SegSlot * {
-        const bool ok = lm_wait(&bars[k % kTaSlots], (k / kTaSlots) & 1, abort, kTaWaitNs);
+        const bool ok = ta_wait(&bars[k % kTaSlots], (k / kTaSlots) & 1, abort);
         return __all_sync(0xFFFFFFFFu, ok) ? &sh.seg[k % kTaSlots] : nullptr;
     };
     auto give = [&](int k) {
@@ -418,6 +443,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         int k = 0, b = -1;
         bool ok = true;
         unsigned long long anc[2] = {0, 0};
+        int low[2] = {0, 0};
         for (long long u = u_first; ok; ++k) {
             Seg s = {};
             if (u < u_last) {
@@ -425,7 +451,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 u += s.n;
             }
             if (k >= kTaSlots)
-                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort, kTaWaitNs));
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort));
             if (!ok) break;
             SegSlot &slot = sh.seg[k % kTaSlots];
             if (lane == 0) {
@@ -433,9 +459,25 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_full[k % kTaSlots]));
             }
             // the loads and scores go ahead; the softmax warps need the paths too
-            if (s.n > 0 && s.b != b) ta_paths(A, b = s.b, s.g.cnt, anc);
-            slot.path[lane] = anc[0];
-            slot.path[lane + 32] = anc[1];
+            if (s.n > 0 && s.b != b) {
+                ta_paths(A, b = s.b, s.g.cnt, anc);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // less the nodes before the window
+                    if (!A.window) break;
+                    low[x] = max(0, s.g.c + __popcll(anc[x]) - A.window);
+                    unsigned long long left = anc[x];
+                    for (int place = s.g.c; left && place < low[x]; ++place) {
+                        const unsigned long long bit = left & (0ull - left);
+                        if (place >= A.sinks) anc[x] &= ~bit;
+                        left ^= bit;
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                slot.path[lane + 32 * x] = anc[x];
+                slot.low[lane + 32 * x] = low[x];
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.path_full[k % kTaSlots]));
             if (s.n == 0) break;
@@ -477,7 +519,19 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 }
                 return p;
             };
-            int base = s.i0, cur = fetch(base), nxt = base + ahead < i_end ? fetch(base + ahead) : 0;
+            // the pages of `ahead` tiles at a time go to shared memory, where the lane that
+            // issues the copies reads them in a loop (unrolled over the boxes its code was
+            // read anew for every tile, 250 cycles a copy); the next ones are on their way
+            int base = s.i0, nxt = fetch(base);
+            int *pages = sh.pages[is_k ? 0 : 1];
+            auto turn = [&](int i) {
+                __syncwarp();
+                pages[lane] = nxt;
+                base = i;
+                nxt = i + ahead < i_end ? fetch(i + ahead) : 0;
+                __syncwarp();
+            };
+            turn(base);
             // Q of this segment once the scores of the last one are done: looked for
             // before every load, so that the tiles need not wait for it
             bool q_due = is_k;
@@ -499,27 +553,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     issue_q();
             };
             for (int i = s.i0; i < i_end && ok; ++i) {
-                if (i >= base + ahead) {
-                    cur = nxt;
-                    base += ahead;
-                    nxt = base + ahead < i_end ? fetch(base + ahead) : 0;
-                }
+                if (i >= base + ahead) turn(i);
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, lane < nb && box_seen(box_pos(i)));
-                const int page = __shfl_sync(0xFFFFFFFFu, cur, ((i - base) * nb + box) & 31);
                 const int tok = (int)(((long long)s.g.tile(i) * kTaKeys) & (A.page - 1));
-                int pages[16];  // of all boxes, in every lane
-#pragma unroll
-                for (int x = 0; x < 16; ++x) pages[x] = __shfl_sync(0xFFFFFFFFu, page, x);
                 look_q();
                 if (fill > 0) {
-                    const unsigned long long t0 = global_ns();
+                    unsigned long long t0 = 0;
                     for (uint32_t tries = 1;; ++tries) {
                         if (__any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u))) break;
                         look_q();
-                        if ((tries & 63u) == 0 && __any_sync(0xFFFFFFFFu, *abort || global_ns() - t0 > kTaWaitNs)) {
-                            *abort = 1;
-                            ok = false;
-                            break;
+                        if ((tries & 63u) == 0) {
+                            const unsigned long long now = global_ns();
+                            if (t0 == 0) t0 = now;
+                            if (__any_sync(0xFFFFFFFFu, *abort || now - t0 > kTaWaitNs)) {
+                                *abort = 1;
+                                ok = false;
+                                break;
+                            }
                         }
                     }
                     if (!ok) break;
@@ -527,20 +577,19 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 uint8_t *tile = tiles + stage * C::kStage;
                 if (elect_one()) {
                     mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        if ((seen >> x) & 1u) {
-#pragma unroll
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_load_4d(tile + h * kTaKeys * 128 + x * A.box * 128, tm, h * 64, tok, s.hk, pages[x],
-                                            &full[stage]);
-                        }
+                    const int *page = pages + (i - base) * nb;
+#pragma unroll 1
+                    for (int x = 0; x < nb; ++x, ++page, tile += A.box * 128) {
+                        if (!((seen >> x) & 1u)) continue;
+                        tma_load_4d(tile, tm, 0, tok, s.hk, *page, &full[stage]);
+                        if (kHalves == 2) tma_load_4d(tile + kTaKeys * 128, tm, 64, tok, s.hk, *page, &full[stage]);
+                    }
                 }
                 __syncwarp();
                 if (++stage == stages) stage = 0, ++fill;
             }
             if (ok && q_due) {
-                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u, abort, kTaWaitNs));
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u, abort));
                 if (ok) issue_q();
             }
         }
@@ -556,11 +605,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         uint32_t use[2] = {0, 0};          // tiles of each stream whose values are through
         int seg_no = 0;
         bool ok = true;
-        constexpr uint32_t kIdS = ta_idesc<DT>(SPLIT_ROWS ? kTaKeys / 2 : kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
+        constexpr uint32_t kIdS = ta_idesc<DT>(kTaKeys, false), kIdO = ta_idesc<DT>(DP, true);
         const uint64_t q_desc = umma_desc_sw128(smem_u32(sh.q)), k_desc = umma_desc_sw128(smem_u32(sh.k[0])),
                        vt_desc = v_desc(smem_u32(sh.v[0]));
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xFFFFFFFFu, lm_wait(bar, parity, abort, kTaWaitNs)) != 0;
+            return __all_sync(0xFFFFFFFFu, ta_wait(bar, parity, abort)) != 0;
         };
         // Scores of stream i against the next K tile: its half h (SPLIT_ROWS), or both
         // halves in one product (h = 0); release: the tile's last use, last: the
@@ -609,31 +658,56 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (h == 1) ++use[i];
             return true;
         };
-        for (; ok; ++seg_no) {
-            const SegSlot *sp = take(sh.seg_full, seg_no);
-            if (!sp || sp->s.n == 0) break;
-            const int n = __shfl_sync(0xFFFFFFFFu, sp->s.n, 0);
-            give(seg_no);
-            ok = wait(&sh.q_full, (uint32_t)seg_no & 1u);
-            if (SPLIT_ROWS) {
-                ok = ok && scores(0, 0, false, false) && scores(1, 0, false, false) && scores(0, 1, false, false) &&
-                     scores(1, 1, true, n == 1);
+        if (SPLIT_ROWS) {
+            for (; ok; ++seg_no) {
+                const SegSlot *sp = take(sh.seg_full, seg_no);
+                if (!sp || sp->s.n == 0) break;
+                const int n = __shfl_sync(0xFFFFFFFFu, sp->s.n, 0);
+                give(seg_no);
+                ok = wait(&sh.q_full, (uint32_t)seg_no & 1u);
+                ok = ok && scores(0, 0, false, false) && scores(1, 0, true, n == 1);
                 for (int t = 0; t < n && ok; ++t) {
                     const bool more = t + 1 < n;
-                    // the results of the segment before have been read out of O
                     if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
-                    ok = ok && values(0, 0, t == 0, false) && (!more || scores(0, 0, false, false)) &&
-                         values(1, 0, t == 0, false) && (!more || scores(1, 0, false, false)) &&
-                         values(0, 1, false, false) && (!more || scores(0, 1, false, false)) &&
-                         values(1, 1, false, true) && (!more || scores(1, 1, true, t + 2 == n));
+                    ok = ok && values(0, 0, t == 0, false) && values(0, 1, false, false) && (!more || scores(0, 0, false, false)) &&
+                         values(1, 0, t == 0, false) && values(1, 1, false, true) && (!more || scores(1, 0, true, t + 2 == n));
                 }
-            } else {
-                ok = ok && scores(0, 0, true, n == 1) && (n == 1 || scores(1, 0, true, n == 2));
-                for (int t = 0; t < n && ok; ++t) {
-                    if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
-                    ok = ok && values(t & 1, 0, t < 2, false) && values(t & 1, 1, false, true) &&
-                         (t + 2 >= n || scores(t & 1, 0, true, t + 3 == n));
+            }
+        } else {
+            // The streams take the CTA's tiles in turn, whatever segment they belong to;
+            // a stream's next scores follow its values at once, also those of the next
+            // segment, so that they are there when its results have been written.
+            const uint32_t tiles = (uint32_t)(u_last - u_first);
+            int s_seg = 0, s_left = 0, v_seg = 0, v_left = 0;  // segments begun by scores and values, tiles left
+            bool fresh0 = false, fresh1 = false;               // the next values are the stream's first of a segment
+            auto next_scores = [&](int i) -> bool {
+                if (s_left == 0) {
+                    if (!wait(&sh.seg_full[s_seg % kTaSlots], (uint32_t)(s_seg / kTaSlots) & 1u)) return false;
+                    s_left = __shfl_sync(0xFFFFFFFFu, sh.seg[s_seg % kTaSlots].s.n, 0);
+                    if (!wait(&sh.q_full, (uint32_t)s_seg & 1u)) return false;
+                    ++s_seg;
                 }
+                return scores(i, 0, true, --s_left == 0);
+            };
+            auto next_values = [&](int i) -> bool {
+                if (v_left == 0) {
+                    if (v_seg > 0 && !wait(&sh.o_free, (uint32_t)(v_seg - 1) & 1u)) return false;
+                    v_left = __shfl_sync(0xFFFFFFFFu, sh.seg[v_seg % kTaSlots].s.n, 0);
+                    ++v_seg;
+                    fresh0 = fresh1 = true;
+                }
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h)
+                    if (!values(i, h, i == 0 ? fresh0 : fresh1, h == 1)) return false;
+                if (i == 0) fresh0 = false;
+                else fresh1 = false;
+                if (--v_left == 0) give(v_seg - 1);
+                return true;
+            };
+#pragma unroll 1
+            for (int e = -2; e < (int)tiles && ok; ++e) {
+                if (e >= 0) ok = next_values(e & 1);
+                if (e + 2 < (int)tiles) ok = ok && next_scores(e & 1);
             }
         }
         // every MMA has finished before the TMEM is freed
@@ -645,8 +719,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S; P over the second half of each half
         const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);        // O
-        const int rows_used = A.np * A.G;
-        uint32_t base = 0, tiles[2] = {0, 0};  // tiles before this segment, tiles done per stream
+        const int rows_used = A.np * A.G, local = row / A.G;
+        uint32_t base = 0;                     // the CTA's tiles before this segment
         int seg_no = 0;
         bool ok = true, joins = false;
         for (; ok; ++seg_no) {
@@ -654,37 +728,48 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             const Geo &g = s.g;
-            const int local = row / A.G, node = s.node0 + (SPLIT_ROWS ? stream * A.np : 0) + local;
+            const int node = s.node0 + (SPLIT_ROWS ? stream * A.np : 0) + local;
             const bool valid = row < rows_used && node < g.cnt;
-            unsigned long long path = valid ? sp->path[node] : 0ull;
+            const unsigned long long path = valid ? sp->path[node] : 0ull;
+            const int low = valid ? sp->low[node] : 0;
             give(seg_no);
-            const int tip = g.c + __popcll(path) - 1;  // the node's place
-            int low = 0;                               // first committed position in its window
-            if (A.window) {
-                low = max(0, tip - A.window + 1);
-                unsigned long long left = path;
-                for (int place = g.c; left; ++place) {
-                    const unsigned long long bit = left & (0ull - left);
-                    if (place < low && place >= A.sinks) path &= ~bit;
-                    left ^= bit;
-                }
-            }
+            const int sinks = A.window ? A.sinks : 0;
             const bool warp_works = __any_sync(0xFFFFFFFFu, valid);
             float m = -INFINITY;                       // reference of the weights, less the lift
             float2 l2 = make_float2(0.f, 0.f);
             const int t_step = SPLIT_ROWS ? 1 : 2;
             bool first = true;
-            for (int t = SPLIT_ROWS ? 0 : stream; t < s.n && ok; t += t_step, first = false) {
+            for (int t = SPLIT_ROWS ? 0 : (int)((base + stream) & 1u); t < s.n && ok; t += t_step, first = false) {
                 const long long j0 = (long long)g.tile(s.i0 + t) * kTaKeys;
-                const uint32_t use = tiles[stream];
+                const uint32_t use = SPLIT_ROWS ? base + (uint32_t)t : (base + (uint32_t)t) >> 1;  // the stream's
+                // values that no node sees may be anything: they are cleared, so that their zero
+                // weights leave them out (SPLIT_ROWS: by stream 0, whose weights are used first);
+                // before the scores are waited for if the tile is there by then
+                const uint32_t v_tile = base + (uint32_t)t, v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
+                bool clear = (!SPLIT_ROWS || stream == 0) &&
+                             (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks));
+                auto clear_v = [&]() {
+                    const long long j = j0 + row;
+                    if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
+#pragma unroll
+                        for (int d = 0; d < kHalves; ++d) {
+                            uint4 *z = reinterpret_cast<uint4 *>(sh.v[v_stage] + d * kTaKeys * 128 + row * 128);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_proxy_async();
+                    clear = false;
+                };
+                if (clear && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh.v_full[v_stage], v_parity))) clear_v();
                 // a tile in two halves of 64 keys, each with its own scores, weights and product:
                 // one half's products run while the other half's weights are formed
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const long long jh = j0 + h * (kTaKeys / 2);
                     const uint32_t th = ts + (uint32_t)(h * (kTaKeys / 2));
-                    if (SPLIT_ROWS || h == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.s_full[stream][h], use & 1u, abort, kTaWaitNs));
+                    if (h == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream][h], use & 1u, abort));
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -693,19 +778,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         tmem_load(th, x);
                         const bool whole = jh + 64 <= g.c && (jh >= low || jh + 64 <= A.sinks);
                         if (!__all_sync(0xFFFFFFFFu, whole || !valid)) {
+                            const unsigned long long bits = valid ? seen_bits(jh, g.c, low, sinks, path) : 0ull;
+                            const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
 #pragma unroll
-                            for (int w = 0; w < 2; ++w) {
-                                const long long jw = jh + 32 * w;
-                                uint32_t bits = 0;
-                                if (valid) {
-                                    bits = range_bits(low, g.c, jw) | (A.window ? range_bits(0, min(A.sinks, g.c), jw) : 0u);
-                                    const long long sft = jw - g.c;  // bit sft of the path is position jw
-                                    if (sft >= 0 && sft < 64) bits |= (uint32_t)(path >> sft);
-                                    else if (sft < 0 && sft > -32) bits |= (uint32_t)(path << -sft);
-                                }
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!((bits >> i) & 1u)) x[32 * w + i] = 0xFF800000u;
+                            for (int i = 0; i < 32; ++i) {
+                                if (!(b0 & (1u << i))) x[i] = 0xFF800000u;
+                                if (!(b1 & (1u << i))) x[32 + i] = 0xFF800000u;
                             }
                             __syncwarp();
                         }
@@ -724,7 +802,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                             l2 = make_float2(l2.x * f, l2.y * f);
                             if (h > 0 || !first) {  // O holds the halves before this one
                                 uint64_t *done = h > 0 ? &sh.pv_done[stream][0] : &sh.pv_done[stream][1];
-                                ok = __all_sync(0xFFFFFFFFu, lm_wait(done, (h > 0 ? use : use - 1) & 1u, abort, kTaWaitNs));
+                                ok = __all_sync(0xFFFFFFFFu, ta_wait(done, (h > 0 ? use : use - 1) & 1u, abort));
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll 1
@@ -756,29 +834,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         l2 = add2(l2, add2(sum[0], sum[1]));
                         tmem_wait_store();
                     }
-                    // values that no node sees may be anything: they are cleared, so that their zero
-                    // weights leave them out (SPLIT_ROWS: stream 0's weights are used first)
-                    if (h == 0 && (!SPLIT_ROWS || stream == 0) &&
-                        (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks))) {
-                        const uint32_t idx = base + (uint32_t)t;
-                        ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.v_full[idx % kVS], (idx / kVS) & 1u, abort, kTaWaitNs));
+                    if (h == 0 && clear) {
+                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.v_full[v_stage], v_parity, abort));
                         if (!ok) break;
-                        const long long j = j0 + row;
-                        if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
-#pragma unroll
-                            for (int d = 0; d < kHalves; ++d) {
-                                uint4 *z = reinterpret_cast<uint4 *>(sh.v[idx % kVS] + d * kTaKeys * 128 + row * 128);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                        }
-                        fence_proxy_async();
+                        clear_v();
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.p_full[stream][h]));
                 }
-                ++tiles[stream];
             }
             if (!ok) break;
             base += (uint32_t)s.n;
@@ -786,31 +850,31 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (!valid) l = 0.f, m = -INFINITY;
 
             // ---- the segment's result
-            const int n_other = SPLIT_ROWS ? 0 : (stream == 0 ? s.n / 2 : (s.n + 1) / 2);
-            if (!SPLIT_ROWS) tiles[stream ^ 1] += (uint32_t)n_other;
+            const uint32_t e1 = base - 1u;                   // its last tile
+            const int a = SPLIT_ROWS ? stream : (int)(e1 & 1u);  // a stream that holds a part
             const bool whole_item = s.n == g.nt;
             // a cut item: its first part in this CTA's slot 1, any later one in slot 0
             const long long slot = (long long)blockIdx.x * 2 + (s.i0 == 0 ? 1 : 0);
             constexpr int kCols = SPLIT_ROWS ? DP : DP / 2;  // columns of O this thread writes
             const int col0 = SPLIT_ROWS ? 0 : stream * kCols;
             const bool two = !SPLIT_ROWS && s.n > 1;         // both streams hold a part
-            float w_a = 1.f, w_b = 0.f;                      // weights of stream 0's (this stream's) part and the other
+            float w_a = 1.f, w_b = 0.f;                      // weights of its part and of the other's
             if (!SPLIT_ROWS) {
                 sh.ml[seg_no & 1][stream][row] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.ml_full));
-                ok = lm_wait(&sh.ml_full, seg_no & 1, abort, kTaWaitNs);
-                ok = ok && lm_wait(&sh.pv_done[0][1], (tiles[0] - 1) & 1u, abort, kTaWaitNs);
-                if (two) ok = ok && lm_wait(&sh.pv_done[1][1], (tiles[1] - 1) & 1u, abort, kTaWaitNs);
+                ok = ta_wait(&sh.ml_full, seg_no & 1, abort);
+                ok = ok && ta_wait(&sh.pv_done[a][1], (e1 >> 1) & 1u, abort);
+                if (two) ok = ok && ta_wait(&sh.pv_done[a ^ 1][1], ((e1 - 1u) >> 1) & 1u, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                const float2 x = sh.ml[seg_no & 1][0][row], y = sh.ml[seg_no & 1][1][row];
+                const float2 x = sh.ml[seg_no & 1][a][row], y = sh.ml[seg_no & 1][a ^ 1][row];
                 m = fmaxf(x.x, y.x);
                 w_a = m == -INFINITY ? 0.f : ex2(x.x - m);
                 w_b = m == -INFINITY ? 0.f : ex2(y.x - m);
                 l = x.y * w_a + y.y * w_b;
             } else {
-                ok = __all_sync(0xFFFFFFFFu, lm_wait(&sh.pv_done[stream][1], (tiles[stream] - 1) & 1u, abort, kTaWaitNs));
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.pv_done[stream][1], e1 & 1u, abort));
                 if (!ok) break;
             }
             tc_fence_after();
@@ -822,17 +886,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int rows_cta = rows_used * (SPLIT_ROWS ? 2 : 1);
             const bool any_write = __any_sync(0xFFFFFFFFu, writes);
             if (any_write) {
-#pragma unroll
+                const uint32_t o_cols = tmem + lanes + 256u + (uint32_t)col0;
+#pragma unroll 1
                 for (int d = 0; d < kCols; d += 32) {
                     uint32_t o[32];
-                    const uint32_t oa = tmem + lanes + 256u + (uint32_t)((SPLIT_ROWS ? stream * DP : 0) + col0 + d);
-                    tmem_load(oa, o);
+                    tmem_load(o_cols + (uint32_t)(a * DP + d), o);
                     if (!SPLIT_ROWS) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w_a);
                         if (two) {
                             uint32_t o2[32];
-                            tmem_load(oa + DP, o2);
+                            tmem_load(o_cols + (uint32_t)((a ^ 1) * DP + d), o2);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), w_b, __uint_as_float(o[i])));
