@@ -1,6 +1,8 @@
-"""Build libspecverify.so in-tree with nvcc for sm_103a."""
+"""Build libspecverify.so (nvcc, sm_103a) and the Python binding of the paged
+cache (_native.so, the host compiler) in-tree."""
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -8,9 +10,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libspecverify.so")
+NATIVE = os.path.join(OUT_DIR, "_native.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "spec_cache.cu", "tree_attn.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \
-    [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_cache.h")]
+BINDING = os.path.join(CSRC, "binding.cpp")
+HEADERS = [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_cache.h")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + HEADERS
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "0"]
@@ -21,23 +25,43 @@ def nvcc():
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(path, deps) -> bool:
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in DEPS if os.path.exists(p))
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-I" + CSRC, *SOURCES, "-o", tmp]
+def stale() -> bool:
+    return _older(LIB, DEPS) or _older(NATIVE, [BINDING] + HEADERS)
+
+
+def _run(cmd, out, verbose):
+    tmp = out + ".tmp%d" % os.getpid()
+    cmd = cmd + ["-o", tmp]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    os.replace(tmp, out)
+
+
+def _binding_cmd():
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + p for p in inc] + [BINDING]
+            + ["-L" + os.path.join(base, "lib"), "-L" + OUT_DIR, "-l:libspecverify.so", "-lc10", "-ltorch_cpu",
+               "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    os.makedirs(OUT_DIR, exist_ok=True)
+    if force or _older(LIB, DEPS):
+        _run([nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-I" + CSRC, *SOURCES], LIB, verbose)
+    if force or _older(NATIVE, [BINDING] + HEADERS):
+        _run(_binding_cmd(), NATIVE, verbose)
     return LIB
 
 

@@ -20,21 +20,15 @@ every step runs in the library's kernels, on torch's current stream or the
 """
 import ctypes
 import functools
-import math
-import struct
+import importlib.util
 
 import torch
+
+from . import _build
 
 DEV_BAD_PAGE, DEV_NO_PAGES, DEV_BAD_SLOT = 16, 32, 64
 DTYPE_F16 = 2
 MAX_SLOTS, MAX_TREE, MAX_HEAD_DIM = 8192, 64, 128
-
-_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: DTYPE_F16}
-
-
-# spec_pages_t: k, v, dtype, layers, num_pages, page_size, heads, head_dim, and
-# the strides of layers, pages, tokens and heads
-_PAGES = struct.Struct("PPiiiiiiqqqq")
 
 
 def declare(L):
@@ -64,18 +58,17 @@ EXPORTED = ["spec_cache_resize", "spec_cache_fork_workspace_bytes", "spec_cache_
 _loaded = None
 
 
-def _lib():
+def _native():
+    """The compiled binding (csrc/binding.cpp), which checks its arguments."""
     global _loaded
     if _loaded is None:
         from . import load_library
-        _loaded = load_library()
+        load_library()
+        spec = importlib.util.spec_from_file_location("_native", _build.NATIVE)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _loaded = module
     return _loaded
-
-
-def _check(status):
-    if status != 0:
-        from . import SpecVerifyError
-        raise SpecVerifyError("%s (%d)" % (_lib().spec_status_str(status).decode(), status))
 
 
 # The handle of torch's current stream on a device, without the Python object
@@ -84,56 +77,7 @@ _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream(stream, t):
-    return _current_stream(t.get_device()) if stream is None else stream.cuda_stream
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _strides(shape, strides, step):
-    """Strides of a tensor's dimensions; a dimension of one element is never
-    stepped over, so its stride is any valid one."""
-    return [st if n > 1 else step for n, st in zip(shape, strides)] if 1 in shape else strides
-
-
-def _pages(k, v, layered):
-    """spec_pages_t of a pool, and its shape."""
-    sh, st = k.shape, k.stride()
-    if len(sh) != (5 if layered else 4) or v.shape != sh or v.dtype is not k.dtype:
-        raise ValueError("k and v must be alike, [%snum_pages, page_size, kv_heads, head_dim]"
-                         % ("layers, " if layered else ""))
-    code = _CODES.get(k.dtype)
-    if code is None:
-        raise TypeError("a cache is bfloat16, float16 or float32, got %s" % k.dtype)
-    if not k.is_cuda or not v.is_cuda:
-        raise ValueError("k and v must be CUDA tensors")
-    other = v.stride()
-    if 1 in sh:
-        st, other = _strides(sh, st, sh[-1]), _strides(sh, other, sh[-1])
-    if st != other or k.stride(-1) != 1:
-        raise ValueError("k and v need the same strides and a contiguous head_dim")
-    n, page, heads, dim = sh[-4:]
-    if layered:
-        return _PAGES.pack(k.data_ptr(), v.data_ptr(), code, sh[0], n, page, heads, dim, *st[:4]), sh
-    return _PAGES.pack(k.data_ptr(), v.data_ptr(), code, 1, n, page, heads, dim, 0, *st[:3]), sh
-
-
-_I32 = torch.int32
-
-
-def _ints(name, t, shape):
-    """An int32 CUDA tensor, contiguous, of this shape."""
-    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
-        raise ValueError("%s must be a contiguous int32 CUDA tensor %s" % (name, list(shape)))
-
-
-def _table(t, slots=None):
-    if (t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.dim() != 2
-            or (slots is not None and t.shape[0] != slots)):
-        raise ValueError("page_table must be a contiguous int32 CUDA tensor [%s, max_pages]"
-                         % ("slots" if slots is None else slots))
-    return t.shape
+    return _current_stream(t.get_device() if t.is_cuda else 0) if stream is None else stream.cuda_stream
 
 
 _scratch = {}
@@ -155,7 +99,14 @@ def _workspace(n, t, handle, stream):
 
 @functools.lru_cache(maxsize=4096)
 def _attention_bytes(B, N, Hq, heads, D):
-    return max(256, _lib().spec_tree_attention_workspace_bytes(B, N, Hq, heads, D))
+    from . import load_library
+    return max(256, load_library().spec_tree_attention_workspace_bytes(B, N, Hq, heads, D))
+
+
+@functools.lru_cache(maxsize=4096)
+def _fork_bytes(F):
+    from . import load_library
+    return max(256, load_library().spec_cache_fork_workspace_bytes(F))
 
 
 def cache_resize(page_table, page_count, page_ref, want_len, page_size, *, extra=0, dev_status=None, stream=None):
@@ -163,14 +114,8 @@ def cache_resize(page_table, page_count, page_ref, want_len, page_size, *, extra
     past that given back, then the missing ones taken, lowest free page first.
     page_table int32 [slots, max_pages], page_count [slots] and page_ref
     [num_pages] are updated; want_len int32 [slots], negative: left as it is."""
-    B, P = _table(page_table)
-    _ints("page_count", page_count, (B,))
-    _ints("want_len", want_len, (B,))
-    pages = page_ref.numel()
-    _ints("page_ref", page_ref, (pages,))
-    _check(_lib().spec_cache_resize(page_table.data_ptr(), page_count.data_ptr(), page_ref.data_ptr(),
-                                    want_len.data_ptr(), extra, page_size, B, P, pages, _ptr(dev_status),
-                                    _stream(stream, page_table)))
+    _native().resize(page_table, page_count, page_ref, want_len, page_size, extra, dev_status,
+                     _stream(stream, page_table))
 
 
 def cache_fork(k, v, page_table, page_count, page_ref, cache_len, src, dst, *, dev_status=None, stream=None):
@@ -178,40 +123,15 @@ def cache_fork(k, v, page_table, page_count, page_ref, cache_len, src, dst, *, d
     pages shared, the last partial page copied in every layer.  k, v [layers,
     num_pages, page_size, kv_heads, head_dim]; page_table, page_count, page_ref
     and cache_len are updated."""
-    pages, shape = _pages(k, v, True)
-    S, P = _table(page_table)
-    _ints("page_count", page_count, (S,))
-    _ints("cache_len", cache_len, (S,))
-    _ints("page_ref", page_ref, (shape[1],))
-    F = src.numel()
-    _ints("src", src, (F,))
-    _ints("dst", dst, (F,))
     handle = _stream(stream, k)
-    ws = _workspace(max(256, _lib().spec_cache_fork_workspace_bytes(F)), k, handle, stream)
-    _check(_lib().spec_cache_fork(pages, page_table.data_ptr(), page_count.data_ptr(), page_ref.data_ptr(),
-                                  cache_len.data_ptr(), src.data_ptr(), dst.data_ptr(), F, S, P, ws.data_ptr(),
-                                  ws.numel(), _ptr(dev_status), handle))
+    _native().fork(k, v, page_table, page_count, page_ref, cache_len, src, dst,
+                   _workspace(_fork_bytes(src.numel()), k, handle, stream), dev_status, handle)
 
 
 def cache_copy(k, v, src_pages, dst_pages, *, dev_status=None, stream=None):
     """Whole pages copied in every layer (spec_cache_copy): k, v [layers,
     num_pages, ...], src_pages and dst_pages int32 [n]."""
-    pages, _ = _pages(k, v, True)
-    n = src_pages.numel()
-    _ints("src_pages", src_pages, (n,))
-    _ints("dst_pages", dst_pages, (n,))
-    _check(_lib().spec_cache_copy(pages, src_pages.data_ptr(), dst_pages.data_ptr(), n, _ptr(dev_status),
-                                  _stream(stream, k)))
-
-
-def _rows(name, t, like, last, heads=None):
-    """Shape and strides of a [B, N, heads, head_dim] tensor of the cache's dtype."""
-    sh = t.shape
-    if (len(sh) != 4 or t.dtype is not like.dtype or not t.is_cuda or sh[3] != last or t.stride(3) != 1
-            or (heads is not None and sh[2] != heads)):
-        raise ValueError("%s must be a CUDA tensor [B, N, %s, %d] of the cache's dtype, its last dimension contiguous"
-                         % (name, "heads" if heads is None else heads, last))
-    return sh, _strides(sh, t.stride(), last)
+    _native().copy(k, v, src_pages, dst_pages, dev_status, _stream(stream, k))
 
 
 def cache_append(k, v, page_table, cache_len, k_new, v_new, *, count=None, dev_status=None, stream=None):
@@ -219,18 +139,7 @@ def cache_append(k, v, page_table, cache_len, k_new, v_new, *, count=None, dev_s
     (spec_cache_append): k, v [num_pages, page_size, kv_heads, head_dim];
     k_new, v_new [B, N, kv_heads, head_dim] of equal strides; count int32 [B]
     tokens of each request, None: all N.  cache_len is not changed."""
-    pages, shape = _pages(k, v, False)
-    new = _rows("k_new", k_new, k, shape[3], shape[2])
-    if _rows("v_new", v_new, k, shape[3], shape[2]) != new:
-        raise ValueError("k_new and v_new need the same shape and strides")
-    (B, N, _, _), st = new
-    _, P = _table(page_table, B)
-    _ints("cache_len", cache_len, (B,))
-    if count is not None:
-        _ints("count", count, (B,))
-    _check(_lib().spec_cache_append(pages, page_table.data_ptr(), cache_len.data_ptr(), k_new.data_ptr(),
-                                    v_new.data_ptr(), st[0], st[1], st[2], _ptr(count), B, N, P, _ptr(dev_status),
-                                    _stream(stream, k)))
+    _native().append(k, v, page_table, cache_len, k_new, v_new, count, dev_status, _stream(stream, k))
 
 
 def cache_commit(k, v, page_table, cache_len, out_nodes, accept_len, *, new_len=None, nodes=None, dev_status=None,
@@ -241,22 +150,10 @@ def cache_commit(k, v, page_table, cache_len, out_nodes, accept_len, *, new_len=
     out_nodes None: linear drafts (nodes: their number with the root), whose
     accepted tokens lie in place.  new_len int32 [B] receives the lengths; None:
     cache_len itself is updated.  Returns the tensor that holds them."""
-    pages, _ = _pages(k, v, True)
-    B, P = _table(page_table)
-    if out_nodes is not None:
-        nodes = out_nodes.shape[-1]
-        _ints("out_nodes", out_nodes, (B, nodes))
-    elif nodes is None:
-        raise ValueError("linear drafts need their number of nodes")
-    _ints("cache_len", cache_len, (B,))
-    _ints("accept_len", accept_len, (B,))
     if new_len is None:
         new_len = cache_len
-    else:
-        _ints("new_len", new_len, (B,))
-    _check(_lib().spec_cache_commit(pages, page_table.data_ptr(), cache_len.data_ptr(), _ptr(out_nodes),
-                                    accept_len.data_ptr(), new_len.data_ptr(), B, nodes, P, _ptr(dev_status),
-                                    _stream(stream, k)))
+    _native().commit(k, v, page_table, cache_len, out_nodes, accept_len, new_len, nodes, dev_status,
+                     _stream(stream, k))
     return new_len
 
 
@@ -270,37 +167,16 @@ def tree_attention(q, k, v, page_table, cache_len, parent=None, *, node_count=No
     window only the last `window` of them along its path and the first `sinks`
     tokens.  Returns out [B, N, q_heads, head_dim], with return_lse also the log
     of the softmax sums, float32 [B, N, q_heads]."""
-    pages, shape = _pages(k, v, False)
-    qshape, st = _rows("q", q, k, shape[3])
-    B, N, Hq, D = qshape
-    _, P = _table(page_table, B)
-    _ints("cache_len", cache_len, (B,))
-    if parent is not None:
-        _ints("parent", parent, (B, N))
-    if node_count is not None:
-        _ints("node_count", node_count, (B,))
     handle = _stream(stream, q)
-    if out is not None and (out.shape != qshape or out.dtype is not q.dtype or not out.is_cuda
-                            or not out.is_contiguous()):
-        raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype")
-    if stream is None:
-        out, lse = _outputs(q, qshape, out, return_lse)
-    else:
-        with torch.cuda.stream(stream):
-            out, lse = _outputs(q, qshape, out, return_lse)
     if workspace is None:
-        workspace = _workspace(_attention_bytes(B, N, Hq, shape[2], D), q, handle, stream)
-    _check(_lib().spec_tree_attention(q.data_ptr(), st[0], st[1], st[2], pages, page_table.data_ptr(),
-                                      cache_len.data_ptr(), _ptr(parent), _ptr(node_count), B, N, Hq, P,
-                                      1.0 / math.sqrt(D) if scale is None else scale, window, sinks, out.data_ptr(),
-                                      _ptr(lse), workspace.data_ptr(), workspace.numel(), _ptr(dev_status), handle))
-    return (out, lse) if return_lse else out
-
-
-def _outputs(q, shape, out, return_lse):
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    return out, torch.empty(shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+        B, N, Hq, D = q.shape
+        workspace = _workspace(_attention_bytes(B, N, Hq, k.shape[2], D), q, handle, stream)
+    if stream is None:
+        return _native().tree_attention(q, k, v, page_table, cache_len, parent, node_count, scale, window, sinks, out,
+                                        return_lse, workspace, dev_status, handle)
+    with torch.cuda.stream(stream):  # what the call allocates belongs to that stream
+        return _native().tree_attention(q, k, v, page_table, cache_len, parent, node_count, scale, window, sinks, out,
+                                        return_lse, workspace, dev_status, handle)
 
 
 class PagedCache:

@@ -1,5 +1,6 @@
 """Refusals of the paged-cache entry points, on the host before any CUDA call."""
 import ctypes
+import struct
 
 import pytest
 
@@ -17,11 +18,10 @@ FIELDS = ("k", "v", "dtype", "layers", "num_pages", "page_size", "heads", "head_
 
 
 def _pages(**kw):
-    from speculative_decoding_verification_69_gb300 import cache
     d = dict(k=0x10000, v=0x10000, dtype=1, layers=1, num_pages=10, page_size=16, heads=2, head_dim=64,
              layer_stride=10 * 16 * 128, page_stride=16 * 128, token_stride=128, head_stride=64)
     d.update(kw)
-    return cache._PAGES.pack(*[d[n] or 0 for n in FIELDS])
+    return struct.pack("PPiiiiiiqqqq", *[d[n] or 0 for n in FIELDS])
 
 
 BAD_POOLS = [dict(k=None), dict(v=None), dict(layers=0), dict(num_pages=0), dict(page_size=4), dict(page_size=24),
