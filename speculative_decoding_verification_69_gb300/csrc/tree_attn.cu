@@ -18,16 +18,13 @@
 // read on the device.  A (request, head, row tile) that a cut falls into
 // leaves float32 partials in the workspace, joined by tree_attn_join.
 //
-// One CTA: a TMA warp, an MMA thread and two streams of softmax, four warps
-// each (thread = row).  Up to 128 rows: the streams take the key tiles in
-// turn, each with its own m, l and O, joined at the end (SPLIT_ROWS false).
-// More rows: the streams take 128 rows each of the same key tile (SPLIT_ROWS
-// true), so a row tile is 256 rows for one read of K and V.  Either way one
-// stream's exponentials run while the tensor cores work for the other.
-//
-// What bounds it: up to about 200 rows per key head the bytes of K and V
-// (4 D bytes per key at 2 D flops per row and key), above that the tensor
-// cores and the exponentials together.
+// One CTA: a warp each that schedules, loads K (and Q), loads V and issues the
+// products, and two streams of softmax, four warps each (thread = row).  Up to
+// 128 rows: the streams take the key tiles in turn, each with its own m, l and
+// O, joined at the end (SPLIT_ROWS false).  More rows: the streams take 128 rows
+// each of the same key tile (SPLIT_ROWS true), so a row tile is 256 rows for one
+// read of K and V.  Either way one stream's exponentials run while the tensor
+// cores work for the other.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -124,7 +121,7 @@ template <int DP, bool SPLIT_ROWS> struct TaShared {
     int pages[2][32];           // K's and V's next pages
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
     uint64_t k_full[C::kStagesK], k_empty[C::kStagesK], v_full[C::kStagesV], v_empty[C::kStagesV];
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half of a tile]
+    uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [stream][half of a tile]
     uint64_t q_full, q_free, o_free, ml_full, done;
     uint32_t tmem_base;
     int abort;
@@ -369,8 +366,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             mbar_init(&sh.v_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
             for (int h = 0; h < 2; ++h) {
-                mbar_init(&sh.s_full[i][h], 1);
                 mbar_init(&sh.p_full[i][h], 4);
                 mbar_init(&sh.pv_done[i][h], 1);
             }
@@ -549,7 +546,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 ++q_loads;
             };
             auto look_q = [&]() {
-                if (q_due && __any_sync(0xFFFFFFFFu, seg_no == 0 || mbar_test_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u)))
+                if (q_due &&
+                    __any_sync(0xFFFFFFFFu, seg_no == 0 || mbar_test_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u)))
                     issue_q();
             };
             for (int i = s.i0; i < i_end && ok; ++i) {
@@ -611,24 +609,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xFFFFFFFFu, ta_wait(bar, parity, abort)) != 0;
         };
-        // Scores of stream i against the next K tile: its half h (SPLIT_ROWS), or both
-        // halves in one product (h = 0); release: the tile's last use, last: the
-        // segment's.  They overwrite the columns of the stream's last weights of that
-        // half: the products of a CTA's one issuing thread execute in the order of
+        // Scores of stream i against the next K tile; release: the tile's last use,
+        // last: the segment's.  They overwrite the columns of the stream's last
+        // weights: the products of a CTA's one issuing thread execute in the order of
         // issue, so those have been consumed by then.
-        auto scores = [&](int i, int h, bool release, bool last) -> bool {
+        auto scores = [&](int i, bool release, bool last) -> bool {
             const uint32_t st = k_tile % kKS;
-            if ((!SPLIT_ROWS || (i == 0 && h == 0)) && !wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
+            if ((!SPLIT_ROWS || i == 0) && !wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
             tc_fence_after();
             const uint64_t qd = q_desc + (uint64_t)((SPLIT_ROWS ? i : 0) * (C::kStreamQ / 16));
-            const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16) + h * (kTaKeys / 2 * 128 / 16));
+            const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {  // the columns past D hold zeros
                     const uint64_t off = (uint64_t)((k >> 2) * (kTaRows * 128 / 16) + (k & 3) * 2);
-                    mma_ss(tmem + (uint32_t)(i * kTaKeys + h * (kTaKeys / 2)), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
+                    mma_ss(tmem + (uint32_t)(i * kTaKeys), qd + off, kd + off, kIdS, k > 0 ? 1u : 0u);
                 }
-                umma_commit(&sh.s_full[i][h]);
+                umma_commit(&sh.s_full[i]);
                 if (release) umma_commit(&sh.k_empty[st]);
                 if (last) umma_commit(&sh.q_free);
             }
@@ -648,8 +645,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kTaKeys / 32; ++k)
-                    mma_ts(tmem + 256u + (uint32_t)(i * DP), p + (uint32_t)(k * 8), vd + (uint64_t)(k * 2048 / 16), kIdO,
-                           fresh && h == 0 && k == 0 ? 0u : 1u);
+                    mma_ts(tmem + 256u + (uint32_t)(i * DP), p + (uint32_t)(k * 8), vd + (uint64_t)(k * 2048 / 16),
+                           kIdO, fresh && h == 0 && k == 0 ? 0u : 1u);
                 umma_commit(&sh.pv_done[i][h]);
                 if (release) umma_commit(&sh.v_empty[st]);
             }
@@ -665,12 +662,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 const int n = __shfl_sync(0xFFFFFFFFu, sp->s.n, 0);
                 give(seg_no);
                 ok = wait(&sh.q_full, (uint32_t)seg_no & 1u);
-                ok = ok && scores(0, 0, false, false) && scores(1, 0, true, n == 1);
+                ok = ok && scores(0, false, false) && scores(1, true, n == 1);
                 for (int t = 0; t < n && ok; ++t) {
                     const bool more = t + 1 < n;
                     if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
-                    ok = ok && values(0, 0, t == 0, false) && values(0, 1, false, false) && (!more || scores(0, 0, false, false)) &&
-                         values(1, 0, t == 0, false) && values(1, 1, false, true) && (!more || scores(1, 0, true, t + 2 == n));
+                    ok = ok && values(0, 0, t == 0, false) && values(0, 1, false, false) &&
+                         (!more || scores(0, false, false)) && values(1, 0, t == 0, false) &&
+                         values(1, 1, false, true) && (!more || scores(1, true, t + 2 == n));
                 }
             }
         } else {
@@ -687,7 +685,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     if (!wait(&sh.q_full, (uint32_t)s_seg & 1u)) return false;
                     ++s_seg;
                 }
-                return scores(i, 0, true, --s_left == 0);
+                return scores(i, true, --s_left == 0);
             };
             auto next_values = [&](int i) -> bool {
                 if (v_left == 0) {
@@ -762,14 +760,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     clear = false;
                 };
                 if (clear && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh.v_full[v_stage], v_parity))) clear_v();
-                // a tile in two halves of 64 keys, each with its own scores, weights and product:
-                // one half's products run while the other half's weights are formed
+                // a tile's weights and values in two halves of 64 keys: one half's products
+                // run while the other half's weights are formed, and 64 scores fit the registers
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const long long jh = j0 + h * (kTaKeys / 2);
                     const uint32_t th = ts + (uint32_t)(h * (kTaKeys / 2));
                     if (h == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream][h], use & 1u, abort));
+                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort));
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -848,6 +846,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             base += (uint32_t)s.n;
             float l = l2.x + l2.y;
             if (!valid) l = 0.f, m = -INFINITY;
+            if (l != l) m = fmaxf(m, 0.f);  // NaN scores leave m alone: the row's part must not pass for empty
 
             // ---- the segment's result
             const uint32_t e1 = base - 1u;                   // its last tile
@@ -878,7 +877,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (!ok) break;
             }
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;  // 0: the row sees nothing
             const bool writes = row < rows_used && node < A.N;
             const int head = s.hk * A.G + (row - local * A.G);
             const long long orow = ((long long)s.b * A.N + node) * A.Hq + head;
@@ -911,7 +910,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                                 uint32_t w[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    w[e] = l > 0.f ? pack2<DT>(__uint_as_float(o[i + 2 * e]) * inv,
+                                    w[e] = l != 0.f ? pack2<DT>(__uint_as_float(o[i + 2 * e]) * inv,
                                                                __uint_as_float(o[i + 2 * e + 1]) * inv)
                                                    : 0u;
                                 dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -931,7 +930,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.o_free));
             if (writes && col0 == 0) {
                 if (whole_item) {
-                    if (A.lse) A.lse[orow] = l > 0.f ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
+                    if (A.lse) A.lse[orow] = l != 0.f ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
                 } else {
                     A.part_ml[slot * rows_cta + prow] = make_float2(m, l);
                 }

@@ -142,6 +142,27 @@ def test_random_shapes(seed):
            scale=r.choice([None, 0.05]))
 
 
+@pytest.mark.parametrize("N,hq,ctx", [(4, 4, 300), (64, 8, 500), (2, 2, 60000)])
+def test_nan_and_infinite_scores_show(N, hq, ctx):
+    """A NaN or an infinity that a row does see makes that row NaN, and no other."""
+    c = _case(N + ctx, [ctx, 200], N, hq, 2, 64, 16, torch.bfloat16)
+    ref_o, ref_l, _ = _run(c)
+    bad = c["q"].clone()
+    bad[0, 1, 0, 3] = float("nan")
+    bad[1, 0, hq - 1] = float("inf")  # scores of both infinities
+    o, l, st = _run(dict(c, q=bad))
+    assert st == 0
+    for b, n, h in ((0, 1, 0), (1, 0, hq - 1)):
+        assert o[b, n, h].isnan().all() and l[b, n, h].isnan()
+        o[b, n, h], l[b, n, h] = ref_o[b, n, h], ref_l[b, n, h]
+    assert torch.equal(o, ref_o) and torch.equal(l, ref_l)
+    # all scores of a row NaN, in every key tile and every part
+    c["k"][c["table"][0, :-(-(ctx + N) // 16)].long()] = float("nan")
+    o, l, st = _run(c)
+    assert st == 0 and o[0].isnan().all() and l[0].isnan().all()
+    assert torch.equal(o[1], ref_o[1]) and torch.equal(l[1], ref_l[1])
+
+
 def test_large_scores():
     """Sharp distributions whose maximum grows along the keys (the running
     maximum moves many times) and falls (it never moves again)."""
