@@ -79,16 +79,22 @@ struct Geo {
     __device__ __forceinline__ int tile(int i) const { return i < st ? i : wt0 + (i - st); }
 };
 
-__device__ __forceinline__ Geo ta_geo(const TaArgs &A, int b) {
-    Geo g;
+// Committed positions and nodes of request b, clamped to what the table can hold.
+__device__ __forceinline__ int2 ta_lens(const TaArgs &A, int b) {
     const int cap = (int)min((long long)A.max_pages << A.page_shift, 0x7FFFFFFFll);
-    g.cnt = A.node_count ? max(0, min(__ldcg(A.node_count + b), A.N)) : A.N;
-    g.c = __ldcg(A.len + b);
-    if (g.c < 0 || g.c > cap - g.cnt) {
+    int cnt = A.node_count ? max(0, min(__ldcg(A.node_count + b), A.N)) : A.N;
+    int c = __ldcg(A.len + b);
+    if (c < 0 || c > cap - cnt) {
         flag(A.status, SPEC_DEV_BAD_LEN);
-        g.c = max(0, min(g.c, cap));
-        g.cnt = min(g.cnt, cap - g.c);
+        c = max(0, min(c, cap));
+        cnt = min(cnt, cap - c);
     }
+    return make_int2(c, cnt);
+}
+__device__ __forceinline__ Geo ta_geo(const TaArgs &A, int2 lens) {
+    Geo g;
+    g.c = lens.x;
+    g.cnt = lens.y;
     g.end = g.c + g.cnt;
     g.wlo = A.window ? max(0, g.c - A.window + 1) : 0;
     g.wt0 = g.wlo / kTaKeys;
@@ -102,7 +108,6 @@ struct Seg {
     Geo g;
     int b, hk, node0;   // node0: first node of the row tile
     int i0, n;          // tiles [i0, i0 + n) of the g.nt
-    long long start;    // unit of tile 0
 };
 
 // A segment as the scheduling warp hands it to the others; n = 0 ends the list.
@@ -116,7 +121,7 @@ template <int DP, bool SPLIT_ROWS> struct TaShared {
     using C = TaCfg<DP, SPLIT_ROWS>;
     uint8_t q[C::kQ];
     uint8_t k[C::kStagesK][C::kStage], v[C::kStagesV][C::kStage];
-    long long incl[kTaChunks];  // units of the requests up to the end of each chunk of them
+    long long incl[kTaChunks];  // units of the requests up to the end of each chunk, from every 32nd chunk on
     SegSlot seg[kTaSlots];
     int pages[2][32];           // K's and V's next pages
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
@@ -131,59 +136,93 @@ template <int DP, bool SPLIT_ROWS> struct TaShared {
 template <bool SPLIT_ROWS> __device__ __forceinline__ int ta_nodes(const TaArgs &A) {
     return A.np * (SPLIT_ROWS ? 2 : 1);
 }
-template <bool SPLIT_ROWS> __device__ __forceinline__ long long ta_units(const TaArgs &A, const Geo &g) {
+// Row tiles of a request with cnt nodes (the host makes them whole for cnt = N).
+template <bool SPLIT_ROWS> __device__ __forceinline__ int ta_row_tiles(const TaArgs &A, int cnt) {
     const int npt = ta_nodes<SPLIT_ROWS>(A);
-    return (long long)g.nt * A.H * ((g.cnt + npt - 1) / npt);
+    return cnt <= npt ? 1 : (cnt + npt - 1) / npt;
+}
+template <bool SPLIT_ROWS> __device__ __forceinline__ long long ta_units(const TaArgs &A, const Geo &g) {
+    return (long long)g.nt * (A.H * ta_row_tiles<SPLIT_ROWS>(A, g.cnt));
+}
+__device__ __forceinline__ long long ta_div(long long a, long long b) {  // a, b >= 0; 32 bits when they fit
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The segment that unit u begins, at most up to unit u1.  Called by whole warps.
-template <bool SPLIT_ROWS>
-__device__ __forceinline__ Seg ta_segment(const TaArgs &A, const long long *incl, long long u, long long u1) {
-    const int lane = threadIdx.x & 31;
-    int chunk = 0;
-#pragma unroll
-    for (int i = 0; i < kTaChunks; i += 32)
-        chunk += __popc(__ballot_sync(0xFFFFFFFFu, incl[i + lane] <= u));
-    long long base = chunk > 0 ? incl[chunk - 1] : 0;
-    const int per = (A.B + kTaChunks - 1) / kTaChunks;
-    int b = chunk * per;
-    if (per > 1) {
-        const int b1 = min(A.B, b + per);
-        for (int b0 = b; b0 < b1; b0 += 32) {
-            long long x = b0 + lane < b1 ? ta_units<SPLIT_ROWS>(A, ta_geo(A, b0 + lane)) : 0;
+// The scheduling warp's place in the list of units.
+template <bool SPLIT_ROWS> struct Walk {
+    int b0;          // the lanes hold the lengths of requests b0 + lane
+    int2 lens;
+    int b, hk, rt, rts, i0;
+    Geo g;
+
+    __device__ __forceinline__ void fetch(const TaArgs &A, int from) {
+        const int lane = threadIdx.x & 31;
+        b0 = from;
+        lens = from + lane < A.B ? ta_lens(A, from + lane) : make_int2(0, 0);
+    }
+    __device__ __forceinline__ void enter(const TaArgs &A, int request) {
+        b = request;
+        g = ta_geo(A, make_int2(__shfl_sync(0xFFFFFFFFu, lens.x, b - b0), __shfl_sync(0xFFFFFFFFu, lens.y, b - b0)));
+        rts = ta_row_tiles<SPLIT_ROWS>(A, g.cnt);
+        hk = rt = i0 = 0;
+    }
+    // To unit u, which exists.
+    __device__ __forceinline__ void find(const TaArgs &A, const long long *incl, long long u) {
+        const int lane = threadIdx.x & 31;
+        int chunk = 0;
+        long long base = 0, before = 0;
+#pragma unroll 1
+        for (int i = 0; i < kTaChunks; i += 32) {  // the chunks that end at or before u
+            const long long x = before + incl[i + lane];
+            const int k = __popc(__ballot_sync(0xFFFFFFFFu, x <= u));
+            if (k > 0) base = __shfl_sync(0xFFFFFFFFu, x, k - 1);
+            before = __shfl_sync(0xFFFFFFFFu, x, 31);
+            chunk += k;
+            if (k < 32) break;
+        }
+        const int per = (A.B + kTaChunks - 1) / kTaChunks;
+#pragma unroll 1
+        for (int from = chunk * per;; from += 32) {  // the requests that end at or before u
+            fetch(A, from);
+            long long x = ta_units<SPLIT_ROWS>(A, ta_geo(A, lens));
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
                 if (lane >= o) x += y;
             }
             const int k = __popc(__ballot_sync(0xFFFFFFFFu, base + x <= u));
-            if (k > 0) {
-                const long long skip = __shfl_sync(0xFFFFFFFFu, x, k - 1);
-                b = b0 + k;
-                base += skip;
-                if (k == 32) continue;
-            } else {
-                b = b0;
+            if (k > 0) base += __shfl_sync(0xFFFFFFFFu, x, k - 1);
+            if (k < 32 || from + 32 >= A.B) {
+                enter(A, min(from + min(k, 31), A.B - 1));
+                break;
             }
-            break;
         }
-        b = min(b, A.B - 1);
+        const int item = (int)ta_div(u - base, max(g.nt, 1));
+        hk = item / rts;
+        rt = item - hk * rts;
+        i0 = (int)(u - base - (long long)item * g.nt);
     }
-    Seg s;
-    s.b = b;
-    s.g = ta_geo(A, b);
-    const long long off = u - base;
-    const int nt = max(s.g.nt, 1);
-    const int item = (int)(off / nt);
-    const int npt = ta_nodes<SPLIT_ROWS>(A);
-    const int rts = max((s.g.cnt + npt - 1) / npt, 1);
-    s.hk = item / rts;
-    s.node0 = (item - s.hk * rts) * npt;
-    s.i0 = (int)(off - (long long)item * nt);
-    s.n = (int)min((long long)(nt - s.i0), u1 - u);
-    s.start = base + (long long)item * nt;
-    return s;
-}
+    // Past n tiles, within or to the end of the item.
+    __device__ __forceinline__ void advance(const TaArgs &A, int n) {
+        i0 += n;
+        if (i0 < g.nt) return;
+        i0 = 0;
+        if (++rt < rts) return;
+        rt = 0;
+        if (++hk < A.H) return;
+        int next = b + 1;  // the next request that has nodes
+        for (;;) {
+            const int lane = threadIdx.x & 31;
+            const uint32_t some = __ballot_sync(0xFFFFFFFFu, lens.y > 0 && b0 + lane >= next);
+            if (some) {
+                enter(A, b0 + __ffs(some) - 1);
+                return;
+            }
+            if (b0 + 32 >= A.B) return;
+            fetch(A, next = b0 + 32);
+        }
+    }
+};
 
 // ------------------------------------------------------------------ PTX
 
@@ -320,8 +359,8 @@ __device__ __forceinline__ void ta_paths(const TaArgs &A, int b, int cnt, unsign
             }
         }
     }
-#pragma unroll
-    for (int r = 0; r < 6; ++r) {
+#pragma unroll 1
+    while (__any_sync(0xFFFFFFFFu, up[0] >= 0 || up[1] >= 0)) {  // at most 6 rounds
         unsigned long long na[2];
         int nu[2];
 #pragma unroll
@@ -399,7 +438,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int per = (A.B + kTaChunks - 1) / kTaChunks;
         const int b0 = threadIdx.x * per, b1 = min(A.B, b0 + per);
         long long x = 0;
-        for (int b = b0; b < b1; ++b) x += ta_units<SPLIT_ROWS>(A, ta_geo(A, b));
+#pragma unroll 2
+        for (int b = b0; b < b1; ++b) x += ta_units<SPLIT_ROWS>(A, ta_geo(A, ta_lens(A, b)));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -410,20 +450,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x < kTaChunks && warp > 0) {  // add the sums of the warps before
-        long long before = 0;
-        for (int w = 0; w < warp; ++w) before += sh.incl[w * 32 + 31];
-        __syncwarp();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        sh.incl[threadIdx.x] += before;
-    } else if (warp == 0) {
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-    }
-    __syncthreads();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
     volatile int *abort = &sh.abort;
-    const long long total = sh.incl[kTaChunks - 1];
-    const long long run = (total + gridDim.x - 1) / gridDim.x;
+    long long total = 0;
+    for (int i = 31; i < kTaChunks; i += 32) total += sh.incl[i];
+    const long long run = ta_div(total + gridDim.x - 1, gridDim.x);
     const long long u_first = min(total, (long long)blockIdx.x * run), u_last = min(total, u_first + run);
 
     // segment k, or nothing when the wait for it ran out
@@ -441,11 +472,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         bool ok = true;
         unsigned long long anc[2] = {0, 0};
         int low[2] = {0, 0};
-        for (long long u = u_first; ok; ++k) {
+        Walk<SPLIT_ROWS> w;
+        if (u_first < u_last) w.find(A, sh.incl, u_first);
+        for (long long left = u_last - u_first; ok; ++k) {
             Seg s = {};
-            if (u < u_last) {
-                s = ta_segment<SPLIT_ROWS>(A, sh.incl, u, u_last);
-                u += s.n;
+            if (left > 0) {
+                s.g = w.g;
+                s.b = w.b;
+                s.hk = w.hk;
+                s.node0 = w.rt * ta_nodes<SPLIT_ROWS>(A);
+                s.i0 = w.i0;
+                s.n = (int)min((long long)(w.g.nt - w.i0), left);
+                left -= s.n;
             }
             if (k >= kTaSlots)
                 ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort));
@@ -455,6 +493,19 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 slot.s = s;
                 mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.seg_full[k % kTaSlots]));
             }
+            if (k == 0 && lane == 0) {
+                // the CTA's first unit lies inside an item: if the item began in the CTA
+                // before, this is its first cut, where its parts are joined
+                const long long start = u_first - s.i0;
+                const bool joins = s.i0 > 0 && start >= u_first - run;
+                if (joins) {
+                    A.joins[2 * blockIdx.x] = make_int4(s.b, s.hk, s.node0, 0);
+                    const int last = (int)ta_div(start + s.g.nt - 1, run);
+                    A.joins[2 * blockIdx.x + 1] = make_int4(1, (int)blockIdx.x - 1, last, 0);
+                } else {
+                    A.joins[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+                }
+            }
             // the loads and scores go ahead; the softmax warps need the paths too
             if (s.n > 0 && s.b != b) {
                 ta_paths(A, b = s.b, s.g.cnt, anc);
@@ -463,6 +514,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     if (!A.window) break;
                     low[x] = max(0, s.g.c + __popcll(anc[x]) - A.window);
                     unsigned long long left = anc[x];
+#pragma unroll 1
                     for (int place = s.g.c; left && place < low[x]; ++place) {
                         const unsigned long long bit = left & (0ull - left);
                         if (place >= A.sinks) anc[x] &= ~bit;
@@ -478,6 +530,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.path_full[k % kTaSlots]));
             if (s.n == 0) break;
+            w.advance(A, s.n);
         }
         __syncwarp();
     } else if (warp == kTaWarpK || warp == kTaWarpV) {  // --------------- loads
@@ -720,7 +773,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int rows_used = A.np * A.G, local = row / A.G;
         uint32_t base = 0;                     // the CTA's tiles before this segment
         int seg_no = 0;
-        bool ok = true, joins = false;
+        bool ok = true;
         for (; ok; ++seg_no) {
             const SegSlot *sp = take(sh.path_full, seg_no);
             if (!sp || sp->s.n == 0) break;
@@ -935,31 +988,22 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     A.part_ml[slot * rows_cta + prow] = make_float2(m, l);
                 }
             }
-            if (s.i0 > 0 && threadIdx.x == 0) {
-                // this CTA's first unit lies inside an item: if the item began in the
-                // CTA before, this is its first cut, where its parts are joined
-                const long long first_cta = s.start / run, last_cta = (s.start + g.nt - 1) / run;
-                if (first_cta == (long long)blockIdx.x - 1) {
-                    joins = true;
-                    A.joins[2 * blockIdx.x] = make_int4(s.b, s.hk, s.node0, 0);
-                    A.joins[2 * blockIdx.x + 1] = make_int4(1, (int)first_cta, (int)last_cta, 0);
-                }
-            }
         }
-        if (threadIdx.x == 0 && !joins) A.joins[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
         if (!ok) *abort = 1;
     }
 
     if (warp < 8) {  // the nodes past every row tile (past the counts) see nothing
         const int npt = ta_nodes<SPLIT_ROWS>(A);
         for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
-            const Geo g = ta_geo(A, b);
-            const int n0 = min(A.N, (g.cnt + npt - 1) / npt * npt);
+            const int2 lens = ta_lens(A, b);
+            const int n0 = lens.y > 0 ? min(A.N, ta_row_tiles<SPLIT_ROWS>(A, lens.y) * npt) : 0;
             if (n0 >= A.N) continue;
             const long long r0 = ((long long)b * A.N + n0) * A.Hq, r1 = ((long long)b * A.N + A.N) * A.Hq;
             uint4 *o = reinterpret_cast<uint4 *>(A.out);
+#pragma unroll 1
             for (long long i = r0 * A.D / 8 + threadIdx.x; i < r1 * A.D / 8; i += 256) o[i] = make_uint4(0u, 0u, 0u, 0u);
             if (A.lse)
+#pragma unroll 1
                 for (long long i = r0 + threadIdx.x; i < r1; i += 256) A.lse[i] = -INFINITY;
         }
     }
