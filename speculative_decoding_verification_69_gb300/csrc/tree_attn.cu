@@ -755,10 +755,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (--v_left == 0) give(v_seg - 1);
                 return true;
             };
+            // Before the last values of a segment no scores are put: its results wait for them.
+            int given = 0;  // tiles whose scores have been issued
 #pragma unroll 1
-            for (int e = -2; e < (int)tiles && ok; ++e) {
+            for (int e = -1; e < (int)tiles && ok; ++e) {
                 if (e >= 0) ok = next_values(e & 1);
-                if (e + 2 < (int)tiles) ok = ok && next_scores(e & 1);
+#pragma unroll 1
+                while (ok && given < min(e + 3, (int)tiles) && (given <= e + 1 || v_left != 1))
+                    ok = next_scores(given++ & 1);
             }
         }
         // every MMA has finished before the TMEM is freed
@@ -803,10 +807,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     const long long j = j0 + row;
                     if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
 #pragma unroll
-                        for (int d = 0; d < kHalves; ++d) {
+                        for (int d = 0; d < kHalves; ++d) {  // neighbours begin 16 bytes apart: other banks
                             uint4 *z = reinterpret_cast<uint4 *>(sh.v[v_stage] + d * kTaKeys * 128 + row * 128);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int i = 0; i < 8; ++i) z[(i + row) & 7] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     fence_proxy_async();
