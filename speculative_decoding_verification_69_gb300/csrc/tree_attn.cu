@@ -799,7 +799,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 const uint32_t use = SPLIT_ROWS ? base + (uint32_t)t : (base + (uint32_t)t) >> 1;  // the stream's
                 // values that no node sees may be anything: they are cleared, so that their zero
                 // weights leave them out (SPLIT_ROWS: by stream 0, whose weights are used first);
-                // before the scores are waited for if the tile is there by then
+                // before the weights if the tile is there by then.  Not looked for before the scores
+                // have come: they follow earlier values, whose tiles have then been there, and a
+                // stage's parity says nothing while the fill before this one is still due
                 const uint32_t v_tile = base + (uint32_t)t, v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
                 bool clear = (!SPLIT_ROWS || stream == 0) &&
                              (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks));
@@ -816,7 +818,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     fence_proxy_async();
                     clear = false;
                 };
-                if (clear && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh.v_full[v_stage], v_parity))) clear_v();
                 // a tile's weights and values in two halves of 64 keys: one half's products
                 // run while the other half's weights are formed, and 64 scores fit the registers
 #pragma unroll 1
@@ -827,6 +828,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort));
                         if (!ok) break;
                         tc_fence_after();
+                        if (clear && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh.v_full[v_stage], v_parity))) clear_v();
                     }
                     if (warp_works) {
                         uint32_t x[64];
