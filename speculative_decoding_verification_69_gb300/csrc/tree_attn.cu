@@ -20,11 +20,12 @@
 //
 // One CTA: a warp each that schedules, loads K (and Q), loads V and issues the
 // products, and two streams of softmax, four warps each (thread = row).  Up to
-// 128 rows: the streams take the key tiles in turn, each with its own m, l and
-// O, joined at the end (SPLIT_ROWS false).  More rows: the streams take 128 rows
-// each of the same key tile (SPLIT_ROWS true), so a row tile is 256 rows for one
-// read of K and V.  Either way one stream's exponentials run while the tensor
-// cores work for the other.
+// 128 rows the streams take the key tiles in turn, each with its own m, l and
+// O, joined at the end (kTaSplitKeys), or, with many requests, a key head each
+// (kTaSplitHeads: a unit is then a pair of heads).  With more rows they take 128
+// rows each of the same key tile (kTaSplitRows), so a row tile is 256 rows for
+// one read of K and V.  Either way one stream's exponentials run while the
+// tensor cores work for the other.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -46,6 +47,9 @@ constexpr int kTaChunks = 128;      // entries of the running sum over requests
 constexpr unsigned long long kTaWaitNs = 2000000000ull;  // 2 s
 constexpr float kTaGrow = 8.f;      // growth of a row's maximum that rescales its O
 
+// What the two streams of a CTA divide between them.
+enum { kTaSplitKeys, kTaSplitRows, kTaSplitHeads };
+
 struct TaArgs {
     const int *table, *len, *parent, *node_count;
     int B, N, Hq, H, G, D, max_pages, num_pages, page, page_shift;
@@ -61,13 +65,13 @@ struct TaArgs {
     uint32_t *status;
 };
 
-template <int DP, bool SPLIT_ROWS> struct TaCfg {
+template <int DP, int MODE> struct TaCfg {
     static constexpr int kStreamQ = kTaRows * DP * 2;            // bytes of one stream's Q
-    static constexpr int kQ = kStreamQ * (SPLIT_ROWS ? 2 : 1);
+    static constexpr int kQ = kStreamQ * (MODE == kTaSplitKeys ? 1 : 2);
     static constexpr int kStage = kTaKeys * DP * 2;              // one K or V tile
     // as many tiles in flight as the shared memory holds beside Q
-    static constexpr int kStagesK = DP == 128 ? 2 : (SPLIT_ROWS ? 5 : 6);
-    static constexpr int kStagesV = DP == 128 ? (SPLIT_ROWS ? 2 : 3) : 6;
+    static constexpr int kStagesK = DP == 128 ? 2 : (MODE == kTaSplitKeys ? 6 : 5);
+    static constexpr int kStagesV = DP == 128 ? (MODE == kTaSplitKeys ? 3 : 2) : 6;
 };
 
 // What one request's tiles cover: positions [0, min(sinks, ...)) in its first
@@ -117,8 +121,8 @@ struct SegSlot {
     int low[SPEC_MAX_TREE];                  // the first committed position in its window
 };
 
-template <int DP, bool SPLIT_ROWS> struct TaShared {
-    using C = TaCfg<DP, SPLIT_ROWS>;
+template <int DP, int MODE> struct TaShared {
+    using C = TaCfg<DP, MODE>;
     uint8_t q[C::kQ];
     uint8_t k[C::kStagesK][C::kStage], v[C::kStagesV][C::kStage];
     long long incl[kTaChunks];  // units of the requests up to the end of each chunk, from every 32nd chunk on
@@ -127,29 +131,29 @@ template <int DP, bool SPLIT_ROWS> struct TaShared {
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
     uint64_t k_full[C::kStagesK], k_empty[C::kStagesK], v_full[C::kStagesV], v_empty[C::kStagesV];
     uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [stream][half of a tile]
-    uint64_t q_full, q_free, o_free, ml_full, done;
+    uint64_t q_full, q_free, o_free[2], ml_full, done;
     uint32_t tmem_base;
     int abort;
-    float2 ml[SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : 2][SPLIT_ROWS ? 1 : kTaRows];  // [segment parity][stream][row]
+    float2 ml[MODE == kTaSplitKeys ? 2 : 1][2][MODE == kTaSplitKeys ? kTaRows : 1];  // [segment parity][stream][row]
 };
 
-template <bool SPLIT_ROWS> __device__ __forceinline__ int ta_nodes(const TaArgs &A) {
-    return A.np * (SPLIT_ROWS ? 2 : 1);
+template <int MODE> __device__ __forceinline__ int ta_nodes(const TaArgs &A) {
+    return A.np * (MODE == kTaSplitRows ? 2 : 1);
 }
 // Row tiles of a request with cnt nodes (the host makes them whole for cnt = N).
-template <bool SPLIT_ROWS> __device__ __forceinline__ int ta_row_tiles(const TaArgs &A, int cnt) {
-    const int npt = ta_nodes<SPLIT_ROWS>(A);
+template <int MODE> __device__ __forceinline__ int ta_row_tiles(const TaArgs &A, int cnt) {
+    const int npt = ta_nodes<MODE>(A);
     return cnt <= npt ? 1 : (cnt + npt - 1) / npt;
 }
-template <bool SPLIT_ROWS> __device__ __forceinline__ long long ta_units(const TaArgs &A, const Geo &g) {
-    return (long long)g.nt * (A.H * ta_row_tiles<SPLIT_ROWS>(A, g.cnt));
+template <int MODE> __device__ __forceinline__ long long ta_units(const TaArgs &A, const Geo &g) {
+    return (long long)g.nt * (A.H * ta_row_tiles<MODE>(A, g.cnt));
 }
 __device__ __forceinline__ long long ta_div(long long a, long long b) {  // a, b >= 0; 32 bits when they fit
     return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // The scheduling warp's place in the list of units.
-template <bool SPLIT_ROWS> struct Walk {
+template <int MODE> struct Walk {
     int b0;          // the lanes hold the lengths of requests b0 + lane
     int2 lens;
     int b, hk, rt, rts, i0;
@@ -163,7 +167,7 @@ template <bool SPLIT_ROWS> struct Walk {
     __device__ __forceinline__ void enter(const TaArgs &A, int request) {
         b = request;
         g = ta_geo(A, make_int2(__shfl_sync(0xFFFFFFFFu, lens.x, b - b0), __shfl_sync(0xFFFFFFFFu, lens.y, b - b0)));
-        rts = ta_row_tiles<SPLIT_ROWS>(A, g.cnt);
+        rts = ta_row_tiles<MODE>(A, g.cnt);
         hk = rt = i0 = 0;
     }
     // To unit u, which exists.
@@ -184,7 +188,7 @@ template <bool SPLIT_ROWS> struct Walk {
 #pragma unroll 1
         for (int from = chunk * per;; from += 32) {  // the requests that end at or before u
             fetch(A, from);
-            long long x = ta_units<SPLIT_ROWS>(A, ta_geo(A, lens));
+            long long x = ta_units<MODE>(A, ta_geo(A, lens));
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -197,10 +201,12 @@ template <bool SPLIT_ROWS> struct Walk {
                 break;
             }
         }
-        const int item = (int)ta_div(u - base, max(g.nt, 1));
+        // (the bounds hold by themselves unless the lengths are written during the call,
+        // which then must not lead out of any array)
+        const int item = (int)min(ta_div(max(u - base, 0ll), max(g.nt, 1)), (long long)A.H * rts - 1);
         hk = item / rts;
         rt = item - hk * rts;
-        i0 = (int)(u - base - (long long)item * g.nt);
+        i0 = (int)min(max(u - base - (long long)item * g.nt, 0ll), max(g.nt - 1ll, 0ll));
     }
     // Past n tiles, within or to the end of the item.
     __device__ __forceinline__ void advance(const TaArgs &A, int n) {
@@ -378,12 +384,12 @@ __device__ __forceinline__ void ta_paths(const TaArgs &A, int b, int cnt, unsign
 
 // ------------------------------------------------------------------ the kernel
 
-template <int DT, int DP, bool SPLIT_ROWS>
+template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, TaArgs A) {
-    using C = TaCfg<DP, SPLIT_ROWS>;
-    using Sh = TaShared<DP, SPLIT_ROWS>;
+    using C = TaCfg<DP, MODE>;
+    using Sh = TaShared<DP, MODE>;
     extern __shared__ uint8_t ta_raw[];
     Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(ta_raw) + 1023) & ~(uintptr_t)1023);
     // through a shuffle, so that the compiler knows the roles' branches, and what is
@@ -391,6 +397,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     constexpr int kKS = C::kStagesK, kVS = C::kStagesV;
     constexpr int kHalves = DP / 64;
+    constexpr int kPer = MODE == kTaSplitHeads ? 2 : 1;  // K and V tiles of a unit
     // P is scaled up to 2^15 in float16, so that weights 2^-29 below the
     // maximum are still normal numbers; bfloat16 has float32's range
     constexpr float kLift = DT == SPEC_DTYPE_F16 ? 7.f : 0.f;
@@ -418,7 +425,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_free, 1);
-        mbar_init(&sh.o_free, 8);
+        mbar_init(&sh.o_free[0], 4);
+        mbar_init(&sh.o_free[1], 4);
         mbar_init(&sh.ml_full, 8);
         mbar_init(&sh.done, 1);
         sh.abort = 0;
@@ -439,7 +447,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int b0 = threadIdx.x * per, b1 = min(A.B, b0 + per);
         long long x = 0;
 #pragma unroll 2
-        for (int b = b0; b < b1; ++b) x += ta_units<SPLIT_ROWS>(A, ta_geo(A, ta_lens(A, b)));
+        for (int b = b0; b < b1; ++b) x += ta_units<MODE>(A, ta_geo(A, ta_lens(A, b)));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         bool ok = true;
         unsigned long long anc[2] = {0, 0};
         int low[2] = {0, 0};
-        Walk<SPLIT_ROWS> w;
+        Walk<MODE> w;
         if (u_first < u_last) w.find(A, sh.incl, u_first);
         for (long long left = u_last - u_first; ok; ++k) {
             Seg s = {};
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 s.g = w.g;
                 s.b = w.b;
                 s.hk = w.hk;
-                s.node0 = w.rt * ta_nodes<SPLIT_ROWS>(A);
+                s.node0 = w.rt * ta_nodes<MODE>(A);
                 s.i0 = w.i0;
                 s.n = (int)min((long long)(w.g.nt - w.i0), left);
                 left -= s.n;
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 const bool joins = s.i0 > 0 && start >= u_first - run;
                 if (joins) {
                     A.joins[2 * blockIdx.x] = make_int4(s.b, s.hk, s.node0, 0);
-                    const int last = (int)ta_div(start + s.g.nt - 1, run);
+                    const int last = (int)min(ta_div(start + s.g.nt - 1, run), gridDim.x - 1ll);
                     A.joins[2 * blockIdx.x + 1] = make_int4(1, (int)blockIdx.x - 1, last, 0);
                 } else {
                     A.joins[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -586,13 +594,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             // before every load, so that the tiles need not wait for it
             bool q_due = is_k;
             auto issue_q = [&]() {
-                constexpr int kQs = SPLIT_ROWS ? 2 : 1;
+                constexpr int kQs = MODE == kTaSplitKeys ? 1 : 2;
                 if (elect_one()) {
                     mbar_expect_tx(&sh.q_full, (uint32_t)(kQs * kHalves * A.np * A.G * 128));
                     for (int q = 0; q < kQs; ++q)
                         for (int h = 0; h < kHalves; ++h)
-                            tma_load_4d(sh.q + q * C::kStreamQ + h * kTaRows * 128, &tm_q, h * 64, s.hk * A.G,
-                                        s.node0 + q * A.np, s.b, &sh.q_full);
+                            tma_load_4d(sh.q + q * C::kStreamQ + h * kTaRows * 128, &tm_q, h * 64,
+                                        (MODE == kTaSplitHeads ? 2 * s.hk + q : s.hk) * A.G,
+                                        MODE == kTaSplitRows ? s.node0 + q * A.np : s.node0, s.b, &sh.q_full);
                 }
                 __syncwarp();
                 q_due = false;
@@ -607,37 +616,40 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (i >= base + ahead) turn(i);
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, lane < nb && box_seen(box_pos(i)));
                 const int tok = (int)(((long long)s.g.tile(i) * kTaKeys) & (A.page - 1));
-                look_q();
-                if (fill > 0) {
-                    unsigned long long t0 = 0;
-                    for (uint32_t tries = 1;; ++tries) {
-                        if (__any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u))) break;
-                        look_q();
-                        if ((tries & 63u) == 0) {
-                            const unsigned long long now = global_ns();
-                            if (t0 == 0) t0 = now;
-                            if (__any_sync(0xFFFFFFFFu, *abort || now - t0 > kTaWaitNs)) {
-                                *abort = 1;
-                                ok = false;
-                                break;
+#pragma unroll 1
+                for (int head = s.hk * kPer; head < (s.hk + 1) * kPer && ok; ++head) {
+                    look_q();
+                    if (fill > 0) {
+                        unsigned long long t0 = 0;
+                        for (uint32_t tries = 1;; ++tries) {
+                            if (__any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u))) break;
+                            look_q();
+                            if ((tries & 63u) == 0) {
+                                const unsigned long long now = global_ns();
+                                if (t0 == 0) t0 = now;
+                                if (__any_sync(0xFFFFFFFFu, *abort || now - t0 > kTaWaitNs)) {
+                                    *abort = 1;
+                                    ok = false;
+                                    break;
+                                }
                             }
                         }
+                        if (!ok) break;
                     }
-                    if (!ok) break;
-                }
-                uint8_t *tile = tiles + stage * C::kStage;
-                if (elect_one()) {
-                    mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
-                    const int *page = pages + (i - base) * nb;
+                    uint8_t *tile = tiles + stage * C::kStage;
+                    if (elect_one()) {
+                        mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
+                        const int *page = pages + (i - base) * nb;
 #pragma unroll 1
-                    for (int x = 0; x < nb; ++x, ++page, tile += A.box * 128) {
-                        if (!((seen >> x) & 1u)) continue;
-                        tma_load_4d(tile, tm, 0, tok, s.hk, *page, &full[stage]);
-                        if (kHalves == 2) tma_load_4d(tile + kTaKeys * 128, tm, 64, tok, s.hk, *page, &full[stage]);
+                        for (int x = 0; x < nb; ++x, ++page, tile += A.box * 128) {
+                            if (!((seen >> x) & 1u)) continue;
+                            tma_load_4d(tile, tm, 0, tok, head, *page, &full[stage]);
+                            if (kHalves == 2) tma_load_4d(tile + kTaKeys * 128, tm, 64, tok, head, *page, &full[stage]);
+                        }
                     }
+                    __syncwarp();
+                    if (++stage == stages) stage = 0, ++fill;
                 }
-                __syncwarp();
-                if (++stage == stages) stage = 0, ++fill;
             }
             if (ok && q_due) {
                 ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u, abort));
@@ -668,9 +680,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         // issue, so those have been consumed by then.
         auto scores = [&](int i, bool release, bool last) -> bool {
             const uint32_t st = k_tile % kKS;
-            if ((!SPLIT_ROWS || i == 0) && !wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
+            if ((MODE != kTaSplitRows || i == 0) && !wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
             tc_fence_after();
-            const uint64_t qd = q_desc + (uint64_t)((SPLIT_ROWS ? i : 0) * (C::kStreamQ / 16));
+            const uint64_t qd = q_desc + (uint64_t)((MODE == kTaSplitKeys ? 0 : i) * (C::kStreamQ / 16));
             const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16));
             if (elect_one()) {
 #pragma unroll
@@ -691,7 +703,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         auto values = [&](int i, int h, bool fresh, bool release) -> bool {
             const uint32_t st = v_tile % kVS;
             if (!wait(&sh.p_full[i][h], use[i] & 1u)) return false;
-            if (h == 0 && (!SPLIT_ROWS || i == 0) && !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
+            if (h == 0 && (MODE != kTaSplitRows || i == 0) && !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
             tc_fence_after();
             const uint64_t vd = vt_desc + (uint64_t)(st * (C::kStage / 16) + h * (kTaKeys / 2 * 128 / 16));
             const uint32_t p = tmem + (uint32_t)(i * kTaKeys + h * (kTaKeys / 2) + kTaKeys / 4);
@@ -708,7 +720,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (h == 1) ++use[i];
             return true;
         };
-        if (SPLIT_ROWS) {
+        if (MODE == kTaSplitRows) {
             for (; ok; ++seg_no) {
                 const SegSlot *sp = take(sh.seg_full, seg_no);
                 if (!sp || sp->s.n == 0) break;
@@ -718,7 +730,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 ok = ok && scores(0, false, false) && scores(1, true, n == 1);
                 for (int t = 0; t < n && ok; ++t) {
                     const bool more = t + 1 < n;
-                    if (t == 0 && seg_no > 0) ok = wait(&sh.o_free, (uint32_t)(seg_no - 1) & 1u);
+                    if (t == 0 && seg_no > 0)
+                        ok = wait(&sh.o_free[0], (uint32_t)(seg_no - 1) & 1u) &&
+                             wait(&sh.o_free[1], (uint32_t)(seg_no - 1) & 1u);
                     ok = ok && values(0, 0, t == 0, false) && values(0, 1, false, false) &&
                          (!more || scores(0, false, false)) && values(1, 0, t == 0, false) &&
                          values(1, 1, false, true) && (!more || scores(1, true, t + 2 == n));
@@ -728,13 +742,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             // The streams take the CTA's tiles in turn, whatever segment they belong to;
             // a stream's next scores follow its values at once, also those of the next
             // segment, so that they are there when its results have been written.
-            const uint32_t tiles = (uint32_t)(u_last - u_first);
+            const uint32_t tiles = (uint32_t)(u_last - u_first) * kPer;
             int s_seg = 0, s_left = 0, v_seg = 0, v_left = 0;  // segments begun by scores and values, tiles left
             bool fresh0 = false, fresh1 = false;               // the next values are the stream's first of a segment
             auto next_scores = [&](int i) -> bool {
                 if (s_left == 0) {
                     if (!wait(&sh.seg_full[s_seg % kTaSlots], (uint32_t)(s_seg / kTaSlots) & 1u)) return false;
-                    s_left = __shfl_sync(0xFFFFFFFFu, sh.seg[s_seg % kTaSlots].s.n, 0);
+                    s_left = __shfl_sync(0xFFFFFFFFu, sh.seg[s_seg % kTaSlots].s.n, 0) * kPer;
                     if (!wait(&sh.q_full, (uint32_t)s_seg & 1u)) return false;
                     ++s_seg;
                 }
@@ -742,10 +756,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             };
             auto next_values = [&](int i) -> bool {
                 if (v_left == 0) {
-                    if (v_seg > 0 && !wait(&sh.o_free, (uint32_t)(v_seg - 1) & 1u)) return false;
-                    v_left = __shfl_sync(0xFFFFFFFFu, sh.seg[v_seg % kTaSlots].s.n, 0);
+                    v_left = __shfl_sync(0xFFFFFFFFu, sh.seg[v_seg % kTaSlots].s.n, 0) * kPer;
                     ++v_seg;
                     fresh0 = fresh1 = true;
+                }
+                // both streams' warps read either stream's O, or each its own (kTaSplitHeads)
+                if (v_seg > 1 && (i == 0 ? fresh0 : fresh1)) {
+                    const uint32_t parity = (uint32_t)(v_seg - 2) & 1u;
+                    if (MODE == kTaSplitKeys && !wait(&sh.o_free[i ^ 1], parity)) return false;
+                    if (!wait(&sh.o_free[i], parity)) return false;
                 }
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h)
@@ -755,13 +774,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (--v_left == 0) give(v_seg - 1);
                 return true;
             };
-            // Before the last values of a segment no scores are put: its results wait for them.
+            // Before the last values of a segment no scores are put: its results wait for
+            // them (kTaSplitHeads: each stream's for its own).
             int given = 0;  // tiles whose scores have been issued
 #pragma unroll 1
             for (int e = -1; e < (int)tiles && ok; ++e) {
                 if (e >= 0) ok = next_values(e & 1);
 #pragma unroll 1
-                while (ok && given < min(e + 3, (int)tiles) && (given <= e + 1 || v_left != 1))
+                while (ok && given < min(e + 3, (int)tiles) && (MODE == kTaSplitHeads || given <= e + 1 || v_left != 1))
                     ok = next_scores(given++ & 1);
             }
         }
@@ -783,7 +803,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             const Geo &g = s.g;
-            const int node = s.node0 + (SPLIT_ROWS ? stream * A.np : 0) + local;
+            const int node = s.node0 + (MODE == kTaSplitRows ? stream * A.np : 0) + local;
             const bool valid = row < rows_used && node < g.cnt;
             const unsigned long long path = valid ? sp->path[node] : 0ull;
             const int low = valid ? sp->low[node] : 0;
@@ -792,18 +812,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const bool warp_works = __any_sync(0xFFFFFFFFu, valid);
             float m = -INFINITY;                       // reference of the weights, less the lift
             float2 l2 = make_float2(0.f, 0.f);
-            const int t_step = SPLIT_ROWS ? 1 : 2;
+            const int t_step = MODE == kTaSplitKeys ? 2 : 1;
             bool first = true;
-            for (int t = SPLIT_ROWS ? 0 : (int)((base + stream) & 1u); t < s.n && ok; t += t_step, first = false) {
+            for (int t = MODE == kTaSplitKeys ? (int)((base + stream) & 1u) : 0; t < s.n && ok; t += t_step, first = false) {
                 const long long j0 = (long long)g.tile(s.i0 + t) * kTaKeys;
-                const uint32_t use = SPLIT_ROWS ? base + (uint32_t)t : (base + (uint32_t)t) >> 1;  // the stream's
+                const uint32_t use = (base + (uint32_t)t) >> (MODE == kTaSplitKeys ? 1 : 0);  // the stream's
                 // values that no node sees may be anything: they are cleared, so that their zero
-                // weights leave them out (SPLIT_ROWS: by stream 0, whose weights are used first);
+                // weights leave them out (kTaSplitRows: by stream 0, whose weights are used first);
                 // before the weights if the tile is there by then.  Not looked for before the scores
                 // have come: they follow earlier values, whose tiles have then been there, and a
                 // stage's parity says nothing while the fill before this one is still due
-                const uint32_t v_tile = base + (uint32_t)t, v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
-                bool clear = (!SPLIT_ROWS || stream == 0) &&
+                const uint32_t v_tile = (base + (uint32_t)t) * kPer + (MODE == kTaSplitHeads ? stream : 0), v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
+                bool clear = (MODE != kTaSplitRows || stream == 0) &&
                              (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks));
                 auto clear_v = [&]() {
                     const long long j = j0 + row;
@@ -909,15 +929,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
             // ---- the segment's result
             const uint32_t e1 = base - 1u;                   // its last tile
-            const int a = SPLIT_ROWS ? stream : (int)(e1 & 1u);  // a stream that holds a part
+            const int a = MODE == kTaSplitKeys ? (int)(e1 & 1u) : stream;  // a stream that holds a part
             const bool whole_item = s.n == g.nt;
             // a cut item: its first part in this CTA's slot 1, any later one in slot 0
             const long long slot = (long long)blockIdx.x * 2 + (s.i0 == 0 ? 1 : 0);
-            constexpr int kCols = SPLIT_ROWS ? DP : DP / 2;  // columns of O this thread writes
-            const int col0 = SPLIT_ROWS ? 0 : stream * kCols;
-            const bool two = !SPLIT_ROWS && s.n > 1;         // both streams hold a part
+            constexpr int kCols = MODE == kTaSplitKeys ? DP / 2 : DP;  // columns of O this thread writes
+            const int col0 = MODE == kTaSplitKeys ? stream * kCols : 0;
+            const bool two = MODE == kTaSplitKeys && s.n > 1;  // both streams hold a part
             float w_a = 1.f, w_b = 0.f;                      // weights of its part and of the other's
-            if (!SPLIT_ROWS) {
+            if (MODE == kTaSplitKeys) {
                 sh.ml[seg_no & 1][stream][row] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.ml_full));
@@ -938,10 +958,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             tc_fence_after();
             const float inv = l != 0.f ? 1.f / l : 0.f;  // 0: the row sees nothing
             const bool writes = row < rows_used && node < A.N;
-            const int head = s.hk * A.G + (row - local * A.G);
+            const int head = (MODE == kTaSplitHeads ? 2 * s.hk + stream : s.hk) * A.G + (row - local * A.G);
             const long long orow = ((long long)s.b * A.N + node) * A.Hq + head;
-            const int prow = (SPLIT_ROWS ? stream * rows_used : 0) + row;
-            const int rows_cta = rows_used * (SPLIT_ROWS ? 2 : 1);
+            const int prow = (MODE == kTaSplitKeys ? 0 : stream * rows_used) + row;
+            const int rows_cta = rows_used * (MODE == kTaSplitKeys ? 1 : 2);
             const bool any_write = __any_sync(0xFFFFFFFFu, writes);
             if (any_write) {
                 const uint32_t o_cols = tmem + lanes + 256u + (uint32_t)col0;
@@ -949,7 +969,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 for (int d = 0; d < kCols; d += 32) {
                     uint32_t o[32];
                     tmem_load(o_cols + (uint32_t)(a * DP + d), o);
-                    if (!SPLIT_ROWS) {
+                    if (MODE == kTaSplitKeys) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w_a);
                         if (two) {
@@ -986,7 +1006,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.o_free));
+            if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.o_free[stream]));
             if (writes && col0 == 0) {
                 if (whole_item) {
                     if (A.lse) A.lse[orow] = l != 0.f ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
@@ -999,10 +1019,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
 
     if (warp < 8) {  // the nodes past every row tile (past the counts) see nothing
-        const int npt = ta_nodes<SPLIT_ROWS>(A);
+        const int npt = ta_nodes<MODE>(A);
         for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
             const int2 lens = ta_lens(A, b);
-            const int n0 = lens.y > 0 ? min(A.N, ta_row_tiles<SPLIT_ROWS>(A, lens.y) * npt) : 0;
+            const int n0 = lens.y > 0 ? min(A.N, ta_row_tiles<MODE>(A, lens.y) * npt) : 0;
             if (n0 >= A.N) continue;
             const long long r0 = ((long long)b * A.N + n0) * A.Hq, r1 = ((long long)b * A.N + A.N) * A.Hq;
             uint4 *o = reinterpret_cast<uint4 *>(A.out);
@@ -1026,7 +1046,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 // joins[2 j + 1].x: the first cut of an item lies at CTA j's first unit; its parts
 // are slot 1 of the CTA where it begins and slot 0 of the CTAs after it.
 template <int DT>
-__global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta) {
+__global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta, int mode) {
     pdl_trigger();
     pdl_wait();
     const int4 z = A.joins[2 * blockIdx.x + 1];
@@ -1035,14 +1055,15 @@ __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, i
     const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (prow >= rows_cta) return;
     const int stream = prow / rows_used, row = prow - stream * rows_used;
-    const int local = row / A.G, node = a.z + stream * A.np + local;
+    const int local = row / A.G, node = a.z + (mode == kTaSplitRows ? stream * A.np : 0) + local;
+    const int hk = mode == kTaSplitHeads ? 2 * a.y + stream : a.y;
     if (node >= A.N) return;
     const int first = z.y, parts = z.z - z.y + 1;
     auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * rows_cta + prow; };
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, A.part_ml[slot(i)].x);
     m = warp_max(m);
-    const long long orow = ((long long)a.x * A.N + node) * A.Hq + (long long)a.y * A.G + (row - local * A.G);
+    const long long orow = ((long long)a.x * A.N + node) * A.Hq + (long long)hk * A.G + (row - local * A.G);
     uint2 *dst = reinterpret_cast<uint2 *>(A.out + orow * A.D) + lane;
     if (m == -INFINITY) {
         if (4 * lane < A.D) *dst = make_uint2(0u, 0u);
@@ -1101,20 +1122,19 @@ static bool ta_tmap(CUtensorMap *tm, int dtype, const void *base, const cuuint64
 }
 
 // Rows of a stream: whole nodes, at most 128 rows.  Up to one stream's worth
-// the streams share the rows and split the keys; more nodes are spread evenly
-// over the streams of as few row tiles as hold them.
+// the streams share the rows and split the keys, or take a key head each; more
+// nodes are spread evenly over the streams of as few row tiles as hold them.
 struct TaRows {
-    int np, used, cta;
-    bool split;
+    int np, used, cta, mode;
 };
-static TaRows ta_rows(int N, int G) {
+static TaRows ta_rows(int N, int G, bool pairs) {
     TaRows r;
     const int most = kTaRows / G;
-    r.split = N > most;
+    r.mode = N > most ? kTaSplitRows : pairs ? kTaSplitHeads : kTaSplitKeys;
     const int tiles = (N + 2 * most - 1) / (2 * most), nodes = (N + tiles - 1) / tiles;
-    r.np = r.split ? (nodes + 1) / 2 : N;
+    r.np = r.mode == kTaSplitRows ? (nodes + 1) / 2 : N;
     r.used = r.np * G;
-    r.cta = r.used * (r.split ? 2 : 1);
+    r.cta = r.used * (r.mode == kTaSplitKeys ? 1 : 2);
     return r;
 }
 
@@ -1123,7 +1143,7 @@ struct TaLayout {
 };
 static TaLayout ta_layout(int N, int Hq, int heads, int D) {
     TaLayout L;
-    const size_t rows = (size_t)kTaMaxCtas * 2 * ta_rows(N, Hq / heads).cta;
+    const size_t rows = (size_t)kTaMaxCtas * 2 * ta_rows(N, Hq / heads, true).cta;
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     L.o = 0;
     L.ml = up(rows * (size_t)D * sizeof(float));
@@ -1132,23 +1152,33 @@ static TaLayout ta_layout(int N, int Hq, int heads, int D) {
     return L;
 }
 
-template <int DT, int DP, bool SPLIT_ROWS>
+template <int DT, int DP, int MODE>
 static spec_status_t ta_launch(const TaArgs &A, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                const TaRows &r, int ctas, int dev, cudaStream_t s) {
-    constexpr size_t smem = sizeof(TaShared<DP, SPLIT_ROWS>) + 1024;
+    constexpr size_t smem = sizeof(TaShared<DP, MODE>) + 1024;
     static_assert(smem <= 232448, "shared memory of a CTA");
     static bool ready[64] = {};
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(tree_attn<DT, DP, SPLIT_ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(tree_attn<DT, DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
             return SPEC_ERR_CUDA;
         ready[dev] = true;
     }
     const spec_status_t st =
-        launch_pdl(tree_attn<DT, DP, SPLIT_ROWS>, dim3((unsigned)ctas), dim3(kTaThreads), smem, s, q, k, v, A);
+        launch_pdl(tree_attn<DT, DP, MODE>, dim3((unsigned)ctas), dim3(kTaThreads), smem, s, q, k, v, A);
     if (st != SPEC_OK) return st;
     return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((r.cta + 7) / 8)), dim3(256), 0, s, A,
-                      r.used, r.cta);
+                      r.used, r.cta, MODE);
+}
+
+template <int DT, int DP>
+static spec_status_t ta_launch_mode(const TaArgs &A, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                                    const TaRows &r, int ctas, int dev, cudaStream_t s) {
+    switch (r.mode) {
+    case kTaSplitRows: return ta_launch<DT, DP, kTaSplitRows>(A, q, k, v, r, ctas, dev, s);
+    case kTaSplitHeads: return ta_launch<DT, DP, kTaSplitHeads>(A, q, k, v, r, ctas, dev, s);
+    default: return ta_launch<DT, DP, kTaSplitKeys>(A, q, k, v, r, ctas, dev, s);
+    }
 }
 
 } // namespace sv
@@ -1191,7 +1221,15 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
         return SPEC_ERR_CUDA;
     const int ctas = sms[dev] < sv::kTaMaxCtas ? sms[dev] : sv::kTaMaxCtas;
 
-    const sv::TaRows r = sv::ta_rows(N, Hq / H);
+    // A key head per stream once there is one for every CTA: the streams then share
+    // nothing but the CTA, where streams that divide the keys meet at the end of
+    // every (request, head).  9 nodes, us, by heads / by keys, 8 key heads:
+    //   head_dim 128, 4096 tokens: B = 32 77 / 84, 256 670 / 758; window 1024: 32 39 / 45, 256 196 / 246
+    //   head_dim 64, window 128:   B = 24 15.6 / 18.9, 64 21.8 / 27.8, 512 108 / 142
+    // With fewer heads a unit of twice the work is cut more coarsely:
+    //   500 tokens, one node, head_dim 128: B = 16 16.5 / 13.3, 1 11.8 / 11.1; 20000 tokens: B = 1 33 / 30
+    const bool pairs = H % 2 == 0 && (long long)B * H >= ctas;
+    const sv::TaRows r = sv::ta_rows(N, Hq / H, pairs);
     const sv::TaLayout L = sv::ta_layout(N, Hq, H, D);
     sv::TaArgs A = {};
     A.table = page_table;
@@ -1201,7 +1239,7 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     A.B = B;
     A.N = N;
     A.Hq = Hq;
-    A.H = H;
+    A.H = r.mode == sv::kTaSplitHeads ? H / 2 : H;
     A.G = Hq / H;
     A.D = D;
     A.max_pages = max_pages;
@@ -1235,18 +1273,11 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
         return SPEC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = pages->dtype == SPEC_DTYPE_BF16;
-    if (D <= 64) {
-        if (r.split)
-            return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 64, true>(A, tq, tk, tv, r, ctas, dev, s)
-                      : sv::ta_launch<SPEC_DTYPE_F16, 64, true>(A, tq, tk, tv, r, ctas, dev, s);
-        return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 64, false>(A, tq, tk, tv, r, ctas, dev, s)
-                  : sv::ta_launch<SPEC_DTYPE_F16, 64, false>(A, tq, tk, tv, r, ctas, dev, s);
-    }
-    if (r.split)
-        return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 128, true>(A, tq, tk, tv, r, ctas, dev, s)
-                  : sv::ta_launch<SPEC_DTYPE_F16, 128, true>(A, tq, tk, tv, r, ctas, dev, s);
-    return bf ? sv::ta_launch<SPEC_DTYPE_BF16, 128, false>(A, tq, tk, tv, r, ctas, dev, s)
-              : sv::ta_launch<SPEC_DTYPE_F16, 128, false>(A, tq, tk, tv, r, ctas, dev, s);
+    if (bf)
+        return D <= 64 ? sv::ta_launch_mode<SPEC_DTYPE_BF16, 64>(A, tq, tk, tv, r, ctas, dev, s)
+                       : sv::ta_launch_mode<SPEC_DTYPE_BF16, 128>(A, tq, tk, tv, r, ctas, dev, s);
+    return D <= 64 ? sv::ta_launch_mode<SPEC_DTYPE_F16, 64>(A, tq, tk, tv, r, ctas, dev, s)
+                   : sv::ta_launch_mode<SPEC_DTYPE_F16, 128>(A, tq, tk, tv, r, ctas, dev, s);
 }
 
 } // extern "C"

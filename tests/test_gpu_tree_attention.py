@@ -125,6 +125,36 @@ def test_many_requests_of_mixed_lengths():
     _check(_case(17, lens, 5, 8, 4, 64, 16, torch.bfloat16))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,G,hkv,D,page,window,sinks", [
+    (1, 1, 80, 64, 16, 0, 0),
+    (9, 8, 40, 64, 16, 128, 0),       # 72 rows
+    (9, 8, 40, 64, 16, 100, 130),     # sinks past a tile
+    (16, 8, 38, 128, 32, 0, 0),       # 128 rows, at one head per CTA
+    (13, 3, 64, 72, 8, 50, 2),
+    (64, 2, 44, 128, 128, 0, 0),      # a node per row pair
+    (7, 5, 102, 40, 256, 700, 1),
+])
+def test_many_heads(N, G, hkv, D, page, window, sinks, dtype):
+    """More (request, key head) pairs than CTAs: each softmax stream has a head of its own."""
+    lens = [0, 3, 127, 128, 129, 300, 1000, 64][:8 if hkv < 100 else 3]
+    c = _case(N * 17 + hkv, lens, N, hkv * G, hkv, D, page, dtype)
+    _check(c, window=window, sinks=sinks)
+    r = torch.Generator().manual_seed(N)
+    cnt = torch.randint(0, N + 1, (len(lens),), generator=r, dtype=torch.int32).cuda()
+    # positions that no node sees hold NaN
+    live = torch.zeros((c["k"].shape[0], page), dtype=torch.bool, device="cuda")
+    for b, n0 in enumerate(lens):
+        seen = set()
+        for path in ch.paths(c["parent"][b].tolist(), int(cnt[b])):
+            seen |= set(ch.seen_positions(n0, path, window, sinks))
+        for j in seen:
+            live[int(c["table"][b, j // page]), j % page] = True
+    for x in (c["k"], c["v"]):
+        x[~live] = float("nan")
+    _check(c, node_count=cnt, window=window, sinks=sinks)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_shapes(seed):
     import random
