@@ -55,17 +55,29 @@ __device__ __forceinline__ void drop_page(const PagesArgs &A, int p) {
     }
 }
 
+// What the bookkeeping knows of an item, kept in shared memory by every CTA.
+template <bool FORK> struct PagesItem;
+template <> struct PagesItem<false> {
+    int held, need;          // pages held and wanted
+};
+template <> struct PagesItem<true> {
+    int src, dst, len, kind; // kind: 0 void, 1 valid without a partial page, 2 with one
+};
+
 // The bookkeeping of spec_cache_resize (FORK false: item i is slot i) and of
 // spec_cache_fork (FORK true: item i is fork i).  Bound by latency: a few
-// dependent loads, three cluster barriers, and a scan of the counts split over
-// the cluster's 256 warps.  8 CTAs of one cluster instead of one CTA: 2^16
-// pages are one load round per warp; instead of a whole grid: no launch
-// between the phases.
+// dependent loads, one cluster barrier (two where pages are taken), and a scan
+// of the counts split over the cluster's 256 warps.  8 CTAs of one cluster
+// instead of one CTA: 2^16 pages are one load round per warp; instead of a
+// whole grid: no launch between the phases.
 template <bool FORK>
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) sv_pages(PagesArgs A) {
-    extern __shared__ uint32_t pg_smem[];
-    uint32_t *incl = pg_smem;                           // [n] running sum of the pages wanted
-    int *owner = reinterpret_cast<int *>(pg_smem + A.n); // FORK: [slots] first fork into a slot
+    constexpr int kWarps = kPgCtas * kPgWarps;
+    extern __shared__ uint4 pg_smem[];
+    using Item = PagesItem<FORK>;
+    Item *items = reinterpret_cast<Item *>(pg_smem);             // [n]
+    uint32_t *incl = reinterpret_cast<uint32_t *>(items + A.n);  // [n] running sum of the pages wanted
+    int *owner = reinterpret_cast<int *>(incl + A.n);            // FORK: [slots] first fork into a slot
     __shared__ uint32_t warp_sum[kPgWarps], cta_free[kPgCtas], is_src[SPEC_MAX_SLOTS / 32];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
@@ -77,46 +89,44 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     pdl_wait();
 
     // ---- what every item wants (each CTA forms all of them)
-    if (FORK) {
+    if constexpr (FORK) {
         for (int i = tid; i < A.slots; i += kPgThreads) owner[i] = INT_MAX;
         for (int i = tid; i < (A.slots + 31) / 32; i += kPgThreads) is_src[i] = 0;
         __syncthreads();
         for (int f = tid; f < A.n; f += kPgThreads) {
             const int s = A.src[f], d = A.dst[f];
+            items[f].src = s;
+            items[f].dst = d;
             if ((unsigned)s < (unsigned)A.slots) atomicOr(&is_src[s >> 5], 1u << (s & 31));
             if ((unsigned)d < (unsigned)A.slots) atomicMin(&owner[d], f);
         }
         __syncthreads();
-    }
-    // FORK: 0 void, 1 valid without, 2 valid with a partial page
-    auto fork_kind = [&](int f) -> int {
-        const int s = A.src[f], d = A.dst[f];
-        if ((unsigned)s >= (unsigned)A.slots || (unsigned)d >= (unsigned)A.slots || owner[d] != f ||
-            ((is_src[d >> 5] >> (d & 31)) & 1u)) {
-            if (rank == 0) flag(A.status, SPEC_DEV_BAD_SLOT);
-            return 0;
+        for (int f = tid; f < A.n; f += kPgThreads) {
+            const int s = items[f].src, d = items[f].dst;
+            int n = 0, kind = 0;
+            if ((unsigned)s >= (unsigned)A.slots || (unsigned)d >= (unsigned)A.slots || owner[d] != f ||
+                ((is_src[d >> 5] >> (d & 31)) & 1u)) {
+                if (rank == 0) flag(A.status, SPEC_DEV_BAD_SLOT);
+            } else {
+                n = A.len[s];
+                if (n < 0 || (n + (long long)page - 1) >> A.page_shift > min(A.count[s], A.max_pages)) {
+                    if (rank == 0) flag(A.status, SPEC_DEV_BAD_LEN);
+                } else {
+                    kind = (n & (page - 1)) ? 2 : 1;
+                }
+            }
+            items[f].len = n;
+            items[f].kind = kind;
+            incl[f] = kind == 2 ? 1u : 0u;
         }
-        const int n = A.len[s], held = min(A.count[s], A.max_pages);
-        if (n < 0 || (n + (long long)page - 1) >> A.page_shift > held) {
-            if (rank == 0) flag(A.status, SPEC_DEV_BAD_LEN);
-            return 0;
+    } else {
+        for (int i = tid; i < A.n; i += kPgThreads) {
+            const int w = A.want[i], c = max(0, min(A.count[i], A.max_pages));
+            const int need = w < 0 ? c : pages_for((long long)w + A.extra, A.page_shift, A.max_pages);
+            items[i].held = c;
+            items[i].need = need;
+            incl[i] = min((uint32_t)max(0, need - c), cap);
         }
-        return (n & (page - 1)) ? 2 : 1;
-    };
-    auto wanted = [&](int b) -> int {
-        const int w = A.want[b], c = max(0, min(A.count[b], A.max_pages));
-        return w < 0 ? c : pages_for((long long)w + A.extra, A.page_shift, A.max_pages);
-    };
-    for (int i = tid; i < A.n; i += kPgThreads) {
-        uint32_t grow;
-        if (FORK) {
-            const int kind = fork_kind(i);
-            grow = kind == 2 ? 1u : 0u;
-        } else {
-            const int c = max(0, min(A.count[i], A.max_pages));
-            grow = (uint32_t)max(0, wanted(i) - c);
-        }
-        incl[i] = min(grow, cap);
     }
     __syncthreads();
     {  // inclusive scan: each thread a run of consecutive items
@@ -135,43 +145,55 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
         }
         if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
-        uint32_t before = __shfl_up_sync(0xFFFFFFFFu, x, 1);
-        if (lane == 0) before = 0;
-        for (int w = 0; w < warp; ++w) before = sat_add(before, warp_sum[w], cap);
+        uint32_t before = lane < warp ? warp_sum[lane] : 0u;  // the warps before this one
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before = sat_add(before, __shfl_xor_sync(0xFFFFFFFFu, before, o), cap);
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, 1);
+        if (lane > 0) before = sat_add(before, y, cap);
         for (int i = i0; i < i1; ++i) incl[i] = sat_add(incl[i], before, cap);
         __syncthreads();
     }
     const uint32_t total = incl[A.n - 1];
 
-    // ---- pages given back (the cluster's warps share the items)
-    for (int i = gwarp; i < A.n; i += kPgCtas * kPgWarps) {
-        if (FORK) {
-            if (fork_kind(i) == 0) continue;
-            const int d = A.dst[i], c = max(0, min(A.count[d], A.max_pages));
-            int *row = A.table + (long long)d * A.max_pages;
-            for (int j = lane; j < c; j += 32) {
-                drop_page(A, row[j]);
-                row[j] = -1;
+    // ---- pages given back, and full pages shared: `ways` warps to an item
+    const int ways = max(1, kWarps / A.n);
+    for (int i = gwarp / ways; i < A.n; i += kWarps / ways) {
+        const int first = (gwarp % ways) * 32 + lane;
+        if constexpr (FORK) {
+            const PagesItem<true> it = items[i];
+            if (it.kind == 0) continue;
+            const int held = max(0, min(A.count[it.dst], A.max_pages)), full = it.len >> A.page_shift;
+            const int *from = A.table + (long long)it.src * A.max_pages;
+            int *to = A.table + (long long)it.dst * A.max_pages;
+            for (int j = first; j < max(held, full); j += ways * 32) {
+                const int old = j < held ? to[j] : 0, p = j < full ? from[j] : -1;
+                if (j < full) {  // its source holds it too: sharing it frees and takes nothing
+                    if ((unsigned)p < (unsigned)A.num_pages) atomicAdd(A.ref + p, 1);
+                    else flag(A.status, SPEC_DEV_BAD_PAGE);
+                }
+                to[j] = p;
+                if (j < held) drop_page(A, old);
             }
         } else {
-            const int c = max(0, min(A.count[i], A.max_pages)), need = wanted(i);
+            const int held = items[i].held;
             int *row = A.table + (long long)i * A.max_pages;
-            for (int j = need + lane; j < c; j += 32) {
+            for (int j = items[i].need + first; j < held; j += ways * 32) {
                 drop_page(A, row[j]);
                 row[j] = -1;
             }
         }
     }
     __threadfence();
-    cluster.sync();
+    cluster.sync();  // the old counts have been read, and what is free is known
 
-    // ---- free pages counted, each warp a run of the pool
-    const int per_warp = (int)(((long long)A.num_pages + kPgCtas * kPgWarps * 32 - 1) / (kPgCtas * kPgWarps * 32)) * 32;
-    const long long p0 = (long long)gwarp * per_warp;
-    const int run = (int)max(0ll, min((long long)per_warp, (long long)A.num_pages - p0));
-    uint32_t mine = 0;
+    uint32_t free_total = 0;
     if (total > 0) {
-        for (int i = 0; i < run; i += 256) {
+        // ---- free pages counted, each warp a run of the pool
+        const int per_warp = (int)(((long long)A.num_pages + kWarps * 32 - 1) / (kWarps * 32)) * 32;
+        const long long p0 = (long long)gwarp * per_warp;
+        const int run = (int)max(0ll, min((long long)per_warp, (long long)A.num_pages - p0));
+        uint32_t mine = 0, mask[8];  // of 256 pages, each lane the same
+        auto look = [&](int i) {
             int r[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -179,102 +201,95 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
                 r[u] = j < run ? __ldcg(A.ref + p0 + j) : 1;
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) mine += (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, r[u] == 0));
+            for (int u = 0; u < 8; ++u) mask[u] = __ballot_sync(0xFFFFFFFFu, r[u] == 0);
+        };
+        for (int i = 0; i < run; i += 256) {
+            look(i);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mine += (uint32_t)__popc(mask[u]);
         }
-    }
-    if (lane == 0) warp_sum[warp] = mine;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-    for (int w = 0; w < kPgWarps; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
-    }
-    if (tid < kPgCtas) *cluster.map_shared_rank(&cta_free[rank], tid) = all;
-    cluster.sync();
-    uint32_t free_total = 0;
-    for (int c = 0; c < kPgCtas; ++c) {
-        if (c < rank) before += cta_free[c];
-        free_total += cta_free[c];
-    }
-    // items are served while their running sum is within the free pages
-    uint32_t served = total;
-    if (total > free_total) {
-        int lo = 0, hi = A.n;  // first item past the free pages
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (incl[mid] > free_total) hi = mid;
-            else lo = mid + 1;
+        if (lane == 0) warp_sum[warp] = mine;
+        __syncthreads();
+        const uint32_t w = warp_sum[lane], all = __reduce_add_sync(0xFFFFFFFFu, w);
+        uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
+        if (tid < kPgCtas) *cluster.map_shared_rank(&cta_free[rank], tid) = all;
+        cluster.sync();
+#pragma unroll
+        for (int c = 0; c < kPgCtas; ++c) {
+            if (c < rank) before += cta_free[c];
+            free_total += cta_free[c];
         }
-        served = lo > 0 ? incl[lo - 1] : 0u;
-        if (rank == 0 && tid == 0) flag(A.status, SPEC_DEV_NO_PAGES);
-    }
+        // items are served while their running sum is within the free pages
+        uint32_t served = total;
+        if (total > free_total) {
+            int lo = 0, hi = A.n;  // first item past the free pages
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (incl[mid] > free_total) hi = mid;
+                else lo = mid + 1;
+            }
+            served = lo > 0 ? incl[lo - 1] : 0u;
+            if (rank == 0 && tid == 0) flag(A.status, SPEC_DEV_NO_PAGES);
+        }
 
-    // ---- the lowest free pages handed out in item order
-    if (before < served && mine > 0) {
-        uint32_t at = before;
-        for (int i = 0; i < run && at < served; i += 32) {
-            const int j = i + lane;
-            const bool is_free = j < run && __ldcg(A.ref + p0 + j) == 0;
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, is_free);
-            const uint32_t r = at + (uint32_t)__popc(mask & ((1u << lane) - 1u));
-            if (is_free && r < served) {
-                int lo = 0, hi = A.n - 1;  // first item whose running sum exceeds r
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (incl[mid] > r) hi = mid;
-                    else lo = mid + 1;
+        // ---- the lowest free pages handed out in item order
+        if (before < served && mine > 0) {
+            uint32_t at = before;
+            for (int i = 0; i < run && at < served; i += 256) {
+                if (run > 256) look(i);  // else the masks are still there
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t r = at + (uint32_t)__popc(mask[u] & ((1u << lane) - 1u));
+                    if (((mask[u] >> lane) & 1u) && r < served) {
+                        int lo = 0, hi = A.n - 1;  // first item whose running sum exceeds r
+                        while (lo < hi) {
+                            const int mid = (lo + hi) >> 1;
+                            if (incl[mid] > r) hi = mid;
+                            else lo = mid + 1;
+                        }
+                        const int first = lo > 0 ? (int)incl[lo - 1] : 0;
+                        const int p = (int)p0 + i + u * 32 + lane;
+                        A.ref[p] = 1;
+                        if constexpr (FORK) {
+                            A.table[(long long)items[lo].dst * A.max_pages + (items[lo].len >> A.page_shift)] = p;
+                            A.copies[3 * lo + 1] = p;
+                        } else {
+                            A.table[(long long)lo * A.max_pages + items[lo].held + (int)r - first] = p;
+                        }
+                    }
+                    at += (uint32_t)__popc(mask[u]);
                 }
-                const int first = lo > 0 ? (int)incl[lo - 1] : 0;
-                int slot = lo, place;
-                if (FORK) {
-                    slot = A.dst[lo];
-                    place = A.len[A.src[lo]] >> A.page_shift;
-                } else {
-                    place = max(0, min(A.count[lo], A.max_pages)) + (int)r - first;
-                }
-                A.ref[p0 + j] = 1;
-                A.table[(long long)slot * A.max_pages + place] = (int)(p0 + j);
-            }
-            at += (uint32_t)__popc(mask);
-        }
-    }
-    if (FORK) {  // full pages shared
-        for (int f = gwarp; f < A.n; f += kPgCtas * kPgWarps) {
-            const int kind = fork_kind(f);
-            if (kind == 0 || (kind == 2 && incl[f] > free_total)) continue;
-            const int s = A.src[f], d = A.dst[f], full = A.len[s] >> A.page_shift;
-            const int *from = A.table + (long long)s * A.max_pages;
-            int *to = A.table + (long long)d * A.max_pages;
-            for (int j = lane; j < full; j += 32) {
-                const int p = from[j];
-                to[j] = p;
-                if ((unsigned)p < (unsigned)A.num_pages) atomicAdd(A.ref + p, 1);
-                else flag(A.status, SPEC_DEV_BAD_PAGE);
             }
         }
+        if constexpr (FORK) {
+            if (total > free_total) {  // forks that found no page share none either
+                for (int i = gwarp / ways; i < A.n; i += kWarps / ways) {
+                    const PagesItem<true> it = items[i];
+                    if (it.kind != 2 || incl[i] <= free_total) continue;
+                    int *to = A.table + (long long)it.dst * A.max_pages;
+                    for (int j = (gwarp % ways) * 32 + lane; j < it.len >> A.page_shift; j += ways * 32) {
+                        drop_page(A, to[j]);
+                        to[j] = -1;
+                    }
+                }
+            }
+        }
     }
-    cluster.sync();  // every CTA has read the old counts
 
     for (int i = rank * kPgThreads + tid; i < A.n; i += kPgCtas * kPgThreads) {
-        const uint32_t excl = i > 0 ? incl[i - 1] : 0u;
-        if (FORK) {
-            const int kind = fork_kind(i);
-            A.copies[3 * i + 2] = 0;
-            if (kind == 0) continue;
-            const int s = A.src[i], d = A.dst[i], n = A.len[s];
-            const bool ok = !(kind == 2 && incl[i] > free_total);
-            if (ok && kind == 2) {
-                const long long place = n >> A.page_shift;
-                A.copies[3 * i] = A.table[(long long)s * A.max_pages + place];
-                A.copies[3 * i + 1] = __ldcg(A.table + (long long)d * A.max_pages + place);
-                A.copies[3 * i + 2] = n & (page - 1);
-            }
-            A.count[d] = ok ? pages_for(n, A.page_shift, A.max_pages) : 0;
-            A.len[d] = ok ? n : 0;
+        if constexpr (FORK) {
+            const PagesItem<true> it = items[i];
+            const bool ok = it.kind != 2 || incl[i] <= free_total;
+            A.copies[3 * i + 2] = it.kind == 2 && ok ? it.len & (page - 1) : 0;
+            if (it.kind == 0) continue;
+            if (it.kind == 2 && ok)
+                A.copies[3 * i] = A.table[(long long)it.src * A.max_pages + (it.len >> A.page_shift)];
+            A.count[it.dst] = ok ? pages_for(it.len, A.page_shift, A.max_pages) : 0;
+            A.len[it.dst] = ok ? it.len : 0;
         } else {
-            const int c = max(0, min(A.count[i], A.max_pages)), need = wanted(i);
-            if (need < c) A.count[i] = need;
-            else A.count[i] = c + (incl[i] <= free_total ? (int)(incl[i] - excl) : 0);
+            const int held = items[i].held, need = items[i].need;
+            const uint32_t excl = i > 0 ? incl[i - 1] : 0u;
+            A.count[i] = need < held ? need : held + (incl[i] <= free_total ? (int)(incl[i] - excl) : 0);
         }
     }
 }
@@ -522,13 +537,16 @@ static int copy_blocks(const Pool &P, dim3 block) {
 
 template <bool FORK>
 static spec_status_t launch_pages(const PagesArgs &A, cudaStream_t s) {
-    const size_t smem = sizeof(uint32_t) * ((size_t)A.n + (FORK ? (size_t)A.slots : 0));
+    constexpr size_t item = sizeof(PagesItem<FORK>) + sizeof(uint32_t);
+    constexpr size_t most = (item + (FORK ? sizeof(int) : 0)) * SPEC_MAX_SLOTS;
+    static_assert(most + 2048 <= 232448, "shared memory of a CTA");
+    const size_t smem = item * A.n + (FORK ? sizeof(int) * (size_t)A.slots : 0);
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
     if (!ready[dev]) {
         if (cudaFuncSetAttribute(sv_pages<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(2 * sizeof(uint32_t) * SPEC_MAX_SLOTS)) != cudaSuccess)
+                                 (int)most) != cudaSuccess)
             return SPEC_ERR_CUDA;
         ready[dev] = true;
     }
