@@ -61,7 +61,7 @@ struct TaArgs {
     float *lse;
     float *part_o;       // [cta][2][rows][D]
     float2 *part_ml;     // [cta][2][rows]: m (base 2), l
-    int4 *joins;         // [cta][2]: the item a cut falls into, see tree_attn_join
+    int4 *joins;         // [cta]: request, key head (or pair), first node and parts (0: none), see tree_attn_join
     uint32_t *status;
 };
 
@@ -170,24 +170,28 @@ template <int MODE> struct Walk {
         rts = ta_row_tiles<MODE>(A, g.cnt);
         hk = rt = i0 = 0;
     }
-    // To unit u, which exists.
+    // To unit u, which exists; the first requests have been fetched.
     __device__ __forceinline__ void find(const TaArgs &A, const long long *incl, long long u) {
         const int lane = threadIdx.x & 31;
-        int chunk = 0;
-        long long base = 0, before = 0;
+        const int per = (A.B + kTaChunks - 1) / kTaChunks;
+        int from = 0;
+        long long base = 0;
 #pragma unroll 1
         for (int i = 0; i < kTaChunks; i += 32) {  // the chunks that end at or before u
-            const long long x = before + incl[i + lane];
+            const long long x = base + incl[i + lane];
             const int k = __popc(__ballot_sync(0xFFFFFFFFu, x <= u));
-            if (k > 0) base = __shfl_sync(0xFFFFFFFFu, x, k - 1);
-            before = __shfl_sync(0xFFFFFFFFu, x, 31);
-            chunk += k;
-            if (k < 32) break;
+            from = i;
+            if (k < 32) {
+                // chunks of one request: the requests of these 32 are looked through below
+                if (per > 1 && k > 0) from = (i + k) * per, base = __shfl_sync(0xFFFFFFFFu, x, k - 1);
+                else from *= per;
+                break;
+            }
+            base = __shfl_sync(0xFFFFFFFFu, x, 31);
         }
-        const int per = (A.B + kTaChunks - 1) / kTaChunks;
 #pragma unroll 1
-        for (int from = chunk * per;; from += 32) {  // the requests that end at or before u
-            fetch(A, from);
+        for (;; from += 32) {  // the requests that end at or before u
+            if (from != b0) fetch(A, from);
             long long x = ta_units<MODE>(A, ta_geo(A, lens));
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -441,13 +445,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     pdl_trigger();
     pdl_wait();
+    Walk<MODE> w;
+    if (warp == kTaWarpPlan) w.fetch(A, 0);
+    bool fewer = false;  // some request has fewer than N nodes
     // the units of all requests, summed up to the end of each chunk of them
     if (threadIdx.x < kTaChunks) {
         const int per = (A.B + kTaChunks - 1) / kTaChunks;
         const int b0 = threadIdx.x * per, b1 = min(A.B, b0 + per);
         long long x = 0;
 #pragma unroll 2
-        for (int b = b0; b < b1; ++b) x += ta_units<MODE>(A, ta_geo(A, ta_lens(A, b)));
+        for (int b = b0; b < b1; ++b) {
+            const int2 lens = ta_lens(A, b);
+            fewer |= lens.y < A.N;
+            x += ta_units<MODE>(A, ta_geo(A, lens));
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         sh.incl[threadIdx.x] = x;
     }
     tc_fence_before();
-    __syncthreads();
+    fewer = __syncthreads_or(fewer) != 0;
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
     volatile int *abort = &sh.abort;
@@ -480,7 +491,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         bool ok = true;
         unsigned long long anc[2] = {0, 0};
         int low[2] = {0, 0};
-        Walk<MODE> w;
         if (u_first < u_last) w.find(A, sh.incl, u_first);
         for (long long left = u_last - u_first; ok; ++k) {
             Seg s = {};
@@ -505,14 +515,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 // the CTA's first unit lies inside an item: if the item began in the CTA
                 // before, this is its first cut, where its parts are joined
                 const long long start = u_first - s.i0;
-                const bool joins = s.i0 > 0 && start >= u_first - run;
-                if (joins) {
-                    A.joins[2 * blockIdx.x] = make_int4(s.b, s.hk, s.node0, 0);
-                    const int last = (int)min(ta_div(start + s.g.nt - 1, run), gridDim.x - 1ll);
-                    A.joins[2 * blockIdx.x + 1] = make_int4(1, (int)blockIdx.x - 1, last, 0);
-                } else {
-                    A.joins[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+                int parts = 0;
+                if (s.i0 > 0 && start >= u_first - run) {
+                    const long long last = min(ta_div(start + s.g.nt - 1, run), gridDim.x - 1ll);
+                    parts = (int)(last - (long long)blockIdx.x) + 2;
                 }
+                A.joins[blockIdx.x] = make_int4(s.b, s.hk, s.node0, parts);
             }
             // the loads and scores go ahead; the softmax warps need the paths too
             if (s.n > 0 && s.b != b) {
@@ -1018,7 +1026,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (!ok) *abort = 1;
     }
 
-    if (warp < 8) {  // the nodes past every row tile (past the counts) see nothing
+    if (warp < 8 && fewer) {  // the nodes past every row tile (past the counts) see nothing
         const int npt = ta_nodes<MODE>(A);
         for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
             const int2 lens = ta_lens(A, b);
@@ -1043,25 +1051,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 // The parts of an item that cuts fell into, joined: one warp per row.
-// joins[2 j + 1].x: the first cut of an item lies at CTA j's first unit; its parts
-// are slot 1 of the CTA where it begins and slot 0 of the CTAs after it.
+// joins[j]: the first cut of an item lies at CTA j's first unit; its parts are
+// slot 1 of the CTA before, where it begins, and slot 0 of CTA j and those after.
 template <int DT>
 __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta, int mode) {
     pdl_trigger();
     pdl_wait();
-    const int4 z = A.joins[2 * blockIdx.x + 1];
-    if (z.x == 0) return;
-    const int4 a = A.joins[2 * blockIdx.x];
     const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (prow >= rows_cta) return;
+    const int first = (int)blockIdx.x - 1;
+    auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * rows_cta + prow; };
+    const int4 a = A.joins[blockIdx.x];
+    const int parts = a.w;
+    // the first 32 parts' m and l, fetched beside the description of the cut
+    float2 x0 = make_float2(-INFINITY, 0.f);
+    if (first >= 0 && first + lane < (int)gridDim.x) x0 = A.part_ml[slot(lane)];
+    if (parts == 0) return;
     const int stream = prow / rows_used, row = prow - stream * rows_used;
     const int local = row / A.G, node = a.z + (mode == kTaSplitRows ? stream * A.np : 0) + local;
     const int hk = mode == kTaSplitHeads ? 2 * a.y + stream : a.y;
     if (node >= A.N) return;
-    const int first = z.y, parts = z.z - z.y + 1;
-    auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * rows_cta + prow; };
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, A.part_ml[slot(i)].x);
+    float m = lane < parts ? x0.x : -INFINITY;
+    for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, A.part_ml[slot(i)].x);
     m = warp_max(m);
     const long long orow = ((long long)a.x * A.N + node) * A.Hq + (long long)hk * A.G + (row - local * A.G);
     uint2 *dst = reinterpret_cast<uint2 *>(A.out + orow * A.D) + lane;
@@ -1075,12 +1086,12 @@ __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, i
     for (int i0 = 0; i0 < parts; i0 += 32) {
         float w = 0.f;
         if (i0 + lane < parts) {
-            const float2 x = A.part_ml[slot(i0 + lane)];
+            const float2 x = i0 == 0 ? x0 : A.part_ml[slot(i0 + lane)];
             w = ex2(x.x - m);
             l = fmaf(x.y, w, l);
         }
         const int k = min(32, parts - i0);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < k; ++i) {
             const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
             if (4 * lane < A.D) {
@@ -1148,7 +1159,7 @@ static TaLayout ta_layout(int N, int Hq, int heads, int D) {
     L.o = 0;
     L.ml = up(rows * (size_t)D * sizeof(float));
     L.joins = up(L.ml + rows * sizeof(float2));
-    L.total = up(L.joins + (size_t)kTaMaxCtas * 2 * sizeof(int4));
+    L.total = up(L.joins + (size_t)kTaMaxCtas * sizeof(int4));
     return L;
 }
 
