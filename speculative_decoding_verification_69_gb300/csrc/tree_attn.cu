@@ -44,7 +44,8 @@ constexpr int kTaWarpK = 8, kTaWarpMma = 9, kTaWarpPlan = 10, kTaWarpV = 11;
 constexpr int kTaSlots = 4;         // segments the scheduler may be ahead
 constexpr int kTaMaxCtas = 160;     // CTAs the workspace has room for
 constexpr int kTaChunks = 128;      // entries of the running sum over requests
-constexpr unsigned long long kTaWaitNs = 2000000000ull;  // 2 s
+constexpr uint32_t kTaTries = 1u << 19;                  // looks of a wait: 2 s
+constexpr unsigned long long kTaWaitNs = 2000000000ull;  // for the waits at the end
 constexpr float kTaGrow = 8.f;      // growth of a row's maximum that rescales its O
 
 // What the two streams of a CTA divide between them.
@@ -85,7 +86,8 @@ struct Geo {
 
 // Committed positions and nodes of request b, clamped to what the table can hold.
 __device__ __forceinline__ int2 ta_lens(const TaArgs &A, int b) {
-    const int cap = (int)min((long long)A.max_pages << A.page_shift, 0x7FFFFFFFll);
+    // (a tile of positions past the last one stays below 2^31)
+    const int cap = (int)min((long long)A.max_pages << A.page_shift, (1ll << 31) - 2 * kTaKeys);
     int cnt = A.node_count ? max(0, min(__ldcg(A.node_count + b), A.N)) : A.N;
     int c = __ldcg(A.len + b);
     if (c < 0 || c > cap - cnt) {
@@ -265,22 +267,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for a phase, at most kTaWaitNs or until another role has given up.  The
-// timer is read on every 64th look only.
+// Waits for a phase, until another role has given up or kTaTries looks have been in
+// vain; a look sleeps for 3.9 us unless the phase ends.  (A limit by count: the wait is
+// inlined in many places, and a timer in each was code to be fetched, 4 us of 105 at a
+// window of 128 and 512 requests.)
 __device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    unsigned long long t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if ((i & 63u) == 0) {
-            const unsigned long long t = global_ns();
-            if (t0 == 0) t0 = t;
-            if (*abort) return false;
-            if (t - t0 > kTaWaitNs) {
-                *abort = 1;
-                return false;
-            }
-        }
+#pragma unroll 1
+    for (uint32_t i = 0; i < kTaTries; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
     }
-    return true;
+    *abort = 1;
+    return false;
 }
 
 // D (TMEM) (+)= A (shared) B (shared)
@@ -335,14 +333,14 @@ template <> __device__ __forceinline__ uint32_t pack2<SPEC_DTYPE_F16>(float lo, 
 
 // The positions [j, j + 64) that a row sees: committed ones from `low` on and the
 // first `sinks`, and the nodes of its path, which lie from position c on.
-__device__ __forceinline__ unsigned long long seen_bits(long long j, int c, int low, int sinks,
-                                                        unsigned long long path) {
+// (Positions are below 2^31, and so are their differences.)
+__device__ __forceinline__ unsigned long long seen_bits(int j, int c, int low, int sinks, unsigned long long path) {
     auto below = [&](int end) -> unsigned long long {  // the positions before `end`
-        const long long n = end - j;
-        return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << (int)n) - 1ull;
+        const int n = end - j;
+        return n <= 0 ? 0ull : ~0ull >> max(64 - n, 0);
     };
-    const long long d = j - c;
-    const unsigned long long nodes = d >= 64 || d <= -64 ? 0ull : d >= 0 ? path >> (int)d : path << (int)-d;
+    const int d = j - c;
+    const unsigned long long nodes = d >= 64 || d <= -64 ? 0ull : d >= 0 ? path >> d : path << -d;
     return (below(c) & ~below(low)) | below(min(sinks, c)) | nodes;
 }
 
@@ -569,14 +567,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int *row = A.table + (long long)s.b * A.max_pages;
             const int i_end = s.i0 + s.n;
             // first position of this lane's box in tile i, and whether some node sees any of it
-            auto box_pos = [&](int i) -> long long { return (long long)s.g.tile(i) * kTaKeys + box * A.box; };
-            auto box_seen = [&](long long j) -> bool {
-                return j < s.g.end && (j + A.box > s.g.wlo || j < A.sinks);
+            auto box_pos = [&](int i) -> int { return s.g.tile(i) * kTaKeys + box * A.box; };
+            auto box_seen = [&](int j) -> bool {
+                return j < s.g.end && (s.g.wlo - j < A.box || j < A.sinks);
             };
             auto fetch = [&](int i0) -> int {  // page of this lane's box in tile i0 + lane / nb
                 const int i = i0 + lane / nb;
                 if (i >= i_end) return 0;
-                const long long j = box_pos(i);
+                const int j = box_pos(i);
                 if (!box_seen(j)) return 0;
                 int p = __ldcg(row + (j >> A.page_shift));
                 if ((unsigned)p >= (unsigned)A.num_pages) {
@@ -588,16 +586,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             // the pages of `ahead` tiles at a time go to shared memory, where the lane that
             // issues the copies reads them in a loop (unrolled over the boxes its code was
             // read anew for every tile, 250 cycles a copy); the next ones are on their way
-            int base = s.i0, nxt = fetch(base);
+            int base = s.i0, at = s.i0, nxt = 0;  // first tile of those in shared memory, next to be fetched
             int *pages = sh.pages[is_k ? 0 : 1];
-            auto turn = [&](int i) {
-                __syncwarp();
-                pages[lane] = nxt;
-                base = i;
-                nxt = i + ahead < i_end ? fetch(i + ahead) : 0;
-                __syncwarp();
-            };
-            turn(base);
             // Q of this segment once the scores of the last one are done: looked for
             // before every load, so that the tiles need not wait for it
             bool q_due = is_k;
@@ -605,7 +595,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 constexpr int kQs = MODE == kTaSplitKeys ? 1 : 2;
                 if (elect_one()) {
                     mbar_expect_tx(&sh.q_full, (uint32_t)(kQs * kHalves * A.np * A.G * 128));
+#pragma unroll 1
                     for (int q = 0; q < kQs; ++q)
+#pragma unroll 1
                         for (int h = 0; h < kHalves; ++h)
                             tma_load_4d(sh.q + q * C::kStreamQ + h * kTaRows * 128, &tm_q, h * 64,
                                         (MODE == kTaSplitHeads ? 2 * s.hk + q : s.hk) * A.G,
@@ -621,29 +613,35 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     issue_q();
             };
             for (int i = s.i0; i < i_end && ok; ++i) {
-                if (i >= base + ahead) turn(i);
+                if (i == s.i0 || i == base + ahead) {
+                    base = i;
+                    int now;
+#pragma unroll 1
+                    do {  // at first these and the next ones, then one load ahead
+                        now = nxt;
+                        nxt = fetch(at);
+                        at += ahead;
+                    } while (at == s.i0 + ahead);
+                    __syncwarp();
+                    pages[lane] = now;
+                    __syncwarp();
+                }
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, lane < nb && box_seen(box_pos(i)));
-                const int tok = (int)(((long long)s.g.tile(i) * kTaKeys) & (A.page - 1));
+                const int tok = (s.g.tile(i) * kTaKeys) & (A.page - 1);
 #pragma unroll 1
                 for (int head = s.hk * kPer; head < (s.hk + 1) * kPer && ok; ++head) {
-                    look_q();
-                    if (fill > 0) {
-                        unsigned long long t0 = 0;
-                        for (uint32_t tries = 1;; ++tries) {
-                            if (__any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u))) break;
-                            look_q();
-                            if ((tries & 63u) == 0) {
-                                const unsigned long long now = global_ns();
-                                if (t0 == 0) t0 = now;
-                                if (__any_sync(0xFFFFFFFFu, *abort || now - t0 > kTaWaitNs)) {
-                                    *abort = 1;
-                                    ok = false;
-                                    break;
-                                }
-                            }
+#pragma unroll 1
+                    for (uint32_t tries = 0;; ++tries) {
+                        look_q();
+                        if (fill == 0 || __any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u)))
+                            break;
+                        if (__any_sync(0xFFFFFFFFu, *abort || tries >= kTaTries)) {
+                            *abort = 1;
+                            ok = false;
+                            break;
                         }
-                        if (!ok) break;
                     }
+                    if (!ok) break;
                     uint8_t *tile = tiles + stage * C::kStage;
                     if (elect_one()) {
                         mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
@@ -823,7 +821,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int t_step = MODE == kTaSplitKeys ? 2 : 1;
             bool first = true;
             for (int t = MODE == kTaSplitKeys ? (int)((base + stream) & 1u) : 0; t < s.n && ok; t += t_step, first = false) {
-                const long long j0 = (long long)g.tile(s.i0 + t) * kTaKeys;
+                const int j0 = g.tile(s.i0 + t) * kTaKeys;
                 const uint32_t use = (base + (uint32_t)t) >> (MODE == kTaSplitKeys ? 1 : 0);  // the stream's
                 // values that no node sees may be anything: they are cleared, so that their zero
                 // weights leave them out (kTaSplitRows: by stream 0, whose weights are used first);
@@ -832,10 +830,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 // stage's parity says nothing while the fill before this one is still due
                 const uint32_t v_tile = (base + (uint32_t)t) * kPer + (MODE == kTaSplitHeads ? stream : 0), v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
                 bool clear = (MODE != kTaSplitRows || stream == 0) &&
-                             (j0 + kTaKeys > g.end || (j0 < g.wlo && j0 + kTaKeys > A.sinks));
+                             (g.end - j0 < kTaKeys || (j0 < g.wlo && A.sinks - j0 < kTaKeys));
                 auto clear_v = [&]() {
-                    const long long j = j0 + row;
-                    if (j >= g.end || (j < g.wlo && j >= A.sinks)) {
+                    if (g.end - j0 <= row || (g.wlo - j0 > row && A.sinks - j0 <= row)) {
 #pragma unroll
                         for (int d = 0; d < kHalves; ++d) {  // neighbours begin 16 bytes apart: other banks
                             uint4 *z = reinterpret_cast<uint4 *>(sh.v[v_stage] + d * kTaKeys * 128 + row * 128);
@@ -850,7 +847,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 // run while the other half's weights are formed, and 64 scores fit the registers
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    const long long jh = j0 + h * (kTaKeys / 2);
+                    const int jh = j0 + h * (kTaKeys / 2);
                     const uint32_t th = ts + (uint32_t)(h * (kTaKeys / 2));
                     if (h == 0) {
                         ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort));
@@ -861,7 +858,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     if (warp_works) {
                         uint32_t x[64];
                         tmem_load(th, x);
-                        const bool whole = jh + 64 <= g.c && (jh >= low || jh + 64 <= A.sinks);
+                        const bool whole = g.c - jh >= 64 && (jh >= low || A.sinks - jh >= 64);
                         if (!__all_sync(0xFFFFFFFFu, whole || !valid)) {
                             const unsigned long long bits = valid ? seen_bits(jh, g.c, low, sinks, path) : 0ull;
                             const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
