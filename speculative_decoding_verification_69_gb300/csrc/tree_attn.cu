@@ -176,37 +176,37 @@ template <int MODE> struct Walk {
     __device__ __forceinline__ void find(const TaArgs &A, const long long *incl, long long u) {
         const int lane = threadIdx.x & 31;
         const int per = (A.B + kTaChunks - 1) / kTaChunks;
-        int from = 0;
+        int from = 0, k = 0;
         long long base = 0;
 #pragma unroll 1
         for (int i = 0; i < kTaChunks; i += 32) {  // the chunks that end at or before u
             const long long x = base + incl[i + lane];
-            const int k = __popc(__ballot_sync(0xFFFFFFFFu, x <= u));
+            k = __popc(__ballot_sync(0xFFFFFFFFu, x <= u));
             from = i;
             if (k < 32) {
-                // chunks of one request: the requests of these 32 are looked through below
-                if (per > 1 && k > 0) from = (i + k) * per, base = __shfl_sync(0xFFFFFFFFu, x, k - 1);
-                else from *= per;
+                if (k > 0) base = __shfl_sync(0xFFFFFFFFu, x, k - 1);
                 break;
             }
             base = __shfl_sync(0xFFFFFFFFu, x, 31);
         }
+        if (per > 1) {  // the requests of the chunk that end at or before u
 #pragma unroll 1
-        for (;; from += 32) {  // the requests that end at or before u
-            if (from != b0) fetch(A, from);
-            long long x = ta_units<MODE>(A, ta_geo(A, lens));
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
+            for (from = (from + k) * per;; from += 32) {
+                fetch(A, from);
+                long long x = ta_units<MODE>(A, ta_geo(A, lens));
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                    if (lane >= o) x += y;
+                }
+                k = __popc(__ballot_sync(0xFFFFFFFFu, base + x <= u));
+                if (k > 0) base += __shfl_sync(0xFFFFFFFFu, x, k - 1);
+                if (k < 32 || from + 32 >= A.B) break;
             }
-            const int k = __popc(__ballot_sync(0xFFFFFFFFu, base + x <= u));
-            if (k > 0) base += __shfl_sync(0xFFFFFFFFu, x, k - 1);
-            if (k < 32 || from + 32 >= A.B) {
-                enter(A, min(from + min(k, 31), A.B - 1));
-                break;
-            }
+        } else if (from != b0) {
+            fetch(A, from);
         }
+        enter(A, min(from + min(k, 31), A.B - 1));
         // (the bounds hold by themselves unless the lengths are written during the call,
         // which then must not lead out of any array)
         const int item = (int)min(ta_div(max(u - base, 0ll), max(g.nt, 1)), (long long)A.H * rts - 1);
