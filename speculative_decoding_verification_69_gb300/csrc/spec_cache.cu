@@ -298,11 +298,11 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 
 // One page to another in every layer: whole pages (copies NULL: src[i] to
 // dst[i]), or the first tokens of a page as the bookkeeping of a fork listed
-// them.  Grid (pairs, layers, {k, v} x token blocks), block (vector columns,
-// tokens).  Bound by HBM: each vector is read once and written once; four
-// loads are in flight per thread before the first store.
+// them.  Grid (pairs, layers, token blocks), block (vector columns, tokens).
+// Bound by HBM: each vector is read once and written once; eight loads, four of
+// keys and four of values, are in flight per thread before the first store.
 __global__ void __launch_bounds__(256) sv_copy_pages(Pool P, const int *src, const int *dst,
-                                                     const int *copies, int blocks, uint32_t *status) {
+                                                     const int *copies, uint32_t *status) {
     pdl_trigger();
     pdl_wait();
     const int i = blockIdx.x;
@@ -320,23 +320,24 @@ __global__ void __launch_bounds__(256) sv_copy_pages(Pool P, const int *src, con
         if (threadIdx.x == 0 && threadIdx.y == 0) flag(status, SPEC_DEV_BAD_PAGE);
         return;
     }
-    const int half = blockIdx.z / blocks, part = blockIdx.z % blocks;
-    uint4 *pool = half ? P.v : P.k;
-    const long long base = (long long)blockIdx.y * P.layer;
-    const uint4 *a = pool + base + (long long)from * P.page_st;
-    uint4 *b = pool + base + (long long)to * P.page_st;
+    const long long base = (long long)blockIdx.y * P.layer, a = base + (long long)from * P.page_st,
+                    b = base + (long long)to * P.page_st;
+    const int step = blockDim.y * gridDim.z;
     for (int c = threadIdx.x; c < P.cols; c += blockDim.x) {
         const int h = c / P.vecs;
         const long long off = (long long)h * P.head + (c - h * P.vecs);
-        const int step = blockDim.y * blocks;
-        for (int t = part * blockDim.y + threadIdx.y; t < used; t += 4 * step) {
-            uint4 x[4];
+        for (int t = blockIdx.z * blockDim.y + threadIdx.y; t < used; t += 4 * step) {
+            uint4 x[4], y[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (t + u * step < used) x[u] = ld_stream_v4(a + off + (long long)(t + u * step) * P.token);
+            for (int u = 0; u < 4; ++u) {
+                const long long at = a + off + (long long)(t + u * step) * P.token;
+                if (t + u * step < used) x[u] = ld_stream_v4(P.k + at), y[u] = ld_stream_v4(P.v + at);
+            }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (t + u * step < used) b[off + (long long)(t + u * step) * P.token] = x[u];
+            for (int u = 0; u < 4; ++u) {
+                const long long at = b + off + (long long)(t + u * step) * P.token;
+                if (t + u * step < used) P.k[at] = x[u], P.v[at] = y[u];
+            }
         }
     }
 }
@@ -614,8 +615,8 @@ spec_status_t spec_cache_fork(const spec_pages_t *pages, int32_t *page_table, in
     if (sp != SPEC_OK) return sp;
     const dim3 block = sv::column_block(P.cols);
     const int blocks = sv::copy_blocks(P, block);
-    return sv::launch_pdl(sv::sv_copy_pages, dim3((unsigned)F, (unsigned)P.layers, 2u * blocks), block, 0, s,
-                          P, (const int *)nullptr, (const int *)nullptr, (const int *)A.copies, blocks,
+    return sv::launch_pdl(sv::sv_copy_pages, dim3((unsigned)F, (unsigned)P.layers, (unsigned)blocks), block, 0, s,
+                          P, (const int *)nullptr, (const int *)nullptr, (const int *)A.copies,
                           dev_status);
 }
 
@@ -627,9 +628,9 @@ spec_status_t spec_cache_copy(const spec_pages_t *pages, const int32_t *src_page
     if (!src_pages || !dst_pages || n < 1) return SPEC_ERR_INVALID_ARG;
     const dim3 block = sv::column_block(P.cols);
     const int blocks = sv::copy_blocks(P, block);
-    return sv::launch_pdl(sv::sv_copy_pages, dim3((unsigned)n, (unsigned)P.layers, 2u * blocks), block, 0,
+    return sv::launch_pdl(sv::sv_copy_pages, dim3((unsigned)n, (unsigned)P.layers, (unsigned)blocks), block, 0,
                           static_cast<cudaStream_t>(stream), P, src_pages, dst_pages,
-                          (const int *)nullptr, blocks, dev_status);
+                          (const int *)nullptr, dev_status);
 }
 
 spec_status_t spec_cache_append(const spec_pages_t *pages, const int32_t *page_table,
