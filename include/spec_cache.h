@@ -58,7 +58,7 @@ typedef struct {
     int page_size;          /* tokens per page: a power of two of at least 8 */
     int heads;              /* key/value heads */
     int head_dim;           /* a multiple of 8 */
-    long long layer_stride; /* strides in elements, multiples of 8 */
+    long long layer_stride; /* strides in elements: multiples of 8, at least head_dim where the extent is above 1 */
     long long page_stride;
     long long token_stride;
     long long head_stride;
@@ -176,22 +176,27 @@ spec_status_t spec_cache_commit(const spec_pages_t *pages, const int32_t *page_t
  * out 0, lse -inf.
  *   q    [B, N, Hq, head_dim] of the pool's dtype, 16-byte aligned, element
  *        (b, n, h, d) at b * q_stride_b + n * q_stride_n + h * q_stride_h + d
- *        (multiples of 8).  out [B, N, Hq, head_dim] contiguous, same dtype.
+ *        (multiples of 8, at least head_dim where the extent is above 1).
+ *        out [B, N, Hq, head_dim] contiguous, same dtype.
  *   page_table [B, max_pages], cache_len [B]: entries of pages that no node of
  *        the request sees are not looked at.  What the pool holds at positions
  *        that no node sees (past the end, before a window) may be anything,
  *        infinities and NaN included; at positions that some node sees it must
  *        be finite.
  *   A parent that is not an earlier node ends the path there (SPEC_DEV_BAD_TREE);
- *   cache_len[b] + node_count[b] beyond what the row of the table reaches is
- *   cut (SPEC_DEV_BAD_LEN); a page outside the pool is read as page 0
- *   (SPEC_DEV_BAD_PAGE; the request's outputs are then undefined).
+ *   cache_len[b] + node_count[b] beyond what the row of the table reaches, or
+ *   beyond 2^31 - 256, is cut (SPEC_DEV_BAD_LEN); a page outside the pool is
+ *   read as page 0 (SPEC_DEV_BAD_PAGE; the request's outputs are then
+ *   undefined).  A wait inside the kernel that is in vain for about 2 s gives
+ *   the call up (SPEC_DEV_TIMEOUT; outputs undefined).
  *   1 <= B < 2^16, 1 <= N <= SPEC_MAX_TREE, head_dim a multiple of 8 up to
  *   SPEC_MAX_HEAD_DIM, Hq a multiple of heads, heads <= 1024, Hq / heads <= 64,
  *   window >= 0, sinks >= 0.  scale > 0.
- *   workspace: spec_tree_attention_workspace_bytes, 256-byte aligned.
+ *   workspace: spec_tree_attention_workspace_bytes, 256-byte aligned; nothing
+ *   in it is read that the call has not written.  Two launches.
  * Scores, softmax statistics and sums are float32; the softmax weights are
- * rounded to the dtype for the product with v (their sum is not).
+ * rounded to the dtype for the product with v (their sum is not).  A row that
+ * sees a NaN score, or infinite ones, comes out NaN.
  */
 size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int heads, int head_dim);
 spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long q_stride_n,

@@ -508,7 +508,8 @@ spec_status_t spec_verify_scheduled_from_host(
  * (outputs then undefined but in range).  In spec_verify_tree calls, each
  * staging of node rows in the sampled walk first waits on such a barrier,
  * reports SPEC_DEV_TIMEOUT and then waits for its copies as usual (outputs
- * unchanged).  0 turns it off.  No counterpart on the pages: it exercises the
+ * unchanged).  In spec_tree_attention calls every wait between the roles of a
+ * CTA gives up at once: SPEC_DEV_TIMEOUT, outputs undefined.  0 turns it off.  No counterpart on the pages: it exercises the
  * failure path of the bounded waits.
  */
 spec_status_t spec_debug_force_wait_timeout(int enable);

@@ -202,7 +202,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // bounded wait: 2 s
 // while the switch is on) make every warp first wait on a barrier nothing
 // completes; that wait runs out after kDiagWaitNs and the warp gives up as on
 // a real timeout (status bit, its copies drained, no items).
-static bool g_diag_timeout = false;
+bool g_diag_timeout = false;
 constexpr unsigned long long kDiagWaitNs = 1000000ull;  // 1 ms
 
 // The diagnostic wait of one warp: true when the warp must give up.

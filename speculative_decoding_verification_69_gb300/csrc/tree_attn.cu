@@ -48,6 +48,8 @@ constexpr uint32_t kTaTries = 1u << 19;                  // looks of a wait: 2 s
 constexpr unsigned long long kTaWaitNs = 2000000000ull;  // for the waits at the end
 constexpr float kTaGrow = 8.f;      // growth of a row's maximum that rescales its O
 
+extern bool g_diag_timeout;  // spec_debug_force_wait_timeout
+
 // What the two streams of a CTA divide between them.
 enum { kTaSplitKeys, kTaSplitRows, kTaSplitHeads };
 
@@ -64,6 +66,7 @@ struct TaArgs {
     float2 *part_ml;     // [cta][2][rows]: m (base 2), l
     int4 *joins;         // [cta]: request, key head (or pair), first node and parts (0: none), see tree_attn_join
     uint32_t *status;
+    uint32_t tries;      // looks of a wait
 };
 
 template <int DP, int MODE> struct TaCfg {
@@ -267,13 +270,13 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for a phase, until another role has given up or kTaTries looks have been in
+// Waits for a phase, until another role has given up or `tries` looks have been in
 // vain; a look sleeps for 3.9 us unless the phase ends.  (A limit by count: the wait is
 // inlined in many places, and a timer in each was code to be fetched, 4 us of 105 at a
 // window of 128 and 512 requests.)
-__device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool ta_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t tries) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kTaTries; ++i) {
+    for (uint32_t i = 0; i < tries; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
     // segment k, or nothing when the wait for it ran out
     auto take = [&](uint64_t *bars, int k) -> const SegSlot * {
-        const bool ok = ta_wait(&bars[k % kTaSlots], (k / kTaSlots) & 1, abort);
+        const bool ok = ta_wait(&bars[k % kTaSlots], (k / kTaSlots) & 1, abort, A.tries);
         return __all_sync(0xFFFFFFFFu, ok) ? &sh.seg[k % kTaSlots] : nullptr;
     };
     auto give = [&](int k) {
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 left -= s.n;
             }
             if (k >= kTaSlots)
-                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort));
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort, A.tries));
             if (!ok) break;
             SegSlot &slot = sh.seg[k % kTaSlots];
             if (lane == 0) {
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         look_q();
                         if (fill == 0 || __any_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], (fill - 1) & 1u)))
                             break;
-                        if (__any_sync(0xFFFFFFFFu, *abort || tries >= kTaTries)) {
+                        if (__any_sync(0xFFFFFFFFu, *abort || tries >= A.tries)) {
                             *abort = 1;
                             ok = false;
                             break;
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 }
             }
             if (ok && q_due) {
-                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u, abort));
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.q_free, (uint32_t)(seg_no - 1) & 1u, abort, A.tries));
                 if (ok) issue_q();
             }
         }
@@ -678,7 +681,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const uint64_t q_desc = umma_desc_sw128(smem_u32(sh.q)), k_desc = umma_desc_sw128(smem_u32(sh.k[0])),
                        vt_desc = v_desc(smem_u32(sh.v[0]));
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xFFFFFFFFu, ta_wait(bar, parity, abort)) != 0;
+            return __all_sync(0xFFFFFFFFu, ta_wait(bar, parity, abort, A.tries)) != 0;
         };
         // Scores of stream i against the next K tile; release: the tile's last use,
         // last: the segment's.  They overwrite the columns of the stream's last
@@ -850,7 +853,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     const int jh = j0 + h * (kTaKeys / 2);
                     const uint32_t th = ts + (uint32_t)(h * (kTaKeys / 2));
                     if (h == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort));
+                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort, A.tries));
                         if (!ok) break;
                         tc_fence_after();
                         if (clear && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh.v_full[v_stage], v_parity))) clear_v();
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                             l2 = make_float2(l2.x * f, l2.y * f);
                             if (h > 0 || !first) {  // O holds the halves before this one
                                 uint64_t *done = h > 0 ? &sh.pv_done[stream][0] : &sh.pv_done[stream][1];
-                                ok = __all_sync(0xFFFFFFFFu, ta_wait(done, (h > 0 ? use : use - 1) & 1u, abort));
+                                ok = __all_sync(0xFFFFFFFFu, ta_wait(done, (h > 0 ? use : use - 1) & 1u, abort, A.tries));
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll 1
@@ -917,7 +920,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         tmem_wait_store();
                     }
                     if (h == 0 && clear) {
-                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.v_full[v_stage], v_parity, abort));
+                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.v_full[v_stage], v_parity, abort, A.tries));
                         if (!ok) break;
                         clear_v();
                     }
@@ -946,9 +949,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 sh.ml[seg_no & 1][stream][row] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.ml_full));
-                ok = ta_wait(&sh.ml_full, seg_no & 1, abort);
-                ok = ok && ta_wait(&sh.pv_done[a][1], (e1 >> 1) & 1u, abort);
-                if (two) ok = ok && ta_wait(&sh.pv_done[a ^ 1][1], ((e1 - 1u) >> 1) & 1u, abort);
+                ok = ta_wait(&sh.ml_full, seg_no & 1, abort, A.tries);
+                ok = ok && ta_wait(&sh.pv_done[a][1], (e1 >> 1) & 1u, abort, A.tries);
+                if (two) ok = ok && ta_wait(&sh.pv_done[a ^ 1][1], ((e1 - 1u) >> 1) & 1u, abort, A.tries);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const float2 x = sh.ml[seg_no & 1][a][row], y = sh.ml[seg_no & 1][a ^ 1][row];
@@ -957,7 +960,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 w_b = m == -INFINITY ? 0.f : ex2(y.x - m);
                 l = x.y * w_a + y.y * w_b;
             } else {
-                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.pv_done[stream][1], e1 & 1u, abort));
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.pv_done[stream][1], e1 & 1u, abort, A.tries));
                 if (!ok) break;
             }
             tc_fence_after();
@@ -1266,6 +1269,7 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     A.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     A.joins = reinterpret_cast<int4 *>(ws + L.joins);
     A.status = dev_status;
+    A.tries = sv::g_diag_timeout ? 0u : sv::kTaTries;
 
     CUtensorMap tq, tk, tv;
     // an extent of one is never stepped over: any valid stride stands for it

@@ -193,6 +193,33 @@ def test_nan_and_infinite_scores_show(N, hq, ctx):
     assert torch.equal(o[1], ref_o[1]) and torch.equal(l[1], ref_l[1])
 
 
+@pytest.mark.parametrize("N,hq,hkv,ctx", [(1, 8, 2, 3000), (9, 8, 2, 700), (64, 16, 2, 900), (4, 64, 64, 250)])
+def test_nothing_unwritten_is_read(N, hq, hkv, ctx):
+    """A workspace and outputs full of NaN and -1 make no difference, and every output is written."""
+    sv = _sv()
+    c = _case(N + hq, [ctx, 0, 40], N, hq, hkv, 64, 16, torch.bfloat16)
+    cnt = torch.tensor([N, N, N // 2], dtype=torch.int32, device="cuda")
+    o, l, _ = _run(c, node_count=cnt)
+    n = sv.load_library().spec_tree_attention_workspace_bytes(3, N, hq, hkv, 64)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    o2, l2, st = _run(c, node_count=cnt, workspace=ws, out=torch.full_like(o, float("nan")))
+    assert st == 0 and torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("N,hq,hkv,D", [(1, 8, 2, 128), (9, 8, 2, 64), (64, 16, 2, 128), (4, 64, 64, 64)])
+def test_wait_that_runs_out_is_reported(N, hq, hkv, D):
+    """Every wait between the kernel's roles gives up at once: the call reports it and ends, the next one is right."""
+    sv = _sv()
+    c = _case(N, [900, 300, 5], N, hq, hkv, D, 16, torch.bfloat16)
+    try:
+        sv.force_wait_timeout(True)
+        _, _, st = _run(c)
+    finally:
+        sv.force_wait_timeout(False)
+    assert st == sv.DEV_TIMEOUT
+    _check(c)
+
+
 def test_large_scores():
     """Sharp distributions whose maximum grows along the keys (the running
     maximum moves many times) and falls (it never moves again)."""
