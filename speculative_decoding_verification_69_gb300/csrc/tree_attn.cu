@@ -43,6 +43,7 @@ constexpr int kTaThreads = 384;     // 8 softmax warps, then K loads, products, 
 constexpr int kTaWarpK = 8, kTaWarpMma = 9, kTaWarpPlan = 10, kTaWarpV = 11;
 constexpr int kTaSlots = 4;         // segments the scheduler may be ahead
 constexpr int kTaMaxCtas = 160;     // CTAs the workspace has room for
+constexpr int kTaJoinLanes = 16;    // lanes of a row in the join
 constexpr int kTaChunks = 128;      // entries of the running sum over requests
 constexpr uint32_t kTaTries = 1u << 19;                  // looks of a wait: 2 s
 constexpr unsigned long long kTaWaitNs = 2000000000ull;  // for the waits at the end
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 left -= s.n;
             }
             if (k >= kTaSlots)
-                ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort, A.tries));
+                ok = __all_sync(0xFFFFFFFFu,
+                                ta_wait(&sh.seg_free[k % kTaSlots], (k / kTaSlots - 1) & 1, abort, A.tries));
             if (!ok) break;
             SegSlot &slot = sh.seg[k % kTaSlots];
             if (lane == 0) {
@@ -801,8 +803,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     } else if (warp < 8) {  // ------------------------------------------- softmax
         const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);          // S; P over the second half of each half
-        const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);        // O
+        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);   // S; P over the second half of each half
+        const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);  // O
         const int rows_used = A.np * A.G, local = row / A.G;
         uint32_t base = 0;                     // the CTA's tiles before this segment
         int seg_no = 0;
@@ -823,7 +825,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             float2 l2 = make_float2(0.f, 0.f);
             const int t_step = MODE == kTaSplitKeys ? 2 : 1;
             bool first = true;
-            for (int t = MODE == kTaSplitKeys ? (int)((base + stream) & 1u) : 0; t < s.n && ok; t += t_step, first = false) {
+            const int t0 = MODE == kTaSplitKeys ? (int)((base + stream) & 1u) : 0;
+            for (int t = t0; t < s.n && ok; t += t_step, first = false) {
                 const int j0 = g.tile(s.i0 + t) * kTaKeys;
                 const uint32_t use = (base + (uint32_t)t) >> (MODE == kTaSplitKeys ? 1 : 0);  // the stream's
                 // values that no node sees may be anything: they are cleared, so that their zero
@@ -831,7 +834,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 // before the weights if the tile is there by then.  Not looked for before the scores
                 // have come: they follow earlier values, whose tiles have then been there, and a
                 // stage's parity says nothing while the fill before this one is still due
-                const uint32_t v_tile = (base + (uint32_t)t) * kPer + (MODE == kTaSplitHeads ? stream : 0), v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
+                const uint32_t v_tile = (base + (uint32_t)t) * kPer + (MODE == kTaSplitHeads ? stream : 0);
+                const uint32_t v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
                 bool clear = (MODE != kTaSplitRows || stream == 0) &&
                              (g.end - j0 < kTaKeys || (j0 < g.wlo && A.sinks - j0 < kTaKeys));
                 auto clear_v = [&]() {
@@ -877,7 +881,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         for (int i = 0; i < 64; i += 8) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
+                                mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + 2 * e]),
+                                                           __uint_as_float(x[i + 2 * e + 1])));
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
                         if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kTaGrow))) {
@@ -887,7 +892,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                             l2 = make_float2(l2.x * f, l2.y * f);
                             if (h > 0 || !first) {  // O holds the halves before this one
                                 uint64_t *done = h > 0 ? &sh.pv_done[stream][0] : &sh.pv_done[stream][1];
-                                ok = __all_sync(0xFFFFFFFFu, ta_wait(done, (h > 0 ? use : use - 1) & 1u, abort, A.tries));
+                                ok = __all_sync(0xFFFFFFFFu,
+                                                ta_wait(done, (h > 0 ? use : use - 1) & 1u, abort, A.tries));
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll 1
@@ -1035,7 +1041,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const long long r0 = ((long long)b * A.N + n0) * A.Hq, r1 = ((long long)b * A.N + A.N) * A.Hq;
             uint4 *o = reinterpret_cast<uint4 *>(A.out);
 #pragma unroll 1
-            for (long long i = r0 * A.D / 8 + threadIdx.x; i < r1 * A.D / 8; i += 256) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (long long i = r0 * A.D / 8 + threadIdx.x; i < r1 * A.D / 8; i += 256)
+                o[i] = make_uint4(0u, 0u, 0u, 0u);
             if (A.lse)
 #pragma unroll 1
                 for (long long i = r0 + threadIdx.x; i < r1; i += 256) A.lse[i] = -INFINITY;
@@ -1050,63 +1057,75 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (threadIdx.x == 0 && sh.abort) flag(A.status, SPEC_DEV_TIMEOUT);
 }
 
-// The parts of an item that cuts fell into, joined: one warp per row.
+// The parts of an item that cuts fell into, joined in the order of the keys.
 // joins[j]: the first cut of an item lies at CTA j's first unit; its parts are
 // slot 1 of the CTA before, where it begins, and slot 0 of CTA j and those after.
+// 16 lanes per row, two vectors of four columns each: bound by the latency of three
+// dependent loads at few rows (3.4 us of the 11.2 of one token at one request) and
+// by instructions at many (10 us of 195 at 64 nodes and 64 requests); a warp per row
+// took 16.7 us there, 8 lanes 9.5 but 3 us more with 20 parts of 64 rows.
 template <int DT>
 __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta, int mode) {
+    constexpr int L = kTaJoinLanes, kVecs = 32 / L;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (prow >= rows_cta) return;
-    const int first = (int)blockIdx.x - 1;
-    auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * rows_cta + prow; };
+    const int lane = threadIdx.x % L, prow = blockIdx.y * (256 / L) + threadIdx.x / L;
     const int4 a = A.joins[blockIdx.x];
-    const int parts = a.w;
-    // the first 32 parts' m and l, fetched beside the description of the cut
+    const int parts = a.w, first = (int)blockIdx.x - 1;
+    auto slot = [&](int i) { return ((first + i) * 2 + (i == 0 ? 1 : 0)) * rows_cta + prow; };
+    // the first L parts' m and l, fetched beside the description of the cut
     float2 x0 = make_float2(-INFINITY, 0.f);
-    if (first >= 0 && first + lane < (int)gridDim.x) x0 = A.part_ml[slot(lane)];
-    if (parts == 0) return;
+    if (first >= 0 && first + lane < (int)gridDim.x && prow < rows_cta) x0 = A.part_ml[slot(lane)];
     const int stream = prow / rows_used, row = prow - stream * rows_used;
     const int local = row / A.G, node = a.z + (mode == kTaSplitRows ? stream * A.np : 0) + local;
     const int hk = mode == kTaSplitHeads ? 2 * a.y + stream : a.y;
-    if (node >= A.N) return;
+    if (parts == 0) return;
+    const bool works = prow < rows_cta && node < A.N;
+    const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, works);
+    if (!works) return;
     float m = lane < parts ? x0.x : -INFINITY;
-    for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, A.part_ml[slot(i)].x);
-    m = warp_max(m);
-    const long long orow = ((long long)a.x * A.N + node) * A.Hq + (long long)hk * A.G + (row - local * A.G);
-    uint2 *dst = reinterpret_cast<uint2 *>(A.out + orow * A.D) + lane;
-    if (m == -INFINITY) {
-        if (4 * lane < A.D) *dst = make_uint2(0u, 0u);
-        if (lane == 0 && A.lse) A.lse[orow] = -INFINITY;
-        return;
-    }
+    for (int i = lane + L; i < parts; i += L) m = fmaxf(m, A.part_ml[slot(i)].x);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o, L));
+    const bool some = m != -INFINITY;  // the row sees something
     float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += 32) {
+    float4 o[kVecs] = {};
+    for (int i0 = 0; i0 < parts; i0 += L) {
         float w = 0.f;
-        if (i0 + lane < parts) {
+        if (some && i0 + lane < parts) {
             const float2 x = i0 == 0 ? x0 : A.part_ml[slot(i0 + lane)];
             w = ex2(x.x - m);
             l = fmaf(x.y, w, l);
         }
-        const int k = min(32, parts - i0);
+        const int k = min(L, parts - i0);
 #pragma unroll 8
         for (int i = 0; i < k; ++i) {
-            const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
-            if (4 * lane < A.D) {
-                const float4 x = reinterpret_cast<const float4 *>(A.part_o + slot(i0 + i) * A.D)[lane];
-                o.x = fmaf(x.x, wi, o.x);
-                o.y = fmaf(x.y, wi, o.y);
-                o.z = fmaf(x.z, wi, o.z);
-                o.w = fmaf(x.w, wi, o.w);
+            const float wi = __shfl_sync(lanes, w, i, L);
+            const float4 *part = reinterpret_cast<const float4 *>(A.part_o + (long long)slot(i0 + i) * A.D);
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                if (4 * (lane + v * L) < A.D) {
+                    const float4 x = part[lane + v * L];
+                    o[v].x = fmaf(x.x, wi, o[v].x);
+                    o[v].y = fmaf(x.y, wi, o[v].y);
+                    o[v].z = fmaf(x.z, wi, o[v].z);
+                    o[v].w = fmaf(x.w, wi, o[v].w);
+                }
             }
         }
     }
-    l = warp_sum(l);
-    const float inv = 1.f / l;
-    if (4 * lane < A.D) *dst = make_uint2(pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv));
-    if (lane == 0 && A.lse) A.lse[orow] = 0.69314718056f * (m + log2f(l));
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) l += __shfl_xor_sync(lanes, l, d, L);
+    const float inv = some ? 1.f / l : 0.f;
+    const long long orow = ((long long)a.x * A.N + node) * A.Hq + (long long)hk * A.G + (row - local * A.G);
+    uint2 *dst = reinterpret_cast<uint2 *>(A.out + orow * A.D);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+        if (4 * (lane + v * L) < A.D)
+            dst[lane + v * L] = some ? make_uint2(pack2<DT>(o[v].x * inv, o[v].y * inv),
+                                                  pack2<DT>(o[v].z * inv, o[v].w * inv))
+                                     : make_uint2(0u, 0u);
+    if (lane == 0 && A.lse) A.lse[orow] = some ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host
@@ -1178,8 +1197,9 @@ static spec_status_t ta_launch(const TaArgs &A, const CUtensorMap &q, const CUte
     const spec_status_t st =
         launch_pdl(tree_attn<DT, DP, MODE>, dim3((unsigned)ctas), dim3(kTaThreads), smem, s, q, k, v, A);
     if (st != SPEC_OK) return st;
-    return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((r.cta + 7) / 8)), dim3(256), 0, s, A,
-                      r.used, r.cta, MODE);
+    constexpr int rows = 256 / kTaJoinLanes;
+    return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((r.cta + rows - 1) / rows)), dim3(256), 0, s,
+                      A, r.used, r.cta, MODE);
 }
 
 template <int DT, int DP>
