@@ -20,8 +20,11 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
               "-Xcompiler", "-fPIC", "-shared", "--threads", "0"]
 
 
+CUDA = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+
+
 def nvcc():
-    cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
+    cand = os.path.join(CUDA, "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
 
 
@@ -49,10 +52,10 @@ def _binding_cmd():
     import torch
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], INCLUDE]
+           sysconfig.get_paths()["include"], os.path.join(CUDA, "include"), INCLUDE]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
              "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + p for p in inc] + [BINDING]
-            + ["-L" + os.path.join(base, "lib"), "-L" + OUT_DIR, "-l:libspecverify.so", "-lc10", "-ltorch_cpu",
+            + ["-L" + os.path.join(base, "lib"), "-L" + OUT_DIR, "-l:libspecverify.so", "-lc10", "-lc10_cuda", "-ltorch_cpu",
                "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 

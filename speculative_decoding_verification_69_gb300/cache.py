@@ -19,7 +19,6 @@ every step runs in the library's kernels, on torch's current stream or the
 `stream` given, and nothing falls back to torch.
 """
 import ctypes
-import functools
 import importlib.util
 
 import torch
@@ -71,42 +70,8 @@ def _native():
     return _loaded
 
 
-# The handle of torch's current stream on a device, without the Python object
-# that torch.cuda.current_stream makes around it (3 us a call).
-_current_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _stream(stream, t):
-    return _current_stream(t.get_device() if t.is_cuda else 0) if stream is None else stream.cuda_stream
-
-
-_scratch = {}
-
-
-def _workspace(n, t, handle, stream):
-    """Scratch that one stream's calls share: they never overlap."""
-    key = (t.get_device(), handle)
-    ws = _scratch.get(key)
-    if ws is None or ws.numel() < n:
-        if stream is None:
-            ws = torch.empty(n, dtype=torch.uint8, device=t.device)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(n, dtype=torch.uint8, device=t.device)
-        _scratch[key] = ws
-    return ws
-
-
-@functools.lru_cache(maxsize=4096)
-def _attention_bytes(B, N, Hq, heads, D):
-    from . import load_library
-    return max(256, load_library().spec_tree_attention_workspace_bytes(B, N, Hq, heads, D))
-
-
-@functools.lru_cache(maxsize=4096)
-def _fork_bytes(F):
-    from . import load_library
-    return max(256, load_library().spec_cache_fork_workspace_bytes(F))
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream  # None: torch's current stream
 
 
 def cache_resize(page_table, page_count, page_ref, want_len, page_size, *, extra=0, dev_status=None, stream=None):
@@ -115,7 +80,7 @@ def cache_resize(page_table, page_count, page_ref, want_len, page_size, *, extra
     page_table int32 [slots, max_pages], page_count [slots] and page_ref
     [num_pages] are updated; want_len int32 [slots], negative: left as it is."""
     _native().resize(page_table, page_count, page_ref, want_len, page_size, extra, dev_status,
-                     _stream(stream, page_table))
+                     _handle(stream))
 
 
 def cache_fork(k, v, page_table, page_count, page_ref, cache_len, src, dst, *, dev_status=None, stream=None):
@@ -123,15 +88,18 @@ def cache_fork(k, v, page_table, page_count, page_ref, cache_len, src, dst, *, d
     pages shared, the last partial page copied in every layer.  k, v [layers,
     num_pages, page_size, kv_heads, head_dim]; page_table, page_count, page_ref
     and cache_len are updated."""
-    handle = _stream(stream, k)
-    _native().fork(k, v, page_table, page_count, page_ref, cache_len, src, dst,
-                   _workspace(_fork_bytes(src.numel()), k, handle, stream), dev_status, handle)
+    args = (k, v, page_table, page_count, page_ref, cache_len, src, dst, dev_status, None)
+    if stream is None:
+        _native().fork(*args)
+    else:
+        with torch.cuda.stream(stream):  # its scratch belongs to that stream
+            _native().fork(*args)
 
 
 def cache_copy(k, v, src_pages, dst_pages, *, dev_status=None, stream=None):
     """Whole pages copied in every layer (spec_cache_copy): k, v [layers,
     num_pages, ...], src_pages and dst_pages int32 [n]."""
-    _native().copy(k, v, src_pages, dst_pages, dev_status, _stream(stream, k))
+    _native().copy(k, v, src_pages, dst_pages, dev_status, _handle(stream))
 
 
 def cache_append(k, v, page_table, cache_len, k_new, v_new, *, count=None, dev_status=None, stream=None):
@@ -139,7 +107,7 @@ def cache_append(k, v, page_table, cache_len, k_new, v_new, *, count=None, dev_s
     (spec_cache_append): k, v [num_pages, page_size, kv_heads, head_dim];
     k_new, v_new [B, N, kv_heads, head_dim] of equal strides; count int32 [B]
     tokens of each request, None: all N.  cache_len is not changed."""
-    _native().append(k, v, page_table, cache_len, k_new, v_new, count, dev_status, _stream(stream, k))
+    _native().append(k, v, page_table, cache_len, k_new, v_new, count, dev_status, _handle(stream))
 
 
 def cache_commit(k, v, page_table, cache_len, out_nodes, accept_len, *, new_len=None, nodes=None, dev_status=None,
@@ -153,7 +121,7 @@ def cache_commit(k, v, page_table, cache_len, out_nodes, accept_len, *, new_len=
     if new_len is None:
         new_len = cache_len
     _native().commit(k, v, page_table, cache_len, out_nodes, accept_len, new_len, nodes, dev_status,
-                     _stream(stream, k))
+                     _handle(stream))
     return new_len
 
 
@@ -167,16 +135,12 @@ def tree_attention(q, k, v, page_table, cache_len, parent=None, *, node_count=No
     window only the last `window` of them along its path and the first `sinks`
     tokens.  Returns out [B, N, q_heads, head_dim], with return_lse also the log
     of the softmax sums, float32 [B, N, q_heads]."""
-    handle = _stream(stream, q)
-    if workspace is None:
-        B, N, Hq, D = q.shape
-        workspace = _workspace(_attention_bytes(B, N, Hq, k.shape[2], D), q, handle, stream)
     if stream is None:
         return _native().tree_attention(q, k, v, page_table, cache_len, parent, node_count, scale, window, sinks, out,
-                                        return_lse, workspace, dev_status, handle)
+                                        return_lse, workspace, dev_status, None)
     with torch.cuda.stream(stream):  # what the call allocates belongs to that stream
         return _native().tree_attention(q, k, v, page_table, cache_len, parent, node_count, scale, window, sinks, out,
-                                        return_lse, workspace, dev_status, handle)
+                                        return_lse, workspace, dev_status, None)
 
 
 class PagedCache:

@@ -9,12 +9,16 @@
 #include <Python.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
+#include <map>
 #include <string>
+#include <utility>
 
 #include "spec_cache.h"
 
@@ -25,18 +29,17 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     return THPVariable_Unpack(o);
 }
 
-uint32_t *status(PyObject *o) {
+void together(const at::Tensor &t, const at::Tensor &with, const char *name) {
+    TORCH_CHECK_VALUE(t.device() == with.device(), name, " is on ", t.device(), ", not on ", with.device());
+}
+
+uint32_t *status(PyObject *o, const at::Tensor &with) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, "dev_status");
     TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.is_cuda() && t.numel() > 0,
                       "dev_status must be an int32 CUDA tensor");
+    together(t, with, "dev_status");
     return reinterpret_cast<uint32_t *>(t.data_ptr<int>());
-}
-
-const at::Tensor &scratch(PyObject *o) {
-    const at::Tensor &t = tensor(o, "workspace");
-    TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous(), "workspace must be a contiguous CUDA tensor");
-    return t;
 }
 
 long long integer(PyObject *o, const char *name) {
@@ -54,8 +57,9 @@ int small(PyObject *o, const char *name) {
     return (int)x;
 }
 
-// An int32 CUDA tensor, contiguous, of this shape (-1: any extent).
-const at::Tensor &ints(PyObject *o, const char *name, int64_t n0, int64_t n1 = -2) {
+// An int32 CUDA tensor, contiguous, of this shape (-1: any extent), on the device of `with`
+// if that is given.
+const at::Tensor &ints(PyObject *o, const char *name, const at::Tensor *with, int64_t n0, int64_t n1 = -2) {
     const at::Tensor &t = tensor(o, name);
     const int dims = n1 == -2 ? 1 : 2;
     bool ok = t.scalar_type() == at::kInt && t.is_cuda() && t.is_contiguous() && t.dim() == dims;
@@ -65,6 +69,7 @@ const at::Tensor &ints(PyObject *o, const char *name, int64_t n0, int64_t n1 = -
         TORCH_CHECK_VALUE(false, name, " must be a contiguous int32 CUDA tensor [", extent(n0),
                           dims == 2 ? ", " + extent(n1) : std::string(), "]");
     }
+    if (with) together(t, *with, name);
     return t;
 }
 
@@ -90,6 +95,7 @@ spec_pages_t pool(PyObject *ko, PyObject *vo, bool layered) {
     default: TORCH_CHECK_TYPE(false, "a cache is bfloat16, float16 or float32");
     }
     TORCH_CHECK_VALUE(k.is_cuda() && v.is_cuda(), "k and v must be CUDA tensors");
+    together(v, k, "v");
     bool same = k.stride(-1) == 1 && v.stride(-1) == 1;
     for (int i = 0; i < 3 + d; ++i) same = same && stride(k, i) == stride(v, i);
     TORCH_CHECK_VALUE(same, "k and v need the same strides and a contiguous head_dim");
@@ -116,10 +122,26 @@ const at::Tensor &rows(PyObject *o, const char *name, const at::Tensor &k, int64
                           t.size(0) <= INT_MAX && t.size(1) <= INT_MAX && t.size(2) <= INT_MAX,
                       name, " must be a CUDA tensor [B, N, ", heads < 0 ? std::string("heads") : std::to_string(heads),
                       ", ", k.size(-1), "] of the cache's dtype, its last dimension contiguous");
+    together(t, k, name);
     return t;
 }
 
-void *handle(PyObject *o) { return reinterpret_cast<void *>((intptr_t)integer(o, "stream")); }
+// The stream given, or torch's current one.
+void *handle(PyObject *o, const at::Tensor &with) {
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(with.device().index()).stream();
+    return reinterpret_cast<void *>((intptr_t)integer(o, "stream"));
+}
+
+// Scratch that one stream's calls share: they never overlap.  (A captured graph keeps
+// the scratch of the stream it was captured on: it is replayed on that stream, or its
+// calls are given a workspace of their own.)
+const at::Tensor &scratch(const at::Tensor &with, void *stream, size_t bytes) {
+    static auto *all = new std::map<std::pair<int, void *>, at::Tensor>;  // outlives the CUDA context
+    at::Tensor &t = (*all)[{with.device().index(), stream}];
+    if (!t.defined() || t.nbytes() < bytes)
+        t = at::empty({(int64_t)std::max<size_t>(bytes, 256)}, with.options().dtype(at::kByte));
+    return t;
+}
 
 PyObject *done(spec_status_t st) {
     if (st == SPEC_OK) Py_RETURN_NONE;
@@ -137,33 +159,36 @@ void count(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "expecte
 PyObject *resize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     count(n, 8);
-    const at::Tensor &table = ints(a[0], "page_table", -1, -1);
+    const at::Tensor &table = ints(a[0], "page_table", nullptr, -1, -1);
     const int64_t B = table.size(0);
-    const at::Tensor &held = ints(a[1], "page_count", B), &ref = ints(a[2], "page_ref", -1),
-                     &want = ints(a[3], "want_len", B);
+    const at::Tensor &held = ints(a[1], "page_count", &table, B), &ref = ints(a[2], "page_ref", &table, -1),
+                     &want = ints(a[3], "want_len", &table, B);
     const c10::DeviceGuard guard(table.device());
     return done(spec_cache_resize(table.data_ptr<int>(), held.data_ptr<int>(), ref.data_ptr<int>(),
                                   want.data_ptr<int>(), small(a[5], "extra"), small(a[4], "page_size"), (int)B,
-                                  (int)table.size(1), (int)ref.size(0), status(a[6]),
-                                  handle(a[7])));
+                                  (int)table.size(1), (int)ref.size(0), status(a[6], table),
+                                  handle(a[7], table)));
     END_HANDLE_TH_ERRORS
 }
 
-// (k, v, page_table, page_count, page_ref, cache_len, src, dst, workspace, dev_status, stream)
+// (k, v, page_table, page_count, page_ref, cache_len, src, dst, dev_status, stream)
 PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    count(n, 11);
+    count(n, 10);
     const spec_pages_t p = pool(a[0], a[1], true);
-    const at::Tensor &table = ints(a[2], "page_table", -1, -1);
+    const at::Tensor &k = tensor(a[0], "k");
+    const at::Tensor &table = ints(a[2], "page_table", &k, -1, -1);
     const int64_t S = table.size(0);
-    const at::Tensor &held = ints(a[3], "page_count", S), &ref = ints(a[4], "page_ref", p.num_pages),
-                     &len = ints(a[5], "cache_len", S), &src = ints(a[6], "src", -1),
-                     &dst = ints(a[7], "dst", src.size(0)), &ws = scratch(a[8]);
+    const at::Tensor &held = ints(a[3], "page_count", &k, S), &ref = ints(a[4], "page_ref", &k, p.num_pages),
+                     &len = ints(a[5], "cache_len", &k, S), &src = ints(a[6], "src", &k, -1),
+                     &dst = ints(a[7], "dst", &k, src.size(0));
     const c10::DeviceGuard guard(table.device());
+    void *stream = handle(a[9], k);
+    const at::Tensor &ws = scratch(k, stream, spec_cache_fork_workspace_bytes((int)src.size(0)));
     return done(spec_cache_fork(&p, table.data_ptr<int>(), held.data_ptr<int>(), ref.data_ptr<int>(),
                                 len.data_ptr<int>(), src.data_ptr<int>(), dst.data_ptr<int>(), (int)src.size(0),
                                 (int)S, (int)table.size(1), ws.data_ptr(), (size_t)ws.nbytes(),
-                                status(a[9]), handle(a[10])));
+                                status(a[8], k), stream));
     END_HANDLE_TH_ERRORS
 }
 
@@ -172,10 +197,11 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     count(n, 6);
     const spec_pages_t p = pool(a[0], a[1], true);
-    const at::Tensor &src = ints(a[2], "src_pages", -1), &dst = ints(a[3], "dst_pages", src.size(0));
+    const at::Tensor &k = tensor(a[0], "k");
+    const at::Tensor &src = ints(a[2], "src_pages", &k, -1), &dst = ints(a[3], "dst_pages", &k, src.size(0));
     const c10::DeviceGuard guard(src.device());
     return done(spec_cache_copy(&p, src.data_ptr<int>(), dst.data_ptr<int>(), (int)src.size(0),
-                                status(a[4]), handle(a[5])));
+                                status(a[4], k), handle(a[5], k)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -190,12 +216,12 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     for (int i = 0; i < 3; ++i) same = same && stride(kn, i) == stride(vn, i);
     TORCH_CHECK_VALUE(same, "k_new and v_new need the same shape and strides");
     const int64_t B = kn.size(0);
-    const at::Tensor &table = ints(a[2], "page_table", B, -1), &len = ints(a[3], "cache_len", B);
-    const int *cnt = a[6] == Py_None ? nullptr : ints(a[6], "count", B).data_ptr<int>();
+    const at::Tensor &table = ints(a[2], "page_table", &k, B, -1), &len = ints(a[3], "cache_len", &k, B);
+    const int *cnt = a[6] == Py_None ? nullptr : ints(a[6], "count", &k, B).data_ptr<int>();
     const c10::DeviceGuard guard(table.device());
     return done(spec_cache_append(&p, table.data_ptr<int>(), len.data_ptr<int>(), kn.data_ptr(), vn.data_ptr(),
                                   stride(kn, 0), stride(kn, 1), stride(kn, 2), cnt, (int)B, (int)kn.size(1),
-                                  (int)table.size(1), status(a[7]), handle(a[8])));
+                                  (int)table.size(1), status(a[7], k), handle(a[8], k)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -204,24 +230,25 @@ PyObject *commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     ::count(n, 10);
     const spec_pages_t p = pool(a[0], a[1], true);
-    const at::Tensor &table = ints(a[2], "page_table", -1, -1);
+    const at::Tensor &k = tensor(a[0], "k");
+    const at::Tensor &table = ints(a[2], "page_table", &k, -1, -1);
     const int64_t B = table.size(0);
-    const at::Tensor &len = ints(a[3], "cache_len", B);
+    const at::Tensor &len = ints(a[3], "cache_len", &k, B);
     const int *out = nullptr;
     int N;
     if (a[4] != Py_None) {
-        const at::Tensor &t = ints(a[4], "out_nodes", B, -1);
+        const at::Tensor &t = ints(a[4], "out_nodes", &k, B, -1);
         out = t.data_ptr<int>();
         N = (int)t.size(1);
     } else {
         TORCH_CHECK_VALUE(a[7] != Py_None, "linear drafts need their number of nodes");
         N = small(a[7], "nodes");
     }
-    const at::Tensor &acc = ints(a[5], "accept_len", B), &fresh = ints(a[6], "new_len", B);
+    const at::Tensor &acc = ints(a[5], "accept_len", &k, B), &fresh = ints(a[6], "new_len", &k, B);
     const c10::DeviceGuard guard(table.device());
     return done(spec_cache_commit(&p, table.data_ptr<int>(), len.data_ptr<int>(), out, acc.data_ptr<int>(),
                                   fresh.data_ptr<int>(), (int)B, N, (int)table.size(1),
-                                  status(a[8]), handle(a[9])));
+                                  status(a[8], k), handle(a[9], k)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -231,11 +258,11 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     count(n, 15);
     const spec_pages_t p = pool(a[1], a[2], false);
-    const at::Tensor &q = rows(a[0], "q", tensor(a[1], "k"), -1);
+    const at::Tensor &k = tensor(a[1], "k"), &q = rows(a[0], "q", k, -1);
     const int64_t B = q.size(0), N = q.size(1), Hq = q.size(2), D = q.size(3);
-    const at::Tensor &table = ints(a[3], "page_table", B, -1), &len = ints(a[4], "cache_len", B);
-    const int *parent = a[5] == Py_None ? nullptr : ints(a[5], "parent", B, N).data_ptr<int>();
-    const int *nodes = a[6] == Py_None ? nullptr : ints(a[6], "node_count", B).data_ptr<int>();
+    const at::Tensor &table = ints(a[3], "page_table", &k, B, -1), &len = ints(a[4], "cache_len", &k, B);
+    const int *parent = a[5] == Py_None ? nullptr : ints(a[5], "parent", &k, B, N).data_ptr<int>();
+    const int *nodes = a[6] == Py_None ? nullptr : ints(a[6], "node_count", &k, B).data_ptr<int>();
     double scale = 1.0 / std::sqrt((double)D);
     if (a[7] != Py_None) {
         scale = PyFloat_AsDouble(a[7]);
@@ -246,20 +273,28 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (a[10] != Py_None) {
         out = tensor(a[10], "out");
         TORCH_CHECK_VALUE(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type() && out.is_cuda() &&
-                              out.is_contiguous(),
+                              out.is_contiguous() && out.device() == q.device(),
                           "out must be a contiguous CUDA tensor of q's shape and dtype");
     } else {
         out = at::empty(q.sizes(), q.options());
     }
     const bool with_lse = PyObject_IsTrue(a[11]) == 1;
     if (with_lse) lse = at::empty({B, N, Hq}, q.options().dtype(at::kFloat));
-    const at::Tensor &ws = scratch(a[12]);
     const c10::DeviceGuard guard(q.device());
+    void *stream = handle(a[14], k);
+    const at::Tensor *ws;
+    if (a[12] != Py_None) {
+        ws = &tensor(a[12], "workspace");
+        TORCH_CHECK_VALUE(ws->is_cuda() && ws->is_contiguous(), "workspace must be a contiguous CUDA tensor");
+        together(*ws, k, "workspace");
+    } else {
+        ws = &scratch(k, stream, spec_tree_attention_workspace_bytes((int)B, (int)N, (int)Hq, p.heads, (int)D));
+    }
     const spec_status_t st = spec_tree_attention(
         q.data_ptr(), stride(q, 0), stride(q, 1), stride(q, 2), &p, table.data_ptr<int>(), len.data_ptr<int>(),
         parent, nodes, (int)B, (int)N, (int)Hq, (int)table.size(1), (float)scale, window, sinks, out.data_ptr(),
-        with_lse ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.nbytes(),
-        status(a[13]), handle(a[14]));
+        with_lse ? lse.data_ptr<float>() : nullptr, ws->data_ptr(), (size_t)ws->nbytes(),
+        status(a[13], k), stream);
     if (st != SPEC_OK) return done(st);
     PyObject *o = THPVariable_Wrap(out);
     if (!with_lse || !o) return o;

@@ -69,7 +69,8 @@ template <> struct PagesItem<true> {
 // dependent loads, one cluster barrier (two where pages are taken), and a scan
 // of the counts split over the cluster's 256 warps.  8 CTAs of one cluster
 // instead of one CTA: 2^16 pages are one load round per warp; instead of a
-// whole grid: no launch between the phases.
+// whole grid: no launch between the phases.  Two resizes and an append of 72
+// tokens: 9.9 us (12.3 with three barriers each and the counts read again).
 template <bool FORK>
 __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) sv_pages(PagesArgs A) {
     constexpr int kWarps = kPgCtas * kPgWarps;
@@ -301,6 +302,8 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 // them.  Grid (pairs, layers, token blocks), block (vector columns, tokens).
 // Bound by HBM: each vector is read once and written once; eight loads, four of
 // keys and four of values, are in flight per thread before the first store.
+// 64 forks, 24 layers: 30.3 us for the call, 6.5 TB/s (four forks share a
+// source, whose reads hit L2); blocks of keys or values alone took 35.2.
 __global__ void __launch_bounds__(256) sv_copy_pages(Pool P, const int *src, const int *dst,
                                                      const int *copies, uint32_t *status) {
     pdl_trigger();
@@ -343,7 +346,9 @@ __global__ void __launch_bounds__(256) sv_copy_pages(Pool P, const int *src, con
 }
 
 // New keys and values into the pages.  Grid (token blocks, requests), block
-// (vector columns, tokens).
+// (vector columns, tokens), a token per thread row: the grid's many small
+// blocks keep enough loads in flight.  Bound by HBM: 16 requests of 2047 tokens,
+// 268 MB, 38 us; a few tokens are bound by latency (two dependent loads).
 __global__ void __launch_bounds__(256) sv_append(Pool P, const int *table,
                                                  const int *len,
                                                  const uint4 *k_new,
@@ -439,7 +444,8 @@ __device__ __forceinline__ int commit_path(const Pool &P, const int *table, cons
 // its place (out_nodes[i] >= i + 1), so a later node is never overwritten by an
 // earlier move: all loads of a batch of moves, a barrier, then its stores.
 // Nodes already in place are not touched.  Bound by latency at small batches
-// (a chain of four dependent loads), by HBM at large ones.
+// (a chain of four dependent loads; 2.8 us at 4 requests of 8 nodes), by HBM at
+// large ones (128 requests of 64 nodes, 36 layers: 34.5 us, 6.7 TB/s).
 constexpr int kMoveUnroll = 4;
 __global__ void __launch_bounds__(256) sv_commit(Pool P, const int *table, const int *len,
                                                  const int *nodes,

@@ -26,6 +26,21 @@
 // rows each of the same key tile (kTaSplitRows), so a row tile is 256 rows for
 // one read of K and V.  Either way one stream's exponentials run while the
 // tensor cores work for the other.
+//
+// What bounds it, with device times of a call, join included, on a GPU that copies
+// 6.7 TB/s and multiplies bfloat16 matrices at 1937 TFLOP/s (32 query and 8 key heads of
+// 128 unless said otherwise):
+//   1 request of 131071 tokens, 16 nodes        94 us   5.7 TB/s    HBM, and a join of 20 parts
+//   32 requests of up to 4096 tokens, 9 nodes   73 us   5.6 TB/s    HBM
+//   64 requests, 64 nodes each (256 rows)      195 us   4.6 TB/s, 1080 TFLOP/s: a stream's chain of
+//                scores, two halves of weights and values; the tensor cores are 49% busy
+//   512 requests, 9 nodes, window of 128       99 us   2.2 TB/s    64 query heads of 64: short segments,
+//                so the softmax warps' latency, half of it in masks, clearing and output
+//   1 request of 1000 tokens, 1 node            11 us   latency: lengths, pages, a tile, the join
+// K, V and P go through 128-key tiles because a product of 64 columns takes 48 cycles where
+// one of 128 takes 64; P lies in the tensor memory, over its scores, since it would
+// otherwise be written to and read from shared memory, the port of which bounds a row
+// tile of 256 rows at about 2050 cycles per key tile.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
