@@ -900,7 +900,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                                                            __uint_as_float(x[i + 2 * e + 1])));
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
-                        if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kTaGrow))) {
+                        // (rows past the last one hold whatever the shared memory held: no vote)
+                        if (__any_sync(0xFFFFFFFFu, valid && top > m + (kLift + kTaGrow))) {
                             const float m_new = top > m + kLift ? top - kLift : m;
                             const float f = m_new == -INFINITY ? 1.f : ex2(m - m_new);
                             m = m_new;

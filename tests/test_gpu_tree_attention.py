@@ -311,6 +311,20 @@ def test_same_inputs_same_bits_on_any_stream():
         assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
+@pytest.mark.parametrize("N,hq,hkv,D", [(1, 5, 1, 8), (1, 4, 4, 128), (3, 14, 2, 64), (9, 24, 4, 128), (33, 20, 4, 64)])
+def test_same_bits_whatever_ran_before(N, hq, hkv, D):
+    """What earlier calls left in shared and tensor memory, under rows that the next call does not have, is not seen."""
+    lens = [(i * 613) % 4001 for i in range(100)]
+    c = _case(31 + N, lens, N, hq, hkv, D, 256, torch.bfloat16, qscale=0.3)
+    others = [_case(32 + i, [700, 90], 64, 8, 2, 64 + 64 * (i % 2), 16, dt, qscale=30.0)
+              for i, dt in enumerate((torch.bfloat16, torch.float16))]
+    o, l, _ = _run(c)
+    for i in range(12):
+        _run(others[i % 2])
+        o2, l2, _ = _run(c)
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
 def test_captured_in_a_graph():
     """One captured call follows the lengths and the data of later replays."""
     c = _case(9, [600, 30], 7, 8, 2, 64, 16, torch.bfloat16)
