@@ -27,7 +27,6 @@ from . import _build
 
 DEV_BAD_PAGE, DEV_NO_PAGES, DEV_BAD_SLOT = 16, 32, 64
 DTYPE_F16 = 2
-MAX_SLOTS, MAX_TREE, MAX_HEAD_DIM = 8192, 64, 128
 
 
 def declare(L):
