@@ -1270,11 +1270,13 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
 
     // A key head per stream once there is one for every CTA: the streams then share
     // nothing but the CTA, where streams that divide the keys meet at the end of
-    // every (request, head).  9 nodes, us, by heads / by keys, 8 key heads:
-    //   head_dim 128, 4096 tokens: B = 32 77 / 84, 256 670 / 758; window 1024: 32 39 / 45, 256 196 / 246
-    //   head_dim 64, window 128:   B = 24 15.6 / 18.9, 64 21.8 / 27.8, 512 108 / 142
+    // every (request, head), which costs most where those are short.  us, by heads /
+    // by keys, 8 key heads:
+    //   head_dim 64, window 128, 9 nodes:  B = 24 13.8 / 16.3, 64 19.5 / 24.4, 512 87 / 120
+    //   head_dim 128, 500 tokens, 1 node:  B = 32 17.5 / 21.9;  window 1024, 9 nodes: 256 191 / 197
+    //   head_dim 128, 4096 tokens, 9 nodes: B = 32 98 / 98, 256 666 / 671
     // With fewer heads a unit of twice the work is cut more coarsely:
-    //   500 tokens, one node, head_dim 128: B = 16 16.5 / 13.3, 1 11.8 / 11.1; 20000 tokens: B = 1 33 / 30
+    //   head_dim 128, 500 tokens, 1 node:  B = 16 14.0 / 13.0, 1 10.9 / 10.2; 20000 tokens: B = 1 28 / 26
     const bool pairs = H % 2 == 0 && (long long)B * H >= ctas;
     const sv::TaRows r = sv::ta_rows(N, Hq / H, pairs);
     const sv::TaLayout L = sv::ta_layout(N, Hq, H, D);
