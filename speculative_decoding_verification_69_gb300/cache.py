@@ -16,7 +16,9 @@ of pages are [num_pages, page_size, kv_heads, head_dim] (one layer) or [layers,
 num_pages, ...] tensors of any strides that leave head_dim contiguous; a pool
 stored heads first is passed as its transpose.  As everywhere in this package
 every step runs in the library's kernels, on torch's current stream or the
-`stream` given, and nothing falls back to torch.
+`stream` given, and nothing falls back to torch.  The calls can be captured in a
+CUDA graph: a call without a `workspace` (a uint8 tensor, 256-byte aligned) takes
+one from torch's allocator, in a capture from the graph's own memory.
 """
 import ctypes
 import importlib.util
@@ -82,16 +84,17 @@ def cache_resize(page_table, page_count, page_ref, want_len, page_size, *, extra
                      _handle(stream))
 
 
-def cache_fork(k, v, page_table, page_count, page_ref, cache_len, src, dst, *, dev_status=None, stream=None):
+def cache_fork(k, v, page_table, page_count, page_ref, cache_len, src, dst, *, workspace=None, dev_status=None,
+               stream=None):
     """Slots dst (int32 [F]) continued from slots src (spec_cache_fork): full
     pages shared, the last partial page copied in every layer.  k, v [layers,
     num_pages, page_size, kv_heads, head_dim]; page_table, page_count, page_ref
     and cache_len are updated."""
-    args = (k, v, page_table, page_count, page_ref, cache_len, src, dst, dev_status, None)
+    args = (k, v, page_table, page_count, page_ref, cache_len, src, dst, workspace, dev_status, None)
     if stream is None:
         _native().fork(*args)
     else:
-        with torch.cuda.stream(stream):  # its scratch belongs to that stream
+        with torch.cuda.stream(stream):  # a workspace of the call's own belongs to that stream
             _native().fork(*args)
 
 
@@ -182,6 +185,6 @@ class PagedCache:
         cache_commit(self.k, self.v, self.page_table, self.cache_len, out_nodes, accept_len, nodes=nodes,
                      dev_status=self.status, stream=stream)
 
-    def fork(self, src, dst, stream=None):
+    def fork(self, src, dst, workspace=None, stream=None):
         cache_fork(self.k, self.v, self.page_table, self.page_count, self.page_ref, self.cache_len, src, dst,
-                   dev_status=self.status, stream=stream)
+                   workspace=workspace, dev_status=self.status, stream=stream)

@@ -16,9 +16,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <map>
 #include <string>
-#include <utility>
 
 #include "spec_cache.h"
 
@@ -132,14 +130,13 @@ void *handle(PyObject *o, const at::Tensor &with) {
     return reinterpret_cast<void *>((intptr_t)integer(o, "stream"));
 }
 
-// Scratch that one stream's calls share: they never overlap.  (A captured graph keeps
-// the scratch of the stream it was captured on: it is replayed on that stream, or its
-// calls are given a workspace of their own.)
-const at::Tensor &scratch(const at::Tensor &with, void *stream, size_t bytes) {
-    static auto *all = new std::map<std::pair<int, void *>, at::Tensor>;  // outlives the CUDA context
-    at::Tensor &t = (*all)[{with.device().index(), stream}];
-    if (!t.defined() || t.nbytes() < bytes)
-        t = at::empty({(int64_t)std::max<size_t>(bytes, 256)}, with.options().dtype(at::kByte));
+// The workspace given, or one of this call's own from torch's allocator, on the current
+// stream: reused in that stream's order, and in a captured graph part of the graph's memory.
+at::Tensor workspace(PyObject *o, const at::Tensor &with, size_t bytes) {
+    if (o == Py_None) return at::empty({(int64_t)std::max<size_t>(bytes, 256)}, with.options().dtype(at::kByte));
+    const at::Tensor &t = tensor(o, "workspace");
+    TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous(), "workspace must be a contiguous CUDA tensor");
+    together(t, with, "workspace");
     return t;
 }
 
@@ -171,10 +168,10 @@ PyObject *resize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (k, v, page_table, page_count, page_ref, cache_len, src, dst, dev_status, stream)
+// (k, v, page_table, page_count, page_ref, cache_len, src, dst, workspace, dev_status, stream)
 PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    count(n, 10);
+    count(n, 11);
     const spec_pages_t p = pool(a[0], a[1], true);
     const at::Tensor &k = tensor(a[0], "k");
     const at::Tensor &table = ints(a[2], "page_table", &k, -1, -1);
@@ -183,12 +180,11 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
                      &len = ints(a[5], "cache_len", &k, S), &src = ints(a[6], "src", &k, -1),
                      &dst = ints(a[7], "dst", &k, src.size(0));
     const c10::DeviceGuard guard(table.device());
-    void *stream = handle(a[9], k);
-    const at::Tensor &ws = scratch(k, stream, spec_cache_fork_workspace_bytes((int)src.size(0)));
+    const at::Tensor ws = workspace(a[8], k, spec_cache_fork_workspace_bytes((int)std::min<int64_t>(src.size(0), INT_MAX)));
     return done(spec_cache_fork(&p, table.data_ptr<int>(), held.data_ptr<int>(), ref.data_ptr<int>(),
                                 len.data_ptr<int>(), src.data_ptr<int>(), dst.data_ptr<int>(), (int)src.size(0),
                                 (int)S, (int)table.size(1), ws.data_ptr(), (size_t)ws.nbytes(),
-                                status(a[8], k), stream));
+                                status(a[9], k), handle(a[10], k)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -281,20 +277,13 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const bool with_lse = PyObject_IsTrue(a[11]) == 1;
     if (with_lse) lse = at::empty({B, N, Hq}, q.options().dtype(at::kFloat));
     const c10::DeviceGuard guard(q.device());
-    void *stream = handle(a[14], k);
-    const at::Tensor *ws;
-    if (a[12] != Py_None) {
-        ws = &tensor(a[12], "workspace");
-        TORCH_CHECK_VALUE(ws->is_cuda() && ws->is_contiguous(), "workspace must be a contiguous CUDA tensor");
-        together(*ws, k, "workspace");
-    } else {
-        ws = &scratch(k, stream, spec_tree_attention_workspace_bytes((int)B, (int)N, (int)Hq, p.heads, (int)D));
-    }
+    const at::Tensor ws =
+        workspace(a[12], k, spec_tree_attention_workspace_bytes((int)B, (int)N, (int)Hq, p.heads, (int)D));
     const spec_status_t st = spec_tree_attention(
         q.data_ptr(), stride(q, 0), stride(q, 1), stride(q, 2), &p, table.data_ptr<int>(), len.data_ptr<int>(),
         parent, nodes, (int)B, (int)N, (int)Hq, (int)table.size(1), (float)scale, window, sinks, out.data_ptr(),
-        with_lse ? lse.data_ptr<float>() : nullptr, ws->data_ptr(), (size_t)ws->nbytes(),
-        status(a[13], k), stream);
+        with_lse ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.nbytes(),
+        status(a[13], k), handle(a[14], k));
     if (st != SPEC_OK) return done(st);
     PyObject *o = THPVariable_Wrap(out);
     if (!with_lse || !o) return o;
