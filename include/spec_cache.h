@@ -144,9 +144,14 @@ spec_status_t spec_cache_append(const spec_pages_t *pages, const int32_t *page_t
  *              them.  out_nodes NULL: linear drafts, whose accepted tokens
  *              are in place already: only the lengths change.
  *   new_len    [B] int32: cache_len itself, or a buffer apart from it.
- * accept_len is clamped to [0, N - 1].  A path with out_nodes[b, i] outside
- * [i + 1, N), or that leaves the slot's pages, is cut there
- * (SPEC_DEV_BAD_TREE / SPEC_DEV_BAD_PAGE), the length too.
+ * accept_len is clamped to [0, N - 1].  A path is cut, the length too, at the
+ * first place without a page (SPEC_DEV_BAD_PAGE) and at an out_nodes[b, i]
+ * outside [i + 1, N) (SPEC_DEV_BAD_TREE); where the root's place has no page, or
+ * cache_len[b] < 0 (SPEC_DEV_BAD_LEN), the length stays as it is.  So a slot
+ * that got no pages for its step does not come to count tokens that were never
+ * written.  Linear drafts past the end of the table's row, for which no page
+ * can ever stand, are counted and reported (SPEC_DEV_BAD_LEN), as every later
+ * call on such a length reports them.
  * 1 <= N <= SPEC_MAX_TREE, 1 <= B < 2^16.  One launch, two when new_len is
  * cache_len.
  */

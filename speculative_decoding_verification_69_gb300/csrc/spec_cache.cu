@@ -389,55 +389,66 @@ __global__ void __launch_bounds__(256) sv_append(Pool P, const int *table,
     }
 }
 
-// The path of one request as vector offsets inside a layer: s_src / s_dst [N],
-// returns its length after the checks.  Called by a whole CTA; warp 0 works.
+// The accepted path of one request: place 0 is the root's, place 1 + i that of node i.
+// Returns how many nodes after the root are kept, those before the first place without a
+// page (nodes: or the first that is no path), and -1 when the root has none: the length
+// grows by one more.  s_src / s_dst [N]: the nodes' vector offsets inside a layer, before
+// and after.  Called by a whole CTA; warp 0 works.
 __device__ __forceinline__ int commit_path(const Pool &P, const int *table, const int *len,
                                            const int *nodes, const int *accept, int b, int N,
                                            int max_pages, long long *s_src, long long *s_dst,
                                            int *s_n, uint32_t *status, bool report) {
     const int lane = threadIdx.y * blockDim.x + threadIdx.x;
     if (lane < 32) {
-        const int want = accept[b];
-        int a = max(0, min(want, N - 1));
+        const int a = max(0, min(accept[b], N - 1));
         const long long n0 = len[b];
+        const int *row = table + (long long)b * max_pages;
         uint32_t bits = 0;
-        int good = a;
-        if (nodes) {
-            if (n0 < 0) {
-                good = 0;
-                bits |= SPEC_DEV_BAD_LEN;
-            }
-            for (int i0 = 0; i0 < a; i0 += 32) {
-                const int i = i0 + lane;
-                bool bad = false;
-                if (i < a && n0 >= 0) {
-                    const int n = nodes[(long long)b * N + i];
-                    if (n < i + 1 || n >= N) {
+        int places = 0;  // the root's and the nodes' that are kept
+        auto offset = [&](long long pos, long long &off) -> bool {  // whether the position has a page
+            const long long place = pos >> P.page_shift;
+            const int p = place < max_pages ? row[place] : -1;
+            off = (long long)p * P.page_st + (pos & (P.page - 1)) * P.token;
+            return (unsigned)p < (unsigned)P.num_pages;
+        };
+        if (n0 < 0) bits = SPEC_DEV_BAD_LEN;
+        else places = a + 1;
+        for (int i0 = 0; i0 < places; i0 += 32) {
+            const int i = i0 + lane;
+            bool bad = false;
+            if (i < places) {
+                long long src, dst;
+                if (!nodes && (n0 + i) >> P.page_shift >= max_pages) {
+                    bits |= SPEC_DEV_BAD_LEN;  // counted: no page will ever stand for it
+                } else if (!offset(n0 + i, dst)) {
+                    bad = true;
+                    bits |= SPEC_DEV_BAD_PAGE;
+                } else if (nodes && i > 0) {
+                    const int n = nodes[(long long)b * N + i - 1];
+                    if (n < i || n >= N) {
                         bad = true;
                         bits |= SPEC_DEV_BAD_TREE;
+                    } else if (!offset(n0 + n, src)) {
+                        bad = true;
+                        bits |= SPEC_DEV_BAD_PAGE;
                     } else {
-                        const long long s = n0 + n, d = n0 + 1 + i;
-                        const long long sp = s >> P.page_shift, dp = d >> P.page_shift;
-                        const int pp = sp < max_pages ? table[(long long)b * max_pages + sp] : -1;
-                        const int qq = dp < max_pages ? table[(long long)b * max_pages + dp] : -1;
-                        if ((unsigned)pp >= (unsigned)P.num_pages || (unsigned)qq >= (unsigned)P.num_pages) {
-                            bad = true;
-                            bits |= SPEC_DEV_BAD_PAGE;
-                        } else {
-                            s_src[i] = (long long)pp * P.page_st + (s & (P.page - 1)) * P.token;
-                            s_dst[i] = (long long)qq * P.page_st + (d & (P.page - 1)) * P.token;
-                        }
+                        s_src[i - 1] = src;
+                        s_dst[i - 1] = dst;
                     }
                 }
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, bad);
-                if (mask) good = min(good, i0 + __ffs(mask) - 1);
             }
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, bad);
+            if (mask) places = i0 + __ffs(mask) - 1;
         }
         if (report && bits) flag(status, bits);
-        if (lane == 0) *s_n = good;
+        if (lane == 0) *s_n = places - 1;
     }
     __syncthreads();
     return *s_n;
+}
+// The length after the root and `kept` nodes (linear drafts may leave 32 bits).
+__device__ __forceinline__ int commit_len(int len, int kept) {
+    return (int)min((long long)len + 1 + kept, (long long)INT_MAX);
 }
 
 // Accepted nodes moved behind their root.  Grid (requests, layers x {k, v}),
@@ -460,7 +471,7 @@ __global__ void __launch_bounds__(256) sv_commit(Pool P, const int *table, const
     const bool first = blockIdx.y == 0;
     const int a = commit_path(P, table, len, nodes, accept, b, N, max_pages, s_src, s_dst, &s_n,
                               status, first);
-    if (first && new_len && threadIdx.x == 0 && threadIdx.y == 0) new_len[b] = len[b] + 1 + a;
+    if (first && new_len && threadIdx.x == 0 && threadIdx.y == 0) new_len[b] = commit_len(len[b], a);
     if (!nodes) return;
     uint4 *pool = ((blockIdx.y & 1) ? P.v : P.k) + (long long)(blockIdx.y >> 1) * P.layer;
     for (int c0 = 0; c0 < P.cols; c0 += blockDim.x) {
@@ -485,18 +496,18 @@ __global__ void __launch_bounds__(256) sv_commit(Pool P, const int *table, const
 }
 
 // The lengths of spec_cache_commit where they are updated in place: after
-// every mover has read the old ones.
+// every mover has read the old ones (and reported what it found).
 __global__ void __launch_bounds__(64) sv_commit_len(Pool P, const int *table, int *len,
-                                                    const int *nodes,
-                                                    const int *accept, int N, int max_pages) {
+                                                    const int *nodes, const int *accept, int N,
+                                                    int max_pages, uint32_t *status) {
     __shared__ long long s_src[SPEC_MAX_TREE], s_dst[SPEC_MAX_TREE];
     __shared__ int s_n;
     pdl_trigger();
     pdl_wait();
     const int b = blockIdx.x;
     const int a = commit_path(P, table, len, nodes, accept, b, N, max_pages, s_src, s_dst, &s_n,
-                              nullptr, false);
-    if (threadIdx.x == 0) len[b] += 1 + a;
+                              status, !nodes);
+    if (threadIdx.x == 0) len[b] = commit_len(len[b], a);
 }
 
 // ------------------------------------------------------------------ host
@@ -683,7 +694,7 @@ spec_status_t spec_cache_commit(const spec_pages_t *pages, const int32_t *page_t
         if (r != SPEC_OK || !in_place) return r;
     }
     return sv::launch_pdl(sv::sv_commit_len, dim3((unsigned)B), dim3(64), 0, s, P, page_table, new_len,
-                          out_nodes, accept_len, N, max_pages);
+                          out_nodes, accept_len, N, max_pages, dev_status);
 }
 
 } // extern "C"

@@ -304,3 +304,85 @@ def test_pools_past_32_bit_offsets():
     assert torch.equal(k[0, a, 61:], kn[0, [3, 10, 19]]) and torch.equal(v[0, a, 61:], -kn[0, [3, 10, 19]])
     sv.cache_copy(k, v, _i32([a]), _i32([0]))
     assert torch.equal(k[:, 0], k[:, a]) and torch.equal(v[:, 0], v[:, a])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("linear", [False, True])
+def test_commit_stops_where_pages_end(linear, in_place):
+    """Neither a tree's path nor linear drafts are kept past the slot's pages, and a
+    root without a page leaves the length alone."""
+    sv = _sv()
+    k = torch.randn((2, 6, 8, 1, 8), device="cuda")
+    v = torch.randn_like(k)
+    ek, ev = k.clone(), v.clone()
+    table = _i32([[0, -1, -1], [-1, -1, -1], [1, -1, -1], [2, 6, -1], [3, -1, 4], [5, -1, -1]])
+    lens, acc = [6, 0, 8, 5, 7, 3], _i32([3, 2, 0, 3, 3, 1])
+    nodes = None if linear else _i32([[1, 2, 3, -1]] * 6)
+    new = None if in_place else torch.full((6,), -9, dtype=torch.int32, device="cuda")
+    st = _status()
+    got = sv.cache_commit(k, v, table, _i32(lens), nodes, acc, new_len=new, nodes=4, dev_status=st)
+    assert got.tolist() == [8, 0, 8, 8, 8, 5]
+    assert int(st) == sv.DEV_BAD_PAGE
+    assert torch.equal(k, ek) and torch.equal(v, ev)
+    st.zero_()
+    got = sv.cache_commit(k, v, table, _i32([-3, 2, 0, 0, 0, 0]), nodes, acc, new_len=new, nodes=4, dev_status=st)
+    assert got.tolist()[:2] == [-3, 2] and int(st) == sv.DEV_BAD_PAGE | sv.DEV_BAD_LEN
+
+
+def test_linear_drafts_past_the_row_are_reported():
+    sv = _sv()
+    k = torch.zeros((1, 4, 8, 1, 8), dtype=torch.bfloat16, device="cuda")
+    for new in (None, _i32([0, 0])):
+        st = _status()
+        got = sv.cache_commit(k, k, _i32([[0], [1]]), _i32([3, 2 ** 31 - 3]), None, _i32([4, 4]), nodes=5, new_len=new,
+                              dev_status=st)
+        assert got.tolist() == [8, 2 ** 31 - 1] and int(st) == sv.DEV_BAD_LEN
+        st.zero_()
+        got = sv.cache_commit(k, k, _i32([[0], [1]]), _i32([3, 6]), None, _i32([4, 4]), nodes=5, new_len=new,
+                              dev_status=st)
+        assert got.tolist() == [8, 11] and int(st) == sv.DEV_BAD_LEN
+
+
+@pytest.mark.parametrize("linear", [False, True])
+def test_a_slot_without_pages_for_its_step_loses_nothing(linear):
+    """While a third request holds the pages, one slot gets none for its step: its
+    length stays at what was written, and it goes on from there when there are some."""
+    sv = _sv()
+    c = sv.PagedCache(1, 6, 8, 1, 8, 3, 4, dtype=torch.bfloat16)
+    c.k.fill_(7.0)
+    c.v.fill_(7.0)
+    N = 6
+    kv = torch.randn((3, 8, 1, 8), device="cuda").bfloat16()
+
+    def resize(want):
+        sv.cache_resize(c.page_table, c.page_count, c.page_ref, _i32(want), 8, dev_status=c.status)
+
+    def append(n):
+        c.append(0, kv[:, :n], kv[:, :n], count=_i32([n, n, 0]))
+
+    def commit(nodes, accept):
+        c.commit(nodes, _i32(accept + [0]), nodes=N)
+        c.cache_len[2] = 0  # the third request does not take part
+
+    path = None if linear else _i32([[1, 2, 3, 4, 5, -1]] * 3)
+    resize([8, 8, 24])
+    append(8)
+    c.cache_len[:2] = 8
+    resize([14, 14, -1])
+    assert int(c.status) == sv.DEV_NO_PAGES and c.page_count.tolist() == [2, 1, 3]
+    c.status.zero_()
+    append(N)
+    commit(path, [5, 5])
+    assert int(c.status) == sv.DEV_BAD_PAGE and c.cache_len.tolist() == [14, 8, 0]
+    c.status.zero_()
+    c.trim()  # the third request is done
+    assert int(c.status) == 0 and c.page_count.tolist() == [2, 1, 0]
+    c.reserve(N)
+    append(N)
+    commit(path, [1, 5])
+    assert int(c.status) == 0 and c.cache_len.tolist() == [16, 14, 0]
+    for b, want in ((0, [kv[0], kv[0, :N], kv[0, :2]]), (1, [kv[1], kv[1, :N]])):
+        want = torch.cat(want)
+        at = torch.arange(len(want), device="cuda")
+        pages = c.page_table[b].long()[at // 8]
+        assert torch.equal(c.k[0, pages, at % 8], want) and torch.equal(c.v[0, pages, at % 8], want)
