@@ -38,9 +38,10 @@
 //                so the softmax warps' latency, half of it in masks, clearing and output
 //   1 request of 1000 tokens, 1 node            11 us   latency: lengths, pages, a tile, the join
 // K, V and P go through 128-key tiles because a product of 64 columns takes 48 cycles where
-// one of 128 takes 64; P lies in the tensor memory, over its scores, since it would
-// otherwise be written to and read from shared memory, the port of which bounds a row
-// tile of 256 rows at about 2050 cycles per key tile.
+// one of 128 takes 64; P lies in the tensor memory (head_dim above 64: over its scores, since
+// two accumulators leave no other columns), since it would otherwise be written to and read
+// from shared memory, the port of which bounds a row tile of 256 rows at about 2050 cycles
+// per key tile.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -86,6 +87,7 @@ struct TaArgs {
 };
 
 template <int DP, int MODE> struct TaCfg {
+    static constexpr bool kOwnP = DP <= 64;  // the weights have tensor-memory columns of their own
     static constexpr int kStreamQ = kTaRows * DP * 2;            // bytes of one stream's Q
     static constexpr int kQ = kStreamQ * (MODE == kTaSplitKeys ? 1 : 2);
     static constexpr int kStage = kTaKeys * DP * 2;              // one K or V tile
@@ -700,13 +702,25 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xFFFFFFFFu, ta_wait(bar, parity, abort, A.tries)) != 0;
         };
+        // The wait for a phase that ends within a product or two: looked at before it is
+        // slept on.
+        auto wait_soon = [&](uint64_t *bar, uint32_t parity) -> bool {
+#pragma unroll 1
+            for (int n = 0; n < 256; ++n)
+                if (mbar_test_wait(bar, parity)) return true;
+            return wait(bar, parity);
+        };
         // Scores of stream i against the next K tile; release: the tile's last use,
-        // last: the segment's.  They overwrite the columns of the stream's last
-        // weights: the products of a CTA's one issuing thread execute in the order of
-        // issue, so those have been consumed by then.
+        // last: the segment's.  Where they overwrite the columns of the stream's last weights
+        // (!kOwnP) the values formed from those have to be through: products of one thread
+        // are only sure to execute in the order of issue when they share accumulator and
+        // shape.  The wait costs 208 us instead of 196 at 64 requests of 64 nodes, 39.3
+        // instead of 38.2 at a window of 4096 and 16 nodes, 0 to 1% elsewhere; scores in two
+        // halves of 64 keys, each behind the values of its own columns, took 249 and 42.8.
         auto scores = [&](int i, bool release, bool last) -> bool {
             const uint32_t st = k_tile % kKS;
             if ((MODE != kTaSplitRows || i == 0) && !wait(&sh.k_full[st], (k_tile / kKS) & 1u)) return false;
+            if (!C::kOwnP && use[i] > 0 && !wait_soon(&sh.pv_done[i][1], (use[i] - 1) & 1u)) return false;
             tc_fence_after();
             const uint64_t qd = q_desc + (uint64_t)((MODE == kTaSplitKeys ? 0 : i) * (C::kStreamQ / 16));
             const uint64_t kd = k_desc + (uint64_t)(st * (C::kStage / 16));
@@ -732,7 +746,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (h == 0 && (MODE != kTaSplitRows || i == 0) && !wait(&sh.v_full[st], (v_tile / kVS) & 1u)) return false;
             tc_fence_after();
             const uint64_t vd = vt_desc + (uint64_t)(st * (C::kStage / 16) + h * (kTaKeys / 2 * 128 / 16));
-            const uint32_t p = tmem + (uint32_t)(i * kTaKeys + h * (kTaKeys / 2) + kTaKeys / 4);
+            const uint32_t p = tmem + (C::kOwnP ? 384u + (uint32_t)(i * (kTaKeys / 2) + h * (kTaKeys / 4))
+                                                : (uint32_t)(i * kTaKeys + h * (kTaKeys / 2) + kTaKeys / 4));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kTaKeys / 32; ++k)
@@ -818,7 +833,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     } else if (warp < 8) {  // ------------------------------------------- softmax
         const int stream = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);   // S; P over the second half of each half
+        const uint32_t ts = tmem + lanes + (uint32_t)(stream * kTaKeys);   // S
+        const uint32_t tp = C::kOwnP ? tmem + lanes + 384u + (uint32_t)(stream * (kTaKeys / 2))
+                                     : ts + kTaKeys / 4;                   // P, or over the second half of each half of S
+        constexpr int kPHalf = C::kOwnP ? kTaKeys / 4 : kTaKeys / 2;       // columns from P's first half to its second
         const uint32_t to = tmem + lanes + 256u + (uint32_t)(stream * DP);  // O
         const int rows_used = A.np * A.G, local = row / A.G;
         uint32_t base = 0;                     // the CTA's tiles before this segment
@@ -866,7 +884,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     clear = false;
                 };
                 // a tile's weights and values in two halves of 64 keys: one half's products
-                // run while the other half's weights are formed, and 64 scores fit the registers
+                // run while the other half's weights are formed, and 64 scores fit the registers.
+                // The weights overwrite those of the tile before, whose values are through: they
+                // were issued before these scores, whose commit covers all products before it
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const int jh = j0 + h * (kTaKeys / 2);
@@ -936,7 +956,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                                 sum[i & 1] = add2(sum[i & 1], e);
                                 p[i] = pack2<DT>(e.x, e.y);
                             }
-                            tmem_store(th + kTaKeys / 4 + 16 * q, p);
+                            tmem_store(tp + (uint32_t)(h * kPHalf + 16 * q), p);
                         }
                         l2 = add2(l2, add2(sum[0], sum[1]));
                         tmem_wait_store();

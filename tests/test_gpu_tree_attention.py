@@ -388,3 +388,22 @@ def test_refusals():
         call(k=x, v=x)
     with pytest.raises(sv.SpecVerifyError):
         call(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("N,hq,hkv,D", [(9, 8, 2, 128), (9, 8, 2, 64), (64, 8, 2, 128), (64, 16, 2, 64),
+                                        (5, 80, 80, 128), (5, 80, 80, 40)])
+def test_same_bits_beside_other_work(N, hq, hkv, D):
+    """Many tiles in every division of work between the streams, while products on another
+    stream take their turns: no tile's weights, scores or values meet those of another."""
+    lens = [2500, 900] if hkv > 2 else [20000, 300, 7000]
+    c = _case(N + hq + D, lens, N, hq, hkv, D, 64, torch.float16)
+    o, l = _check(c)
+    a = torch.randn((4096, 4096), device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            b = a @ a
+        o2, l2, st = _run(c)
+        assert st == 0 and torch.equal(o, o2) and torch.equal(l, l2)
+    del b
