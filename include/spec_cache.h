@@ -200,8 +200,9 @@ spec_status_t spec_cache_commit(const spec_pages_t *pages, const int32_t *page_t
  *   workspace: spec_tree_attention_workspace_bytes, 256-byte aligned; nothing
  *   in it is read that the call has not written.  Two launches.
  * Scores, softmax statistics and sums are float32; the softmax weights are
- * rounded to the dtype for the product with v (their sum is not).  A row that
- * sees a NaN score, or infinite ones, comes out NaN.
+ * rounded to the dtype for the product with v (their sum is not).  A score of
+ * -inf beside finite ones has the weight 0.  A row that sees a NaN score or one
+ * of +inf, or whose scores are all -inf, comes out NaN, lse included.
  */
 size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int heads, int head_dim);
 spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long q_stride_n,

@@ -405,6 +405,13 @@ __device__ __forceinline__ void ta_paths(const TaArgs &A, int b, int cnt, unsign
     }
 }
 
+// log sum exp of a row from its reference (base 2) and sum, which is 0 or NaN where no
+// score is above -inf or one is not a number.
+__device__ __forceinline__ float ta_lse(bool exists, float m, float l) {
+    if (!exists) return -INFINITY;
+    return l > 0.f ? 0.69314718056f * (m + log2f(l)) : __uint_as_float(0x7FFFFFFFu);
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int DT, int DP, int MODE>
@@ -1006,7 +1013,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (!ok) break;
             }
             tc_fence_after();
-            const float inv = l != 0.f ? 1.f / l : 0.f;  // 0: the row sees nothing
+            // a row sees itself at least, so in some part its sum is above 0 unless all its scores
+            // are -inf, which then makes it NaN (0 / 0); a part of which it sees nothing has a
+            // finite reference all the same, by which the join knows it from rows that do not exist
+            if (valid) m = fmaxf(m, -FLT_MAX);
+            const float inv = 1.f / l;
             const bool writes = row < rows_used && node < A.N;
             const int head = (MODE == kTaSplitHeads ? 2 * s.hk + stream : s.hk) * A.G + (row - local * A.G);
             const long long orow = ((long long)s.b * A.N + node) * A.Hq + head;
@@ -1039,9 +1050,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                                 uint32_t w[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    w[e] = l != 0.f ? pack2<DT>(__uint_as_float(o[i + 2 * e]) * inv,
-                                                               __uint_as_float(o[i + 2 * e + 1]) * inv)
-                                                   : 0u;
+                                    w[e] = valid ? pack2<DT>(__uint_as_float(o[i + 2 * e]) * inv,
+                                                             __uint_as_float(o[i + 2 * e + 1]) * inv)
+                                                 : 0u;
                                 dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         }
@@ -1059,7 +1070,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.o_free[stream]));
             if (writes && col0 == 0) {
                 if (whole_item) {
-                    if (A.lse) A.lse[orow] = l != 0.f ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
+                    if (A.lse) A.lse[orow] = ta_lse(valid, m, l);
                 } else {
                     A.part_ml[slot * rows_cta + prow] = make_float2(m, l);
                 }
@@ -1123,7 +1134,7 @@ __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, i
     for (int i = lane + L; i < parts; i += L) m = fmaxf(m, A.part_ml[slot(i)].x);
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o, L));
-    const bool some = m != -INFINITY;  // the row sees something
+    const bool some = m != -INFINITY;  // the row exists
     float l = 0.f;
     float4 o[kVecs] = {};
     for (int i0 = 0; i0 < parts; i0 += L) {
@@ -1161,7 +1172,7 @@ __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, i
             dst[lane + v * L] = some ? make_uint2(pack2<DT>(o[v].x * inv, o[v].y * inv),
                                                   pack2<DT>(o[v].z * inv, o[v].w * inv))
                                      : make_uint2(0u, 0u);
-    if (lane == 0 && A.lse) A.lse[orow] = some ? 0.69314718056f * (m + log2f(l)) : -INFINITY;
+    if (lane == 0 && A.lse) A.lse[orow] = ta_lse(some, m, l);
 }
 
 // ------------------------------------------------------------------ host

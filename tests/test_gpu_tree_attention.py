@@ -407,3 +407,53 @@ def test_same_bits_beside_other_work(N, hq, hkv, D):
         o2, l2, st = _run(c)
         assert st == 0 and torch.equal(o, o2) and torch.equal(l, l2)
     del b
+
+
+SPLITS = [(1, 2, 1, [0, 5]),                # the only key; streams that divide the keys
+          (4, 4, 2, [300, 0, 90]),
+          (3, 8, 2, [60000]),               # parts of many CTAs
+          (64, 8, 2, [500, 130]),           # streams that divide the rows
+          (64, 8, 1, [9000]),
+          (5, 160, 80, [200, 3]),           # a key head each
+          (2, 64, 64, [2900, 2500, 3000])]  # and cut
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,hq,hkv,lens", SPLITS)
+def test_rows_of_infinitely_low_scores_are_nan(N, hq, hkv, lens, dtype):
+    """Where all the scores a row sees are -inf there is no softmax: NaN, as for
+    a NaN score, and not the 0 of a row that does not exist."""
+    c = _case(N + hq, lens, N, hq, hkv, 64, 16, dtype)
+    c["k"][..., 3] = 1.0
+    cnt = torch.tensor([N] + [max(1, N // 2)] * (len(lens) - 1), dtype=torch.int32, device="cuda")
+    ref_o, ref_l, _ = _run(c, node_count=cnt)
+    q = c["q"].clone()
+    rows = {(b, n, h) for b in range(len(lens)) for n, h in ((0, 0), (int(cnt[b]) - 1, hq - 1), (N - 1, hq // 2))}
+    for r in rows:
+        q[r][3] = -math.inf
+    o, l, st = _run(dict(c, q=q), node_count=cnt)
+    assert st == 0
+    for b, n, h in rows:
+        if n < int(cnt[b]):
+            assert o[b, n, h].isnan().all() and l[b, n, h].isnan()
+            o[b, n, h], l[b, n, h] = ref_o[b, n, h], ref_l[b, n, h]
+    assert torch.equal(o, ref_o) and torch.equal(l, ref_l)  # rows past the counts among them: 0 and -inf
+
+
+@pytest.mark.parametrize("N,hq,hkv,lens", SPLITS)
+def test_one_infinitely_low_score_has_no_weight(N, hq, hkv, lens):
+    """A score below float32's range counts as one that is merely far below the others."""
+    c = _case(N + hq, lens, N, hq, hkv, 64, 16, torch.bfloat16)
+    c["k"][..., 3] = 0.0
+    for b, n0 in enumerate(lens):
+        if n0:
+            p = int(c["table"][b, (n0 - 1) // 16])
+            c["k"][p, (n0 - 1) % 16, :, 3] = 2.0 ** 20
+    got = []
+    for low in (-1.0, -2.0 ** 120):
+        q = c["q"].clone()
+        q[..., 3] = low
+        o, l, st = _run(dict(c, q=q))
+        assert st == 0 and torch.isfinite(o).all() and torch.isfinite(l).all()
+        got.append((o, l))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
