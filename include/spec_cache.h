@@ -186,8 +186,9 @@ spec_status_t spec_cache_commit(const spec_pages_t *pages, const int32_t *page_t
  *   page_table [B, max_pages], cache_len [B]: entries of pages that no node of
  *        the request sees are not looked at.  What the pool holds at positions
  *        that no node sees (past the end, before a window) may be anything,
- *        infinities and NaN included; at positions that some node sees it must
- *        be finite.
+ *        infinities and NaN included.  At a position that only some nodes see (a
+ *        node of another branch, the low end of a window) a key or value that is
+ *        not finite shows in the rows of those nodes and in no others.
  *   A parent that is not an earlier node ends the path there (SPEC_DEV_BAD_TREE);
  *   cache_len[b] + node_count[b] beyond what the row of the table reaches, or
  *   beyond 2^31 - 256, is cut (SPEC_DEV_BAD_LEN); a page outside the pool is

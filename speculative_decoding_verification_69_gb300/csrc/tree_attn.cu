@@ -81,6 +81,8 @@ struct TaArgs {
     float *lse;
     float *part_o;       // [cta][2][rows][D]
     float2 *part_ml;     // [cta][2][rows]: m (base 2), l
+    const uint16_t *v;   // the pool's values and their strides in elements (K and V come through tensor
+    long long v_page, v_token, v_head;  // maps: these are for values that are not finite)
     int4 *joins;         // [cta]: request, key head (or pair), first node and parts (0: none), see tree_attn_join
     uint32_t *status;
     uint32_t tries;      // looks of a wait
@@ -157,6 +159,8 @@ template <int DP, int MODE> struct TaShared {
     uint64_t q_full, q_free, o_free[2], ml_full, done;
     uint32_t tmem_base;
     int abort;
+    int bad_v[2][2];            // [stream with kTaSplitHeads, else 0][segment parity]: 1 + the segment that
+                                // held values that are not finite where only some rows see them
     float2 ml[MODE == kTaSplitKeys ? 2 : 1][2][MODE == kTaSplitKeys ? kTaRows : 1];  // [segment parity][stream][row]
 };
 
@@ -352,6 +356,23 @@ template <> __device__ __forceinline__ uint32_t pack2<SPEC_DTYPE_F16>(float lo, 
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
+// Whether the two 16-bit elements of x are infinities or NaN: bits 15 and 31.  (All bits of
+// the exponent are then set, and its lowest one more carries there.)
+template <int DT> __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+    constexpr uint32_t kExp = DT == SPEC_DTYPE_BF16 ? 0x7F807F80u : 0x7C007C00u;
+    constexpr uint32_t kLow = DT == SPEC_DTYPE_BF16 ? 0x00800080u : 0x04000400u;
+    return (x & kExp) + kLow;
+}
+// The same two with 0 for those.
+template <int DT> __device__ __forceinline__ uint32_t finite_part(uint32_t x) {
+    const uint32_t bad = not_finite<DT>(x);
+    return x & (((bad >> 15) & 1u ? 0u : 0xFFFFu) | (bad >> 31 ? 0u : 0xFFFF0000u));
+}
+template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t x) {
+    if (DT == SPEC_DTYPE_BF16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+
 // The positions [j, j + 64) that a row sees: committed ones from `low` on and the
 // first `sinks`, and the nodes of its path, which lie from position c on.
 // (Positions are below 2^31, and so are their differences.)
@@ -412,12 +433,67 @@ __device__ __forceinline__ float ta_lse(bool exists, float m, float l) {
     return l > 0.f ? 0.69314718056f * (m + log2f(l)) : __uint_as_float(0x7FFFFFFFu);
 }
 
+// Adds to a row's accumulators the elements that were taken out of the values because they are
+// not finite and not all rows see them: from the pool, those that the row does see (its weight
+// for them is above 0, however small).  Stream `of` of a, a ^ 1 (two) holds the segment's tiles
+// whose number from base0 on has its parity (kTaSplitKeys), or all of them.  Rare, and so out
+// of line: the kernel's code is fetched anew by every short call.
+template <int DT, int DP, int MODE>
+__device__ __noinline__ void ta_add_not_finite(const TaArgs &A, Seg s, int hk, uint32_t o_cols, int col0, int a,
+                                               bool two, bool valid, int sinks, int edge, int low,
+                                               unsigned long long path, uint32_t base0) {
+    constexpr int kCols = MODE == kTaSplitKeys ? DP / 2 : DP;
+    const Geo &g = s.g;
+    const int *table = A.table + (long long)s.b * A.max_pages;
+    const uint16_t *v = A.v + hk * A.v_head + col0;
+#pragma unroll 1
+    for (int x = 0; x < (two ? 2 : 1); ++x) {
+        const int of = a ^ x;
+#pragma unroll 1
+        for (int d = 0; d < kCols; d += 32) {
+            uint32_t o[32];
+            tmem_load(o_cols + (uint32_t)(of * DP + d), o);
+#pragma unroll 1
+            for (int i = 0; i < 2 * SPEC_MAX_TREE && valid; ++i) {
+                const bool node_at = i >= SPEC_MAX_TREE;
+                const int j = node_at ? g.c + (i - SPEC_MAX_TREE) : g.wlo + i;
+                if (node_at ? j >= g.end || g.cnt == 1 : j >= edge || j < sinks) continue;
+                if (!(node_at ? (path >> (j - g.c)) & 1ull : j >= low)) continue;
+                const int t = g.st + j / kTaKeys - g.wt0 - s.i0;  // its tile of the segment
+                if (t < 0 || t >= s.n) continue;
+                if (MODE == kTaSplitKeys && ((base0 + (uint32_t)t) & 1u) != (uint32_t)of) continue;
+                int page = __ldcg(table + (j >> A.page_shift));
+                if ((unsigned)page >= (unsigned)A.num_pages) page = 0;
+                const uint4 *src =
+                    reinterpret_cast<const uint4 *>(v + page * A.v_page + (j & (A.page - 1)) * A.v_token + d);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    if (col0 + d + e >= A.D) break;
+                    const uint4 y = __ldcg(src + e / 8);
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t bad = not_finite<DT>(w[q]);
+                        const float2 f = unpack2<DT>(w[q]);
+                        uint32_t &lo = o[e + 2 * q], &hi = o[e + 2 * q + 1];
+                        if ((bad >> 15) & 1u) lo = __float_as_uint(__uint_as_float(lo) + f.x);
+                        if (bad >> 31) hi = __float_as_uint(__uint_as_float(hi) + f.y);
+                    }
+                }
+            }
+            __syncwarp();
+            tmem_store(o_cols + (uint32_t)(of * DP + d), o);
+        }
+    }
+    tmem_wait_store();
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v, TaArgs A) {
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TaArgs A) {
     using C = TaCfg<DP, MODE>;
     using Sh = TaShared<DP, MODE>;
     extern __shared__ uint8_t ta_raw[];
@@ -460,6 +536,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         mbar_init(&sh.ml_full, 8);
         mbar_init(&sh.done, 1);
         sh.abort = 0;
+        for (int i = 0; i < 4; ++i) sh.bad_v[i >> 1][i & 1] = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_q);
         tma_prefetch_map(&tm_k);
@@ -860,6 +937,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int low = valid ? sp->low[node] : 0;
             give(seg_no);
             const int sinks = A.window ? A.sinks : 0;
+            // positions that some rows of the request see and others do not: its nodes, and before
+            // them [wlo, edge) without the sinks
+            const int edge = A.window && g.cnt > 1 ? min(g.c, g.c + g.cnt - A.window) : 0;
+            int *bad_v = &sh.bad_v[MODE == kTaSplitHeads ? stream : 0][seg_no & 1];
             const bool warp_works = __any_sync(0xFFFFFFFFu, valid);
             float m = -INFINITY;                       // reference of the weights, less the lift
             float2 l2 = make_float2(0.f, 0.f);
@@ -870,15 +951,42 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 const int j0 = g.tile(s.i0 + t) * kTaKeys;
                 const uint32_t use = (base + (uint32_t)t) >> (MODE == kTaSplitKeys ? 1 : 0);  // the stream's
                 // values that no node sees may be anything: they are cleared, so that their zero
-                // weights leave them out (kTaSplitRows: by stream 0, whose weights are used first);
-                // before the weights if the tile is there by then.  Not looked for before the scores
-                // have come: they follow earlier values, whose tiles have then been there, and a
-                // stage's parity says nothing while the fill before this one is still due
+                // weights leave them out (kTaSplitRows: by stream 0, whose weights are used first).
+                // So are elements that are not finite where only some rows see them; those rows
+                // get them with the result (the check makes 208.9 us of 207.4 at 64 requests of 64
+                // nodes, 101.0 of 99.1 at a window of 128, 11.5 of 11.2 at one token).
+                // The tile is waited for before its scores, which leaves the time they take, where
+                // the stage's parity can be trusted by then (kEarly): not while the fill before
+                // this one may be due.  The stream has seen its last tile's scores, which were
+                // issued when the values up to one tile before that (kTaSplitRows) or two (the
+                // streams in turn, so 4 before this one) had their tiles.  Otherwise the scores
+                // come first, which were issued after the values two tiles before.
+                constexpr bool kEarly = MODE == kTaSplitRows || kVS >= 4;
                 const uint32_t v_tile = (base + (uint32_t)t) * kPer + (MODE == kTaSplitHeads ? stream : 0);
                 const uint32_t v_stage = v_tile % kVS, v_parity = (v_tile / kVS) & 1u;
-                bool clear = (MODE != kTaSplitRows || stream == 0) &&
-                             (g.end - j0 < kTaKeys || (j0 < g.wlo && A.sinks - j0 < kTaKeys));
-                auto clear_v = [&]() {
+                const bool clear = (MODE != kTaSplitRows || stream == 0) &&
+                                   (g.end - j0 < kTaKeys || (j0 < g.wlo && A.sinks - j0 < kTaKeys) ||
+                                    (g.cnt > 1 && (g.c - j0 < kTaKeys || (j0 < edge && g.wlo - j0 < kTaKeys))));
+                auto clear_v = [&]() -> bool {
+                    if (!__all_sync(0xFFFFFFFFu, ta_wait(&sh.v_full[v_stage], v_parity, abort, A.tries))) return false;
+                    // positions that only some see, 16 bytes of a value to a thread
+                    const int lo0 = max(max(g.wlo, sinks), j0), lo1 = max(g.c, j0);
+                    const int n0 = max(0, min(edge, j0 + kTaKeys) - lo0);
+                    const int n1 = g.cnt > 1 ? max(0, min(g.end, j0 + kTaKeys) - lo1) : 0;
+#pragma unroll 1
+                    for (int x = row; x < (n0 + n1) * 8 * kHalves; x += kTaRows) {
+                        const int k = x / (8 * kHalves), key = (k < n0 ? lo0 + k : lo1 + (k - n0)) - j0;
+                        uint4 *z = reinterpret_cast<uint4 *>(sh.v[v_stage] + (x / 8 % kHalves) * kTaKeys * 128 +
+                                                             key * 128 + x % 8 * 16);
+                        const uint4 y = *z;
+                        const uint32_t bad = not_finite<DT>(y.x) | not_finite<DT>(y.y) | not_finite<DT>(y.z) |
+                                             not_finite<DT>(y.w);
+                        if (bad & 0x80008000u) {
+                            *z = make_uint4(finite_part<DT>(y.x), finite_part<DT>(y.y), finite_part<DT>(y.z),
+                                            finite_part<DT>(y.w));
+                            *(volatile int *)bad_v = seg_no + 1;
+                        }
+                    }
                     if (g.end - j0 <= row || (g.wlo - j0 > row && A.sinks - j0 <= row)) {
 #pragma unroll
                         for (int d = 0; d < kHalves; ++d) {  // neighbours begin 16 bytes apart: other banks
@@ -888,7 +996,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         }
                     }
                     fence_proxy_async();
-                    clear = false;
+                    return true;
                 };
                 // a tile's weights and values in two halves of 64 keys: one half's products
                 // run while the other half's weights are formed, and 64 scores fit the registers.
@@ -899,10 +1007,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     const int jh = j0 + h * (kTaKeys / 2);
                     const uint32_t th = ts + (uint32_t)(h * (kTaKeys / 2));
                     if (h == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort, A.tries));
+                        ok = !(kEarly && clear) || clear_v();
+                        ok = ok && __all_sync(0xFFFFFFFFu, ta_wait(&sh.s_full[stream], use & 1u, abort, A.tries));
                         if (!ok) break;
                         tc_fence_after();
-                        if (clear && __all_sync(0xFFFFFFFFu, mbar_test_wait(&sh.v_full[v_stage], v_parity))) clear_v();
+                        ok = !(!kEarly && clear) || clear_v();
+                        if (!ok) break;
                     }
                     if (warp_works) {
                         uint32_t x[64];
@@ -968,11 +1078,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                         l2 = add2(l2, add2(sum[0], sum[1]));
                         tmem_wait_store();
                     }
-                    if (h == 0 && clear) {
-                        ok = __all_sync(0xFFFFFFFFu, ta_wait(&sh.v_full[v_stage], v_parity, abort, A.tries));
-                        if (!ok) break;
-                        clear_v();
-                    }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(reinterpret_cast<unsigned long long *>(&sh.p_full[stream][h]));
@@ -1024,8 +1129,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int prow = (MODE == kTaSplitKeys ? 0 : stream * rows_used) + row;
             const int rows_cta = rows_used * (MODE == kTaSplitKeys ? 1 : 2);
             const bool any_write = __any_sync(0xFFFFFFFFu, writes);
+            const uint32_t o_cols = tmem + lanes + 256u + (uint32_t)col0;
+            if (any_write && __any_sync(0xFFFFFFFFu, *(volatile int *)bad_v == seg_no + 1))
+                ta_add_not_finite<DT, DP, MODE>(A, s, MODE == kTaSplitHeads ? 2 * s.hk + stream : s.hk, o_cols, col0, a,
+                                                two, valid, sinks, edge, low, path, base - (uint32_t)s.n);
             if (any_write) {
-                const uint32_t o_cols = tmem + lanes + 256u + (uint32_t)col0;
 #pragma unroll 1
                 for (int d = 0; d < kCols; d += 32) {
                     uint32_t o[32];
@@ -1337,6 +1445,10 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     A.part_o = reinterpret_cast<float *>(ws + L.o);
     A.part_ml = reinterpret_cast<float2 *>(ws + L.ml);
     A.joins = reinterpret_cast<int4 *>(ws + L.joins);
+    A.v = static_cast<const uint16_t *>(pages->v);
+    A.v_page = pages->page_stride;
+    A.v_token = pages->token_stride;
+    A.v_head = pages->head_stride;
     A.status = dev_status;
     A.tries = sv::g_diag_timeout ? 0u : sv::kTaTries;
 

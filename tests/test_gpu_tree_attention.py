@@ -457,3 +457,77 @@ def test_one_infinitely_low_score_has_no_weight(N, hq, hkv, lens):
         assert st == 0 and torch.isfinite(o).all() and torch.isfinite(l).all()
         got.append((o, l))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def _some_see(c, window, sinks):
+    """Per request the positions that some of its nodes see and others do not."""
+    out = []
+    for b, n0 in enumerate(c["len"].tolist()):
+        par = None if c["parent"] is None else c["parent"][b].tolist()
+        sets = [set(ch.seen_positions(n0, p, window, sinks)) for p in ch.paths(par, c["q"].shape[1])]
+        out.append(sorted(set().union(*sets) - set.intersection(*sets)))
+    return out
+
+
+def _check_with_non_finite(c, got, **kw):
+    """As ch.check_attention where the definition is finite; elsewhere the same infinity, or NaN."""
+    (o, l), ref = got, ch.ref_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"], **kw)
+    want, oc = ref[0], o.cpu().double()
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(oc), torch.isnan(want))
+    assert torch.equal(torch.isfinite(oc), ~odd)
+    inf = torch.isinf(want)
+    assert torch.equal(oc[inf], want[inf])
+    clean = [x.masked_fill(odd, 0.0) for x in (oc, want, ref[2])]
+    ch.check_attention(clean[0], l, (clean[1], ref[1], clean[2], ref[3]), o.dtype, o.shape[-1])
+    return odd
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,hq,hkv,D,page,lens,window,sinks", [
+    (2, 2, 1, 64, 16, [0, 5, 127], 0, 0),
+    (9, 8, 2, 128, 16, [0, 119, 124, 700], 0, 0),          # nodes in one tile and across two
+    (9, 8, 2, 72, 8, [40000], 0, 0),                        # parts of many CTAs
+    (12, 8, 2, 64, 16, [300, 3, 1000, 65], 40, 3),          # the low end of a window
+    (12, 8, 2, 128, 64, [300, 130, 1000], 5, 130),          # nodes that leave their own window
+    (64, 8, 2, 128, 32, [200, 100, 0], 0, 0),               # rows divided between the streams
+    (64, 8, 1, 64, 16, [900, 64], 100, 2),                  # several row tiles
+    (7, 160, 80, 64, 16, [250, 30], 0, 0),                  # a key head each
+    (7, 80, 80, 128, 16, [1000, 300], 128, 1),
+])
+def test_values_that_are_not_finite_stay_in_their_branch(N, hq, hkv, D, page, lens, window, sinks, dtype):
+    c = _case(N * 7 + D, lens, N, hq, hkv, D, page, dtype, qscale=0.3)
+    before = _run(c, window=window, sinks=sinks)
+    g = torch.Generator().manual_seed(N)
+    odd = [float("inf"), float("-inf"), float("nan")]
+    hit = 0
+    for b, spots in enumerate(_some_see(c, window, sinks)):
+        for j in spots[::3]:
+            at = (int(c["table"][b, j // page]), j % page)
+            for _ in range(2):
+                h, d, x = (int(torch.randint(n, (1,), generator=g)) for n in (hkv, D, 3))
+                c["v"][at][h, d] = odd[x]
+                hit += 1
+    assert hit > 0
+    o, l, st = _run(c, window=window, sinks=sinks)
+    assert st == 0
+    odd = _check_with_non_finite(c, (o, l), window=window, sinks=sinks)
+    assert odd.any() and not odd.all()
+    assert torch.equal(o[~odd.cuda()], before[0][~odd.cuda()]) and torch.equal(l, before[1])
+
+
+@pytest.mark.parametrize("N,hq,hkv,lens", [(9, 8, 2, [119, 700]), (64, 8, 2, [200, 0]), (7, 160, 80, [250])])
+def test_keys_that_are_not_finite_stay_in_their_branch(N, hq, hkv, lens):
+    c = _case(N, lens, N, hq, hkv, 64, 16, torch.bfloat16, qscale=0.3)
+    ref_o, ref_l, _ = _run(c)
+    par = c["parent"].tolist()
+    for b, n0 in enumerate(lens):
+        c["k"][int(c["table"][b, (n0 + 1) // 16]), (n0 + 1) % 16] = float("nan")
+    o, l, st = _run(c)
+    assert st == 0
+    for b in range(len(lens)):
+        for n, path in enumerate(ch.paths(par[b], N)):
+            if 1 in path:
+                assert o[b, n].isnan().all() and l[b, n].isnan().all()
+            else:
+                assert torch.equal(o[b, n], ref_o[b, n]) and torch.equal(l[b, n], ref_l[b, n])
