@@ -45,7 +45,7 @@ def load_library():
         return _lib
     path = _build.LIB
     if _build.stale():
-        _build.build()
+        _build.build_library()
     if not os.path.exists(path):
         raise SpecVerifyError("libspecverify.so is not built: run __graft_entry__.build()")
     L = ctypes.CDLL(path)

@@ -1,8 +1,12 @@
 """Build libspecverify.so (nvcc, sm_103a) and the Python binding of the paged
-cache (_native.so, the host compiler) in-tree."""
+cache (the host compiler; torch's and Python's headers) in-tree.  The library
+is built and loaded without the binding, which only cache.py uses."""
 import os
+import re
 import subprocess
 import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -10,7 +14,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libspecverify.so")
-NATIVE = os.path.join(OUT_DIR, "_native.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "spec_cache.cu", "tree_attn.cu")]
 BINDING = os.path.join(CSRC, "binding.cpp")
 HEADERS = [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_cache.h")]
@@ -36,7 +39,19 @@ def _older(path, deps) -> bool:
 
 
 def stale() -> bool:
-    return _older(LIB, DEPS) or _older(NATIVE, [BINDING] + HEADERS)
+    return _older(LIB, DEPS)
+
+
+def native_path() -> str:
+    """The binding for this Python and this torch: it reads their objects, whose
+    layouts change from version to version."""
+    tag = "%s.torch%s.abi%d" % (sysconfig.get_config_var("SOABI"), torch.__version__,
+                                int(torch._C._GLIBCXX_USE_CXX11_ABI))
+    return os.path.join(OUT_DIR, "_native.%s.so" % re.sub(r"[^\w.-]", "_", tag))
+
+
+def binding_stale() -> bool:
+    return _older(native_path(), [BINDING] + HEADERS)
 
 
 def _run(cmd, out, verbose):
@@ -49,7 +64,6 @@ def _run(cmd, out, verbose):
 
 
 def _binding_cmd():
-    import torch
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(CUDA, "include"), INCLUDE]
@@ -59,12 +73,24 @@ def _binding_cmd():
                "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build_library(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    if force or _older(LIB, DEPS):
+    if force or stale():
         _run([nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-I" + CSRC, *SOURCES], LIB, verbose)
-    if force or _older(NATIVE, [BINDING] + HEADERS):
-        _run(_binding_cmd(), NATIVE, verbose)
+    return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Links against the library, which has to be there."""
+    path = native_path()
+    if force or binding_stale():
+        _run(_binding_cmd(), path, verbose)
+    return path
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)
+    build_binding(force, verbose)
     return LIB
 
 

@@ -22,6 +22,7 @@ one from torch's allocator, in a capture from the graph's own memory.
 """
 import ctypes
 import importlib.util
+import subprocess
 
 import torch
 
@@ -59,12 +60,17 @@ _loaded = None
 
 
 def _native():
-    """The compiled binding (csrc/binding.cpp), which checks its arguments."""
+    """The compiled binding (csrc/binding.cpp), which checks its arguments; built
+    first if it is missing or stale."""
     global _loaded
     if _loaded is None:
-        from . import load_library
+        from . import SpecVerifyError, load_library
         load_library()
-        spec = importlib.util.spec_from_file_location("_native", _build.NATIVE)
+        try:
+            path = _build.build_binding()
+        except (OSError, subprocess.CalledProcessError) as e:
+            raise SpecVerifyError("the binding of the paged cache is not built, and building it failed: %s" % e) from e
+        spec = importlib.util.spec_from_file_location("_native", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _loaded = module
