@@ -18,7 +18,8 @@ stored heads first is passed as its transpose.  As everywhere in this package
 every step runs in the library's kernels, on torch's current stream or the
 `stream` given, and nothing falls back to torch.  The calls can be captured in a
 CUDA graph: a call without a `workspace` (a uint8 tensor, 256-byte aligned) takes
-one from torch's allocator, in a capture from the graph's own memory.
+one from torch's allocator, in a capture from the graph's own memory.  Nothing here
+has a backward pass: with gradients enabled, tensors that require one are refused.
 """
 import ctypes
 import importlib.util

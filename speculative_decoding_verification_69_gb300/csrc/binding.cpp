@@ -9,6 +9,7 @@
 #include <Python.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -77,6 +78,12 @@ long long stride(const at::Tensor &t, int dim) {
     return t.size(dim) > 1 ? t.stride(dim) : t.size(-1);
 }
 
+// The operators have no backward pass: a call whose gradient would be lost is refused.
+void no_gradient(const at::Tensor &t, const char *name) {
+    TORCH_CHECK_VALUE(!(t.requires_grad() && c10::GradMode::is_enabled()), name,
+                      " requires a gradient, and this call has none: make it under torch.no_grad(), or detach ", name);
+}
+
 // A pool of pages, [num_pages, page_size, heads, head_dim], with the layers in
 // front of them when `layered`.
 spec_pages_t pool(PyObject *ko, PyObject *vo, bool layered) {
@@ -94,6 +101,8 @@ spec_pages_t pool(PyObject *ko, PyObject *vo, bool layered) {
     }
     TORCH_CHECK_VALUE(k.is_cuda() && v.is_cuda(), "k and v must be CUDA tensors");
     together(v, k, "v");
+    no_gradient(k, "k");
+    no_gradient(v, "v");
     bool same = k.stride(-1) == 1 && v.stride(-1) == 1;
     for (int i = 0; i < 3 + d; ++i) same = same && stride(k, i) == stride(v, i);
     TORCH_CHECK_VALUE(same, "k and v need the same strides and a contiguous head_dim");
@@ -121,6 +130,7 @@ const at::Tensor &rows(PyObject *o, const char *name, const at::Tensor &k, int64
                       name, " must be a CUDA tensor [B, N, ", heads < 0 ? std::string("heads") : std::to_string(heads),
                       ", ", k.size(-1), "] of the cache's dtype, its last dimension contiguous");
     together(t, k, name);
+    no_gradient(t, name);
     return t;
 }
 

@@ -386,3 +386,32 @@ def test_a_slot_without_pages_for_its_step_loses_nothing(linear):
         at = torch.arange(len(want), device="cuda")
         pages = c.page_table[b].long()[at // 8]
         assert torch.equal(c.k[0, pages, at % 8], want) and torch.equal(c.v[0, pages, at % 8], want)
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """There is no backward pass: instead of a result cut off from the graph, an error."""
+    sv = _sv()
+    k = torch.randn((1, 4, 8, 1, 8), device="cuda").bfloat16()
+    v = k.clone()
+    table, one = _i32([[0, 1]]), _i32([1])
+    count, ref, zero = _i32([2]), _i32([1, 1, 0, 0]), _i32([0])
+    new = torch.randn((1, 2, 1, 8), device="cuda").bfloat16()
+
+    def grad(t):
+        return t.detach().clone().requires_grad_(True)
+    calls = [lambda k, v, x: sv.tree_attention(x, k[0], v[0], table, one),
+             lambda k, v, x: sv.cache_append(k[0], v[0], table, one, x, x),
+             lambda k, v, x: sv.cache_append(k[0], v[0], table, one, new, x),
+             lambda k, v, x: sv.cache_commit(k, v, table, one.clone(), _i32([[1, -1]]), one),
+             lambda k, v, x: sv.cache_copy(k, v, zero, _i32([3])),
+             lambda k, v, x: sv.cache_fork(k, v, table, count, ref, one, zero, _i32([5]))]
+    for i, call in enumerate(calls):
+        for args in ((grad(k), v, new), (k, grad(v), new)) + (((k, v, grad(new)),) if i < 3 else ()):
+            with pytest.raises(ValueError, match="gradient"):
+                call(*args)
+            with torch.no_grad():
+                call(*args)
+        call(k, v, new)
+    out = sv.tree_attention(new.detach(), k[0], v[0], table, one)
+    with torch.no_grad():
+        assert torch.equal(sv.tree_attention(grad(new), k[0], v[0], table, one), out)
