@@ -58,7 +58,8 @@ typedef struct {
     int page_size;          /* tokens per page: a power of two of at least 8 */
     int heads;              /* key/value heads */
     int head_dim;           /* a multiple of 8 */
-    long long layer_stride; /* strides in elements: multiples of 8, at least head_dim where the extent is above 1 */
+    long long layer_stride; /* strides in elements: multiples of 8; where the extent is above 1 a stride steps over
+                               head_dim and all that the smaller strides reach, so no two elements share a place */
     long long page_stride;
     long long token_stride;
     long long head_stride;

@@ -523,8 +523,16 @@ spec_status_t make_pool(const spec_pages_t *p, Pool &P) {
     if (((uintptr_t)p->k & 15) || ((uintptr_t)p->v & 15)) return SPEC_ERR_INVALID_ARG;
     const long long st[4] = {p->layer_stride, p->page_stride, p->token_stride, p->head_stride};
     const int extent[4] = {p->layers, p->num_pages, p->page_size, p->heads};
-    for (int i = 0; i < 4; ++i)  // no two elements may share a place
-        if (st[i] < (extent[i] > 1 ? p->head_dim : 0) || st[i] % 8) return SPEC_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i) {
+        if (st[i] < 0 || st[i] % 8) return SPEC_ERR_INVALID_ARG;
+        if (extent[i] == 1) continue;
+        // no two elements may share a place: a stride steps over all that the smaller
+        // strides reach (of equal ones the other reaches as far as it steps)
+        __int128 reach = p->head_dim;
+        for (int j = 0; j < 4; ++j)
+            if (j != i && st[j] <= st[i]) reach += (__int128)(extent[j] - 1) * st[j];
+        if (st[i] < reach) return SPEC_ERR_INVALID_ARG;
+    }
     const int per = p->dtype == SPEC_DTYPE_F32 ? 4 : 8;  // elements of a 16-byte vector
     P.k = static_cast<uint4 *>(p->k);
     P.v = static_cast<uint4 *>(p->v);
