@@ -92,7 +92,8 @@ spec_status_t spec_cache_resize(int32_t *page_table, int32_t *page_count, int32_
  * tokens it holds, in every layer.  Free pages are taken as by
  * spec_cache_resize, in the order of the forks; a fork that finds none leaves
  * dst[f] empty (SPEC_DEV_NO_PAGES).  Pages that src[f] holds past its length
- * are not shared.
+ * are not shared.  Shared pages are not to be written again: neither slot's length
+ * may be taken back behind the fork while the other holds them.
  *   page_table [slots, max_pages], page_count [slots], page_ref [num_pages],
  *   cache_len [slots] int32: updated.  src, dst [F] int32: a slot may be the
  *   source of many forks; a dst that is also a source, or another fork's dst

@@ -154,7 +154,10 @@ def tree_attention(q, k, v, page_table, cache_len, parent=None, *, node_count=No
 
 class PagedCache:
     """The cache of a batch of `slots` requests: pools of pages for every layer,
-    the page table, the lengths, and the status word the calls report in."""
+    the page table, the lengths, and the status word the calls report in.  The
+    methods work on all slots; single slots are filled, kept or released with
+    cache_resize and want_len (0: released, negative: left alone).  dtype:
+    bfloat16 or float16, or float32 for the pages alone (attention refuses it)."""
 
     def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, slots, max_pages, *,
                  dtype=torch.bfloat16, device="cuda"):

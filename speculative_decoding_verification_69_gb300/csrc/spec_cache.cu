@@ -301,10 +301,12 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 // One page to another in every layer: whole pages (copies NULL: src[i] to
 // dst[i]), or the first tokens of a page as the bookkeeping of a fork listed
 // them.  Grid (pairs, layers, token blocks), block (vector columns, tokens).
-// Bound by HBM: each vector is read once and written once; eight loads, four of
-// keys and four of values, are in flight per thread before the first store.
-// 64 forks, 24 layers: 30.3 us for the call, 6.5 TB/s (four forks share a
-// source, whose reads hit L2); blocks of keys or values alone took 35.2.
+// Eight loads, four of keys and four of values, are in flight per thread before the
+// first store.  64 forks of 16 slots, 24 layers: 31 us for the call, 8 of them the
+// bookkeeping, and 124 MB that have to move.  The copy reads a source anew for each of its
+// four forks, three times from L2, and by its counters (DRAM 31%, issue 33%) its 12288
+// blocks are bound by their chains of dependent loads, not by HBM; blocks of
+// keys or values alone took 35 us.
 __global__ void __launch_bounds__(256) sv_copy_pages(Pool P, const int *src, const int *dst,
                                                      const int *copies, uint32_t *status) {
     pdl_trigger();
@@ -456,8 +458,10 @@ __device__ __forceinline__ int commit_len(int len, int kept) {
 // its place (out_nodes[i] >= i + 1), so a later node is never overwritten by an
 // earlier move: all loads of a batch of moves, a barrier, then its stores.
 // Nodes already in place are not touched.  Bound by latency at small batches
-// (a chain of four dependent loads; 2.8 us at 4 requests of 8 nodes), by HBM at
-// large ones (128 requests of 64 nodes, 36 layers: 34.5 us, 6.7 TB/s).
+// (a chain of four dependent loads; 3.0 us at 4 requests of 8 nodes).  128 requests of 64
+// nodes, 36 layers: 34 to 36 us for the 180 MB of the nodes that do not lie in place already, a
+// floor of 27; DRAM is 48% busy inside the kernel and issue 41% (the same chain, then
+// one batch of moves between two barriers).
 constexpr int kMoveUnroll = 4;
 __global__ void __launch_bounds__(256) sv_commit(Pool P, const int *table, const int *len,
                                                  const int *nodes,

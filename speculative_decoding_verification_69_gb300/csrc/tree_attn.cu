@@ -6,9 +6,11 @@
 // form one matrix: S = Q K^T, softmax over the keys each row sees, O = P V.
 // One pass over the keys keeps per row a reference m (near the running maximum
 // of the scaled scores, base 2), l = sum 2^(s - m) and O = sum 2^(s - m) v:
-// a later, larger maximum rescales l and O by 2^(m - m').  O is rescaled only
-// when the maximum has grown by more than 2^8: until then the weights are
-// merely larger than 1, exactly representable in scale, and O stays untouched
+// a later, larger maximum rescales l and O by 2^(m - m'), the online softmax of
+// M. Milakov and N. Gimelshein, "Online normalizer calculation for softmax" (2018).
+// O is rescaled only when the maximum has grown by more than 2^8, a refinement
+// published since for accumulators that are dear to rescale: until then the weights
+// are merely larger than 1, exactly representable in scale, and O stays untouched
 // in the tensor memory.  Partial results over disjoint keys join the same way.
 //
 // Split.  The work is a list of units, one per (request, key head, row tile,
@@ -30,13 +32,13 @@
 // What bounds it, with device times of a call, join included, on a GPU that copies
 // 6.7 TB/s and multiplies bfloat16 matrices at 1937 TFLOP/s (32 query and 8 key heads of
 // 128 unless said otherwise):
-//   1 request of 131071 tokens, 16 nodes        94 us   5.7 TB/s    HBM, and a join of 20 parts
-//   32 requests of up to 4096 tokens, 9 nodes   73 us   5.6 TB/s    HBM
-//   64 requests, 64 nodes each (256 rows)      195 us   4.6 TB/s, 1080 TFLOP/s: a stream's chain of
-//                scores, two halves of weights and values; the tensor cores are 49% busy
-//   512 requests, 9 nodes, window of 128       99 us   2.2 TB/s    64 query heads of 64: short segments,
+//   1 request of 131071 tokens, 16 nodes        96 us   5.6 TB/s    HBM, and a join of 20 parts
+//   32 requests of up to 4096 tokens, 9 nodes   75 us   5.5 TB/s    HBM
+//   64 requests, 64 nodes each (256 rows)      210 us   4.2 TB/s, 1000 TFLOP/s: a stream's chain of
+//                scores, two halves of weights and values; the tensor cores are 45% busy
+//   512 requests, 9 nodes, window of 128      101 us   2.2 TB/s    64 query heads of 64: short segments,
 //                so the softmax warps' latency, half of it in masks, clearing and output
-//   1 request of 1000 tokens, 1 node            11 us   latency: lengths, pages, a tile, the join
+//   1 request of 1000 tokens, 1 node          11.5 us   latency: lengths, pages, a tile, the join
 // K, V and P go through 128-key tiles because a product of 64 columns takes 48 cycles where
 // one of 128 takes 64; P lies in the tensor memory (head_dim above 64: over its scores, since
 // two accumulators leave no other columns), since it would otherwise be written to and read
@@ -1071,6 +1073,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                                                                   __uint_as_float(x[32 * q + 2 * i + 1])), c2, nm2);
                                 const float2 e = make_float2(ex2(z.x), ex2(z.y));
                                 sum[i & 1] = add2(sum[i & 1], e);
+                                // rounded to V's type, as operands of one product have to be; the sum
+                                // takes them unrounded, so the errors (2^-9 or 2^-12 each) average out
                                 p[i] = pack2<DT>(e.x, e.y);
                             }
                             tmem_store(tp + (uint32_t)(h * kPHalf + 16 * q), p);
@@ -1216,8 +1220,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 // joins[j]: the first cut of an item lies at CTA j's first unit; its parts are
 // slot 1 of the CTA before, where it begins, and slot 0 of CTA j and those after.
 // 16 lanes per row, two vectors of four columns each: bound by the latency of three
-// dependent loads at few rows (3.4 us of the 11.2 of one token at one request) and
-// by instructions at many (10 us of 195 at 64 nodes and 64 requests); a warp per row
+// dependent loads at few rows (3.4 us of a call of one token at one request) and
+// by instructions at many (10 us at 64 nodes and 64 requests); a warp per row
 // took 16.7 us there, 8 lanes 9.5 but 3 us more with 20 parts of 64 rows.
 template <int DT>
 __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta, int mode) {
@@ -1411,11 +1415,11 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     // nothing but the CTA, where streams that divide the keys meet at the end of
     // every (request, head), which costs most where those are short.  us, by heads /
     // by keys, 8 key heads:
-    //   head_dim 64, window 128, 9 nodes:  B = 24 13.8 / 16.3, 64 19.5 / 24.4, 512 87 / 120
-    //   head_dim 128, 500 tokens, 1 node:  B = 32 17.5 / 21.9;  window 1024, 9 nodes: 256 191 / 197
-    //   head_dim 128, 4096 tokens, 9 nodes: B = 32 98 / 98, 256 666 / 671
+    //   head_dim 64, window 128, 9 nodes:  B = 24 13.7 / 16.3, 64 19.3 / 24.6, 512 90 / 121
+    //   head_dim 128, 500 tokens, 1 node:  B = 32 18.3 / 22.5;  window 1024, 9 nodes: 256 194 / 211
+    //   head_dim 128, 4096 tokens, 9 nodes: B = 32 96 / 96, 256 656 / 664
     // With fewer heads a unit of twice the work is cut more coarsely:
-    //   head_dim 128, 500 tokens, 1 node:  B = 16 14.0 / 13.0, 1 10.9 / 10.2; 20000 tokens: B = 1 28 / 26
+    //   head_dim 128, 500 tokens, 1 node:  B = 16 14.5 / 13.3, 1 10.7 / 10.4; 20000 tokens, 2 nodes: B = 1 29.5 / 26.8
     const bool pairs = H % 2 == 0 && (long long)B * H >= ctas;
     const sv::TaRows r = sv::ta_rows(N, Hq / H, pairs);
     const sv::TaLayout L = sv::ta_layout(N, Hq, H, D);
