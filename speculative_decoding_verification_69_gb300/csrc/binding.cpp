@@ -281,6 +281,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type() && out.is_cuda() &&
                               out.is_contiguous() && out.device() == q.device(),
                           "out must be a contiguous CUDA tensor of q's shape and dtype");
+        no_gradient(out, "out");
     } else {
         out = at::empty(q.sizes(), q.options());
     }

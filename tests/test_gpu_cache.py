@@ -415,3 +415,14 @@ def test_tensors_that_require_a_gradient_are_refused():
     out = sv.tree_attention(new.detach(), k[0], v[0], table, one)
     with torch.no_grad():
         assert torch.equal(sv.tree_attention(grad(new), k[0], v[0], table, one), out)
+
+
+def test_an_output_that_requires_a_gradient_is_refused():
+    sv = _sv()
+    k = torch.randn((2, 8, 1, 8), device="cuda").bfloat16()
+    q = torch.randn((1, 2, 1, 8), device="cuda").bfloat16()
+    out = torch.zeros_like(q).requires_grad_(True)
+    with pytest.raises(ValueError, match="gradient"):
+        sv.tree_attention(q, k, k, _i32([[0, 1]]), _i32([1]), out=out)
+    with torch.no_grad():
+        assert sv.tree_attention(q, k, k, _i32([[0, 1]]), _i32([1]), out=out).data_ptr() == out.data_ptr()
