@@ -285,7 +285,8 @@ PyObject *tree_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
         out = at::empty(q.sizes(), q.options());
     }
-    const bool with_lse = PyObject_IsTrue(a[11]) == 1;
+    const int with_lse = PyObject_IsTrue(a[11]);
+    if (with_lse < 0) return nullptr;
     if (with_lse) lse = at::empty({B, N, Hq}, q.options().dtype(at::kFloat));
     const c10::DeviceGuard guard(q.device());
     const at::Tensor ws =

@@ -531,3 +531,9 @@ def test_keys_that_are_not_finite_stay_in_their_branch(N, hq, hkv, lens):
                 assert o[b, n].isnan().all() and l[b, n].isnan().all()
             else:
                 assert torch.equal(o[b, n], ref_o[b, n]) and torch.equal(l[b, n], ref_l[b, n])
+
+
+def test_a_flag_without_a_truth_value_is_refused():
+    c = _case(1, [20, 30], 4, 4, 2, 64, 16, torch.bfloat16)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        _sv().tree_attention(c["q"], c["k"], c["v"], c["table"], c["len"], c["parent"], return_lse=torch.ones(2))
