@@ -550,6 +550,11 @@ def exact(case, seed):
             "sparse": _exact_sparse}[case["op"]](s)
 
 
+def _power(e):
+    """2^e for whole e, in 64 bits, exact on every device."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _stored(pool, page, D, pg, at, values):
     """The numbers that a 4-bit pool [pages, hkv, bytes] holds at places (pg, at) [L], as [L, hkv, D] in 64 bits,
     each fetched by the position of its byte."""
@@ -572,7 +577,7 @@ def _stored(pool, page, D, pg, at, values):
         return pool[pg.view(-1, 1, 1), head, index.unsqueeze(1)].long()
     c = (take(base + code + bit // 8) >> (bit % 8).unsqueeze(1)) & 15
     b = take(base + scale)
-    return (c - 8).double() * torch.ldexp(1.0 + (b % 8).double() / 8.0, (b // 8 - 19))
+    return (c - 8).double() * ((1.0 + (b % 8).double() / 8.0) * _power(b // 8 - 19))
 
 
 def _exact_rows(q, kk, vv, seen):
@@ -623,7 +628,7 @@ def _exact_kept(x):
     D, C = x.shape[-1], _channels(x.shape[-1])
     g = torch.nn.functional.pad(x.double(), (0, C - D)).unflatten(-1, (-1, 32))
     m, e = torch.frexp(g.abs().amax(-1, keepdim=True) / 7.0)             # m in [1/2, 1)
-    s = torch.ldexp(torch.round(m * 16.0) / 16.0, e)
+    s = torch.round(m * 16.0) / 16.0 * _power(e)
     s = s.clamp(2.0 ** -19, 1.875 * 2.0 ** 12)
     return (torch.round(g / s).clamp(-8, 7) * s).flatten(-2)[..., :D]
 
