@@ -46,6 +46,8 @@ extern "C" {
 #define SPEC_DEV_NO_PAGES 32u /* too few free pages: the requests not served keep what they had */
 #define SPEC_DEV_BAD_SLOT 64u /* a fork whose slots are out of range or in use twice */
 
+#define SPEC_DEV_BAD_VALUE 128u /* a key or value that is not finite was written to a 4-bit cache */
+
 #define SPEC_MAX_SLOTS 8192   /* largest number of slots (rows of the page table) */
 #define SPEC_MAX_HEAD_DIM 128 /* largest head dimension of spec_tree_attention */
 
@@ -215,6 +217,178 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
                                   int Hq, int max_pages, float scale, int window, int sinks,
                                   void *out, float *lse, void *workspace, size_t workspace_bytes,
                                   uint32_t *dev_status, void *stream);
+
+/*
+ * The 4-bit cache.  Keys and values in 17/64 of their 16-bit size, for a drafter
+ * or any model that reads a long cache once per token.  Its pages are taken,
+ * returned and listed as those above (spec_cache_resize); every call below is
+ * the 4-bit form of the one above it is named after.
+ *
+ * 32 channels of one token and key head share a scale s = (1 + m/8) 2^(e - 19),
+ * kept as the byte 8 e + m (every byte is a finite scale): a seventh of their
+ * largest magnitude, rounded to the nearest such number, ties to even.  A
+ * number x is kept as the code clamp(rint(x / s), -8, 7) + 8 and stands for
+ * (code - 8) s, which bfloat16 and float16 hold exactly.  Whatever bytes a pool
+ * holds, the numbers they stand for are finite: a NaN is kept as 0 and an infinity
+ * as the largest number of its sign, both reported (SPEC_DEV_BAD_VALUE); magnitudes
+ * above 7 * 7680 (8 * 7680 below 0) are kept as that.
+ *
+ * Layout.  C = head_dim rounded up to 32.  The bytes of one page and head are
+ * page_size / T blocks of T = min(page_size, 128) tokens, one after the other,
+ * each (t: token of the block)
+ *   keys' codes    [T / 8][C / 32][8 tokens][16 bytes]   32 channels of a token
+ *   values' codes  [T / 8][C][4 bytes]                   8 tokens of a channel
+ *   keys' scales   [C / 32][T]
+ *   values' scales [C / 32][T]
+ * The eight codes of a 4-byte word (channels or tokens 0 .. 7) lie at its bits
+ * 0, 16, 4, 20, 8, 24, 12, 28.
+ */
+typedef struct {
+    void *data; /* 16-byte aligned */
+    int layers; /* layers the call works on */
+    int num_pages;
+    int page_size; /* tokens per page: a power of two of at least 8 */
+    int heads;     /* key/value heads */
+    int head_dim;  /* a multiple of 8, at most SPEC_MAX_HEAD_DIM */
+    long long layer_stride; /* strides in bytes: multiples of 16; where the extent is above 1 a stride steps over */
+    long long page_stride;  /* spec_cache4_page_bytes and all that the smaller strides reach */
+    long long head_stride;
+} spec_pages4_t;
+
+/* Bytes of one page and head: page_size * C * 17 / 16; 0 for sizes that are refused. */
+size_t spec_cache4_page_bytes(int page_size, int head_dim);
+
+/*
+ * spec_cache4_append -- as spec_cache_append, k_new and v_new of `dtype`
+ * (SPEC_DTYPE_BF16 or SPEC_DTYPE_F16) quantised on the way.  Rows of the table
+ * must not share the pages that are written.
+ */
+spec_status_t spec_cache4_append(const spec_pages4_t *pages, const int32_t *page_table, const int32_t *cache_len,
+                                 const void *k_new, const void *v_new, spec_dtype_t dtype, long long new_stride_b,
+                                 long long new_stride_n, long long new_stride_h, const int32_t *count, int B, int N,
+                                 int max_pages, uint32_t *dev_status, void *stream);
+
+/*
+ * spec_cache4_read -- the numbers that a 4-bit cache stands for: positions
+ * start[b] + n, n < count[b] (NULL: N each), of request b in every layer of the
+ * pool, written to k and v [layers, B, N, heads, head_dim] contiguous, 16-byte
+ * aligned, of `dtype`.  Rows from count[b] on, positions that the table does
+ * not reach (SPEC_DEV_BAD_LEN) and pages outside the pool (SPEC_DEV_BAD_PAGE)
+ * give 0.  1 <= B < 2^16, 1 <= N.  One launch.
+ */
+spec_status_t spec_cache4_read(const spec_pages4_t *pages, const int32_t *page_table, const int32_t *start,
+                               const int32_t *count, void *k, void *v, spec_dtype_t dtype, int B, int N,
+                               int max_pages, uint32_t *dev_status, void *stream);
+
+/* spec_cache4_commit, spec_cache4_copy, spec_cache4_fork -- as spec_cache_commit,
+   spec_cache_copy and spec_cache_fork.  (A fork copies the last partial page whole.) */
+spec_status_t spec_cache4_commit(const spec_pages4_t *pages, const int32_t *page_table, const int32_t *cache_len,
+                                 const int32_t *out_nodes, const int32_t *accept_len, int32_t *new_len, int B, int N,
+                                 int max_pages, uint32_t *dev_status, void *stream);
+spec_status_t spec_cache4_copy(const spec_pages4_t *pages, const int32_t *src_pages, const int32_t *dst_pages, int n,
+                               uint32_t *dev_status, void *stream);
+spec_status_t spec_cache4_fork(const spec_pages4_t *pages, int32_t *page_table, int32_t *page_count,
+                               int32_t *page_ref, int32_t *cache_len, const int32_t *src, const int32_t *dst, int F,
+                               int slots, int max_pages, void *workspace, size_t workspace_bytes,
+                               uint32_t *dev_status, void *stream);
+
+/*
+ * spec_tree_attention4 -- spec_tree_attention over a 4-bit cache: q and out of
+ * `dtype`, the keys and values the numbers that the codes stand for.
+ *   per_head   0: page_table [B, max_pages]; 1: [B, heads, max_pages], a list of
+ *              pages for every key head, as spec_page_select writes them.
+ *   workspace: spec_tree_attention4_workspace_bytes, 256-byte aligned.
+ * All else, rows that are empty or not finite included, is as there.
+ */
+size_t spec_tree_attention4_workspace_bytes(int B, int N, int Hq, int heads, int head_dim);
+spec_status_t spec_tree_attention4(const void *q, spec_dtype_t dtype, long long q_stride_b, long long q_stride_n,
+                                   long long q_stride_h, const spec_pages4_t *pages, const int32_t *page_table,
+                                   int per_head, const int32_t *cache_len, const int32_t *parent,
+                                   const int32_t *node_count, int B, int N, int Hq, int max_pages, float scale,
+                                   int window, int sinks, void *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
+/*
+ * Attention over selected pages.  A page's bounds are the smallest and the
+ * largest key of each channel over its committed tokens; sum_d max(q_d lo_d, q_d
+ * hi_d) is above every q . k of the page, and a score cheap enough to be formed
+ * for all pages.  One step of a layer:
+ *   spec_cache_bounds     bounds of the pages written since the last step;
+ *   spec_page_scores      a score for every page, request and key head;
+ *   spec_page_select      the best pages of each, as lists of pages;
+ *   spec_sparse_attention (or spec_tree_attention4) over those lists.
+ * The drafted nodes' own keys are attended to as always: their pages follow the
+ * selected ones.
+ */
+
+/*
+ * spec_cache_bounds -- for every page that holds one of the positions [start[b],
+ * cache_len[b]) (start NULL: 0): over the page's positions before cache_len[b]
+ *   bounds[page, h, 0, d] = min k_d,  bounds[page, h, 1, d] = max k_d
+ * (a NaN makes both NaN).  pages->layers = 1; its v is not read.
+ *   bounds  [num_pages, heads, 2, head_dim] of the pool's dtype (`dtype` for a
+ *           4-bit pool), 16-byte aligned.  Other pages keep theirs.
+ * start[b] < 0 counts as 0.  Positions that the table does not reach, and pages outside the pool,
+ * are skipped (SPEC_DEV_BAD_LEN, SPEC_DEV_BAD_PAGE).  1 <= B < 2^16.
+ * SPEC_DTYPE_BF16 and SPEC_DTYPE_F16.  One launch.
+ */
+spec_status_t spec_cache_bounds(const spec_pages_t *pages, const int32_t *page_table, const int32_t *start,
+                                const int32_t *cache_len, void *bounds, int B, int max_pages, uint32_t *dev_status,
+                                void *stream);
+spec_status_t spec_cache4_bounds(const spec_pages4_t *pages, const int32_t *page_table, const int32_t *start,
+                                 const int32_t *cache_len, void *bounds, spec_dtype_t dtype, int B, int max_pages,
+                                 uint32_t *dev_status, void *stream);
+
+/*
+ * spec_page_scores -- scores[b, h, i], the score of the page at place i of
+ * request b's row for key head h: the largest over the nodes n < node_count[b]
+ * (NULL: N each) and the query heads of h of
+ *   sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d
+ * in float32; -inf at places that hold no committed position, or without nodes.  A
+ * score that is not a number is written as NaN.
+ *   q       [B, N, Hq, head_dim] of `dtype`, strides as for spec_tree_attention.
+ *   bounds  [num_pages, heads, 2, head_dim] of `dtype`.
+ *   scores  [B, heads, max_pages] float32.
+ * A page outside the pool scores -inf (SPEC_DEV_BAD_PAGE).  1 <= B < 2^16, 1 <= N <= SPEC_MAX_TREE, Hq a multiple of
+ * heads, Hq / heads <= 64, heads <= 1024, head_dim a multiple of 8 up to SPEC_MAX_HEAD_DIM.
+ * One launch.
+ */
+spec_status_t spec_page_scores(const void *q, spec_dtype_t dtype, long long q_stride_b, long long q_stride_n,
+                               long long q_stride_h, const void *bounds, const int32_t *page_table,
+                               const int32_t *cache_len, const int32_t *node_count, float *scores, int B, int N,
+                               int Hq, int heads, int head_dim, int max_pages, int num_pages, int page_size,
+                               uint32_t *dev_status, void *stream);
+
+/*
+ * spec_page_select -- for each request and key head, of the n =
+ * ceil(cache_len[b] / page_size) pages that hold committed positions, the min(n, keep) that
+ * rank highest, in the order of their places: the first `first` and the last
+ * `recent` ones before all others, then by score (a NaN before all numbers),
+ * equal scores by place, the earlier one first.
+ *   scores     [B, heads, max_pages] float32.
+ *   out_table  [B, heads, keep + tail] int32, tail = ceil(extra / page_size):
+ *              the selected pages, then the `tail` entries that follow the
+ *              committed pages in the request's row (those of `extra` drafted tokens; -1 past
+ *              its end), then -1.
+ *   out_len    [B] int32: the committed positions that the selected pages hold.
+ * So a position p >= cache_len[b] of the cache is position p - cache_len[b] +
+ * out_len[b] of the lists.  cache_len[b] outside [0, max_pages * page_size] is
+ * cut (SPEC_DEV_BAD_LEN).  1 <= B < 2^16, 1 <= heads <= 1024, first >= 0, recent >= 1,
+ * first + recent <= keep, extra >= 0, max_pages <= SPEC_MAX_SELECT.  One launch.
+ */
+#define SPEC_MAX_SELECT 131072 /* largest row of the page table that spec_page_select takes */
+spec_status_t spec_page_select(const float *scores, const int32_t *page_table, const int32_t *cache_len,
+                               int32_t *out_table, int32_t *out_len, int B, int heads, int max_pages, int page_size,
+                               int keep, int first, int recent, int extra, uint32_t *dev_status, void *stream);
+
+/* spec_sparse_attention -- spec_tree_attention with a list of pages for every key
+   head: page_table [B, heads, max_pages], cache_len the positions that each
+   list of the request holds. */
+spec_status_t spec_sparse_attention(const void *q, long long q_stride_b, long long q_stride_n, long long q_stride_h,
+                                    const spec_pages_t *pages, const int32_t *page_table, const int32_t *cache_len,
+                                    const int32_t *parent, const int32_t *node_count, int B, int N, int Hq,
+                                    int max_pages, float scale, int window, int sinks, void *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

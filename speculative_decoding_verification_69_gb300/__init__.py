@@ -10,8 +10,8 @@ raises.
     out_tokens, accept_len = verify(target, draft, tokens, verify_len, temperature, seed)
     verify_len = schedule_len(draft_maxprob, threshold)
 
-The paged key/value cache and the tree attention that precede the step are in
-cache.py.
+The paged key/value cache (in 16 or 4 bits) and the tree attention that precede the
+step, over all pages or selected ones, are in cache.py.
 """
 import ctypes
 import os
@@ -19,8 +19,10 @@ import os
 import torch
 
 from . import _build, cache
-from .cache import (DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_NO_PAGES, DTYPE_F16, PagedCache,  # noqa: F401
-                    cache_append, cache_commit, cache_copy, cache_fork, cache_resize, tree_attention)
+from .cache import (DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_BAD_VALUE, DEV_NO_PAGES, DTYPE_F16, PagedCache,  # noqa: F401
+                    PagedCache4, cache4_append, cache4_bounds, cache4_commit, cache4_copy, cache4_fork,
+                    cache4_page_bytes, cache4_read, cache_append, cache_bounds, cache_commit, cache_copy, cache_fork,
+                    cache_resize, page_scores, page_select, tree_attention, tree_attention4)
 
 SPEC_OK = 0
 DTYPE_F32, DTYPE_BF16 = 0, 1

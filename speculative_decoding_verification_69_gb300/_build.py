@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libspecverify.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "spec_cache.cu", "tree_attn.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "spec_cache.cu", "tree_attn.cu", "cache4.cu",
+                                              "tree_attn4.cu", "page_select.cu")]
 BINDING = os.path.join(CSRC, "binding.cpp")
 HEADERS = [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_cache.h")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + HEADERS

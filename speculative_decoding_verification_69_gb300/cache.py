@@ -20,6 +20,19 @@ every step runs in the library's kernels, on torch's current stream or the
 CUDA graph: a call without a `workspace` (a uint8 tensor, 256-byte aligned) takes
 one from torch's allocator, in a capture from the graph's own memory.  Nothing here
 has a backward pass: with gradients enabled, tensors that require one are refused.
+
+A long cache that is read once per token, as a drafter's, can be made cheap in two
+ways.  PagedCache4 holds it in 4 bits: the same methods, its attention called
+tree_attention4.  Attention over selected pages reads only the pages that a
+cheap score picks, of either cache:
+
+    bounds = cache.new_bounds()                       # of one layer
+    cache.append(layer, k_new, v_new)
+    pages = cache.select(layer, q, bounds, keep=64, extra=N, start=start)
+    o = cache.attention(layer, q, parent, pages=pages)
+
+`start` int32 [slots]: the lengths up to which the bounds have been formed (None:
+not at all); the pages that hold positions from there on are summarised first.
 """
 import ctypes
 import importlib.util
@@ -29,7 +42,7 @@ import torch
 
 from . import _build
 
-DEV_BAD_PAGE, DEV_NO_PAGES, DEV_BAD_SLOT = 16, 32, 64
+DEV_BAD_PAGE, DEV_NO_PAGES, DEV_BAD_SLOT, DEV_BAD_VALUE = 16, 32, 64, 128
 DTYPE_F16 = 2
 
 
@@ -47,14 +60,33 @@ def declare(L):
     L.spec_tree_attention_workspace_bytes.restype = sz
     L.spec_tree_attention.argtypes = [vp, ll, ll, ll, vp, vp, vp, vp, vp, i, i, i, i, ctypes.c_float, i, i,
                                       vp, vp, vp, sz, vp, vp]
-    for name in ("resize", "fork", "copy", "append", "commit"):
-        getattr(L, "spec_cache_" + name).restype = i
-    L.spec_tree_attention.restype = i
+    L.spec_sparse_attention.argtypes = L.spec_tree_attention.argtypes
+    L.spec_cache4_page_bytes.argtypes = [i, i]
+    L.spec_cache4_page_bytes.restype = sz
+    L.spec_cache4_append.argtypes = [vp, vp, vp, vp, vp, i, ll, ll, ll, vp, i, i, i, vp, vp]
+    L.spec_cache4_read.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp, vp]
+    L.spec_cache4_commit.argtypes = L.spec_cache_commit.argtypes
+    L.spec_cache4_copy.argtypes = L.spec_cache_copy.argtypes
+    L.spec_cache4_fork.argtypes = L.spec_cache_fork.argtypes
+    L.spec_tree_attention4_workspace_bytes.argtypes = [i] * 5
+    L.spec_tree_attention4_workspace_bytes.restype = sz
+    L.spec_tree_attention4.argtypes = [vp, i, ll, ll, ll, vp, vp, i, vp, vp, vp, i, i, i, i, ctypes.c_float, i, i,
+                                       vp, vp, vp, sz, vp, vp]
+    L.spec_cache_bounds.argtypes = [vp, vp, vp, vp, vp, i, i, vp, vp]
+    L.spec_cache4_bounds.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp, vp]
+    L.spec_page_scores.argtypes = [vp, i, ll, ll, ll, vp, vp, vp, vp, vp] + [i] * 8 + [vp, vp]
+    L.spec_page_select.argtypes = [vp] * 5 + [i] * 8 + [vp, vp]
+    for name in EXPORTED:
+        if not name.endswith("_bytes"):
+            getattr(L, name).restype = i
 
 
 EXPORTED = ["spec_cache_resize", "spec_cache_fork_workspace_bytes", "spec_cache_fork", "spec_cache_copy",
             "spec_cache_append", "spec_cache_commit", "spec_tree_attention_workspace_bytes",
-            "spec_tree_attention"]
+            "spec_tree_attention", "spec_sparse_attention", "spec_cache4_page_bytes", "spec_cache4_append",
+            "spec_cache4_read", "spec_cache4_commit", "spec_cache4_copy", "spec_cache4_fork",
+            "spec_tree_attention4_workspace_bytes", "spec_tree_attention4", "spec_cache_bounds", "spec_cache4_bounds",
+            "spec_page_scores", "spec_page_select"]
 
 
 _loaded = None
@@ -142,8 +174,10 @@ def tree_attention(q, k, v, page_table, cache_len, parent=None, *, node_count=No
     (None: chains, N = 1 being the decoding of single tokens); node n of request
     b sees the positions [0, cache_len[b]), its ancestors and itself, with a
     window only the last `window` of them along its path and the first `sinks`
-    tokens.  Returns out [B, N, q_heads, head_dim], with return_lse also the log
-    of the softmax sums, float32 [B, N, q_heads]."""
+    tokens.  page_table [B, max_pages], or [B, kv_heads, max_pages] (with cache_len as
+    page_select returns them): a list of pages for every key head.  Returns out
+    [B, N, q_heads, head_dim], with return_lse also the log of the softmax sums,
+    float32 [B, N, q_heads]."""
     if stream is None:
         return _native().tree_attention(q, k, v, page_table, cache_len, parent, node_count, scale, window, sinks, out,
                                         return_lse, workspace, dev_status, None)
@@ -152,21 +186,117 @@ def tree_attention(q, k, v, page_table, cache_len, parent=None, *, node_count=No
                                         return_lse, workspace, dev_status, None)
 
 
-class PagedCache:
-    """The cache of a batch of `slots` requests: pools of pages for every layer,
-    the page table, the lengths, and the status word the calls report in.  The
-    methods work on all slots; single slots are filled, kept or released with
-    cache_resize and want_len (0: released, negative: left alone).  dtype:
-    bfloat16 or float16, or float32 for the pages alone (attention refuses it)."""
+def cache4_page_bytes(page_size, head_dim):
+    """Bytes of one page and head of a 4-bit pool (spec_cache4_page_bytes)."""
+    from . import load_library
+    n = load_library().spec_cache4_page_bytes(page_size, head_dim)
+    if n == 0:
+        raise ValueError("page_size must be a power of two of at least 8, head_dim a multiple of 8 up to 128")
+    return n
 
-    def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, slots, max_pages, *,
-                 dtype=torch.bfloat16, device="cuda"):
-        shape = (layers, num_pages, page_size, kv_heads, head_dim)
-        self.page_size = page_size
-        self.k = torch.empty(shape, dtype=dtype, device=device)
-        self.v = torch.empty(shape, dtype=dtype, device=device)
-        self._layers = list(zip(self.k.unbind(0), self.v.unbind(0)))
+
+def cache4_append(pool, page_table, cache_len, k_new, v_new, page_size, *, count=None, dev_status=None, stream=None):
+    """New keys and values of one layer quantised into a 4-bit pool (spec_cache4_append): pool uint8
+    [num_pages, kv_heads, cache4_page_bytes(page_size, head_dim)]; the rest as for cache_append,
+    k_new and v_new bfloat16 or float16."""
+    _native().append4(pool, page_table, cache_len, k_new, v_new, page_size, count, dev_status, _handle(stream))
+
+
+def cache4_read(pool, page_table, start, n, page_size, head_dim, *, count=None, dtype=torch.bfloat16, dev_status=None,
+                stream=None):
+    """The numbers that a 4-bit pool stands for (spec_cache4_read): positions start[b] + i, i < count[b] (None: n)
+    of every request b.  start and count int32 [B].  Returns k and v [B, n, kv_heads, head_dim], for a pool
+    [layers, num_pages, ...] with the layers in front; rows from count[b] on are 0."""
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("the numbers come as bfloat16 or float16")
+    args = (pool, page_table, start, n, page_size, head_dim, count, dtype == torch.float16, dev_status, None)
+    if stream is None:
+        return _native().read4(*args)
+    with torch.cuda.stream(stream):  # what the call allocates belongs to that stream
+        return _native().read4(*args)
+
+
+def cache4_commit(pool, page_table, cache_len, out_nodes, accept_len, page_size, head_dim, *, new_len=None, nodes=None,
+                  dev_status=None, stream=None):
+    """cache_commit for a 4-bit pool [layers, num_pages, ...] (spec_cache4_commit)."""
+    if new_len is None:
+        new_len = cache_len
+    _native().commit4(pool, page_table, cache_len, out_nodes, accept_len, page_size, head_dim, new_len, nodes,
+                      dev_status, _handle(stream))
+    return new_len
+
+
+def cache4_copy(pool, src_pages, dst_pages, page_size, head_dim, *, dev_status=None, stream=None):
+    """cache_copy for a 4-bit pool [layers, num_pages, ...] (spec_cache4_copy)."""
+    _native().copy4(pool, src_pages, dst_pages, page_size, head_dim, dev_status, _handle(stream))
+
+
+def cache4_fork(pool, page_table, page_count, page_ref, cache_len, src, dst, page_size, head_dim, *, workspace=None,
+                dev_status=None, stream=None):
+    """cache_fork for a 4-bit pool [layers, num_pages, ...] (spec_cache4_fork)."""
+    args = (pool, page_table, page_count, page_ref, cache_len, src, dst, page_size, head_dim, workspace, dev_status,
+            None)
+    if stream is None:
+        _native().fork4(*args)
+    else:
+        with torch.cuda.stream(stream):  # a workspace of the call's own belongs to that stream
+            _native().fork4(*args)
+
+
+def tree_attention4(q, pool, page_table, cache_len, page_size, parent=None, *, node_count=None, scale=None, window=0,
+                    sinks=0, out=None, return_lse=False, workspace=None, dev_status=None, stream=None):
+    """tree_attention over one layer of a 4-bit cache (spec_tree_attention4): pool uint8 [num_pages,
+    kv_heads, page_bytes], q [B, N, q_heads, head_dim] bfloat16 or float16; all else as there."""
+    args = (q, pool, page_table, cache_len, page_size, parent, node_count, scale, window, sinks, out, return_lse,
+            workspace, dev_status, None)
+    if stream is None:
+        return _native().tree_attention4(*args)
+    with torch.cuda.stream(stream):  # what the call allocates belongs to that stream
+        return _native().tree_attention4(*args)
+
+
+def cache_bounds(k, bounds, page_table, cache_len, *, start=None, dev_status=None, stream=None):
+    """Smallest and largest key of each channel (spec_cache_bounds) of the pages that hold positions [start[b],
+    cache_len[b]): bounds [num_pages, kv_heads, 2, head_dim] of the keys' dtype, updated; k [num_pages,
+    page_size, kv_heads, head_dim] bfloat16 or float16, start int32 [B], None: 0."""
+    _native().bounds(k, bounds, page_table, cache_len, start, dev_status, _handle(stream))
+
+
+def cache4_bounds(pool, bounds, page_table, cache_len, page_size, *, start=None, dev_status=None, stream=None):
+    """cache_bounds for one layer of a 4-bit pool (spec_cache4_bounds), bounds bfloat16 or float16."""
+    _native().bounds4(pool, bounds, page_table, cache_len, page_size, start, dev_status, _handle(stream))
+
+
+def page_scores(q, bounds, page_table, cache_len, page_size, *, node_count=None, out=None, dev_status=None, stream=None):
+    """An upper bound of q . k over every page (spec_page_scores), the largest over the nodes and query heads of
+    a key head: q [B, N, q_heads, head_dim] of the bounds' dtype.  Returns float32 [B, kv_heads,
+    max_pages], -inf where a place holds no committed position."""
+    args = (q, bounds, page_table, cache_len, page_size, node_count, out, dev_status, None)
+    if stream is None:
+        return _native().scores(*args)
+    with torch.cuda.stream(stream):  # what the call allocates belongs to that stream
+        return _native().scores(*args)
+
+
+def page_select(scores, page_table, cache_len, page_size, keep, *, first=1, recent=1, extra=0, dev_status=None,
+                stream=None):
+    """The `keep` pages of each request and key head that rank highest (spec_page_select), the first `first` and
+    last `recent` ones before all others, and behind them the pages of `extra` drafted tokens.  Returns
+    (table, length): int32 [B, kv_heads, keep + ceil(extra / page_size)] and [B], the page_table
+    and cache_len of attention over these pages."""
+    args = (scores, page_table, cache_len, page_size, keep, first, recent, extra, dev_status, None)
+    if stream is None:
+        return _native().select(*args)
+    with torch.cuda.stream(stream):  # what the call allocates belongs to that stream
+        return _native().select(*args)
+
+
+class _Slots:
+    """The page table, the lengths and the status word of a batch of `slots` requests."""
+
+    def _slots(self, num_pages, page_size, slots, max_pages, device):
         i32 = dict(dtype=torch.int32, device=device)
+        self.page_size = page_size
         self.page_table = torch.full((slots, max_pages), -1, **i32)
         self.page_count = torch.zeros((slots,), **i32)
         self.page_ref = torch.zeros((num_pages,), **i32)
@@ -182,14 +312,52 @@ class PagedCache:
         """The pages past every slot's length given back."""
         self.reserve(0, stream=stream)
 
+    def select(self, layer, q, bounds, keep, *, start=None, first=1, recent=1, extra=0, stream=None):
+        """Pages for attention(..., pages=): the bounds of the pages written since `start` formed, all pages
+        scored and the best `keep` of each key head taken."""
+        self.summarise(layer, bounds, start=start, stream=stream)
+        scores = page_scores(q, bounds, self.page_table, self.cache_len, self.page_size, dev_status=self.status,
+                             stream=stream)
+        return page_select(scores, self.page_table, self.cache_len, self.page_size, keep, first=first, recent=recent,
+                           extra=extra, dev_status=self.status, stream=stream)
+
+    def _lists(self, pages):
+        return (self.page_table, self.cache_len) if pages is None else pages
+
+
+class PagedCache(_Slots):
+    """The cache of a batch of `slots` requests: pools of pages for every layer,
+    the page table, the lengths, and the status word the calls report in.  The
+    methods work on all slots; single slots are filled, kept or released with
+    cache_resize and want_len (0: released, negative: left alone).  dtype:
+    bfloat16 or float16, or float32 for the pages alone (attention refuses it)."""
+
+    def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, slots, max_pages, *,
+                 dtype=torch.bfloat16, device="cuda"):
+        shape = (layers, num_pages, page_size, kv_heads, head_dim)
+        self.k = torch.empty(shape, dtype=dtype, device=device)
+        self.v = torch.empty(shape, dtype=dtype, device=device)
+        self._layers = list(zip(self.k.unbind(0), self.v.unbind(0)))
+        self._slots(num_pages, page_size, slots, max_pages, device)
+
+    def new_bounds(self):
+        """Bounds of one layer's pages, for select."""
+        _, num_pages, _, heads, head_dim = self.k.shape
+        return torch.zeros((num_pages, heads, 2, head_dim), dtype=self.k.dtype, device=self.k.device)
+
+    def summarise(self, layer, bounds, start=None, stream=None):
+        cache_bounds(self._layers[layer][0], bounds, self.page_table, self.cache_len, start=start,
+                     dev_status=self.status, stream=stream)
+
     def append(self, layer, k_new, v_new, count=None, stream=None):
         k, v = self._layers[layer]
         cache_append(k, v, self.page_table, self.cache_len, k_new, v_new, count=count,
                      dev_status=self.status, stream=stream)
 
-    def attention(self, layer, q, parent=None, **kw):
+    def attention(self, layer, q, parent=None, pages=None, **kw):
         k, v = self._layers[layer]
-        return tree_attention(q, k, v, self.page_table, self.cache_len, parent, dev_status=self.status, **kw)
+        table, length = self._lists(pages)
+        return tree_attention(q, k, v, table, length, parent, dev_status=self.status, **kw)
 
     def commit(self, out_nodes, accept_len, nodes=None, stream=None):
         cache_commit(self.k, self.v, self.page_table, self.cache_len, out_nodes, accept_len, nodes=nodes,
@@ -198,3 +366,50 @@ class PagedCache:
     def fork(self, src, dst, workspace=None, stream=None):
         cache_fork(self.k, self.v, self.page_table, self.page_count, self.page_ref, self.cache_len, src, dst,
                    workspace=workspace, dev_status=self.status, stream=stream)
+
+
+class PagedCache4(_Slots):
+    """PagedCache held in 4 bits: 17/64 of the bytes of bfloat16.  dtype: bfloat16 or float16, that of the
+    queries, of new keys and values and of what is read back."""
+
+    def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, slots, max_pages, *, dtype=torch.bfloat16,
+                 device="cuda"):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("a 4-bit cache serves bfloat16 or float16")
+        self.head_dim, self.dtype = head_dim, dtype
+        self.pool = torch.empty((layers, num_pages, kv_heads, cache4_page_bytes(page_size, head_dim)),
+                                dtype=torch.uint8, device=device)
+        self._layers = list(self.pool.unbind(0))
+        self._slots(num_pages, page_size, slots, max_pages, device)
+
+    def new_bounds(self):
+        """Bounds of one layer's pages, for select."""
+        _, num_pages, heads, _ = self.pool.shape
+        return torch.zeros((num_pages, heads, 2, self.head_dim), dtype=self.dtype, device=self.pool.device)
+
+    def summarise(self, layer, bounds, start=None, stream=None):
+        cache4_bounds(self._layers[layer], bounds, self.page_table, self.cache_len, self.page_size, start=start,
+                      dev_status=self.status, stream=stream)
+
+    def append(self, layer, k_new, v_new, count=None, stream=None):
+        cache4_append(self._layers[layer], self.page_table, self.cache_len, k_new, v_new, self.page_size, count=count,
+                      dev_status=self.status, stream=stream)
+
+    def read(self, start, n, layer=None, count=None, stream=None):
+        """Keys and values of `n` positions from `start` on (int32 [slots]), of one layer or of all."""
+        pool = self.pool if layer is None else self._layers[layer]
+        return cache4_read(pool, self.page_table, start, n, self.page_size, self.head_dim, count=count,
+                           dtype=self.dtype, dev_status=self.status, stream=stream)
+
+    def attention(self, layer, q, parent=None, pages=None, **kw):
+        table, length = self._lists(pages)
+        return tree_attention4(q, self._layers[layer], table, length, self.page_size, parent, dev_status=self.status,
+                               **kw)
+
+    def commit(self, out_nodes, accept_len, nodes=None, stream=None):
+        cache4_commit(self.pool, self.page_table, self.cache_len, out_nodes, accept_len, self.page_size, self.head_dim,
+                      nodes=nodes, dev_status=self.status, stream=stream)
+
+    def fork(self, src, dst, workspace=None, stream=None):
+        cache4_fork(self.pool, self.page_table, self.page_count, self.page_ref, self.cache_len, src, dst,
+                    self.page_size, self.head_dim, workspace=workspace, dev_status=self.status, stream=stream)

@@ -1,0 +1,454 @@
+// page_select.cu -- what chooses the pages that attention reads: the bounds of
+// a page's keys, a score for every page, and the best pages as lists.
+#include "cache4.cuh"
+
+namespace sv {
+
+// ------------------------------------------------------------------ bounds
+
+struct BoundsArgs {
+    Pool P;             // 16-bit pool (vectors)
+    Pool4 P4;           // or 4-bit pool
+    const int *table, *start, *len;
+    uint4 *bounds;      // [page][head][2][vecs]
+    int heads, vecs, page, page_shift, num_pages, max_pages;
+    uint32_t *status;
+};
+
+template <int DT> __device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b);
+template <int DT> __device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b);
+#define SV_PAIR(name, dt, type, fn)                                                                  \
+    template <> __device__ __forceinline__ uint32_t name<dt>(uint32_t a, uint32_t b) {               \
+        const type r = fn(*reinterpret_cast<const type *>(&a), *reinterpret_cast<const type *>(&b)); \
+        return *reinterpret_cast<const uint32_t *>(&r);                                              \
+    }
+SV_PAIR(min16, SPEC_DTYPE_BF16, __nv_bfloat162, __hmin2_nan)
+SV_PAIR(max16, SPEC_DTYPE_BF16, __nv_bfloat162, __hmax2_nan)
+SV_PAIR(min16, SPEC_DTYPE_F16, __half2, __hmin2_nan)
+SV_PAIR(max16, SPEC_DTYPE_F16, __half2, __hmax2_nan)
+#undef SV_PAIR
+
+template <int DT> __device__ __forceinline__ void take_bounds(uint4 &lo, uint4 &hi, uint4 a, uint4 b) {
+    lo.x = min16<DT>(lo.x, a.x), lo.y = min16<DT>(lo.y, a.y), lo.z = min16<DT>(lo.z, a.z), lo.w = min16<DT>(lo.w, a.w);
+    hi.x = max16<DT>(hi.x, b.x), hi.y = max16<DT>(hi.y, b.y), hi.z = max16<DT>(hi.z, b.z), hi.w = max16<DT>(hi.w, b.w);
+}
+
+// Grid (runs of pages, requests), block (vector columns, tokens): the columns' threads take
+// every blockDim.y-th token and join in shared memory.
+template <int DT, bool FOUR>
+__global__ void __launch_bounds__(256) sv_bounds(const __grid_constant__ BoundsArgs A) {
+    __shared__ uint4 part[2][256];
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.y, from = A.start ? max(A.start[b], 0) : 0;
+    long long end = A.len[b];
+    const bool lead = blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0;
+    if (end < 0 || end > (long long)A.max_pages << A.page_shift) {
+        if (lead) flag(A.status, SPEC_DEV_BAD_LEN);
+        end = end < 0 ? 0 : (long long)A.max_pages << A.page_shift;
+    }
+    if (from >= end) return;
+    const int last = (int)((end - 1) >> A.page_shift);
+    const int cols = A.heads * A.vecs;
+    for (int i = (from >> A.page_shift) + blockIdx.x; i <= last; i += gridDim.x) {
+        const int p = A.table[(long long)b * A.max_pages + i];
+        if ((unsigned)p >= (unsigned)A.num_pages) {
+            if (threadIdx.x == 0 && threadIdx.y == 0) flag(A.status, SPEC_DEV_BAD_PAGE);
+            continue;
+        }
+        const int used = (int)min((long long)A.page, end - ((long long)i << A.page_shift));
+        for (int c0 = 0; c0 < cols; c0 += blockDim.x) {
+            const int c = c0 + threadIdx.x, h = c / A.vecs, d8 = c - h * A.vecs;
+            const uint32_t pinf = DT == SPEC_DTYPE_BF16 ? 0x7F807F80u : 0x7C007C00u, ninf = pinf | 0x80008000u;
+            uint4 lo = make_uint4(pinf, pinf, pinf, pinf), hi = make_uint4(ninf, ninf, ninf, ninf);
+            if (c < cols) {
+                if constexpr (!FOUR) {
+                    const uint4 *k = A.P.k + (long long)p * A.P.page_st + (long long)h * A.P.head + d8;
+#pragma unroll 8
+                    for (int t = threadIdx.y; t < used; t += blockDim.y) {
+                        const uint4 x = ld_stream_v4(k + (long long)t * A.P.token);
+                        take_bounds<DT>(lo, hi, x, x);
+                    }
+                } else {
+                    const uint8_t *k = A.P4.data + p * A.P4.page_st + h * A.P4.head;
+#pragma unroll 4
+                    for (int t = threadIdx.y; t < used; t += blockDim.y) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t *>(k + key4(A.P4, t, d8 >> 2) + (d8 & 3) * 4);
+                        const float s = scale_of(k[scale4(A.P4, t, d8 >> 2, false)]);
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2)
+                            y[e / 2] = pack16<DT>(((float)((w >> bit4(e)) & 15u) - 8.f) * s,
+                                                  ((float)((w >> bit4(e + 1)) & 15u) - 8.f) * s);
+                        const uint4 x = make_uint4(y[0], y[1], y[2], y[3]);
+                        take_bounds<DT>(lo, hi, x, x);
+                    }
+                }
+            }
+            if (blockDim.y > 1) {
+                const int at = threadIdx.y * blockDim.x + threadIdx.x;
+                __syncthreads();
+                part[0][at] = lo, part[1][at] = hi;
+                __syncthreads();
+                if (threadIdx.y == 0)
+                    for (int y = 1; y < blockDim.y; ++y)
+                        take_bounds<DT>(lo, hi, part[0][y * blockDim.x + threadIdx.x], part[1][y * blockDim.x + threadIdx.x]);
+            }
+            if (threadIdx.y == 0 && c < cols) {
+                uint4 *to = A.bounds + ((long long)p * A.heads + h) * 2 * A.vecs + d8;
+                to[0] = lo;
+                to[A.vecs] = hi;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ scores
+
+struct ScoreArgs {
+    const uint4 *q, *bounds;
+    long long qb, qn, qh;  // strides of q in 16-byte vectors
+    const int *table, *len, *node_count;
+    float *scores;
+    int B, N, G, heads, vecs, max_pages, num_pages, page, page_shift, tiles;
+    uint32_t *status;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// c += A (16 pages x 16 channels) B (16 channels x 8 rows)
+template <int DT>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    if (DT == SPEC_DTYPE_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A warp scores 16 pages for one key head: the product of the pages' bounds [hi | lo] with the
+// rows' [max(q, 0) | min(q, 0)], 16 pages by 8 rows at a time.  Bound by reading the bounds once
+// (4 bytes per channel), which the warps' mma.sync keeps up with to about 64 rows: the operands
+// go from HBM to registers in the product's own layout (a thread's share of the channels is
+// contiguous, since any order of them gives the same sum) and pass no shared memory.
+template <int DT, int BLOCKS>  // BLOCKS of 32 channels
+__global__ void __launch_bounds__(256) sv_scores(const __grid_constant__ ScoreArgs A) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int h = (int)(unit % A.heads), tile = (int)(unit / A.heads % A.tiles), b = (int)(unit / A.heads / A.tiles);
+    if (b >= A.B) return;
+    long long len = A.len[b];
+    if (len < 0 || len > (long long)A.max_pages << A.page_shift) {
+        if (tile == 0 && h == 0 && lane == 0) flag(A.status, SPEC_DEV_BAD_LEN);
+        len = len < 0 ? 0 : (long long)A.max_pages << A.page_shift;
+    }
+    const int n = (int)((len + A.page - 1) >> A.page_shift);
+    const int rows = (A.node_count ? max(0, min(A.node_count[b], A.N)) : A.N) * A.G;
+    float *out = A.scores + ((long long)b * A.heads + h) * A.max_pages;
+    const int i0 = tile * 16;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 lo[2][BLOCKS], hi[2][BLOCKS];
+    bool there[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = i0 + g + 8 * u;
+        int p = i < n ? A.table[(long long)b * A.max_pages + i] : -1;
+        there[u] = (unsigned)p < (unsigned)A.num_pages;
+        if (i < n && !there[u] && t == 0) flag(A.status, SPEC_DEV_BAD_PAGE);
+        const uint4 *x = A.bounds + ((long long)(there[u] ? p : 0) * A.heads + h) * 2 * A.vecs;
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+            const bool real = there[u] && rows > 0 && k * 4 + t < A.vecs;
+            lo[u][k] = real ? ld_stream_v4(x + k * 4 + t) : none;
+            hi[u][k] = real ? ld_stream_v4(x + A.vecs + k * 4 + t) : none;
+        }
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        const int r = r0 + g, node = r / A.G;
+        const uint4 *q = A.q + b * A.qb + node * A.qn + (long long)(h * A.G + r - node * A.G) * A.qh;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+            const uint4 y = r < rows && k * 4 + t < A.vecs ? __ldg(q + k * 4 + t) : none;
+            mma16<DT>(c, hi[0][k].x, hi[1][k].x, hi[0][k].y, hi[1][k].y, max16<DT>(y.x, 0u), max16<DT>(y.y, 0u));
+            mma16<DT>(c, hi[0][k].z, hi[1][k].z, hi[0][k].w, hi[1][k].w, max16<DT>(y.z, 0u), max16<DT>(y.w, 0u));
+            mma16<DT>(c, lo[0][k].x, lo[1][k].x, lo[0][k].y, lo[1][k].y, min16<DT>(y.x, 0u), min16<DT>(y.y, 0u));
+            mma16<DT>(c, lo[0][k].z, lo[1][k].z, lo[0][k].w, lo[1][k].w, min16<DT>(y.z, 0u), min16<DT>(y.w, 0u));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (r0 + 2 * t + e < rows) {
+                best[0] = max_nan(best[0], c[e]);
+                best[1] = max_nan(best[1], c[2 + e]);
+            }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        best[u] = max_nan(best[u], __shfl_xor_sync(0xFFFFFFFFu, best[u], 1));
+        best[u] = max_nan(best[u], __shfl_xor_sync(0xFFFFFFFFu, best[u], 2));
+        const int i = i0 + g + 8 * u;
+        if (t == 0 && i < A.max_pages) out[i] = there[u] ? best[u] : -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------------ selection
+
+struct SelectArgs {
+    const float *scores;
+    const int *table, *len;
+    int *out_table, *out_len;
+    int heads, max_pages, page, page_shift, keep, first, recent, tail;
+    uint32_t *status;
+};
+
+// A score as a number that orders alike, NaN before all others; 0 for no page.
+__device__ __forceinline__ uint32_t rank_of(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);  // (-0 is 0)
+    if (x != x) return 0xFFFFFFFEu;
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// A CTA selects for one request and key head.  The threads own runs of consecutive places, in
+// registers where they fit; the rank of the last page taken is found two bits at a time by
+// counting (16 rounds of three counts and one barrier, instead of histograms whose few bins, as
+// scores lie close together, would be fought over); then a scan gives every page its place.
+template <int THREADS, int ITEMS>  // ITEMS 0: any number, read anew in every round
+__global__ void __launch_bounds__(THREADS) sv_select(const __grid_constant__ SelectArgs A) {
+    constexpr int kWarps = THREADS / 32;
+    __shared__ int counts[2][3][kWarps];
+    __shared__ int scan[2][kWarps];
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    long long len = A.len[b];
+    if (len < 0 || len > (long long)A.max_pages << A.page_shift) {
+        if (h == 0 && tid == 0) flag(A.status, SPEC_DEV_BAD_LEN);
+        len = len < 0 ? 0 : (long long)A.max_pages << A.page_shift;
+    }
+    const int n = (int)((len + A.page - 1) >> A.page_shift), kept = min(n, A.keep);
+    if (h == 0 && tid == 0) A.out_len[b] = (int)(len - ((long long)(n - kept) << A.page_shift));
+    const float *scores = A.scores + ((long long)b * A.heads + h) * A.max_pages;
+    const int *row = A.table + (long long)b * A.max_pages;
+    const int width = A.keep + A.tail;
+    int *out = A.out_table + ((long long)b * A.heads + h) * width;
+    for (int i = tid; i < width - kept; i += THREADS)  // the drafted tokens' pages, and none
+        out[kept + i] = i < A.tail && n + i < A.max_pages ? row[n + i] : -1;
+    if (n <= A.keep) {
+        for (int i = tid; i < n; i += THREADS) out[i] = row[i];
+        return;
+    }
+    const int per = ITEMS ? ITEMS : (n + THREADS - 1) / THREADS, i0 = tid * per;
+    auto rank_at = [&](int i) -> uint32_t {
+        if (i >= n) return 0u;
+        if (i < A.first || i >= n - A.recent) return 0xFFFFFFFFu;
+        return rank_of(scores[i]);
+    };
+    uint32_t mine[ITEMS ? ITEMS : 1];
+    if (ITEMS) {
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) mine[e] = rank_at(i0 + e);
+    }
+    auto each = [&](auto &&f) {
+        if constexpr (ITEMS > 0) {
+#pragma unroll
+            for (int e = 0; e < ITEMS; ++e) f(i0 + e, mine[e]);
+        } else {
+            for (int e = 0; e < per; ++e) f(i0 + e, rank_at(i0 + e));
+        }
+    };
+    // the largest rank that at least `keep` pages reach
+    uint32_t bar = 0;
+    for (int shift = 30, side = 0; shift >= 0; shift -= 2, side ^= 1) {
+        int c[3] = {0, 0, 0};
+        each([&](int, uint32_t r) {
+#pragma unroll
+            for (int x = 0; x < 3; ++x) c[x] += r >= (bar | ((uint32_t)(x + 1) << shift)) ? 1 : 0;
+        });
+#pragma unroll
+        for (int x = 0; x < 3; ++x) c[x] = __reduce_add_sync(0xFFFFFFFFu, c[x]);
+        if (lane == 0)
+            for (int x = 0; x < 3; ++x) counts[side][x][warp] = c[x];
+        __syncthreads();
+        int step = 0;
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (__reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? counts[side][x][lane] : 0) >= A.keep) step = x + 1;
+        bar |= (uint32_t)step << shift;
+    }
+    // pages above the bar are all taken, of those at it the first ones
+    int above = 0, at = 0;
+    each([&](int, uint32_t r) { above += r > bar ? 1 : 0, at += r == bar ? 1 : 0; });
+    int x = above, y = at;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, x, o), v = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) x += u, y += v;
+    }
+    if (lane == 31) scan[0][warp] = x, scan[1][warp] = y;
+    __syncthreads();
+    const int w0 = lane < kWarps ? scan[0][lane] : 0, w1 = lane < kWarps ? scan[1][lane] : 0;
+    const int ties = A.keep - __reduce_add_sync(0xFFFFFFFFu, w0);  // taken of those at the bar
+    int over = x - above + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w0 : 0);
+    int equal = y - at + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w1 : 0);
+    each([&](int i, uint32_t r) {
+        const bool tie = r == bar;
+        if (r > bar || (tie && equal < ties)) out[over + min(equal, ties)] = row[i];
+        over += r > bar ? 1 : 0;
+        equal += tie ? 1 : 0;
+    });
+}
+
+template <class K> static spec_status_t launch_bounds(K kernel, const BoundsArgs &A, int B, cudaStream_t s) {
+    const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256;
+    const int want = (16 * 152 + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
+    return launch_pdl(kernel, dim3((unsigned)runs, (unsigned)B), dim3((unsigned)x, (unsigned)(256 / x)), 0, s, A);
+}
+
+} // namespace sv
+
+extern "C" {
+
+spec_status_t spec_cache_bounds(const spec_pages_t *pages, const int32_t *page_table, const int32_t *start,
+                                const int32_t *cache_len, void *bounds, int B, int max_pages, uint32_t *dev_status,
+                                void *stream) {
+    sv::BoundsArgs A = {};
+    const spec_status_t st = sv::make_pool(pages, A.P);
+    if (st != SPEC_OK) return st;
+    if (pages->dtype != SPEC_DTYPE_BF16 && pages->dtype != SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
+    if (pages->layers != 1 || !page_table || !cache_len || !bounds || ((uintptr_t)bounds & 15) || B < 1 ||
+        B >= (1 << 16) || max_pages < 1)
+        return SPEC_ERR_INVALID_ARG;
+    A.table = page_table;
+    A.start = start;
+    A.len = cache_len;
+    A.bounds = static_cast<uint4 *>(bounds);
+    A.heads = pages->heads;
+    A.vecs = A.P.vecs;
+    A.page = A.P.page;
+    A.page_shift = A.P.page_shift;
+    A.num_pages = A.P.num_pages;
+    A.max_pages = max_pages;
+    A.status = dev_status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return pages->dtype == SPEC_DTYPE_BF16 ? sv::launch_bounds(sv::sv_bounds<SPEC_DTYPE_BF16, false>, A, B, s)
+                                           : sv::launch_bounds(sv::sv_bounds<SPEC_DTYPE_F16, false>, A, B, s);
+}
+
+spec_status_t spec_cache4_bounds(const spec_pages4_t *pages, const int32_t *page_table, const int32_t *start,
+                                 const int32_t *cache_len, void *bounds, spec_dtype_t dtype, int B, int max_pages,
+                                 uint32_t *dev_status, void *stream) {
+    sv::BoundsArgs A = {};
+    const spec_status_t st = sv::make_pool4(pages, A.P4);
+    if (st != SPEC_OK) return st;
+    if (dtype != SPEC_DTYPE_BF16 && dtype != SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
+    if (pages->layers != 1 || !page_table || !cache_len || !bounds || ((uintptr_t)bounds & 15) || B < 1 ||
+        B >= (1 << 16) || max_pages < 1)
+        return SPEC_ERR_INVALID_ARG;
+    A.table = page_table;
+    A.start = start;
+    A.len = cache_len;
+    A.bounds = static_cast<uint4 *>(bounds);
+    A.heads = pages->heads;
+    A.vecs = A.P4.D / 8;
+    A.page = A.P4.page;
+    A.page_shift = A.P4.page_shift;
+    A.num_pages = A.P4.num_pages;
+    A.max_pages = max_pages;
+    A.status = dev_status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_DTYPE_BF16 ? sv::launch_bounds(sv::sv_bounds<SPEC_DTYPE_BF16, true>, A, B, s)
+                                    : sv::launch_bounds(sv::sv_bounds<SPEC_DTYPE_F16, true>, A, B, s);
+}
+
+spec_status_t spec_page_scores(const void *q, spec_dtype_t dtype, long long q_stride_b, long long q_stride_n,
+                               long long q_stride_h, const void *bounds, const int32_t *page_table,
+                               const int32_t *cache_len, const int32_t *node_count, float *scores, int B, int N,
+                               int Hq, int heads, int head_dim, int max_pages, int num_pages, int page_size,
+                               uint32_t *dev_status, void *stream) {
+    if (dtype != SPEC_DTYPE_BF16 && dtype != SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
+    if (!q || !bounds || !page_table || !cache_len || !scores || ((uintptr_t)q & 15) || ((uintptr_t)bounds & 15) ||
+        B < 1 || B >= (1 << 16) || N < 1 || N > SPEC_MAX_TREE || heads < 1 || heads > 1024 || Hq < heads ||
+        Hq % heads || Hq / heads > 64 || head_dim < 8 || head_dim % 8 || head_dim > SPEC_MAX_HEAD_DIM ||
+        max_pages < 1 || num_pages < 1 || page_size < 8 || page_size > (1 << 20) || (page_size & (page_size - 1)))
+        return SPEC_ERR_INVALID_ARG;
+    const long long qst[3] = {q_stride_h, q_stride_n, q_stride_b};
+    const int qext[3] = {Hq, N, B};
+    for (int i = 0; i < 3; ++i)
+        if (qst[i] % 8 || qst[i] < (qext[i] > 1 ? head_dim : 0)) return SPEC_ERR_INVALID_ARG;
+    sv::ScoreArgs A = {};
+    A.q = static_cast<const uint4 *>(q);
+    A.bounds = static_cast<const uint4 *>(bounds);
+    A.qb = q_stride_b / 8;
+    A.qn = q_stride_n / 8;
+    A.qh = q_stride_h / 8;
+    A.table = page_table;
+    A.len = cache_len;
+    A.node_count = node_count;
+    A.scores = scores;
+    A.B = B;
+    A.N = N;
+    A.G = Hq / heads;
+    A.heads = heads;
+    A.vecs = head_dim / 8;
+    A.max_pages = max_pages;
+    A.num_pages = num_pages;
+    A.page = page_size;
+    while ((1 << A.page_shift) < page_size) ++A.page_shift;
+    A.tiles = (max_pages - 1) / 16 + 1;
+    A.status = dev_status;
+    const long long ctas = ((long long)B * heads * A.tiles + 7) / 8;
+    if (ctas >= (1ll << 31)) return SPEC_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)ctas), block(256);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf = dtype == SPEC_DTYPE_BF16;
+    if (head_dim <= 64)
+        return bf ? sv::launch_pdl(sv::sv_scores<SPEC_DTYPE_BF16, 2>, grid, block, 0, s, A)
+                  : sv::launch_pdl(sv::sv_scores<SPEC_DTYPE_F16, 2>, grid, block, 0, s, A);
+    return bf ? sv::launch_pdl(sv::sv_scores<SPEC_DTYPE_BF16, 4>, grid, block, 0, s, A)
+              : sv::launch_pdl(sv::sv_scores<SPEC_DTYPE_F16, 4>, grid, block, 0, s, A);
+}
+
+spec_status_t spec_page_select(const float *scores, const int32_t *page_table, const int32_t *cache_len,
+                               int32_t *out_table, int32_t *out_len, int B, int heads, int max_pages, int page_size,
+                               int keep, int first, int recent, int extra, uint32_t *dev_status, void *stream) {
+    if (!scores || !page_table || !cache_len || !out_table || !out_len || B < 1 || B >= (1 << 16) || heads < 1 ||
+        heads > 1024 || max_pages < 1 || max_pages > SPEC_MAX_SELECT || page_size < 8 || page_size > (1 << 20) ||
+        (page_size & (page_size - 1)) || keep < 1 || keep > SPEC_MAX_SELECT || first < 0 || recent < 1 ||
+        first > keep - recent || extra < 0 || extra > (1 << 20))
+        return SPEC_ERR_INVALID_ARG;
+    sv::SelectArgs A = {};
+    A.scores = scores;
+    A.table = page_table;
+    A.len = cache_len;
+    A.out_table = out_table;
+    A.out_len = out_len;
+    A.heads = heads;
+    A.max_pages = max_pages;
+    A.page = page_size;
+    while ((1 << A.page_shift) < page_size) ++A.page_shift;
+    A.keep = keep;
+    A.first = first;
+    A.recent = recent;
+    A.tail = (extra + page_size - 1) / page_size;
+    A.status = dev_status;
+    const dim3 grid((unsigned)heads, (unsigned)B);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (max_pages <= 256 * 4) return sv::launch_pdl(sv::sv_select<256, 4>, grid, dim3(256), 0, s, A);
+    if (max_pages <= 1024 * 8) return sv::launch_pdl(sv::sv_select<1024, 8>, grid, dim3(1024), 0, s, A);
+    if (max_pages <= 1024 * 16) return sv::launch_pdl(sv::sv_select<1024, 16>, grid, dim3(1024), 0, s, A);
+    return sv::launch_pdl(sv::sv_select<1024, 0>, grid, dim3(1024), 0, s, A);
+}
+
+} // extern "C"

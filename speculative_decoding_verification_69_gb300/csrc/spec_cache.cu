@@ -24,15 +24,6 @@ constexpr int kPgCtas = 8;       // CTAs of the bookkeeping cluster
 constexpr int kPgThreads = 1024; // threads of each
 constexpr int kPgWarps = kPgThreads / 32;
 
-struct PagesArgs {
-    int *table, *count, *ref, *len;  // len: forks only
-    const int *want;                 // resize only
-    const int *src, *dst;            // forks only
-    int *copies;                     // forks only: [n, 3] page to copy, its copy, tokens (0: none)
-    int extra, page_shift, n, slots, max_pages, num_pages;  // n: items (slots or forks)
-    uint32_t *status;
-};
-
 // Saturating sum of page counts: anything above the pool's size is as good as
 // cap = num_pages + 1 (nothing that large is ever served), and sums capped this
 // way stay associative and within 32 bits.
@@ -282,7 +273,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
         if constexpr (FORK) {
             const PagesItem<true> it = items[i];
             const bool ok = it.kind != 2 || incl[i] <= free_total;
-            A.copies[3 * i + 2] = it.kind == 2 && ok ? it.len & (page - 1) : 0;
+            A.copies[3 * i + 2] = it.kind == 2 && ok ? (A.whole ? A.whole : it.len & (page - 1)) : 0;
             if (it.kind == 0) continue;
             if (it.kind == 2 && ok)
                 A.copies[3 * i] = A.table[(long long)it.src * A.max_pages + (it.len >> A.page_shift)];
@@ -389,68 +380,6 @@ __global__ void __launch_bounds__(256) sv_append(Pool P, const int *table,
             P.v[to + (long long)h * P.head + d] = y;
         }
     }
-}
-
-// The accepted path of one request: place 0 is the root's, place 1 + i that of node i.
-// Returns how many nodes after the root are kept, those before the first place without a
-// page (nodes: or the first that is no path), and -1 when the root has none: the length
-// grows by one more.  s_src / s_dst [N]: the nodes' vector offsets inside a layer, before
-// and after.  Called by a whole CTA; warp 0 works.
-__device__ __forceinline__ int commit_path(const Pool &P, const int *table, const int *len,
-                                           const int *nodes, const int *accept, int b, int N,
-                                           int max_pages, long long *s_src, long long *s_dst,
-                                           int *s_n, uint32_t *status, bool report) {
-    const int lane = threadIdx.y * blockDim.x + threadIdx.x;
-    if (lane < 32) {
-        const int a = max(0, min(accept[b], N - 1));
-        const long long n0 = len[b];
-        const int *row = table + (long long)b * max_pages;
-        uint32_t bits = 0;
-        int places = 0;  // the root's and the nodes' that are kept
-        auto offset = [&](long long pos, long long &off) -> bool {  // whether the position has a page
-            const long long place = pos >> P.page_shift;
-            const int p = place < max_pages ? row[place] : -1;
-            off = (long long)p * P.page_st + (pos & (P.page - 1)) * P.token;
-            return (unsigned)p < (unsigned)P.num_pages;
-        };
-        if (n0 < 0) bits = SPEC_DEV_BAD_LEN;
-        else places = a + 1;
-        for (int i0 = 0; i0 < places; i0 += 32) {
-            const int i = i0 + lane;
-            bool bad = false;
-            if (i < places) {
-                long long src, dst;
-                if (!nodes && (n0 + i) >> P.page_shift >= max_pages) {
-                    bits |= SPEC_DEV_BAD_LEN;  // counted: no page will ever stand for it
-                } else if (!offset(n0 + i, dst)) {
-                    bad = true;
-                    bits |= SPEC_DEV_BAD_PAGE;
-                } else if (nodes && i > 0) {
-                    const int n = nodes[(long long)b * N + i - 1];
-                    if (n < i || n >= N) {
-                        bad = true;
-                        bits |= SPEC_DEV_BAD_TREE;
-                    } else if (!offset(n0 + n, src)) {
-                        bad = true;
-                        bits |= SPEC_DEV_BAD_PAGE;
-                    } else {
-                        s_src[i - 1] = src;
-                        s_dst[i - 1] = dst;
-                    }
-                }
-            }
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, bad);
-            if (mask) places = i0 + __ffs(mask) - 1;
-        }
-        if (report && bits) flag(status, bits);
-        if (lane == 0) *s_n = places - 1;
-    }
-    __syncthreads();
-    return *s_n;
-}
-// The length after the root and `kept` nodes (linear drafts may leave 32 bits).
-__device__ __forceinline__ int commit_len(int len, int kept) {
-    return (int)min((long long)len + 1 + kept, (long long)INT_MAX);
 }
 
 // Accepted nodes moved behind their root.  Grid (requests, layers x {k, v}),
@@ -584,6 +513,25 @@ static spec_status_t launch_pages(const PagesArgs &A, cudaStream_t s) {
     return launch_pdl(sv_pages<FORK>, dim3(kPgCtas), dim3(kPgThreads), smem, s, A);
 }
 
+spec_status_t launch_fork(const PagesArgs &A, const Pool &P, cudaStream_t s) {
+    const spec_status_t sp = launch_pages<true>(A, s);
+    if (sp != SPEC_OK) return sp;
+    return launch_copy(P, nullptr, nullptr, A.copies, A.n, A.status, s);
+}
+
+spec_status_t launch_copy(const Pool &P, const int *src, const int *dst, const int *copies, int n, uint32_t *status,
+                          cudaStream_t s) {
+    const dim3 block = column_block(P.cols);
+    return launch_pdl(sv_copy_pages, dim3((unsigned)n, (unsigned)P.layers, (unsigned)copy_blocks(P, block)), block, 0,
+                      s, P, src, dst, copies, status);
+}
+
+spec_status_t launch_commit_len(const Pool &P, const int *table, int *len, const int *nodes, const int *accept, int B,
+                                int N, int max_pages, uint32_t *status, cudaStream_t s) {
+    return launch_pdl(sv_commit_len, dim3((unsigned)B), dim3(64), 0, s, P, table, len, nodes, accept, N, max_pages,
+                      status);
+}
+
 } // namespace sv
 
 extern "C" {
@@ -640,14 +588,7 @@ spec_status_t spec_cache_fork(const spec_pages_t *pages, int32_t *page_table, in
     A.max_pages = max_pages;
     A.num_pages = P.num_pages;
     A.status = dev_status;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const spec_status_t sp = sv::launch_pages<true>(A, s);
-    if (sp != SPEC_OK) return sp;
-    const dim3 block = sv::column_block(P.cols);
-    const int blocks = sv::copy_blocks(P, block);
-    return sv::launch_pdl(sv::sv_copy_pages, dim3((unsigned)F, (unsigned)P.layers, (unsigned)blocks), block, 0, s,
-                          P, (const int *)nullptr, (const int *)nullptr, (const int *)A.copies,
-                          dev_status);
+    return sv::launch_fork(A, P, static_cast<cudaStream_t>(stream));
 }
 
 spec_status_t spec_cache_copy(const spec_pages_t *pages, const int32_t *src_pages,
@@ -656,11 +597,7 @@ spec_status_t spec_cache_copy(const spec_pages_t *pages, const int32_t *src_page
     const spec_status_t st = sv::make_pool(pages, P);
     if (st != SPEC_OK) return st;
     if (!src_pages || !dst_pages || n < 1) return SPEC_ERR_INVALID_ARG;
-    const dim3 block = sv::column_block(P.cols);
-    const int blocks = sv::copy_blocks(P, block);
-    return sv::launch_pdl(sv::sv_copy_pages, dim3((unsigned)n, (unsigned)P.layers, (unsigned)blocks), block, 0,
-                          static_cast<cudaStream_t>(stream), P, src_pages, dst_pages,
-                          (const int *)nullptr, dev_status);
+    return sv::launch_copy(P, src_pages, dst_pages, nullptr, n, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 spec_status_t spec_cache_append(const spec_pages_t *pages, const int32_t *page_table,
@@ -705,8 +642,7 @@ spec_status_t spec_cache_commit(const spec_pages_t *pages, const int32_t *page_t
                            in_place ? (int *)nullptr : new_len, N, max_pages, dev_status);
         if (r != SPEC_OK || !in_place) return r;
     }
-    return sv::launch_pdl(sv::sv_commit_len, dim3((unsigned)B), dim3(64), 0, s, P, page_table, new_len,
-                          out_nodes, accept_len, N, max_pages, dev_status);
+    return sv::launch_commit_len(P, page_table, new_len, out_nodes, accept_len, B, N, max_pages, dev_status, s);
 }
 
 } // extern "C"

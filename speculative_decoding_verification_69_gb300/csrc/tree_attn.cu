@@ -74,6 +74,7 @@ enum { kTaSplitKeys, kTaSplitRows, kTaSplitHeads };
 
 struct TaArgs {
     const int *table, *len, *parent, *node_count;
+    long long row_b, row_h;  // from one request's row of the table to the next, from one key head's (0: one for all)
     int B, N, Hq, H, G, D, max_pages, num_pages, page, page_shift;
     int window, sinks;
     int np;              // nodes of one stream's rows
@@ -446,7 +447,7 @@ __device__ __noinline__ void ta_add_not_finite(const TaArgs &A, Seg s, int hk, u
                                                unsigned long long path, uint32_t base0) {
     constexpr int kCols = MODE == kTaSplitKeys ? DP / 2 : DP;
     const Geo &g = s.g;
-    const int *table = A.table + (long long)s.b * A.max_pages;
+    const int *table = A.table + s.b * A.row_b + hk * A.row_h;
     const uint16_t *v = A.v + hk * A.v_head + col0;
 #pragma unroll 1
     for (int x = 0; x < (two ? 2 : 1); ++x) {
@@ -672,7 +673,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             give(seg_no);
-            const int *row = A.table + (long long)s.b * A.max_pages;
+            // (lists of their own for the key heads: not with kTaSplitHeads)
+            const int *row = A.table + s.b * A.row_b + s.hk * A.row_h;
             const int i_end = s.i0 + s.n;
             // first position of this lane's box in tile i, and whether some node sees any of it
             auto box_pos = [&](int i) -> int { return s.g.tile(i) * kTaKeys + box * A.box; };
@@ -1371,26 +1373,14 @@ static spec_status_t ta_launch_mode(const TaArgs &A, const CUtensorMap &q, const
     }
 }
 
-} // namespace sv
-
-extern "C" {
-
-size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int heads, int head_dim) {
-    if (B < 1 || B >= (1 << 16) || N < 1 || N > SPEC_MAX_TREE || heads < 1 || heads > 1024 || Hq < heads ||
-        Hq % heads || Hq / heads > 64 || head_dim < 8 || head_dim % 8 || head_dim > SPEC_MAX_HEAD_DIM)
-        return 0;
-    return sv::ta_layout(N, Hq, heads, head_dim).total;
-}
-
-spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long q_stride_n,
-                                  long long q_stride_h, const spec_pages_t *pages,
-                                  const int32_t *page_table, const int32_t *cache_len,
-                                  const int32_t *parent, const int32_t *node_count, int B, int N,
-                                  int Hq, int max_pages, float scale, int window, int sinks,
-                                  void *out, float *lse, void *workspace, size_t workspace_bytes,
-                                  uint32_t *dev_status, void *stream) {
-    sv::Pool P;
-    const spec_status_t st = sv::make_pool(pages, P);
+// spec_tree_attention (per_head false) and spec_sparse_attention.
+static spec_status_t ta_call(const void *q, long long q_stride_b, long long q_stride_n, long long q_stride_h,
+                             const spec_pages_t *pages, const int32_t *page_table, bool per_head,
+                             const int32_t *cache_len, const int32_t *parent, const int32_t *node_count, int B, int N,
+                             int Hq, int max_pages, float scale, int window, int sinks, void *out, float *lse,
+                             void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    Pool P;
+    const spec_status_t st = make_pool(pages, P);
     if (st != SPEC_OK) return st;
     if (pages->dtype != SPEC_DTYPE_BF16 && pages->dtype != SPEC_DTYPE_F16) return SPEC_ERR_UNSUPPORTED;
     const int D = pages->head_dim, H = pages->heads;
@@ -1409,7 +1399,7 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
     if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return SPEC_ERR_CUDA;
-    const int ctas = sms[dev] < sv::kTaMaxCtas ? sms[dev] : sv::kTaMaxCtas;
+    const int ctas = sms[dev] < kTaMaxCtas ? sms[dev] : kTaMaxCtas;
 
     // A key head per stream once there is one for every CTA: the streams then share
     // nothing but the CTA, where streams that divide the keys meet at the end of
@@ -1420,18 +1410,20 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     //   head_dim 128, 4096 tokens, 9 nodes: B = 32 96 / 96, 256 656 / 664
     // With fewer heads a unit of twice the work is cut more coarsely:
     //   head_dim 128, 500 tokens, 1 node:  B = 16 14.5 / 13.3, 1 10.7 / 10.4; 20000 tokens, 2 nodes: B = 1 29.5 / 26.8
-    const bool pairs = H % 2 == 0 && (long long)B * H >= ctas;
-    const sv::TaRows r = sv::ta_rows(N, Hq / H, pairs);
-    const sv::TaLayout L = sv::ta_layout(N, Hq, H, D);
-    sv::TaArgs A = {};
+    const bool pairs = H % 2 == 0 && (long long)B * H >= ctas && !per_head;
+    const TaRows r = ta_rows(N, Hq / H, pairs);
+    const TaLayout L = ta_layout(N, Hq, H, D);
+    TaArgs A = {};
     A.table = page_table;
+    A.row_b = (long long)max_pages * (per_head ? H : 1);
+    A.row_h = per_head ? max_pages : 0;
     A.len = cache_len;
     A.parent = parent;
     A.node_count = node_count;
     A.B = B;
     A.N = N;
     A.Hq = Hq;
-    A.H = r.mode == sv::kTaSplitHeads ? H / 2 : H;
+    A.H = r.mode == kTaSplitHeads ? H / 2 : H;
     A.G = Hq / H;
     A.D = D;
     A.max_pages = max_pages;
@@ -1441,7 +1433,7 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     A.window = window;
     A.sinks = sinks;
     A.np = r.np;
-    A.box = P.page < sv::kTaKeys ? P.page : sv::kTaKeys;
+    A.box = P.page < kTaKeys ? P.page : kTaKeys;
     A.scale_log2 = scale * 1.44269504089f;
     A.out = static_cast<uint16_t *>(out);
     A.lse = lse;
@@ -1454,7 +1446,7 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     A.v_token = pages->token_stride;
     A.v_head = pages->head_stride;
     A.status = dev_status;
-    A.tries = sv::g_diag_timeout ? 0u : sv::kTaTries;
+    A.tries = g_diag_timeout ? 0u : kTaTries;
 
     CUtensorMap tq, tk, tv;
     // an extent of one is never stepped over: any valid stride stands for it
@@ -1464,17 +1456,48 @@ spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long
     const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)P.page, (cuuint64_t)H, (cuuint64_t)P.num_pages};
     const cuuint64_t ks[3] = {bytes(pages->token_stride, P.page), bytes(pages->head_stride, H),
                               bytes(pages->page_stride, P.num_pages)};
-    if (!sv::ta_tmap(&tq, pages->dtype, q, qd, qs, (cuuint32_t)A.G, (cuuint32_t)r.np) ||
-        !sv::ta_tmap(&tk, pages->dtype, pages->k, kd, ks, (cuuint32_t)A.box, 1) ||
-        !sv::ta_tmap(&tv, pages->dtype, pages->v, kd, ks, (cuuint32_t)A.box, 1))
+    if (!ta_tmap(&tq, pages->dtype, q, qd, qs, (cuuint32_t)A.G, (cuuint32_t)r.np) ||
+        !ta_tmap(&tk, pages->dtype, pages->k, kd, ks, (cuuint32_t)A.box, 1) ||
+        !ta_tmap(&tv, pages->dtype, pages->v, kd, ks, (cuuint32_t)A.box, 1))
         return SPEC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = pages->dtype == SPEC_DTYPE_BF16;
     if (bf)
-        return D <= 64 ? sv::ta_launch_mode<SPEC_DTYPE_BF16, 64>(A, tq, tk, tv, r, ctas, dev, s)
-                       : sv::ta_launch_mode<SPEC_DTYPE_BF16, 128>(A, tq, tk, tv, r, ctas, dev, s);
-    return D <= 64 ? sv::ta_launch_mode<SPEC_DTYPE_F16, 64>(A, tq, tk, tv, r, ctas, dev, s)
-                   : sv::ta_launch_mode<SPEC_DTYPE_F16, 128>(A, tq, tk, tv, r, ctas, dev, s);
+        return D <= 64 ? ta_launch_mode<SPEC_DTYPE_BF16, 64>(A, tq, tk, tv, r, ctas, dev, s)
+                       : ta_launch_mode<SPEC_DTYPE_BF16, 128>(A, tq, tk, tv, r, ctas, dev, s);
+    return D <= 64 ? ta_launch_mode<SPEC_DTYPE_F16, 64>(A, tq, tk, tv, r, ctas, dev, s)
+                   : ta_launch_mode<SPEC_DTYPE_F16, 128>(A, tq, tk, tv, r, ctas, dev, s);
+}
+
+} // namespace sv
+
+extern "C" {
+
+size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int heads, int head_dim) {
+    if (B < 1 || B >= (1 << 16) || N < 1 || N > SPEC_MAX_TREE || heads < 1 || heads > 1024 || Hq < heads ||
+        Hq % heads || Hq / heads > 64 || head_dim < 8 || head_dim % 8 || head_dim > SPEC_MAX_HEAD_DIM)
+        return 0;
+    return sv::ta_layout(N, Hq, heads, head_dim).total;
+}
+
+spec_status_t spec_tree_attention(const void *q, long long q_stride_b, long long q_stride_n,
+                                  long long q_stride_h, const spec_pages_t *pages,
+                                  const int32_t *page_table, const int32_t *cache_len,
+                                  const int32_t *parent, const int32_t *node_count, int B, int N,
+                                  int Hq, int max_pages, float scale, int window, int sinks,
+                                  void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                  uint32_t *dev_status, void *stream) {
+    return sv::ta_call(q, q_stride_b, q_stride_n, q_stride_h, pages, page_table, false, cache_len, parent, node_count, B,
+                       N, Hq, max_pages, scale, window, sinks, out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+spec_status_t spec_sparse_attention(const void *q, long long q_stride_b, long long q_stride_n, long long q_stride_h,
+                                    const spec_pages_t *pages, const int32_t *page_table, const int32_t *cache_len,
+                                    const int32_t *parent, const int32_t *node_count, int B, int N, int Hq,
+                                    int max_pages, float scale, int window, int sinks, void *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    return sv::ta_call(q, q_stride_b, q_stride_n, q_stride_h, pages, page_table, true, cache_len, parent, node_count, B,
+                       N, Hq, max_pages, scale, window, sinks, out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 } // extern "C"
