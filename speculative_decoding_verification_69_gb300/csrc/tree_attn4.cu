@@ -23,8 +23,8 @@
 // per 32 channels, those of a channel 4 bytes per 8 tokens, each without bank
 // conflicts, and the scales of a warp's 32 channels of V are the same for all lanes.
 //
-// One CTA per SM: four warps unpack K, four V, four form the weights, and a warp
-// each loads (one bulk copy per page and head), issues the products and
+// One CTA per SM: four warps unpack K, four V, four (of 64 rows: eight) form the weights, and a warp
+// each loads, issues the products and
 // schedules.  Tiles of keys alternate between two buffers of K, V, S and P, so the
 // stages of consecutive tiles overlap.  Heads of up to 64 are taken in pairs (the
 // lanes of V^T are two heads' channels; the quarter of the product that mixes them is
@@ -34,8 +34,6 @@
 
 namespace sv {
 
-constexpr int kT4Threads = 480;  // 4 softmax warps, 4 of K, 4 of V, then loads, products, scheduling
-constexpr int kT4WarpLoad = 12, kT4WarpMma = 13, kT4WarpPlan = 14;
 // tensor-memory columns: K, V and S two buffers each, then O
 constexpr uint32_t kT4K = 0, kT4V = 128, kT4S = 256, kT4O = 384, kT4Buf = 64;
 
@@ -54,7 +52,10 @@ template <int DP, int PACK, int RP> struct T4Cfg {
     static constexpr int kStage = PACK * DP * 136;       // one tile, packed
     static constexpr int kStages = kCols == 64 ? 6 : 8;
     static constexpr int kQ = PACK * RP * DP * 2;
-    static constexpr int kW = kCols < 32 ? kCols : 32;   // columns a softmax warp has in hand at a time
+    static constexpr int kW = kCols < 32 ? kCols : 32;   // columns of a group of softmax warps
+    static constexpr int kSoft = 4 * (kCols / kW);       // softmax warps; then 4 of K and 4 of V
+    static constexpr int kLoad = kSoft + 8, kMma = kSoft + 9, kPlan = kSoft + 10;
+    static constexpr int kThreads = (kSoft + 11) * 32;
     static constexpr int kSwizzle = kCols == 64 ? 2 : kCols == 32 ? 4 : 6;  // 128, 64 or 32 bytes
 };
 
@@ -62,22 +63,70 @@ template <int DP, int PACK, int RP> struct T4Shared {
     using C = T4Cfg<DP, PACK, RP>;
     uint8_t q[kTaSlots][C::kQ];
     uint8_t p[2][kTaKeys * C::kRowP];
-    uint8_t tile[C::kStages][C::kStage];
-    uint4 scale[4][32];                      // V's scales and their biases, four keys of a warp's group each
-    uint4 bias[4][32];
-    float m[4][C::kCols], f[4][C::kCols];    // per warp: references and their last factors
-    float top[4][C::kCols], sum[4][C::kCols];
+    uint8_t tile[C::kStages][C::kStage];     // per head: K's codes, V's codes, scales
+    uint4 scale[4][32];                      // of a V warp: V's multipliers and addends for its keys
+    float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references and their last factors
+    float top[C::kSoft][C::kW], sum[C::kSoft][C::kW];
+    float inv[C::kCols];
     long long incl[kTaChunks];
     SegSlot seg[kTaSlots];
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots], q_full[kTaSlots], q_free[kTaSlots];
     uint64_t full[C::kStages], empty[C::kStages];
-    uint64_t k_full[2], v_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free, meet, done;
-    int4 votes[2];                           // of the softmax warps, by the parity of their meeting
+    uint64_t s_ready[2], s_full[2];          // K is there and the scores before are read; scores are there
+    uint64_t pv_ready[2], pv_done[2];        // V and the weights are there; their product is in O
+    uint64_t o_free, done;
     uint32_t tmem_base;
     int abort;
 };
 
 // ------------------------------------------------------------------ PTX
+
+// 16 bytes from global to shared memory, without waiting; the arrival of this thread's copies so far on
+// `bar`, and the wait for all of them.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// ta_wait in one statement: the compiler's code around its loop doubles the 67 cycles of a look that succeeds at
+// once, and a tile's stages wait for each other half a dozen times.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *abort, uint32_t tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n, a;\n\t"
+        "mov.u32 n, %4;\n\t"
+        "mov.u32 %0, 1;\n\t"
+        "LOOK%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE%=;\n\t"
+        "ld.volatile.shared.u32 a, [%3];\n\t"
+        "setp.ne.u32 p, a, 0;\n\t"
+        "@p bra GIVEUP%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra LOOK%=;\n\t"
+        "mov.u32 a, 1;\n\t"
+        "st.volatile.shared.u32 [%3], a;\n\t"
+        "GIVEUP%=: mov.u32 %0, 0;\n\t"
+        "DONE%=:\n\t}"
+        : "=&r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(abort)), "r"(tries)
+        : "memory");
+    return ok != 0;
+}
+
+// A barrier of the 128 threads of a group of softmax warps; whether any of them says so.
+__device__ __forceinline__ bool meet128(int group, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(1 + group)
+        : "memory");
+    return r != 0;
+}
 
 // Shared-memory descriptor of the weights as the B operand [keys x rows]: the rows (N) are
 // contiguous, kRowP bytes to a key, which is the swizzle's span; 8 keys an atom, the next 8
@@ -114,56 +163,54 @@ template <int DT> __device__ __forceinline__ uint2 unpack_scale(float lo, float 
 // ------------------------------------------------------------------ the kernel
 
 template <int DT, int DP, int PACK, int RP>
-__global__ void __launch_bounds__(kT4Threads, 1)
+__global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
     tree_attn4(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ T4Args T) {
     using C = T4Cfg<DP, PACK, RP>;
     using Sh = T4Shared<DP, PACK, RP>;
     extern __shared__ uint8_t t4_raw[];
-    Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(t4_raw) + 1023) & ~(uintptr_t)1023);
+    // (an offset, so that the compiler keeps knowing the address to be in shared memory)
+    Sh &sh = *reinterpret_cast<Sh *>(t4_raw + ((0u - smem_u32(t4_raw)) & 1023u));
     const TaArgs &A = T.a;
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    constexpr int kCols = C::kCols, kStages = C::kStages, kW = C::kW;
+    constexpr int kCols = C::kCols, kStages = C::kStages, kW = C::kW, kSoft = C::kSoft;
     constexpr float kLift = 7.f;  // weights up to 2^15: those 2^-29 below the maximum are still normal in float16
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTaSlots; ++i) {
             mbar_init(&sh.seg_full[i], 1);
             mbar_init(&sh.path_full[i], 1);
-            mbar_init(&sh.seg_free[i], 4 + 2);
+            mbar_init(&sh.seg_free[i], kSoft + 2);
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_free[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.full[i], 32);
             mbar_init(&sh.empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.k_full[i], 4);
-            mbar_init(&sh.v_full[i], 4);
+            mbar_init(&sh.s_ready[i], 4 + kSoft);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], 4);
-            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.pv_ready[i], 4 + kSoft);
             mbar_init(&sh.pv_done[i], 1);
         }
-        mbar_init(&sh.o_free, 4);
-        mbar_init(&sh.meet, 4);
+        mbar_init(&sh.o_free, kSoft);
         mbar_init(&sh.done, 1);
-        sh.abort = 0;
+        sh.abort = A.tries == 0;  // (a wait in vain then gives up at its first look)
         fence_mbar_init();
         tma_prefetch_map(&tm_q);
     }
     // the rows of Q past the last one stay 0
-    for (int i = threadIdx.x; i < (int)sizeof(sh.q) / 16; i += kT4Threads)
+    for (int i = threadIdx.x; i < (int)sizeof(sh.q) / 16; i += C::kThreads)
         reinterpret_cast<uint4 *>(sh.q)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
-    if (warp == kT4WarpMma) {
+    if (warp == C::kMma) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
     }
     pdl_trigger();
     pdl_wait();
     Walk<kTaSplitKeys> w;
-    if (warp == kT4WarpPlan) w.fetch(A, 0);
+    if (warp == C::kPlan) w.fetch(A, 0);
     bool fewer = false;
     if (threadIdx.x < kTaChunks) fewer = ta_sum_units<kTaSplitKeys>(A, sh.incl);
     tc_fence_before();
@@ -178,7 +225,7 @@ __global__ void __launch_bounds__(kT4Threads, 1)
     const uint32_t tiles = (uint32_t)(u_last - u_first);
 
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xFFFFFFFFu, ta_wait(bar, parity & 1u, abort, A.tries)) != 0;
+        return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity & 1u, &sh.abort, A.tries)) != 0;
     };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
@@ -189,13 +236,28 @@ __global__ void __launch_bounds__(kT4Threads, 1)
         return wait(&bars[k % kTaSlots], (uint32_t)(k / kTaSlots)) ? &sh.seg[k % kTaSlots] : nullptr;
     };
 
-    if (warp == kT4WarpPlan) {  // ------------------------------------------- scheduling
+    if (warp == C::kPlan) {  // ------------------------------------------- scheduling
         ta_schedule<kTaSplitKeys>(A, w, sh.incl, sh.seg, sh.seg_full, sh.path_full, sh.seg_free, u_first, u_last, run,
                                   abort);
-    } else if (warp == kT4WarpLoad) {  // ------------------------------------- loads
+    } else if (warp == C::kLoad) {  // ------------------------------------- loads
         const int recs = kTaKeys >> T.block_shift;           // blocks of a head's tile
-        const int nb = PACK * recs, ahead = 32 / nb;         // copies of a tile, tiles whose pages are fetched at once
-        const int mine = lane % nb, slot = mine / recs, rec = mine % recs;
+        const int nb = PACK * recs, ahead = 32 / nb;         // blocks of a tile, tiles whose pages are fetched at once
+        const int slot = lane % nb / recs, rec = lane % recs;  // of the pages that the lane fetches
+        // 8 tokens of K's or V's codes are 4 C bytes: 16 to a lane, a half-warp to a head of a pack
+        constexpr int kHalf = 32 / PACK;
+        const int to_slot = lane / kHalf, part = lane % kHalf;
+        const bool copies = part * 4 < T.C;
+        const uint32_t codes = (uint32_t)(T.block * T.C / 2), scales = (uint32_t)(T.block * T.groups * 2);
+        const uint32_t to0 = smem_u32(sh.tile[0]) + (uint32_t)(to_slot * (kTaKeys / 16 * 17) * T.C);
+        // the lane's 16-byte pieces of a head's scales: block of tokens, and place in it
+        constexpr int kScaleVecs = DP / 2 / kHalf;
+        int scale_rec[kScaleVecs], scale_off[kScaleVecs];
+#pragma unroll
+        for (int x = 0; x < kScaleVecs; ++x) {
+            const int at = (x * kHalf + part) * 16;
+            scale_rec[x] = at / (int)scales;
+            scale_off[x] = 2 * (int)codes + at - scale_rec[x] * (int)scales;
+        }
         uint32_t stage = 0, fill = 0;
         int seg_no = 0;
         bool ok = true;
@@ -218,25 +280,21 @@ __global__ void __launch_bounds__(kT4Threads, 1)
             __syncwarp();
             const int head = s.hk * PACK + slot, i_end = s.i0 + s.n;
             const int *row = A.table + s.b * A.row_b + head * A.row_h;
-            const uint8_t *from = T.data + head * T.head_st;
-            // the first position of this lane's block in tile i, and whether a node sees any of it
-            auto block_pos = [&](int i) -> int { return s.g.tile(i) * kTaKeys + (rec << T.block_shift); };
-            auto block_seen = [&](int j) -> bool {
-                return head < T.heads && j < s.g.end && (s.g.wlo - j < T.block || j < A.sinks);
-            };
-            auto fetch = [&](int i0) -> int {  // the page of this lane's block in tile i0 + lane / nb
+            // the block's place in memory: of this lane's block in tile i0 + lane / nb, 0 where no node sees any of it
+            auto fetch = [&](int i0) -> const uint8_t * {
                 const int i = i0 + lane / nb;
-                if (i >= i_end) return 0;
-                const int j = block_pos(i);
-                if (!block_seen(j)) return 0;
+                if (i >= i_end || head >= T.heads) return nullptr;
+                const int j = s.g.tile(i) * kTaKeys + (rec << T.block_shift);  // its first position
+                if (j >= s.g.end || (s.g.wlo - j >= T.block && j >= A.sinks)) return nullptr;
                 int p = __ldcg(row + (j >> A.page_shift));
                 if ((unsigned)p >= (unsigned)A.num_pages) {
                     flag(A.status, SPEC_DEV_BAD_PAGE);
                     p = 0;
                 }
-                return p;
+                return T.data + p * T.page_st + head * T.head_st + ((j & (A.page - 1)) >> T.block_shift) * T.bytes;
             };
-            int base = s.i0, now = fetch(base), next = fetch(base + ahead);
+            int base = s.i0;
+            const uint8_t *now = fetch(base), *next = fetch(base + ahead);
             for (int i = s.i0; i < i_end; ++i) {
                 if (i == base + ahead) {
                     base = i;
@@ -247,30 +305,42 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                     ok = false;
                     break;
                 }
-                const int j = block_pos(i);
-                const bool load = lane / nb == i - base && block_seen(j);
-                const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, load);
-                if (elect_one()) mbar_expect_tx(&sh.full[stage], (uint32_t)(__popc(lanes) * T.bytes));
-                __syncwarp();
-                if (load)
-                    bulk_g2s(sh.tile[stage] + mine * T.bytes,
-                             from + now * T.page_st + ((j & (A.page - 1)) >> T.block_shift) * T.bytes,
-                             (uint32_t)T.bytes, &sh.full[stage]);
+                const uint32_t to = to0 + stage * C::kStage;
+                const int from_lane = (i - base) * nb + to_slot * recs;
+                auto place = [&](int r) -> const uint8_t * {
+                    return reinterpret_cast<const uint8_t *>(
+                        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(now), from_lane + r));
+                };
+                // (unrolled, so that a copy does not wait for the one before it to have read its addresses)
+#pragma unroll 8
+                for (int x = 0; x < kTaKeys / 8; ++x) {
+                    const uint8_t *src = place(x * 8 >> T.block_shift);
+                    const uint32_t off = (uint32_t)((x * 8 & (T.block - 1)) * T.C / 2 + part * 16);
+                    const uint32_t k = to + (uint32_t)(x * T.C * 4 + part * 16);
+                    if (copies && src) {
+                        copy16(k, src + off);
+                        copy16(k + (uint32_t)(kTaKeys / 2 * T.C), src + codes + off);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kScaleVecs; ++x) {
+                    const uint8_t *src = place(scale_rec[x] & (recs - 1));
+                    if (scale_rec[x] < recs && src)
+                        copy16(to + (uint32_t)(kTaKeys * T.C + (x * kHalf + part) * 16), src + scale_off[x]);
+                }
+                copy_arrive(&sh.full[stage]);
                 __syncwarp();
                 if (++stage == kStages) stage = 0, ++fill;
             }
         }
         // every copy has landed before the CTA may exit
-        for (uint32_t x = 0; x < (uint32_t)kStages; ++x) {
-            const uint32_t n = fill + (x < stage ? 1u : 0u);
-            if (n > 0) mbar_wait_bounded(&sh.full[x], (n - 1) & 1u, kTaWaitNs);
-        }
+        copy_wait_all();
         for (int x = 0; x < kTaSlots; ++x) {
             const int n = (seg_no + kTaSlots - 1 - x) / kTaSlots;
             if (n > 0) mbar_wait_bounded(&sh.q_full[x], (uint32_t)(n - 1) & 1u, kTaWaitNs);
         }
         __syncwarp();
-    } else if (warp == kT4WarpMma) {  // -------------------------------------- products
+    } else if (warp == C::kMma) {  // -------------------------------------- products
         constexpr uint32_t kIdS = (ta_idesc<DT>(RP, false)), kIdO = ta_idesc<SPEC_DTYPE_F16>(kCols, true);
         const uint64_t q_desc = umma_desc_sw128(smem_u32(sh.q[0]));
         const uint64_t w_desc = p_desc<C::kRowP, C::kSwizzle>(smem_u32(sh.p[0]));
@@ -286,8 +356,7 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                 ++s_seg;
             }
             const int qb = (s_seg - 1) % kTaSlots;
-            if (!wait(&sh.k_full[buf], use)) return false;
-            if (use > 0 && !wait(&sh.s_free[buf], use - 1)) return false;
+            if (!wait(&sh.s_ready[buf], use)) return false;
             tc_fence_after();
             --s_left;
             if (elect_one()) {
@@ -315,7 +384,7 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                 ++v_seg;
                 fresh = true;
             }
-            if (!wait(&sh.v_full[buf], use) || !wait(&sh.p_full[buf], use)) return false;
+            if (!wait(&sh.pv_ready[buf], use)) return false;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -340,27 +409,29 @@ __global__ void __launch_bounds__(kT4Threads, 1)
         if (elect_one()) umma_commit(&sh.done);
         mbar_wait_bounded(&sh.done, 0u, kTaWaitNs);
         __syncwarp();
-    } else if (warp >= 8) {  // ------------------------------------------------ V
+    } else if (warp >= kSoft + 4) {  // ----------------------------------------- V
         const int quad = warp & 3, slot = quad * 32 / DP, ch = (quad * 32 + lane) % DP;
         const bool works = slot < PACK && ch - lane < T.C;  // the warp's lanes alike
-        const int g = ch >> 5, block_mask = T.block - 1;
+        const int t = 4 * lane;                             // the keys whose scales the lane unpacks
+        const int head_off = slot * (kTaKeys / 16 * 17) * T.C, word_off = head_off + kTaKeys / 2 * T.C + ch * 4;
+        const int scale_off = head_off + kTaKeys * T.C + (t >> T.block_shift) * T.block * T.groups * 2 +
+                              (T.groups + (ch >> 5)) * T.block + (t & (T.block - 1));
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kT4V;
-        const int head_off = slot * ((kTaKeys >> T.block_shift) * T.bytes);
+        uint4 *scale = sh.scale[quad];
         for (uint32_t e = 0, stage = 0, fill = 0; e < tiles; ++e) {
             if (!wait(&sh.full[stage], fill)) break;
-            const uint8_t *tile = sh.tile[stage] + head_off;
-            uint4 *scale = sh.scale[quad], *bias = sh.bias[quad];
-            if (works) {  // scales of keys 4 lane .. 4 lane + 3
-                const int t = 4 * lane;
-                const uint32_t x = *reinterpret_cast<const uint32_t *>(
-                    tile + (t >> T.block_shift) * T.bytes + T.block * (T.C + T.groups + g) + (t & block_mask));
+            const uint8_t *tile = sh.tile[stage];
+            uint32_t word[16];
+            if (works) {
+                const uint32_t x = *reinterpret_cast<const uint32_t *>(tile + scale_off);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    word[i] = *reinterpret_cast<const uint32_t *>(tile + word_off + i * T.C * 4);
                 const uint2 a = unpack_scale<SPEC_DTYPE_F16>(scale_of(x & 255u), scale_of((x >> 8) & 255u));
                 const uint2 b = unpack_scale<SPEC_DTYPE_F16>(scale_of((x >> 16) & 255u), scale_of(x >> 24));
-                __syncwarp();
-                reinterpret_cast<uint2 *>(scale)[lane] = make_uint2(a.x, b.x);
-                reinterpret_cast<uint2 *>(bias)[lane] = make_uint2(a.y, b.y);
-                __syncwarp();
+                scale[lane] = make_uint4(a.x, a.y, b.x, b.y);
             }
+            arrive(&sh.empty[stage]);
             if (e >= 2 && !wait(&sh.pv_done[e & 1u], (e >> 1) - 1)) break;
             if (works) {
                 tc_fence_after();
@@ -369,96 +440,92 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                     uint32_t v[32];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int t = (h * 8 + i) * 8;
-                        const uint32_t x = *reinterpret_cast<const uint32_t *>(
-                            tile + (t >> T.block_shift) * T.bytes + T.block * (T.C >> 1) +
-                            (((t & block_mask) >> 3) * T.C + ch) * 4);
-                        const uint4 s = scale[h * 8 + i], b = bias[h * 8 + i];
-                        v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, s.x, b.x);
-                        v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, s.y, b.y);
-                        v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, s.z, b.z);
-                        v[4 * i + 3] = unpack_pair<SPEC_DTYPE_F16>(x, 3, s.w, b.w);
+                        const uint4 a = scale[(h * 8 + i) * 2], b = scale[(h * 8 + i) * 2 + 1];
+                        const uint32_t x = word[h * 8 + i];
+                        v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, a.x, a.y);
+                        v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, a.z, a.w);
+                        v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, b.x, b.y);
+                        v[4 * i + 3] = unpack_pair<SPEC_DTYPE_F16>(x, 3, b.z, b.w);
                     }
                     tmem_store(to + (e & 1u) * kT4Buf + (uint32_t)(h * 32), v);
                 }
                 tmem_wait_store();
                 tc_fence_before();
             }
-            arrive(&sh.empty[stage]);
-            arrive(&sh.v_full[e & 1u]);
+            arrive(&sh.pv_ready[e & 1u]);
             if (++stage == (uint32_t)kStages) stage = 0, ++fill;
         }
-    } else if (warp >= 4) {  // ------------------------------------------------ K
+    } else if (warp >= kSoft) {  // --------------------------------------------- K
         const int quad = warp & 3, key = quad * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kT4K;
-        const int t = key & (T.block - 1), recs = kTaKeys >> T.block_shift;
-        const int code_off = (key >> T.block_shift) * T.bytes + ((t >> 3) * T.groups * 8 + (t & 7)) * 16;
-        const int scale_off = (key >> T.block_shift) * T.bytes + T.block * T.C + t;
+        const int code_off = ((key >> 3) * T.groups * 8 + (key & 7)) * 16;
+        const int scale_off = kTaKeys * T.C + (key >> T.block_shift) * T.block * T.groups * 2 + (key & (T.block - 1));
         for (uint32_t e = 0, stage = 0, fill = 0; e < tiles; ++e) {
             if (!wait(&sh.full[stage], fill)) break;
+            uint4 code[PACK * DP / 32];
+            uint32_t byte[PACK * DP / 32];
+#pragma unroll
+            for (int x = 0; x < PACK * DP / 32; ++x) {
+                const uint8_t *tile = sh.tile[stage] + x / (DP / 32) * (kTaKeys / 16 * 17) * T.C;
+                const int g = x % (DP / 32) < T.groups ? x % (DP / 32) : 0;  // (past the last group: not multiplied)
+                code[x] = *reinterpret_cast<const uint4 *>(tile + code_off + g * 128);
+                byte[x] = tile[scale_off + g * T.block];
+            }
+            arrive(&sh.empty[stage]);
             if (e >= 2 && !wait(&sh.s_full[e & 1u], (e >> 1) - 1)) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < PACK * DP / 64; ++x) {  // 64 channels of a head at a time
-                const int slot = x / (DP / 64), g0 = x % (DP / 64) * 2;
-                const uint8_t *tile = sh.tile[stage] + slot * recs * T.bytes;
+            for (int x = 0; x < PACK * DP / 64; ++x) {
                 uint32_t k[32];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int g = g0 + i < T.groups ? g0 + i : 0;  // (past the last group: not multiplied)
-                    const uint4 c = *reinterpret_cast<const uint4 *>(tile + code_off + g * 128);
-                    const float f = scale_of(tile[scale_off + g * T.block]);
+                for (int y = 0; y < 2; ++y) {
+                    const float f = scale_of(byte[2 * x + y]);
                     const uint2 s = unpack_scale<DT>(f, f);
+                    const uint4 c = code[2 * x + y];
                     const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) k[16 * i + 4 * y + z] = unpack_pair<DT>(word[y], z, s.x, s.y);
+                    for (int i = 0; i < 16; ++i) k[16 * y + i] = unpack_pair<DT>(word[i / 4], i % 4, s.x, s.y);
                 }
                 tmem_store(to + (e & 1u) * kT4Buf + (uint32_t)(x * 32), k);
             }
             tmem_wait_store();
             tc_fence_before();
-            arrive(&sh.empty[stage]);
-            arrive(&sh.k_full[e & 1u]);
+            arrive(&sh.s_ready[e & 1u]);
             if (++stage == (uint32_t)kStages) stage = 0, ++fill;
         }
     } else {  // ---------------------------------------------------------------- softmax
-        const int key = warp * 32 + lane;  // of a tile; and the channel (of a slot) in O
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const int slot = warp * 32 / DP, ch = (warp * 32 + lane) % DP;
+        const int group = warp >> 2, quad = warp & 3;  // a group of four warps has kW columns
+        const int key = quad * 32 + lane;              // of a tile; and the channel (of all heads) in O
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16, col0 = (uint32_t)(group * kW);
+        const int slot = quad * 32 / DP, ch = key % DP;
         const int rows_used = A.np * A.G, rows_cta = PACK * rows_used;
         // a quarter of the keys' scale was multiplied in float16
         const float scale = A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
         const int sinks = A.window ? A.sinks : 0;
         float *m = sh.m[warp], *f = sh.f[warp];
-        uint32_t e = 0, meeting = 0;
-        int seg_no = 0;
+        uint32_t e = 0;
         bool ok = true;
-        // Waits for all four warps; whether a thread of any says so.  (Bounded like every wait: a
-        // warp that has given up is not waited for for ever, as it would be at a hardware barrier.)
-        auto any = [&](bool x) -> bool {
-            const bool mine = __any_sync(0xFFFFFFFFu, x);
-            int4 *votes = &sh.votes[meeting & 1u];
-            if (lane == 0) reinterpret_cast<volatile int *>(votes)[warp] = mine;
-            arrive(&sh.meet);
-            ok = ok && wait(&sh.meet, meeting++);
-            const volatile int *v = reinterpret_cast<const volatile int *>(votes);
-            return (v[0] | v[1] | v[2] | v[3]) != 0;
-        };
-        for (; ok; ++seg_no) {
+        arrive(&sh.s_ready[0]);  // no scores to be read yet
+        arrive(&sh.s_ready[1]);
+        // The warps of a group leave together: a wait in vain is told at their next meeting, so that
+        // no warp stands at a barrier that another one has left for good.
+        for (int seg_no = 0;; ++seg_no) {
             const SegSlot *sp = take(sh.path_full, seg_no);
-            if (!sp || sp->s.n == 0) break;
-            const Seg s = sp->s;
+            if (meet128(group, !sp)) {
+                ok = false;
+                break;
+            }
+            if (sp->s.n == 0) break;
+            const Seg &s = sp->s;  // (read where it is used: registers are dear here)
             const Geo &g = s.g;
             // positions from `whole` on (to g.c) are seen by all nodes
             const int whole = A.window ? max(g.wlo, min(g.c, g.c + g.cnt - A.window)) : 0;
-            float2 l[kCols / 2];
+            float l[kW];
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i) l[i] = make_float2(0.f, 0.f);
-            for (int i = lane; i < kCols; i += 32) m[i] = -FLT_MAX;
+            for (int i = 0; i < kW; ++i) l[i] = 0.f;
+            if (lane < kW) m[lane] = -FLT_MAX;
             __syncwarp();
-            for (int t = 0; t < s.n && ok; ++t, ++e) {
+            for (int t = 0; t < s.n; ++t, ++e) {
                 const int j0 = g.tile(s.i0 + t) * kTaKeys;
                 const uint32_t buf = e & 1u, use = e >> 1;
                 const bool all = g.c - j0 >= kTaKeys && (j0 >= whole || sinks - j0 >= kTaKeys);
@@ -477,166 +544,151 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                             if (yes) seen |= one << (n * A.G);
                         }
                     }
+                    if (PACK == 1) seen >>= col0;
+                    __syncwarp();
                 }
-                ok = wait(&sh.s_full[buf], use);
-                if (!ok) break;
+                ok = ok && wait(&sh.s_full[buf], use);
                 tc_fence_after();
+                float2 z[kW / 2];
+                auto scores = [&](uint32_t (&x)[kW]) {  // -inf where they are not seen
+                    tmem_load(tmem + lanes + kT4S + buf * kT4Buf + col0, x);
+                    if (!all) {
 #pragma unroll
-                for (int h = 0; h < kCols / kW; ++h) {
-                    const int c0 = h * kW;  // first column
-                    float2 z[kW / 2];
-                    auto scores = [&](uint32_t (&x)[kW]) {  // -inf where they are not seen
-                        tmem_load(tmem + lanes + kT4S + buf * kT4Buf + (uint32_t)c0, x);
-                        if (!all) {
-#pragma unroll
-                            for (int i = 0; i < kW; ++i)
-                                if (!((seen >> ((c0 + i) % RP)) & 1ull)) x[i] = 0xFF800000u;
-                            __syncwarp();
-                        }
-                    };
-                    auto shift = [&](const uint32_t (&x)[kW]) -> float {  // scaled, less the references; the largest
-                        const float2 c2 = make_float2(scale, scale);
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < kW; i += 4) {
-                            const float4 r = *reinterpret_cast<const float4 *>(m + c0 + i);
-                            z[i / 2] = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2,
-                                            make_float2(-r.x, -r.y));
-                            z[i / 2 + 1] = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), c2,
-                                                make_float2(-r.z, -r.w));
-                            mx = fmaxf(mx, fmaxf(fmaxf(z[i / 2].x, z[i / 2].y), fmaxf(z[i / 2 + 1].x, z[i / 2 + 1].y)));
-                        }
-                        return mx;
-                    };
-                    float largest;
-                    {
-                        uint32_t x[kW];
-                        scores(x);
-                        largest = shift(x);
-                    }
-                    const bool grown = any(largest > kLift + kTaGrow);
-                    if (!ok) break;
-                    if (grown) {
-                        // new references: the columns' maxima over the four warps' keys
-                        uint32_t x[kW];
-                        scores(x);
-                        float mine = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < kW; ++i) {
-                            float y = __uint_as_float(x[i]);
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
-                            if (lane == i) mine = y;
-                        }
-                        if (lane < kW) sh.top[warp][c0 + lane] = mine;
-                        any(false);
-                        if (!ok) break;
-                        if (lane < kW) {
-                            float y = fmaxf(fmaxf(sh.top[0][c0 + lane], sh.top[1][c0 + lane]),
-                                            fmaxf(sh.top[2][c0 + lane], sh.top[3][c0 + lane])) * scale;
-                            const float old = m[c0 + lane];
-                            y = y > old + kLift ? y - kLift : old;
-                            f[c0 + lane] = ex2(old - y);
-                            m[c0 + lane] = y;
-                        }
+                        for (int i = 0; i < kW; ++i)
+                            if (!((seen >> (i % RP)) & 1ull)) x[i] = 0xFF800000u;
                         __syncwarp();
-                        shift(x);
+                    }
+                };
+                auto shift = [&](const uint32_t (&x)[kW]) -> float {  // scaled, less the references; the largest
+                    const float2 c2 = make_float2(scale, scale);
+                    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < kW / 2; ++i) {
-                            const float2 y = *reinterpret_cast<const float2 *>(f + c0 + 2 * i);
-                            l[c0 / 2 + i] = make_float2(l[c0 / 2 + i].x * y.x, l[c0 / 2 + i].y * y.y);
-                        }
-                        if (t > 0) {  // O holds the tiles before this one
-                            ok = wait(&sh.pv_done[buf ^ 1u], (e - 1) >> 1);
-                            if (!ok) break;
+                    for (int i = 0; i < kW; i += 4) {
+                        const float4 r = *reinterpret_cast<const float4 *>(m + i);
+                        z[i / 2] = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2,
+                                        make_float2(-r.x, -r.y));
+                        z[i / 2 + 1] = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), c2,
+                                            make_float2(-r.z, -r.w));
+                        mx[0] = fmaxf(mx[0], fmaxf(z[i / 2].x, z[i / 2].y));
+                        mx[1] = fmaxf(mx[1], fmaxf(z[i / 2 + 1].x, z[i / 2 + 1].y));
+                    }
+                    return fmaxf(mx[0], mx[1]);
+                };
+                float largest;
+                {
+                    uint32_t x[kW];
+                    scores(x);
+                    largest = shift(x);
+                }
+                if (meet128(group, !ok || largest > kLift + kTaGrow)) {
+                    if (meet128(group, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    // new references: the columns' maxima over the four warps' keys
+                    float mine = -INFINITY;
+                    uint32_t x[kW];
+                    scores(x);
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) {
+                        // (as integers that order alike; a NaN's column is NaN whatever its reference)
+                        const int u = (int)x[i], y = __reduce_max_sync(0xFFFFFFFFu, u ^ ((u >> 31) & 0x7FFFFFFF));
+                        if (lane == i) mine = __int_as_float(y ^ ((y >> 31) & 0x7FFFFFFF));
+                    }
+                    if (lane < kW) sh.top[warp][lane] = mine;
+                    meet128(group, false);
+                    if (lane < kW) {
+                        const int w0 = group * 4;
+                        float y = fmaxf(fmaxf(sh.top[w0][lane], sh.top[w0 + 1][lane]),
+                                        fmaxf(sh.top[w0 + 2][lane], sh.top[w0 + 3][lane])) * scale;
+                        const float old = m[lane];
+                        y = y > old + kLift ? y - kLift : old;
+                        f[lane] = ex2(old - y);
+                        m[lane] = y;
+                    }
+                    __syncwarp();
+                    scores(x);
+                    shift(x);
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) l[i] *= f[i];
+                    if (t > 0) {  // O holds the tiles before this one
+                        ok = wait(&sh.pv_done[buf ^ 1u], (e - 1) >> 1);
+                        if (ok) {
                             tc_fence_after();
 #pragma unroll
                             for (int d = 0; d < kW; d += 16) {
                                 uint32_t o[16];
-                                tmem_load(tmem + lanes + kT4O + (uint32_t)(c0 + d), o);
+                                tmem_load(tmem + lanes + kT4O + col0 + (uint32_t)d, o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f[c0 + d + i]);
-                                tmem_store(tmem + lanes + kT4O + (uint32_t)(c0 + d), o);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[d + i]);
+                                tmem_store(tmem + lanes + kT4O + col0 + (uint32_t)d, o);
                             }
                             tmem_wait_store();
                         }
                     }
-                    if (h == kCols / kW - 1) {
-                        tc_fence_before();
-                        arrive(&sh.s_free[buf]);
-                    }
-                    if (h == 0 && e >= 2) {  // the weights of the tile before the last are through
-                        ok = wait(&sh.pv_done[buf], use - 1);
-                        if (!ok) break;
-                    }
-                    uint8_t *to = sh.p[buf] + key * C::kRowP;
-                    constexpr int kSwap = C::kRowP / 16 - 1;
-                    const int swap = C::kRowP == 128 ? key & 7 : C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1;
-                    static_assert(kSwap == 7 || kSwap == 3 || kSwap == 1, "bytes of a key's weights");
-#pragma unroll
-                    for (int i = 0; i < kW; i += 8) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float2 w2 = make_float2(ex2(z[i / 2 + y].x), ex2(z[i / 2 + y].y));
-                            l[(c0 + i) / 2 + y] = add2(l[(c0 + i) / 2 + y], w2);
-                            // rounded to float16 for the product; the sum takes them unrounded, and the
-                            // errors, 2^-12 each, average out
-                            p[y] = pack2<SPEC_DTYPE_F16>(w2.x, w2.y);
-                        }
-                        *reinterpret_cast<uint4 *>(to + ((((c0 + i) / 8) ^ swap) * 16)) =
-                            make_uint4(p[0], p[1], p[2], p[3]);
-                    }
                 }
-                if (!ok) break;
+                tc_fence_before();
+                arrive(&sh.s_ready[buf]);
+                // (the weights before the last are through: their product was issued before these scores,
+                // whose commit covers all products before it)
+                uint8_t *to = sh.p[buf] + key * C::kRowP;
+                const int swap = C::kRowP == 128 ? key & 7 : C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1;
+#pragma unroll
+                for (int i = 0; i < kW; i += 8) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float2 w2 = make_float2(ex2(z[i / 2 + y].x), ex2(z[i / 2 + y].y));
+                        const float2 sum = add2(make_float2(l[i + 2 * y], l[i + 2 * y + 1]), w2);
+                        l[i + 2 * y] = sum.x, l[i + 2 * y + 1] = sum.y;
+                        // rounded to float16 for the product; the sum takes them unrounded, and the
+                        // errors, 2^-12 each, average out
+                        p[y] = pack2<SPEC_DTYPE_F16>(w2.x, w2.y);
+                    }
+                    *reinterpret_cast<uint4 *>(to + (((group * (kW / 8) + i / 8) ^ swap) * 16)) =
+                        make_uint4(p[0], p[1], p[2], p[3]);
+                }
                 fence_proxy_async();
                 tc_fence_before();
-                arrive(&sh.p_full[buf]);
+                arrive(&sh.pv_ready[buf]);
             }
-            if (!ok) break;
-            arrive(&sh.seg_free[seg_no % kTaSlots]);
 
-            // ---- the segment's result: sums over the warp's keys, a column to a lane (two where there are 64)
-            constexpr int kPerLane = kCols == 64 ? 2 : 1;
-            float *part = reinterpret_cast<float *>(l);
+            // ---- the segment's result: sums over the warp's keys, a column to a lane
 #pragma unroll
-            for (int o = 16, n = kCols; o > 0; o >>= 1) {
-                if (n > kPerLane) {  // lanes o apart take half of the columns each
+            for (int o = 16, n = kW; o > 0; o >>= 1) {
+                if (n > 1) {  // lanes o apart take half of the columns each
                     n >>= 1;
 #pragma unroll
-                    for (int i = 0; i < kCols / 2; ++i) {
+                    for (int i = 0; i < kW / 2; ++i) {
                         if (i >= n) break;
                         const bool up = (lane & o) != 0;
-                        const float give = up ? part[i] : part[i + n];
-                        part[i] = (up ? part[i + n] : part[i]) + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                        const float give = up ? l[i] : l[i + n];
+                        l[i] = (up ? l[i + n] : l[i]) + __shfl_xor_sync(0xFFFFFFFFu, give, o);
                     }
                 } else {
-                    part[0] += __shfl_xor_sync(0xFFFFFFFFu, part[0], o);
+                    l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], o);
                 }
             }
-            // lane bits from the top choose the upper halves: with 16 columns lanes 2 i and 2 i + 1 hold column i,
-            // with 32 lane i column i, with 64 lane i columns 2 i and 2 i + 1
-            if (kCols == 16) {
-                if ((lane & 1) == 0) sh.sum[warp][lane >> 1] = part[0];
-            } else {
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i) sh.sum[warp][lane * kPerLane + i] = part[i];
-            }
-            any(false);
+            // the lane's bits, from the top, chose the upper halves: lane i holds column i of 32, lanes 2 i and
+            // 2 i + 1 column i of 16
+            if (kW == 32 || (lane & 1) == 0) sh.sum[warp][kW == 32 ? lane : lane >> 1] = l[0];
             const uint32_t last = e - 1;
             ok = ok && wait(&sh.pv_done[last & 1u], last >> 1);
-            if (!ok) break;
+            if (meet128(group, !ok)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
             const bool whole_item = s.n == g.nt;
             const long long place = (long long)blockIdx.x * 2 + (s.i0 == 0 ? 1 : 0);  // a cut item's part
-            for (int c = warp * 32 + lane; c < kCols; c += 128) {  // a thread per row: its sum's reciprocal and lse
-                const float total = sh.sum[0][c] + sh.sum[1][c] + sh.sum[2][c] + sh.sum[3][c];
+            if (key < kW) {  // a thread per row: its sum's reciprocal and lse
+                const int w0 = group * 4, c = (int)col0 + key;
+                const float total = sh.sum[w0][key] + sh.sum[w0 + 1][key] + sh.sum[w0 + 2][key] + sh.sum[w0 + 3][key];
                 const int r = c % RP, local = r / A.G, node = s.node0 + local, hk = s.hk * PACK + c / RP;
                 const bool exists = r < rows_used && node < A.N && hk < T.heads, valid = exists && node < g.cnt;
-                float ref = sh.m[0][c];
+                float ref = sh.m[w0][key];
                 if (total != total) ref = fmaxf(ref, 0.f);  // the row's part must not pass for empty
-                sh.top[0][c] = 4.f / total;                 // (O is a quarter of itself)
+                sh.inv[c] = 4.f / total;                    // (O is a quarter of itself)
                 if (exists) {
                     if (whole_item) {
                         const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + (r - local * A.G);
@@ -647,37 +699,33 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                     }
                 }
             }
-            any(false);
-            if (!ok) break;
+            meet128(group, false);
             const int hk = s.hk * PACK + slot;
-            if (slot < PACK && hk < T.heads && ch - lane < A.D) {
-                constexpr int kO = RP < 32 ? RP : 32;
-                int local = 0, in_group = 0;
-#pragma unroll 1
-                for (int c0 = 0; c0 < rows_used; c0 += kO) {
-                    uint32_t o[kO];
-                    __syncwarp();
-                    tmem_load(tmem + lanes + kT4O + (uint32_t)(slot * RP + c0), o);
+            constexpr int kO = RP < kW ? RP : kW;                                  // columns of the head in this group
+            const int c0 = max(slot * RP, (int)col0), r0 = c0 - slot * RP;         // the first, and its row
+            if (slot < PACK && hk < T.heads && ch - lane < A.D && c0 < min(slot * RP + RP, (int)col0 + kW)) {
+                int local = r0 / A.G, in_group = r0 - local * A.G;
+                uint32_t o[kO];
+                tmem_load(tmem + lanes + kT4O + (uint32_t)c0, o);
 #pragma unroll
-                    for (int i = 0; i < kO; ++i) {
-                        const int node = s.node0 + local;
-                        if (c0 + i < rows_used && node < A.N && ch < A.D) {
-                            const bool valid = node < g.cnt;
-                            const float y = __uint_as_float(o[i]);
-                            if (whole_item) {
-                                const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + in_group;
-                                A.out[orow * A.D + ch] =
-                                    valid ? (uint16_t)pack2<DT>(y * sh.top[0][slot * RP + c0 + i], 0.f) : (uint16_t)0;
-                            } else if (valid) {
-                                A.part_o[(place * rows_cta + slot * rows_used + c0 + i) * A.D + ch] = 4.f * y;
-                            }
+                for (int i = 0; i < kO; ++i) {
+                    const int node = s.node0 + local;
+                    if (r0 + i < rows_used && node < A.N && ch < A.D) {
+                        const bool valid = node < g.cnt;
+                        const float y = __uint_as_float(o[i]);
+                        if (whole_item) {
+                            const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + in_group;
+                            A.out[orow * A.D + ch] = valid ? (uint16_t)pack2<DT>(y * sh.inv[c0 + i], 0.f) : (uint16_t)0;
+                        } else if (valid) {
+                            A.part_o[(place * rows_cta + slot * rows_used + r0 + i) * A.D + ch] = 4.f * y;
                         }
-                        if (++in_group == A.G) in_group = 0, ++local;
                     }
+                    if (++in_group == A.G) in_group = 0, ++local;
                 }
             }
             tc_fence_before();
             arrive(&sh.o_free);
+            arrive(&sh.seg_free[seg_no % kTaSlots]);
         }
         if (!ok) *abort = 1;
         if (fewer) {  // the nodes past every row tile (past the counts) see nothing
@@ -688,17 +736,17 @@ __global__ void __launch_bounds__(kT4Threads, 1)
                 const long long r0 = ((long long)b * A.N + n0) * A.Hq, r1 = ((long long)b * A.N + A.N) * A.Hq;
                 uint4 *o = reinterpret_cast<uint4 *>(A.out);
 #pragma unroll 1
-                for (long long i = r0 * A.D / 8 + threadIdx.x; i < r1 * A.D / 8; i += 128)
+                for (long long i = r0 * A.D / 8 + threadIdx.x; i < r1 * A.D / 8; i += kSoft * 32)
                     o[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (A.lse)
 #pragma unroll 1
-                    for (long long i = r0 + threadIdx.x; i < r1; i += 128) A.lse[i] = -INFINITY;
+                    for (long long i = r0 + threadIdx.x; i < r1; i += kSoft * 32) A.lse[i] = -INFINITY;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kT4WarpMma) {
+    if (warp == C::kMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -751,7 +799,7 @@ static spec_status_t t4_launch(const T4Args &T, const CUtensorMap &q, int ctas, 
         ready[dev] = true;
     }
     const spec_status_t st =
-        launch_pdl(tree_attn4<DT, DP, PACK, RP>, dim3((unsigned)ctas), dim3(kT4Threads), smem, s, q, T);
+        launch_pdl(tree_attn4<DT, DP, PACK, RP>, dim3((unsigned)ctas), dim3(T4Cfg<DP, PACK, RP>::kThreads), smem, s, q, T);
     if (st != SPEC_OK) return st;
     constexpr int rows = 256 / kTaJoinLanes;
     const int used = T.a.np * T.a.G, cta = PACK * used;
