@@ -34,8 +34,8 @@
 
 namespace sv {
 
-// tensor-memory columns: K, V and S two buffers each, then O
-constexpr uint32_t kT4K = 0, kT4V = 128, kT4S = 256, kT4O = 384, kT4Buf = 64;
+// tensor-memory columns: two buffers each of K, V, S and O
+constexpr uint32_t kT4K = 0, kT4V = 128, kT4S = 256, kT4O = 384, kT4Buf = 64;  // (an O for each stream)
 
 struct T4Args {
     TaArgs a;             // a.H: packs of heads
@@ -46,16 +46,30 @@ struct T4Args {
     int block, block_shift, bytes;  // tokens of a block, its bytes
 };
 
+#ifndef T4_TURNS
+#define T4_TURNS(c) ((c) == 16 ? 2 : 1)
+#endif
 template <int DP, int PACK, int RP> struct T4Cfg {
     static constexpr int kCols = PACK * RP;              // rows of all heads of a pack
     static constexpr int kRowP = kCols * 2;              // bytes of a key's weights
     static constexpr int kStage = PACK * DP * 136;       // one tile, packed
     static constexpr int kStages = kCols == 64 ? 6 : 8;
     static constexpr int kQ = PACK * RP * DP * 2;
-    static constexpr int kW = kCols < 32 ? kCols : 32;   // columns of a group of softmax warps
-    static constexpr int kSoft = 4 * (kCols / kW);       // softmax warps; then 4 of K and 4 of V
-    static constexpr int kLoad = kSoft + 8, kMma = kSoft + 9, kPlan = kSoft + 10;
-    static constexpr int kThreads = (kSoft + 11) * 32;
+    static constexpr int kW = kCols < 32 ? kCols : 32;   // columns of a softmax warp
+    // two warpgroups of softmax: a tile each in turn, or with 64 columns half of every tile's
+    static constexpr int kStreams = kCols > 32 ? 1 : 2;
+    // a tile's K and V: a warpgroup each, or two in turn
+    static constexpr int kTurns = T4_TURNS(kCols);
+    static constexpr int kSoft = 8, kV = kSoft + 4 * kTurns;  // softmax warps, then K's, then V's
+    static constexpr int kLoad = kV + 4 * kTurns, kMma = kLoad + 2, kPlan = kLoad + 3;  // (two warps load)
+    static constexpr int kWarps = kLoad + 4, kThreads = kWarps * 32;
+    // registers: at launch as many as fit; then the softmax takes what the others give back
+    static constexpr int kRegs = kTurns == 2 ? 72 : 96;
+    static constexpr int kRegSoft = kTurns == 2 ? 104 : 136, kRegUnpack = kTurns == 2 ? 56 : 72;
+    static constexpr int kRegHelp = kTurns == 2 ? 72 : 64;
+    static_assert(kSoft * kRegSoft + 8 * kTurns * kRegUnpack + 4 * kRegHelp <= kWarps * kRegs &&
+                      kWarps * kRegs * 32 <= 65536,
+                  "more registers than the CTA has: setmaxnreg would wait for ever");
     static constexpr int kSwizzle = kCols == 64 ? 2 : kCols == 32 ? 4 : 6;  // 128, 64 or 32 bytes
 };
 
@@ -64,10 +78,10 @@ template <int DP, int PACK, int RP> struct T4Shared {
     uint8_t q[kTaSlots][C::kQ];
     uint8_t p[2][kTaKeys * C::kRowP];
     uint8_t tile[C::kStages][C::kStage];     // per head: K's codes, V's codes, scales
-    uint4 scale[4][32];                      // of a V warp: V's multipliers and addends for its keys
-    float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references and their last factors
+    uint4 scale[4 * C::kTurns][32];                      // of a V warp: V's multipliers and addends for its keys
+    float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references, negated, and their last factors
     float top[C::kSoft][C::kW], sum[C::kSoft][C::kW];
-    float inv[C::kCols];
+    float w[2][C::kCols];                    // the streams' factors in the result
     long long incl[kTaChunks];
     SegSlot seg[kTaSlots];
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots], q_full[kTaSlots], q_free[kTaSlots];
@@ -117,15 +131,21 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *
     return ok != 0;
 }
 
-// A barrier of the 128 threads of a group of softmax warps; whether any of them says so.
-__device__ __forceinline__ bool meet128(int group, bool x) {
+// A barrier of THREADS threads, the softmax warps or a warpgroup of them; whether any of them says so.
+template <int THREADS> __device__ __forceinline__ bool meet(int id, bool x) {
     uint32_t r;
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+        "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; barrier.cta.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
         : "=r"(r)
-        : "r"((uint32_t)x), "r"(1 + group)
+        : "r"((uint32_t)x), "r"(id), "n"(THREADS)
         : "memory");
     return r != 0;
+}
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Shared-memory descriptor of the weights as the B operand [keys x rows]: the rows (N) are
@@ -172,14 +192,15 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
     Sh &sh = *reinterpret_cast<Sh *>(t4_raw + ((0u - smem_u32(t4_raw)) & 1023u));
     const TaArgs &A = T.a;
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    constexpr int kCols = C::kCols, kStages = C::kStages, kW = C::kW, kSoft = C::kSoft;
+    constexpr int kCols = C::kCols, kStages = C::kStages, kW = C::kW, kSoft = C::kSoft, kStreams = C::kStreams,
+                  kTurns = C::kTurns;
     constexpr float kLift = 7.f;  // weights up to 2^15: those 2^-29 below the maximum are still normal in float16
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTaSlots; ++i) {
             mbar_init(&sh.seg_full[i], 1);
             mbar_init(&sh.path_full[i], 1);
-            mbar_init(&sh.seg_free[i], kSoft + 2);
+            mbar_init(&sh.seg_free[i], kSoft + 3);
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_free[i], 1);
         }
@@ -188,9 +209,9 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             mbar_init(&sh.empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_ready[i], 4 + kSoft);
+            mbar_init(&sh.s_ready[i], 4 + kSoft / kStreams);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.pv_ready[i], 4 + kSoft);
+            mbar_init(&sh.pv_ready[i], 4 + kSoft / kStreams);
             mbar_init(&sh.pv_done[i], 1);
         }
         mbar_init(&sh.o_free, kSoft);
@@ -236,10 +257,12 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         return wait(&bars[k % kTaSlots], (uint32_t)(k / kTaSlots)) ? &sh.seg[k % kTaSlots] : nullptr;
     };
 
+    if (C::kRegHelp < C::kRegs && warp >= C::kLoad) fewer_registers<C::kRegHelp>();
     if (warp == C::kPlan) {  // ------------------------------------------- scheduling
         ta_schedule<kTaSplitKeys>(A, w, sh.incl, sh.seg, sh.seg_full, sh.path_full, sh.seg_free, u_first, u_last, run,
                                   abort);
-    } else if (warp == C::kLoad) {  // ------------------------------------- loads
+    } else if (warp == C::kLoad || warp == C::kLoad + 1) {  // ---------------- loads
+        const uint32_t turn = (uint32_t)(warp - C::kLoad);   // the warps take the tiles in turn
         const int recs = kTaKeys >> T.block_shift;           // blocks of a head's tile
         const int nb = PACK * recs, ahead = 32 / nb;         // blocks of a tile, tiles whose pages are fetched at once
         const int slot = lane % nb / recs, rec = lane % recs;  // of the pages that the lane fetches
@@ -258,7 +281,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             scale_rec[x] = at / (int)scales;
             scale_off[x] = 2 * (int)codes + at - scale_rec[x] * (int)scales;
         }
-        uint32_t stage = 0, fill = 0;
+        uint32_t e = 0, stage = 0, fill = 0;
         int seg_no = 0;
         bool ok = true;
         for (; ok; ++seg_no) {
@@ -267,8 +290,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             const Seg s = sp->s;
             arrive(&sh.seg_free[seg_no % kTaSlots]);
             const int qb = seg_no % kTaSlots;
-            if (seg_no >= kTaSlots && !wait(&sh.q_free[qb], (uint32_t)(seg_no / kTaSlots - 1))) break;
-            if (elect_one()) {
+            if (turn == 0 && seg_no >= kTaSlots && !wait(&sh.q_free[qb], (uint32_t)(seg_no / kTaSlots - 1))) break;
+            if (turn == 0 && elect_one()) {
                 mbar_expect_tx(&sh.q_full[qb], (uint32_t)(PACK * (DP / 64) * A.np * A.G * 128));
 #pragma unroll
                 for (int x = 0; x < PACK; ++x)
@@ -295,11 +318,15 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             };
             int base = s.i0;
             const uint8_t *now = fetch(base), *next = fetch(base + ahead);
-            for (int i = s.i0; i < i_end; ++i) {
+            for (int i = s.i0; i < i_end; ++i, ++e) {
                 if (i == base + ahead) {
                     base = i;
                     now = next;
                     next = fetch(base + ahead);
+                }
+                if ((e & 1u) != turn) {
+                    if (++stage == kStages) stage = 0, ++fill;
+                    continue;
                 }
                 if (fill > 0 && !wait(&sh.empty[stage], fill - 1)) {
                     ok = false;
@@ -312,7 +339,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(now), from_lane + r));
                 };
                 // (unrolled, so that a copy does not wait for the one before it to have read its addresses)
-#pragma unroll 8
+#pragma unroll 4
                 for (int x = 0; x < kTaKeys / 8; ++x) {
                     const uint8_t *src = place(x * 8 >> T.block_shift);
                     const uint32_t off = (uint32_t)((x * 8 & (T.block - 1)) * T.C / 2 + part * 16);
@@ -335,7 +362,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         }
         // every copy has landed before the CTA may exit
         copy_wait_all();
-        for (int x = 0; x < kTaSlots; ++x) {
+        for (int x = 0; x < kTaSlots && turn == 0; ++x) {
             const int n = (seg_no + kTaSlots - 1 - x) / kTaSlots;
             if (n > 0) mbar_wait_bounded(&sh.q_full[x], (uint32_t)(n - 1) & 1u, kTaWaitNs);
         }
@@ -344,72 +371,71 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         constexpr uint32_t kIdS = (ta_idesc<DT>(RP, false)), kIdO = ta_idesc<SPEC_DTYPE_F16>(kCols, true);
         const uint64_t q_desc = umma_desc_sw128(smem_u32(sh.q[0]));
         const uint64_t w_desc = p_desc<C::kRowP, C::kSwizzle>(smem_u32(sh.p[0]));
-        const int steps = T.C / 16;
         int s_seg = 0, s_left = 0, v_seg = 0, v_left = 0;
-        bool fresh = false, ok = true;
-        auto scores = [&](uint32_t e) -> bool {
-            const uint32_t buf = e & 1u, use = e >> 1;
-            if (s_left == 0) {
-                if (!take(sh.seg_full, s_seg)) return false;
-                s_left = __shfl_sync(0xFFFFFFFFu, sh.seg[s_seg % kTaSlots].s.n, 0);
-                if (!wait(&sh.q_full[s_seg % kTaSlots], (uint32_t)(s_seg / kTaSlots))) return false;
-                ++s_seg;
-            }
-            const int qb = (s_seg - 1) % kTaSlots;
-            if (!wait(&sh.s_ready[buf], use)) return false;
-            tc_fence_after();
-            --s_left;
-            if (elect_one()) {
-#pragma unroll
-                for (int x = 0; x < PACK; ++x) {
-                    const uint64_t qd = q_desc + (uint64_t)((qb * C::kQ + x * RP * DP * 2) / 16);
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        if (k < steps)
-                            mma_ts(tmem + kT4S + buf * kT4Buf + (uint32_t)(x * RP),
-                                   tmem + kT4K + buf * kT4Buf + (uint32_t)(x * DP / 2 + k * 8),
-                                   qd + (uint64_t)((k >> 2) * (RP * 128 / 16) + (k & 3) * 2), kIdS, k > 0 ? 1u : 0u);
+        bool ok = true;
+        uint32_t fresh = 0;  // streams whose next values are the segment's first
+        // The next tile's scores go before a tile's values, whose weights take longer.  (Groups of channels that
+        // the head does not have were written with another's codes, and meet zeros of Q.)
+#pragma unroll 1
+        for (uint32_t e = 0; e <= tiles && tiles > 0 && ok; ++e) {
+            if (e < tiles) {
+                const uint32_t buf = e & 1u, use = e >> 1;
+                if (s_left == 0) {
+                    if (!take(sh.seg_full, s_seg)) break;
+                    s_left = __shfl_sync(0xFFFFFFFFu, sh.seg[s_seg % kTaSlots].s.n, 0);
+                    if (!wait(&sh.q_full[s_seg % kTaSlots], (uint32_t)(s_seg / kTaSlots))) break;
+                    ++s_seg;
                 }
-                umma_commit(&sh.s_full[buf]);
-                if (s_left == 0) umma_commit(&sh.q_free[qb]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](uint32_t e) -> bool {
-            const uint32_t buf = e & 1u, use = e >> 1;
-            if (v_left == 0) {
-                v_left = __shfl_sync(0xFFFFFFFFu, sh.seg[v_seg % kTaSlots].s.n, 0);
-                if (v_seg > 0 && !wait(&sh.o_free, (uint32_t)(v_seg - 1))) return false;
-                ++v_seg;
-                fresh = true;
-            }
-            if (!wait(&sh.pv_ready[buf], use)) return false;
-            tc_fence_after();
-            if (elect_one()) {
+                const int qb = (s_seg - 1) % kTaSlots;
+                if (!wait(&sh.s_ready[buf], use)) break;
+                tc_fence_after();
+                --s_left;
+                const uint32_t d = tmem + kT4S + buf * kT4Buf, a = tmem + kT4K + buf * kT4Buf;
+                const uint64_t qd = q_desc + (uint64_t)(qb * (C::kQ / 16));
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kTaKeys / 16; ++k)
-                    mma_ts(tmem + kT4O, tmem + kT4V + buf * kT4Buf + (uint32_t)(k * 8),
-                           w_desc + (uint64_t)((buf * (uint32_t)(kTaKeys * C::kRowP) + k * 16 * C::kRowP) / 16), kIdO,
-                           fresh && k == 0 ? 0u : 1u);
-                umma_commit(&sh.pv_done[buf]);
+                    for (int x = 0; x < PACK; ++x)
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k)
+                            mma_ts(d + (uint32_t)(x * RP), a + (uint32_t)(x * DP / 2 + k * 8),
+                                   qd + (uint64_t)((x * RP * DP * 2 + (k >> 2) * (RP * 128) + (k & 3) * 32) / 16), kIdS,
+                                   k > 0 ? 1u : 0u);
+                    umma_commit(&sh.s_full[buf]);
+                    if (s_left == 0) umma_commit(&sh.q_free[qb]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            fresh = false;
-            if (--v_left == 0) arrive(&sh.seg_free[(v_seg - 1) % kTaSlots]);
-            return true;
-        };
-        // the next tile's scores go before a tile's values, whose weights take longer
-        if (tiles > 0) ok = scores(0);
-        for (uint32_t e = 0; e < tiles && ok; ++e) {
-            if (e + 1 < tiles) ok = scores(e + 1);
-            ok = ok && values(e);
+            if (e > 0) {
+                const uint32_t buf = (e - 1) & 1u, use = (e - 1) >> 1, stream = kStreams == 2 ? buf : 0u;
+                if (v_left == 0) {
+                    v_left = __shfl_sync(0xFFFFFFFFu, sh.seg[v_seg % kTaSlots].s.n, 0);
+                    if (v_seg > 0 && !wait(&sh.o_free, (uint32_t)(v_seg - 1))) break;
+                    ++v_seg;
+                    fresh = 3;
+                }
+                if (!wait(&sh.pv_ready[buf], use)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + kT4O + stream * kT4Buf, a = tmem + kT4V + buf * kT4Buf;
+                const uint64_t wd = w_desc + (uint64_t)(buf * (uint32_t)(kTaKeys * C::kRowP / 16));
+                const uint32_t add = (fresh >> stream) & 1u ? 0u : 1u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kTaKeys / 16; ++k)
+                        mma_ts(d, a + (uint32_t)(k * 8), wd + (uint64_t)(k * C::kRowP), kIdO, k > 0 ? 1u : add);
+                    umma_commit(&sh.pv_done[buf]);
+                }
+                __syncwarp();
+                fresh &= ~(1u << stream);
+                if (--v_left == 0) arrive(&sh.seg_free[(v_seg - 1) % kTaSlots]);
+            }
         }
         // every MMA has finished before the TMEM is freed
         if (elect_one()) umma_commit(&sh.done);
         mbar_wait_bounded(&sh.done, 0u, kTaWaitNs);
         __syncwarp();
-    } else if (warp >= kSoft + 4) {  // ----------------------------------------- V
+    } else if (warp >= C::kV && warp < C::kLoad) {  // ------------------------- V
+        fewer_registers<C::kRegUnpack>();
+        const uint32_t turn = kTurns == 2 ? (uint32_t)(warp - C::kV) >> 2 : 0u;  // the warpgroups take the tiles in turn
         const int quad = warp & 3, slot = quad * 32 / DP, ch = (quad * 32 + lane) % DP;
         const bool works = slot < PACK && ch - lane < T.C;  // the warp's lanes alike
         const int t = 4 * lane;                             // the keys whose scales the lane unpacks
@@ -417,8 +443,9 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int scale_off = head_off + kTaKeys * T.C + (t >> T.block_shift) * T.block * T.groups * 2 +
                               (T.groups + (ch >> 5)) * T.block + (t & (T.block - 1));
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kT4V;
-        uint4 *scale = sh.scale[quad];
-        for (uint32_t e = 0, stage = 0, fill = 0; e < tiles; ++e) {
+        uint4 *scale = sh.scale[warp - C::kV];
+        for (uint32_t e = turn, stage = turn, fill = 0; e < tiles; e += kTurns) {
+            const uint32_t buf = kTurns == 2 ? turn : e & 1u;
             if (!wait(&sh.full[stage], fill)) break;
             const uint8_t *tile = sh.tile[stage];
             uint32_t word[16];
@@ -432,35 +459,38 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 scale[lane] = make_uint4(a.x, a.y, b.x, b.y);
             }
             arrive(&sh.empty[stage]);
-            if (e >= 2 && !wait(&sh.pv_done[e & 1u], (e >> 1) - 1)) break;
+            if (e >= 2 && !wait(&sh.pv_done[buf], (e >> 1) - 1)) break;
             if (works) {
                 tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t v[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 a = scale[(h * 8 + i) * 2], b = scale[(h * 8 + i) * 2 + 1];
-                        const uint32_t x = word[h * 8 + i];
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 a = scale[(h * 4 + i) * 2], b = scale[(h * 4 + i) * 2 + 1];
+                        const uint32_t x = word[h * 4 + i];
                         v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, a.x, a.y);
                         v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, a.z, a.w);
                         v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, b.x, b.y);
                         v[4 * i + 3] = unpack_pair<SPEC_DTYPE_F16>(x, 3, b.z, b.w);
                     }
-                    tmem_store(to + (e & 1u) * kT4Buf + (uint32_t)(h * 32), v);
+                    tmem_store(to + buf * kT4Buf + (uint32_t)(h * 16), v);
                 }
                 tmem_wait_store();
                 tc_fence_before();
             }
-            arrive(&sh.pv_ready[e & 1u]);
-            if (++stage == (uint32_t)kStages) stage = 0, ++fill;
+            arrive(&sh.pv_ready[buf]);
+            if ((stage += kTurns) >= (uint32_t)kStages) stage = turn, ++fill;
         }
-    } else if (warp >= kSoft) {  // --------------------------------------------- K
+    } else if (warp >= kSoft && warp < C::kV) {  // ---------------------------- K
+        fewer_registers<C::kRegUnpack>();
+        const uint32_t turn = kTurns == 2 ? (uint32_t)(warp - kSoft) >> 2 : 0u;
         const int quad = warp & 3, key = quad * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kT4K;
         const int code_off = ((key >> 3) * T.groups * 8 + (key & 7)) * 16;
         const int scale_off = kTaKeys * T.C + (key >> T.block_shift) * T.block * T.groups * 2 + (key & (T.block - 1));
-        for (uint32_t e = 0, stage = 0, fill = 0; e < tiles; ++e) {
+        for (uint32_t e = turn, stage = turn, fill = 0; e < tiles; e += kTurns) {
+            const uint32_t buf = kTurns == 2 ? turn : e & 1u;
             if (!wait(&sh.full[stage], fill)) break;
             uint4 code[PACK * DP / 32];
             uint32_t byte[PACK * DP / 32];
@@ -472,62 +502,66 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 byte[x] = tile[scale_off + g * T.block];
             }
             arrive(&sh.empty[stage]);
-            if (e >= 2 && !wait(&sh.s_full[e & 1u], (e >> 1) - 1)) break;
+            if (e >= 2 && !wait(&sh.s_full[buf], (e >> 1) - 1)) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < PACK * DP / 64; ++x) {
-                uint32_t k[32];
+            for (int x = 0; x < PACK * DP / 32; ++x) {
+                const float f = scale_of(byte[x]);
+                const uint2 s = unpack_scale<DT>(f, f);
+                const uint32_t word[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+                uint32_t k[16];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float f = scale_of(byte[2 * x + y]);
-                    const uint2 s = unpack_scale<DT>(f, f);
-                    const uint4 c = code[2 * x + y];
-                    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) k[16 * y + i] = unpack_pair<DT>(word[i / 4], i % 4, s.x, s.y);
-                }
-                tmem_store(to + (e & 1u) * kT4Buf + (uint32_t)(x * 32), k);
+                for (int i = 0; i < 16; ++i) k[i] = unpack_pair<DT>(word[i / 4], i % 4, s.x, s.y);
+                tmem_store(to + buf * kT4Buf + (uint32_t)(x * 16), k);
             }
             tmem_wait_store();
             tc_fence_before();
-            arrive(&sh.s_ready[e & 1u]);
-            if (++stage == (uint32_t)kStages) stage = 0, ++fill;
+            arrive(&sh.s_ready[buf]);
+            if ((stage += kTurns) >= (uint32_t)kStages) stage = turn, ++fill;
         }
-    } else {  // ---------------------------------------------------------------- softmax
-        const int group = warp >> 2, quad = warp & 3;  // a group of four warps has kW columns
+    } else if (warp < kSoft) {  // ---------------------------------------------- softmax
+        more_registers<C::kRegSoft>();
+        const int wg = warp >> 2, quad = warp & 3;
+        const int stream = kStreams == 2 ? wg : 0;     // takes the tiles of this parity, or all
         const int key = quad * 32 + lane;              // of a tile; and the channel (of all heads) in O
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16, col0 = (uint32_t)(group * kW);
+        const uint32_t col0 = kStreams == 2 ? 0u : (uint32_t)(wg * kW);  // the warp's columns
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t ts = tmem + lanes + kT4S + col0, to = tmem + lanes + kT4O + (uint32_t)stream * kT4Buf + col0;
         const int slot = quad * 32 / DP, ch = key % DP;
         const int rows_used = A.np * A.G, rows_cta = PACK * rows_used;
         // a quarter of the keys' scale was multiplied in float16
         const float scale = A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
         const int sinks = A.window ? A.sinks : 0;
         float *m = sh.m[warp], *f = sh.f[warp];
-        uint32_t e = 0;
+        uint32_t base = 0;  // the CTA's tiles before this segment
         bool ok = true;
-        arrive(&sh.s_ready[0]);  // no scores to be read yet
-        arrive(&sh.s_ready[1]);
-        // The warps of a group leave together: a wait in vain is told at their next meeting, so that
-        // no warp stands at a barrier that another one has left for good.
+        arrive(&sh.s_ready[kStreams == 2 ? stream : 0]);  // no scores to be read yet
+        if (kStreams == 1) arrive(&sh.s_ready[1]);
+        // The warps leave together: a wait in vain is told at their next meeting, so that no warp stands
+        // at a barrier that another one has left for good.
         for (int seg_no = 0;; ++seg_no) {
             const SegSlot *sp = take(sh.path_full, seg_no);
-            if (meet128(group, !sp)) {
+            if (meet<256>(3, !sp)) {
                 ok = false;
                 break;
             }
-            if (sp->s.n == 0) break;
-            const Seg &s = sp->s;  // (read where it is used: registers are dear here)
-            const Geo &g = s.g;
+            const Seg &s = sp->s;
+            const int n = s.n;
+            if (n == 0) break;
+            const Geo g = s.g;
             // positions from `whole` on (to g.c) are seen by all nodes
             const int whole = A.window ? max(g.wlo, min(g.c, g.c + g.cnt - A.window)) : 0;
             float l[kW];
 #pragma unroll
             for (int i = 0; i < kW; ++i) l[i] = 0.f;
-            if (lane < kW) m[lane] = -FLT_MAX;
+            if (lane < kW) m[lane] = FLT_MAX;
             __syncwarp();
-            for (int t = 0; t < s.n; ++t, ++e) {
-                const int j0 = g.tile(s.i0 + t) * kTaKeys;
-                const uint32_t buf = e & 1u, use = e >> 1;
+            const int t0 = kStreams == 2 ? (int)((base + (uint32_t)stream) & 1u) : 0;
+            const int i0 = s.i0;
+#pragma unroll 1
+            for (int t = t0; t < n; t += kStreams) {
+                const int j0 = g.tile(i0 + t) * kTaKeys;
+                const uint32_t e = base + (uint32_t)t, buf = e & 1u, use = e >> 1;
                 const bool all = g.c - j0 >= kTaKeys && (j0 >= whole || sinks - j0 >= kTaKeys);
                 unsigned long long seen = ~0ull;  // the rows of a head that see this key
                 if (!all) {
@@ -536,12 +570,12 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     if (j < g.end) {
                         const unsigned long long one = A.G >= 64 ? ~0ull : (1ull << A.G) - 1ull;
 #pragma unroll 1
-                        for (int n = 0; n < A.np; ++n) {
-                            const int node = s.node0 + n;
+                        for (int x = 0; x < A.np; ++x) {
+                            const int node = s.node0 + x;
                             if (node >= g.cnt) break;
                             const bool yes = j < g.c ? j >= sp->low[node] || j < sinks
                                                      : ((sp->path[node] >> (j - g.c)) & 1ull) != 0;
-                            if (yes) seen |= one << (n * A.G);
+                            if (yes) seen |= one << (x * A.G);
                         }
                     }
                     if (PACK == 1) seen >>= col0;
@@ -551,7 +585,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 tc_fence_after();
                 float2 z[kW / 2];
                 auto scores = [&](uint32_t (&x)[kW]) {  // -inf where they are not seen
-                    tmem_load(tmem + lanes + kT4S + buf * kT4Buf + col0, x);
+                    tmem_load(ts + buf * kT4Buf, x);
                     if (!all) {
 #pragma unroll
                         for (int i = 0; i < kW; ++i)
@@ -566,11 +600,11 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     for (int i = 0; i < kW; i += 4) {
                         const float4 r = *reinterpret_cast<const float4 *>(m + i);
                         z[i / 2] = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2,
-                                        make_float2(-r.x, -r.y));
+                                        make_float2(r.x, r.y));
                         z[i / 2 + 1] = fma2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), c2,
-                                            make_float2(-r.z, -r.w));
-                        mx[0] = fmaxf(mx[0], fmaxf(z[i / 2].x, z[i / 2].y));
-                        mx[1] = fmaxf(mx[1], fmaxf(z[i / 2 + 1].x, z[i / 2 + 1].y));
+                                            make_float2(r.z, r.w));
+                        mx[0] = fmaxf(fmaxf(mx[0], z[i / 2].x), z[i / 2].y);
+                        mx[1] = fmaxf(fmaxf(mx[1], z[i / 2 + 1].x), z[i / 2 + 1].y);
                     }
                     return fmaxf(mx[0], mx[1]);
                 };
@@ -580,8 +614,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     scores(x);
                     largest = shift(x);
                 }
-                if (meet128(group, !ok || largest > kLift + kTaGrow)) {
-                    if (meet128(group, !ok)) {
+                if (meet<128>(1 + wg, !ok || largest > kLift + kTaGrow)) {
+                    if (meet<128>(1 + wg, !ok)) {
                         ok = false;
                         break;
                     }
@@ -596,32 +630,33 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         if (lane == i) mine = __int_as_float(y ^ ((y >> 31) & 0x7FFFFFFF));
                     }
                     if (lane < kW) sh.top[warp][lane] = mine;
-                    meet128(group, false);
+                    meet<128>(1 + wg, false);
                     if (lane < kW) {
-                        const int w0 = group * 4;
+                        const int w0 = wg * 4;
                         float y = fmaxf(fmaxf(sh.top[w0][lane], sh.top[w0 + 1][lane]),
                                         fmaxf(sh.top[w0 + 2][lane], sh.top[w0 + 3][lane])) * scale;
-                        const float old = m[lane];
+                        const float old = -m[lane];
                         y = y > old + kLift ? y - kLift : old;
                         f[lane] = ex2(old - y);
-                        m[lane] = y;
+                        m[lane] = -y;
                     }
                     __syncwarp();
                     scores(x);
                     shift(x);
 #pragma unroll
                     for (int i = 0; i < kW; ++i) l[i] *= f[i];
-                    if (t > 0) {  // O holds the tiles before this one
-                        ok = wait(&sh.pv_done[buf ^ 1u], (e - 1) >> 1);
+                    if (t > t0) {  // O holds the stream's tiles before this one
+                        // (through, of two streams, since before these scores: see below)
+                        if (kStreams == 1) ok = wait(&sh.pv_done[buf ^ 1u], (e - 1) >> 1);
                         if (ok) {
                             tc_fence_after();
 #pragma unroll
                             for (int d = 0; d < kW; d += 16) {
                                 uint32_t o[16];
-                                tmem_load(tmem + lanes + kT4O + col0 + (uint32_t)d, o);
+                                tmem_load(to + (uint32_t)d, o);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[d + i]);
-                                tmem_store(tmem + lanes + kT4O + col0 + (uint32_t)d, o);
+                                tmem_store(to + (uint32_t)d, o);
                             }
                             tmem_wait_store();
                         }
@@ -631,7 +666,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 arrive(&sh.s_ready[buf]);
                 // (the weights before the last are through: their product was issued before these scores,
                 // whose commit covers all products before it)
-                uint8_t *to = sh.p[buf] + key * C::kRowP;
+                uint8_t *p_row = sh.p[buf] + key * C::kRowP;
                 const int swap = C::kRowP == 128 ? key & 7 : C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1;
 #pragma unroll
                 for (int i = 0; i < kW; i += 8) {
@@ -645,7 +680,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         // errors, 2^-12 each, average out
                         p[y] = pack2<SPEC_DTYPE_F16>(w2.x, w2.y);
                     }
-                    *reinterpret_cast<uint4 *>(to + (((group * (kW / 8) + i / 8) ^ swap) * 16)) =
+                    *reinterpret_cast<uint4 *>(p_row + ((((int)col0 / 8 + i / 8) ^ swap) * 16)) =
                         make_uint4(p[0], p[1], p[2], p[3]);
                 }
                 fence_proxy_async();
@@ -655,15 +690,15 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
 
             // ---- the segment's result: sums over the warp's keys, a column to a lane
 #pragma unroll
-            for (int o = 16, n = kW; o > 0; o >>= 1) {
-                if (n > 1) {  // lanes o apart take half of the columns each
-                    n >>= 1;
+            for (int o = 16, w = kW; o > 0; o >>= 1) {
+                if (w > 1) {  // lanes o apart take half of the columns each
+                    w >>= 1;
 #pragma unroll
                     for (int i = 0; i < kW / 2; ++i) {
-                        if (i >= n) break;
+                        if (i >= w) break;
                         const bool up = (lane & o) != 0;
-                        const float give = up ? l[i] : l[i + n];
-                        l[i] = (up ? l[i + n] : l[i]) + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                        const float give = up ? l[i] : l[i + w];
+                        l[i] = (up ? l[i + w] : l[i]) + __shfl_xor_sync(0xFFFFFFFFu, give, o);
                     }
                 } else {
                     l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], o);
@@ -672,23 +707,44 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             // the lane's bits, from the top, chose the upper halves: lane i holds column i of 32, lanes 2 i and
             // 2 i + 1 column i of 16
             if (kW == 32 || (lane & 1) == 0) sh.sum[warp][kW == 32 ? lane : lane >> 1] = l[0];
-            const uint32_t last = e - 1;
+            base += (uint32_t)n;
+            // the last tiles' products (of the other stream's last tile too, if the segment has two)
+            const uint32_t last = base - 1;
             ok = ok && wait(&sh.pv_done[last & 1u], last >> 1);
-            if (meet128(group, !ok)) {
+            if (kStreams == 2 && n > 1) ok = ok && wait(&sh.pv_done[(last - 1) & 1u], (last - 1) >> 1);
+            if (meet<256>(3, !ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const bool whole_item = s.n == g.nt;
-            const long long place = (long long)blockIdx.x * 2 + (s.i0 == 0 ? 1 : 0);  // a cut item's part
-            if (key < kW) {  // a thread per row: its sum's reciprocal and lse
-                const int w0 = group * 4, c = (int)col0 + key;
-                const float total = sh.sum[w0][key] + sh.sum[w0 + 1][key] + sh.sum[w0 + 2][key] + sh.sum[w0 + 3][key];
+            const bool whole_item = n == g.nt;
+            const long long place = (long long)blockIdx.x * 2 + (i0 == 0 ? 1 : 0);  // a cut item's part
+            const int only = kStreams == 2 && n == 1 ? (int)(last & 1u) : -1;      // the one stream with a part
+            if ((int)threadIdx.x < kCols) {  // a thread per row: its sum and lse, and the factors of its parts
+                const int c = (int)threadIdx.x;
+                float ref, total;
+                auto part = [&](int w0, int at, float &mm, float &ll) {  // of the warps w0 .. w0 + 3
+                    mm = -sh.m[w0][at];
+                    ll = sh.sum[w0][at] + sh.sum[w0 + 1][at] + sh.sum[w0 + 2][at] + sh.sum[w0 + 3][at];
+                };
+                float w0 = 1.f, w1 = 0.f;
+                if (kStreams == 1) {
+                    part(c / kW * 4, c % kW, ref, total);
+                } else if (only >= 0) {
+                    part(only * 4, c, ref, total);
+                } else {
+                    float ma, la, mb, lb;
+                    part(0, c, ma, la);
+                    part(4, c, mb, lb);
+                    ref = fmaxf(ma, mb);
+                    w0 = ex2(ma - ref), w1 = ex2(mb - ref);
+                    total = la * w0 + lb * w1;
+                }
                 const int r = c % RP, local = r / A.G, node = s.node0 + local, hk = s.hk * PACK + c / RP;
                 const bool exists = r < rows_used && node < A.N && hk < T.heads, valid = exists && node < g.cnt;
-                float ref = sh.m[w0][key];
                 if (total != total) ref = fmaxf(ref, 0.f);  // the row's part must not pass for empty
-                sh.inv[c] = 4.f / total;                    // (O is a quarter of itself)
+                const float inv = whole_item ? 4.f / total : 4.f;  // (O is a quarter of itself)
+                sh.w[0][c] = w0 * inv, sh.w[1][c] = w1 * inv;
                 if (exists) {
                     if (whole_item) {
                         const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + (r - local * A.G);
@@ -699,14 +755,24 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     }
                 }
             }
-            meet128(group, false);
+            meet<256>(3, false);
+            // a warpgroup writes half of the columns of every head
             const int hk = s.hk * PACK + slot;
-            constexpr int kO = RP < kW ? RP : kW;                                  // columns of the head in this group
-            const int c0 = max(slot * RP, (int)col0), r0 = c0 - slot * RP;         // the first, and its row
-            if (slot < PACK && hk < T.heads && ch - lane < A.D && c0 < min(slot * RP + RP, (int)col0 + kW)) {
+            constexpr int kO = RP / 2;
+            const int r0 = wg * kO, c0 = slot * RP + r0;
+            if (slot < PACK && hk < T.heads && ch - lane < A.D && r0 < rows_used) {
                 int local = r0 / A.G, in_group = r0 - local * A.G;
                 uint32_t o[kO];
-                tmem_load(tmem + lanes + kT4O + (uint32_t)c0, o);
+                tmem_load(tmem + lanes + kT4O + (uint32_t)((only < 0 ? 0 : only) * (int)kT4Buf + c0), o);
+#pragma unroll
+                for (int i = 0; i < kO; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.w[0][c0 + i]);
+                if (kStreams == 2 && only < 0) {
+                    uint32_t y[kO];
+                    tmem_load(tmem + lanes + kT4O + kT4Buf + (uint32_t)c0, y);
+#pragma unroll
+                    for (int i = 0; i < kO; ++i)
+                        o[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), sh.w[1][c0 + i], __uint_as_float(o[i])));
+                }
 #pragma unroll
                 for (int i = 0; i < kO; ++i) {
                     const int node = s.node0 + local;
@@ -715,9 +781,9 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         const float y = __uint_as_float(o[i]);
                         if (whole_item) {
                             const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + in_group;
-                            A.out[orow * A.D + ch] = valid ? (uint16_t)pack2<DT>(y * sh.inv[c0 + i], 0.f) : (uint16_t)0;
+                            A.out[orow * A.D + ch] = valid ? (uint16_t)pack2<DT>(y, 0.f) : (uint16_t)0;
                         } else if (valid) {
-                            A.part_o[(place * rows_cta + slot * rows_used + r0 + i) * A.D + ch] = 4.f * y;
+                            A.part_o[(place * rows_cta + slot * rows_used + r0 + i) * A.D + ch] = y;
                         }
                     }
                     if (++in_group == A.G) in_group = 0, ++local;
