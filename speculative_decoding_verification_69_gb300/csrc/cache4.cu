@@ -49,20 +49,72 @@ __device__ __forceinline__ bool block8(const Move4Args &A, int b, int i, int n0,
     return true;
 }
 
-// Largest magnitude of a group: over a thread's 8 channels and the four threads of the group.
-__device__ __forceinline__ float group_max(const float (&f)[8], uint32_t mask) {
-    float m = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-    m = fmaxf(m, __shfl_xor_sync(mask, m, 1));
-    return fmaxf(m, __shfl_xor_sync(mask, m, 2));
-}
 template <int DT> __device__ __forceinline__ void widen(uint4 x, float (&f)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 y = unpack16<DT>(w[e]);
         f[2 * e] = y.x, f[2 * e + 1] = y.y;
+    }
+}
+
+// The scale byte of a group that holds what is not finite, or out of the codes' range, and the codes of a
+// thread's 8 channels in it, 4 bits each.  (Out of line: it would be half of the kernel's code.)
+template <int DT> __device__ __noinline__ uint2 quantise8_any(uint4 x, uint32_t lanes) {
+    float f[8], top = 0.f;
+    widen<DT>(x, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));  // (of those that are numbers, infinities among them)
+    top = fmaxf(top, __shfl_xor_sync(lanes, top, 1));
+    const uint32_t byte = scale_byte(fmaxf(top, __shfl_xor_sync(lanes, top, 2)));
+    const float s = scale_of(byte);
+    uint32_t codes = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) codes |= code_of(f[e], s) << (4 * e);
+    return make_uint2(byte, codes);
+}
+
+// Codes of a thread's 8 channels, each handed to `put`, and the scale byte of their group of 32,
+// which the four threads of the group find together.  Magnitudes are compared as whole numbers, which
+// order alike, NaN above all.  Returns whether all are finite.
+template <int DT, class F>
+__device__ __forceinline__ bool quantise8(uint4 x, uint32_t lanes, uint32_t &byte, F &&put) {
+    constexpr uint32_t kInf = DT == SPEC_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
+    auto magnitude = [](uint32_t w) { return w & 0x7FFF7FFFu; };
+    uint32_t m = __vmaxu2(__vmaxu2(magnitude(x.x), magnitude(x.y)), __vmaxu2(magnitude(x.z), magnitude(x.w)));
+    m = __vmaxu2(m, __shfl_xor_sync(lanes, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(lanes, m, 2));
+    m = max(m & 0xFFFFu, m >> 16);
+    byte = scale_byte(unpack16<DT>(m).x);
+    if (m < kInf && byte < 255u) {
+        float f[8];
+        widen<DT>(x, f);
+        const float s = scale_of(byte), inv = near_reciprocal(s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) put(e, code_sum(f[e], s, inv) & 15u);
+        return true;
+    }
+    const uint2 y = quantise8_any<DT>(x, lanes);
+    byte = y.x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) put(e, (y.y >> (4 * e)) & 15u);
+    return m < kInf;
+}
+
+// The words of a block's keys in one group, from thread j of its four holding word j of the 8 tokens to
+// holding word a of token 2 j + b at 2 a + b, or back.
+__device__ __forceinline__ void exchange(uint32_t (&w)[8], int j, uint32_t lanes) {
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {
+        const bool up = (j & o) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if ((i >> 1) & o) continue;
+            const uint32_t give = up ? w[i] : w[i + 2 * o];
+            const uint32_t got = __shfl_xor_sync(lanes, give, o);
+            if (up) w[i] = got;
+            else w[i + 2 * o] = got;
+        }
     }
 }
 
@@ -108,29 +160,37 @@ template <int DT> __global__ void __launch_bounds__(256) sv_append4(const __grid
             w[4] = z.x & keep, w[5] = z.y & keep, w[6] = z.z & keep, w[7] = z.w & keep;
         }
         bool finite = true;
+        const bool whole = x.t1 - x.t0 == 8;
+        uint32_t kw[8] = {}, bytes[2][2] = {};  // words of the keys; scales of keys and values, a byte for each token
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             if (t < x.t0 || t >= x.t1) continue;
-            float f[8];
-            widen<DT>(k[t], f);
-            uint32_t byte = scale_byte(group_max(f, group_lanes)), word = 0;
-            float s = scale_of(byte);
+            uint32_t byte;
+            finite = quantise8<DT>(k[t], group_lanes, byte, [&](int e, uint32_t c) { kw[t] |= c << bit4(e); }) && finite;
+            bytes[0][t >> 2] |= byte << (8 * (t & 3));
+            finite = quantise8<DT>(v[t], group_lanes, byte, [&](int e, uint32_t c) { w[e] |= c << bit4(t); }) && finite;
+            bytes[1][t >> 2] |= byte << (8 * (t & 3));
+        }
+        uint8_t *codes = to + key4(P, x.tok, g);
+        if (whole) {
+            // each of a group's four threads writes two tokens: 32 bytes, not eight times 4 beside other threads'
+            const int j = d8 & 3;
+            exchange(kw, j, group_lanes);
+            uint4 *two = reinterpret_cast<uint4 *>(codes) + 2 * j;
+            two[0] = make_uint4(kw[0], kw[2], kw[4], kw[6]);
+            two[1] = make_uint4(kw[1], kw[3], kw[5], kw[7]);
+            if (j < 2)
+                *reinterpret_cast<uint2 *>(to + scale4(P, x.tok, g, j == 1)) =
+                    j == 1 ? make_uint2(bytes[1][0], bytes[1][1]) : make_uint2(bytes[0][0], bytes[0][1]);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                word |= code_of(f[e], s) << bit4(e);
-                finite = finite && fabsf(f[e]) < INFINITY;
+            for (int t = 0; t < 8; ++t) {
+                if (t < x.t0 || t >= x.t1) continue;
+                *reinterpret_cast<uint32_t *>(codes + t * 16 + (d8 & 3) * 4) = kw[t];
+                if ((d8 & 3) < 2)
+                    to[scale4(P, x.tok + t, g, (d8 & 3) == 1)] =
+                        (uint8_t)((d8 & 3) == 1 ? bytes[1][t >> 2] >> (8 * (t & 3)) : bytes[0][t >> 2] >> (8 * (t & 3)));
             }
-            *reinterpret_cast<uint32_t *>(to + key4(P, x.tok + t, g) + (d8 & 3) * 4) = word;
-            if ((d8 & 3) == 0) to[scale4(P, x.tok + t, g, false)] = (uint8_t)byte;
-            widen<DT>(v[t], f);
-            byte = scale_byte(group_max(f, group_lanes));
-            s = scale_of(byte);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                w[e] |= code_of(f[e], s) << bit4(t);
-                finite = finite && fabsf(f[e]) < INFINITY;
-            }
-            if ((d8 & 3) == 0) to[scale4(P, x.tok + t, g, true)] = (uint8_t)byte;
         }
         words[0] = make_uint4(w[0], w[1], w[2], w[3]);
         words[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -158,24 +218,28 @@ template <int DT> __global__ void __launch_bounds__(256) sv_read4(const __grid_c
     const int t0 = first < 0 ? (int)-first : 0, t1 = (int)min(8ll, A.N - first);
     if (t1 <= t0) return;
     const int per = P.C >> 3, vecs = P.D >> 3;
+    const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
+    const uint32_t group_lanes = 0xFu << (lane & 28);
     for (int c = threadIdx.x; c < P.heads * per; c += blockDim.x) {
         const int h = c / per, d8 = c - h * per, g = d8 >> 2;
-        if (d8 >= vecs) continue;
         uint32_t kw[8], vw[8], ks[8], vs[8];
         if (there) {
             const uint8_t *from = x.at + blockIdx.z * P.layer + h * P.head;
             const uint4 *words = reinterpret_cast<const uint4 *>(from + value4(P, x.tok, d8 * 8));
-            const uint4 a = words[0], z = words[1];
-            vw[0] = a.x, vw[1] = a.y, vw[2] = a.z, vw[3] = a.w, vw[4] = z.x, vw[5] = z.y, vw[6] = z.z, vw[7] = z.w;
+            const uint4 *two = reinterpret_cast<const uint4 *>(from + key4(P, x.tok, g)) + 2 * (d8 & 3);
+            const uint4 a = words[0], z = words[1], y0 = two[0], y1 = two[1];
             const uint2 sk = *reinterpret_cast<const uint2 *>(from + scale4(P, x.tok, g, false));
             const uint2 sv = *reinterpret_cast<const uint2 *>(from + scale4(P, x.tok, g, true));
+            vw[0] = a.x, vw[1] = a.y, vw[2] = a.z, vw[3] = a.w, vw[4] = z.x, vw[5] = z.y, vw[6] = z.z, vw[7] = z.w;
+            kw[0] = y0.x, kw[2] = y0.y, kw[4] = y0.z, kw[6] = y0.w, kw[1] = y1.x, kw[3] = y1.y, kw[5] = y1.z, kw[7] = y1.w;
+            exchange(kw, d8 & 3, group_lanes);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                kw[t] = *reinterpret_cast<const uint32_t *>(from + key4(P, x.tok + t, g) + (d8 & 3) * 4);
                 ks[t] = ((t < 4 ? sk.x : sk.y) >> (8 * (t & 3))) & 255u;
                 vs[t] = ((t < 4 ? sv.x : sv.y) >> (8 * (t & 3))) & 255u;
             }
         }
+        if (d8 >= vecs) continue;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             if (t < t0 || t >= t1) continue;
@@ -197,88 +261,123 @@ template <int DT> __global__ void __launch_bounds__(256) sv_read4(const __grid_c
     }
 }
 
-// Accepted nodes moved behind their root.  Grid (requests, layers x heads), 128 threads.
+// Accepted nodes moved behind their root.  Grid (requests, shares of the layers and heads): a CTA finds the
+// request's path and the places of its pieces once, then a warp takes a layer and head at a time.
 // All that moves is read before anything is written: the keys' codes and all scales into
 // registers, the values' words (which hold other tokens' codes too) into shared memory, where a
-// thread takes one channel's codes from node to place in the order of the path (place <= node, so no
-// code is overwritten before it is read), and writes the words back that changed.
-constexpr int kC4Threads = 128, kC4Blocks = SPEC_MAX_TREE / 8 + 1;
-__global__ void __launch_bounds__(kC4Threads) sv_commit4(Pool4 P, Pool ids, const int *table, const int *len,
-                                                         const int *nodes, const int *accept, int *new_len, int N,
-                                                         int max_pages, uint32_t *status) {
+// lane takes four channels' codes from node to place in the order of the path (place <= node, so no
+// code is overwritten before it is read), and writes the words back that changed.  Bound by
+// instructions, so by how much is found once; a thread per channel took 77 us where this takes
+// (64 requests of 32 nodes, 36 layers of 8 heads)
+constexpr int kC4Warps = 8, kC4Blocks = SPEC_MAX_TREE / 8 + 1, kC4Pieces = SPEC_MAX_TREE * 4;
+struct Piece4 {  // 16 bytes of codes of a moved key, and the scales beside them: offsets from a layer's head
+    long long src, dst;
+    int src_scale, dst_scale;  // from those: of the key; the value's lies `groups` blocks on
+};
+__global__ void __launch_bounds__(kC4Warps * 32) sv_commit4(Pool4 P, Pool ids, const int *table, const int *len,
+                                                            const int *nodes, const int *accept, int *new_len, int N,
+                                                            int max_pages, uint32_t *status) {
     // places as page * page_size + token
-    __shared__ long long s_src[SPEC_MAX_TREE], s_dst[SPEC_MAX_TREE];
-    __shared__ uint32_t words[kC4Blocks][kC4Threads];
-    __shared__ int s_n, s_node[SPEC_MAX_TREE];
+    __shared__ long long s_src[SPEC_MAX_TREE], s_dst[SPEC_MAX_TREE], s_block[kC4Blocks];
+    __shared__ Piece4 pieces[kC4Pieces];
+    __shared__ uint4 words[kC4Warps][kC4Blocks][32];
+    __shared__ int s_n, s_move[SPEC_MAX_TREE], s_last;
     pdl_trigger();
     pdl_wait();
-    const int b = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const bool first = blockIdx.y == 0;
     const int a = commit_path(ids, table, len, nodes, accept, b, N, max_pages, s_src, s_dst, &s_n, status, first);
-    const int n0 = len[b];
+    const int n0 = len[b], n8 = n0 & 7;
     if (first && new_len && tid == 0) new_len[b] = commit_len(n0, a);
     if (a <= 0 || !nodes) return;
-    if (tid < a) s_node[tid] = nodes[(long long)b * N + tid];
-    uint8_t *base = P.data + (blockIdx.y / P.heads) * P.layer + (blockIdx.y % P.heads) * P.head;
-    auto page_of = [&](long long id) { return base + (id >> P.page_shift) * P.page_st; };
-    auto tok_of = [&](long long id) { return (int)(id & (P.page - 1)); };
+    if (tid == 0) s_last = 0;
     __syncthreads();
-    // the blocks of 8 tokens from the root's to the last node's (a path need not be in order)
-    int last = 0;
-    for (int i = 0; i < a; ++i) last = max(last, s_node[i]);
-    const int n8 = n0 & 7, blocks = ((n8 + last) >> 3) + 1;
-    auto block_at = [&](int i) -> uint8_t * {  // nullptr: no page, so nothing moves from or to it
-        const long long pos = ((long long)(n0 >> 3) + i) << 3, place = pos >> P.page_shift;
+    if (tid < a) {  // the blocks and bits that node tid's codes move between
+        const int node = nodes[(long long)b * N + tid], from = n8 + node, to = n8 + 1 + tid;
+        s_move[tid] = (from >> 3) | bit4(from & 7) << 8 | (to >> 3) << 16 | bit4(to & 7) << 24;
+        atomicMax(&s_last, node);  // (a path need not be in order)
+    }
+    if (tid < kC4Blocks) {  // the blocks of 8 tokens from the root's on; -1: no page, so nothing moves from or to it
+        const long long pos = ((long long)(n0 >> 3) + tid) << 3, place = pos >> P.page_shift;
         const int p = place < max_pages ? table[(long long)b * max_pages + place] : -1;
-        if ((unsigned)p >= (unsigned)P.num_pages) return nullptr;
-        return base + p * P.page_st + value4(P, (int)(pos & (P.page - 1)), tid);
-    };
-    if (tid < P.C) {
-#pragma unroll
-        for (int i = 0; i < kC4Blocks; ++i) {
-            if (i >= blocks) break;
-            const uint8_t *w = block_at(i);
-            words[i][tid] = w ? *reinterpret_cast<const uint32_t *>(w) : 0u;
-        }
+        s_block[tid] = (unsigned)p < (unsigned)P.num_pages
+                           ? (long long)p * P.page_st + value4(P, (int)(pos & (P.page - 1)), 0)
+                           : -1ll;
     }
-    constexpr int kMost = (SPEC_MAX_TREE * 4 + kC4Threads - 1) / kC4Threads;
-    uint4 code[kMost];
-    uint8_t sk[kMost], sv[kMost];
-#pragma unroll
-    for (int u = 0; u < kMost; ++u) {
-        const int x = u * kC4Threads + tid, i = x / P.groups, g = x - i * P.groups;
-        if (i < a && s_src[i] != s_dst[i]) {
-            const uint8_t *from = page_of(s_src[i]);
-            const int t = tok_of(s_src[i]);
-            code[u] = *reinterpret_cast<const uint4 *>(from + key4(P, t, g));
-            sk[u] = from[scale4(P, t, g, false)];
-            sv[u] = from[scale4(P, t, g, true)];
-        }
-    }
-    if (tid < P.C) {
-        uint32_t changed = 0;
-        for (int i = 0; i < a; ++i) {
-            const int from = n8 + s_node[i], to = n8 + 1 + i;
-            if (from == to) continue;
-            const uint32_t c = (words[from >> 3][tid] >> bit4(from & 7)) & 15u;
-            uint32_t &w = words[to >> 3][tid];
-            w = (w & ~(15u << bit4(to & 7))) | (c << bit4(to & 7));
-            changed |= 1u << (to >> 3);
-        }
-        for (int i = 0; i < blocks; ++i)
-            if ((changed >> i) & 1u) *reinterpret_cast<uint32_t *>(block_at(i)) = words[i][tid];
+    const int count = a * P.groups;
+    for (int x = tid; x < count; x += kC4Warps * 32) {
+        const int i = x / P.groups, g = x - i * P.groups;
+        Piece4 y;
+        auto place = [&](long long id, long long &at, int &scale) {
+            const int tok = (int)(id & (P.page - 1)), key = key4(P, tok, g);
+            at = (id >> P.page_shift) * P.page_st + key;
+            scale = scale4(P, tok, g, false) - key;
+        };
+        place(s_src[i], y.src, y.src_scale);
+        place(s_dst[i], y.dst, y.dst_scale);
+        pieces[x] = y;
     }
     __syncthreads();
+    const int blocks = ((n8 + s_last) >> 3) + 1, value_scale = P.groups * P.block;
+    uint4(&w)[kC4Blocks][32] = words[tid >> 5];
+    for (int item = blockIdx.y * kC4Warps + (tid >> 5); item < P.layers * P.heads; item += gridDim.y * kC4Warps) {
+        uint8_t *base = P.data + item / P.heads * P.layer + item % P.heads * P.head;
+        const bool mine = lane * 4 < P.C;
+        if (mine) {
 #pragma unroll
-    for (int u = 0; u < kMost; ++u) {
-        const int x = u * kC4Threads + tid, i = x / P.groups, g = x - i * P.groups;
-        if (i < a && s_src[i] != s_dst[i]) {
-            uint8_t *to = page_of(s_dst[i]);
-            const int t = tok_of(s_dst[i]);
-            *reinterpret_cast<uint4 *>(to + key4(P, t, g)) = code[u];
-            to[scale4(P, t, g, false)] = sk[u];
-            to[scale4(P, t, g, true)] = sv[u];
+            for (int i = 0; i < kC4Blocks; ++i) {
+                if (i >= blocks) break;
+                w[i][lane] = s_block[i] >= 0 ? *reinterpret_cast<const uint4 *>(base + s_block[i] + lane * 16)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+            }
         }
+        constexpr int kMost = kC4Pieces / 32;
+        uint4 code[kMost];
+        uint8_t sk[kMost], sv[kMost];
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
+            if (u * 32 >= count) break;
+            if (u * 32 + lane < count) {
+                const Piece4 &y = pieces[u * 32 + lane];
+                const uint8_t *from = base + y.src;
+                code[u] = *reinterpret_cast<const uint4 *>(from);
+                sk[u] = from[y.src_scale];
+                sv[u] = from[y.src_scale + value_scale];
+            }
+        }
+        __syncwarp();
+        if (mine) {
+            uint32_t changed = 0;
+            for (int i = 0; i < a; ++i) {
+                const int move = s_move[i], from = move & 255, to = (move >> 16) & 255;
+                const int right = (move >> 8) & 255, left = move >> 24;
+                if (from == to && right == left) continue;
+                const uint4 x = w[from][lane];
+                uint4 y = w[to][lane];
+                const uint32_t keep = ~(15u << left);
+                y.x = (y.x & keep) | ((x.x >> right) & 15u) << left;
+                y.y = (y.y & keep) | ((x.y >> right) & 15u) << left;
+                y.z = (y.z & keep) | ((x.z >> right) & 15u) << left;
+                y.w = (y.w & keep) | ((x.w >> right) & 15u) << left;
+                w[to][lane] = y;
+                changed |= 1u << to;
+            }
+            for (int i = 0; i < blocks; ++i)
+                if ((changed >> i) & 1u) *reinterpret_cast<uint4 *>(base + s_block[i] + lane * 16) = w[i][lane];
+        }
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
+            if (u * 32 >= count) break;
+            if (u * 32 + lane < count) {
+                const Piece4 &y = pieces[u * 32 + lane];
+                if (y.src == y.dst) continue;
+                uint8_t *to = base + y.dst;
+                *reinterpret_cast<uint4 *>(to) = code[u];
+                to[y.dst_scale] = sk[u];
+                to[y.dst_scale + value_scale] = sv[u];
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -421,7 +520,7 @@ spec_status_t spec_cache4_commit(const spec_pages4_t *pages, const int32_t *page
     const spec_status_t st = sv::make_pool4(pages, P);
     if (st != SPEC_OK) return st;
     if (!page_table || !cache_len || !accept_len || !new_len || B < 1 || B >= (1 << 16) || N < 1 ||
-        N > SPEC_MAX_TREE || max_pages < 1 || (long long)P.layers * P.heads > 65535)
+        N > SPEC_MAX_TREE || max_pages < 1)
         return SPEC_ERR_INVALID_ARG;
     sv::Pool ids = {};  // in which a place's offset is its number
     ids.page_st = P.page;
@@ -432,10 +531,13 @@ spec_status_t spec_cache4_commit(const spec_pages4_t *pages, const int32_t *page
     const bool in_place = new_len == cache_len;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (out_nodes || !in_place) {
-        const unsigned each = out_nodes ? (unsigned)(P.layers * P.heads) : 1u;
-        const spec_status_t r = sv::launch_pdl(sv::sv_commit4, dim3((unsigned)B, each), dim3(sv::kC4Threads), 0, s, P,
-                                               ids, page_table, cache_len, out_nodes, accept_len,
-                                               in_place ? (int *)nullptr : new_len, N, max_pages, dev_status);
+        // about four CTAs to an SM: more would find the paths anew
+        const long long shares = ((long long)P.layers * P.heads + sv::kC4Warps - 1) / sv::kC4Warps, fit = 608 / B + 1;
+        const unsigned each = out_nodes ? (unsigned)(shares < fit ? shares : fit) : 1u;
+        const spec_status_t r = sv::launch_pdl(sv::sv_commit4, dim3((unsigned)B, each),
+                                               dim3(sv::kC4Warps * 32), 0, s, P, ids, page_table, cache_len,
+                                               out_nodes, accept_len, in_place ? (int *)nullptr : new_len, N,
+                                               max_pages, dev_status);
         if (r != SPEC_OK || !in_place) return r;
     }
     return sv::launch_commit_len(ids, page_table, new_len, out_nodes, accept_len, B, N, max_pages, dev_status, s);

@@ -43,14 +43,32 @@ __device__ __forceinline__ int bit4(int i) { return 4 * (i >> 1) + 16 * (i & 1);
 __device__ __forceinline__ float scale_of(uint32_t byte) {
     return __uint_as_float((byte + ((127u - 19u) << 3)) << 20);
 }
+// x / d for inv near 1 / d: one residual correction of the quotient (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  Where x / d has few bits it is exact.
+__device__ __forceinline__ float quotient(float x, float d, float inv) {
+    const float y = x * inv;
+    return fmaf(fmaf(-d, y, x), inv, y);
+}
 // The byte of the scale nearest to amax / 7 (ties to even), of the smallest or largest one beyond
 // the ends.  The true quotient of a number of 11 bits is no nearer to the middle between
-// two scales than 2^-13 of it, unless it is one, which a correctly rounded division gives exactly.
+// two scales than 2^-13 of it, unless it is one, and then it has few bits.
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-    const uint32_t b = __float_as_uint(__fdiv_rn(amax, 7.f));
+    const uint32_t b = __float_as_uint(amax < INFINITY ? quotient(amax, 7.f, 1.f / 7.f) : amax);
     const int r = (int)((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127 - 19) << 3);
     return (uint32_t)max(0, min(r, 255));
 }
+// The code of x, which is finite, |x| / s within 7.5: the low four bits of the sum.  inv: 1 / s to 2^-22.
+// Ties are exact (see quotient); all other quotients of a number of 11 bits and one of 4 are 2^-12 or
+// more from a tie.  Adding 1.5 * 2^23 (+ 8) rounds to a whole number, ties to even.
+__device__ __forceinline__ uint32_t code_sum(float x, float s, float inv) {
+    return __float_as_uint(quotient(x, s, inv) + (12582912.f + 8.f));
+}
+__device__ __forceinline__ float near_reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The same for any x: NaN gives 0, and what is out of range the end of it.
 __device__ __forceinline__ uint32_t code_of(float x, float s) {
     return (uint32_t)(max(-8, min(__float2int_rn(__fdiv_rn(x, s)), 7)) + 8);  // (NaN converts to 0)
 }

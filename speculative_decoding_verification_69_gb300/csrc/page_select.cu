@@ -140,66 +140,91 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
 // (4 bytes per channel), which the warps' mma.sync keeps up with to about 64 rows: the operands
 // go from HBM to registers in the product's own layout (a thread's share of the channels is
 // contiguous, since any order of them gives the same sum) and pass no shared memory.
+// The grid is as many CTAs as run at once; a warp's next page numbers come while it
+// multiplies, so that each unit waits for memory once.
 template <int DT, int BLOCKS>  // BLOCKS of 32 channels
-__global__ void __launch_bounds__(256) sv_scores(const __grid_constant__ ScoreArgs A) {
+__global__ void __launch_bounds__(256, 2) sv_scores(const __grid_constant__ ScoreArgs A) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int h = (int)(unit % A.heads), tile = (int)(unit / A.heads % A.tiles), b = (int)(unit / A.heads / A.tiles);
-    if (b >= A.B) return;
-    long long len = A.len[b];
-    if (len < 0 || len > (long long)A.max_pages << A.page_shift) {
-        if (tile == 0 && h == 0 && lane == 0) flag(A.status, SPEC_DEV_BAD_LEN);
-        len = len < 0 ? 0 : (long long)A.max_pages << A.page_shift;
-    }
-    const int n = (int)((len + A.page - 1) >> A.page_shift);
-    const int rows = (A.node_count ? max(0, min(A.node_count[b], A.N)) : A.N) * A.G;
-    float *out = A.scores + ((long long)b * A.heads + h) * A.max_pages;
-    const int i0 = tile * 16;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-    uint4 lo[2][BLOCKS], hi[2][BLOCKS];
-    bool there[2];
+    // unit (b, tile, h), the heads of a tile side by side; a step of the grid as such a triple
+    long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long step = (long long)gridDim.x * 8;
+    int h = (int)(unit % A.heads), tile = (int)(unit / A.heads % A.tiles);
+    long long b = unit / A.heads / A.tiles;
+    const int step_h = (int)(step % A.heads), step_t = (int)(step / A.heads % A.tiles);
+    const long long step_b = step / A.heads / A.tiles;
+    int n = 0, rows = 0, page[2] = {-1, -1};
+    auto fetch = [&]() {  // the unit's pages and sizes
+        if (b >= A.B) return;
+        long long len = A.len[b];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int i = i0 + g + 8 * u;
-        int p = i < n ? A.table[(long long)b * A.max_pages + i] : -1;
-        there[u] = (unsigned)p < (unsigned)A.num_pages;
-        if (i < n && !there[u] && t == 0) flag(A.status, SPEC_DEV_BAD_PAGE);
-        const uint4 *x = A.bounds + ((long long)(there[u] ? p : 0) * A.heads + h) * 2 * A.vecs;
-#pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) {
-            const bool real = there[u] && rows > 0 && k * 4 + t < A.vecs;
-            lo[u][k] = real ? ld_stream_v4(x + k * 4 + t) : none;
-            hi[u][k] = real ? ld_stream_v4(x + A.vecs + k * 4 + t) : none;
+        for (int u = 0; u < 2; ++u) {
+            const int i = tile * 16 + g + 8 * u;
+            page[u] = i < A.max_pages ? A.table[b * A.max_pages + i] : -1;
         }
-    }
-    float best[2] = {-INFINITY, -INFINITY};
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-        const int r = r0 + g, node = r / A.G;
-        const uint4 *q = A.q + b * A.qb + node * A.qn + (long long)(h * A.G + r - node * A.G) * A.qh;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) {
-            const uint4 y = r < rows && k * 4 + t < A.vecs ? __ldg(q + k * 4 + t) : none;
-            mma16<DT>(c, hi[0][k].x, hi[1][k].x, hi[0][k].y, hi[1][k].y, max16<DT>(y.x, 0u), max16<DT>(y.y, 0u));
-            mma16<DT>(c, hi[0][k].z, hi[1][k].z, hi[0][k].w, hi[1][k].w, max16<DT>(y.z, 0u), max16<DT>(y.w, 0u));
-            mma16<DT>(c, lo[0][k].x, lo[1][k].x, lo[0][k].y, lo[1][k].y, min16<DT>(y.x, 0u), min16<DT>(y.y, 0u));
-            mma16<DT>(c, lo[0][k].z, lo[1][k].z, lo[0][k].w, lo[1][k].w, min16<DT>(y.z, 0u), min16<DT>(y.w, 0u));
+        rows = (A.node_count ? max(0, min(A.node_count[b], A.N)) : A.N) * A.G;
+        if (len < 0 || len > (long long)A.max_pages << A.page_shift) {
+            if (tile == 0 && h == 0 && lane == 0) flag(A.status, SPEC_DEV_BAD_LEN);
+            len = len < 0 ? 0 : (long long)A.max_pages << A.page_shift;
         }
+        n = (int)((len + A.page - 1) >> A.page_shift);
+    };
+    fetch();
+    while (b < A.B) {
+        const int i0 = tile * 16, rows_now = rows, h_now = h;
+        const long long b_now = b;
+        uint4 lo[2][BLOCKS], hi[2][BLOCKS];
+        bool there[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (r0 + 2 * t + e < rows) {
-                best[0] = max_nan(best[0], c[e]);
-                best[1] = max_nan(best[1], c[2 + e]);
+        for (int u = 0; u < 2; ++u) {
+            const int i = i0 + g + 8 * u;
+            there[u] = i < n && (unsigned)page[u] < (unsigned)A.num_pages;
+            if (i < n && !there[u] && t == 0) flag(A.status, SPEC_DEV_BAD_PAGE);
+            const uint4 *x = A.bounds + ((long long)(there[u] ? page[u] : 0) * A.heads + h) * 2 * A.vecs;
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) {
+                const bool real = there[u] && rows > 0 && k * 4 + t < A.vecs;
+                lo[u][k] = real ? ld_stream_v4(x + k * 4 + t) : none;
+                hi[u][k] = real ? ld_stream_v4(x + A.vecs + k * 4 + t) : none;
             }
-    }
+        }
+        h += step_h;
+        tile += step_t;
+        b += step_b;
+        if (h >= A.heads) h -= A.heads, ++tile;
+        if (tile >= A.tiles) tile -= A.tiles, ++b;
+        fetch();
+        float best[2] = {-INFINITY, -INFINITY};
+        const bool any = __any_sync(0xFFFFFFFFu, there[0] || there[1]);
+        for (int r0 = 0; r0 < rows_now && any; r0 += 8) {
+            const int r = r0 + g, node = r / A.G;
+            const uint4 *q = A.q + b_now * A.qb + node * A.qn + (long long)(h_now * A.G + r - node * A.G) * A.qh;
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        best[u] = max_nan(best[u], __shfl_xor_sync(0xFFFFFFFFu, best[u], 1));
-        best[u] = max_nan(best[u], __shfl_xor_sync(0xFFFFFFFFu, best[u], 2));
-        const int i = i0 + g + 8 * u;
-        if (t == 0 && i < A.max_pages) out[i] = there[u] ? best[u] : -INFINITY;
+            for (int k = 0; k < BLOCKS; ++k) {
+                const uint4 y = r < rows_now && k * 4 + t < A.vecs ? __ldg(q + k * 4 + t) : none;
+                mma16<DT>(c, hi[0][k].x, hi[1][k].x, hi[0][k].y, hi[1][k].y, max16<DT>(y.x, 0u), max16<DT>(y.y, 0u));
+                mma16<DT>(c, hi[0][k].z, hi[1][k].z, hi[0][k].w, hi[1][k].w, max16<DT>(y.z, 0u), max16<DT>(y.w, 0u));
+                mma16<DT>(c, lo[0][k].x, lo[1][k].x, lo[0][k].y, lo[1][k].y, min16<DT>(y.x, 0u), min16<DT>(y.y, 0u));
+                mma16<DT>(c, lo[0][k].z, lo[1][k].z, lo[0][k].w, lo[1][k].w, min16<DT>(y.z, 0u), min16<DT>(y.w, 0u));
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (r0 + 2 * t + e < rows_now) {
+                    best[0] = max_nan(best[0], c[e]);
+                    best[1] = max_nan(best[1], c[2 + e]);
+                }
+        }
+        float *out = A.scores + (b_now * A.heads + h_now) * A.max_pages;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            best[u] = max_nan(best[u], __shfl_xor_sync(0xFFFFFFFFu, best[u], 1));
+            best[u] = max_nan(best[u], __shfl_xor_sync(0xFFFFFFFFu, best[u], 2));
+            const int i = i0 + g + 8 * u;
+            if (t == 0 && i < A.max_pages) out[i] = there[u] ? best[u] : -INFINITY;
+        }
     }
 }
 
@@ -213,7 +238,8 @@ struct SelectArgs {
     uint32_t *status;
 };
 
-// A score as a number that orders alike, NaN before all others; 0 for no page.
+// A score as a whole number that orders alike, NaN before all others.  (-inf gives 0x007FFFFF: 0 stands for
+// no page, and 0xFFFFFFFF for one that has to be taken.)
 __device__ __forceinline__ uint32_t rank_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);  // (-0 is 0)
     if (x != x) return 0xFFFFFFFEu;
@@ -221,17 +247,24 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 }
 
 // A CTA selects for one request and key head.  The threads own runs of consecutive places, in
-// registers where they fit; the rank of the last page taken is found two bits at a time by
-// counting (16 rounds of three counts and one barrier, instead of histograms whose few bins, as
-// scores lie close together, would be fought over); then a scan gives every page its place.
+// registers where they fit.  The rank of the last page taken is found digit by digit: the ranks
+// in question span [lo, lo + 2^bits), are counted in up to 2^11 equal parts of that, and the part in
+// which the keep-th largest lies is the next span.  (Parts of the span that occurs, not digits of the whole
+// number: scores of one sign and size share their upper digits, which all threads would count
+// in one place.  Three rounds at most, most often two, instead of sixteen of a search by bits, which
+// took 13 us for 8 heads of 4096 pages and 22 for 256 of 1024.)  Then a scan gives every page its place.
+constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
 template <int THREADS, int ITEMS>  // ITEMS 0: any number, read anew in every round
 __global__ void __launch_bounds__(THREADS) sv_select(const __grid_constant__ SelectArgs A) {
-    constexpr int kWarps = THREADS / 32;
-    __shared__ int counts[2][3][kWarps];
+    constexpr int kWarps = THREADS / 32, kEach = kSelBins / THREADS;
+    __shared__ __align__(16) int bins[kSelBins];
     __shared__ int scan[2][kWarps];
+    __shared__ uint32_t ends[2][kWarps];
+    __shared__ int found[2];
     pdl_trigger();
-    pdl_wait();
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kSelBins; i += THREADS) bins[i] = 0;
+    pdl_wait();
     long long len = A.len[b];
     if (len < 0 || len > (long long)A.max_pages << A.page_shift) {
         if (h == 0 && tid == 0) flag(A.status, SPEC_DEV_BAD_LEN);
@@ -268,26 +301,59 @@ __global__ void __launch_bounds__(THREADS) sv_select(const __grid_constant__ Sel
             for (int e = 0; e < per; ++e) f(i0 + e, rank_at(i0 + e));
         }
     };
-    // the largest rank that at least `keep` pages reach
-    uint32_t bar = 0;
-    for (int shift = 30, side = 0; shift >= 0; shift -= 2, side ^= 1) {
-        int c[3] = {0, 0, 0};
+    // the span of the ranks that are up for choice
+    uint32_t low = 0xFFFFFFFFu, high = 0u;
+    each([&](int, uint32_t r) {
+        if (r - 1u < 0xFFFFFFFEu) low = min(low, r), high = max(high, r);
+    });
+    low = __reduce_min_sync(0xFFFFFFFFu, low), high = __reduce_max_sync(0xFFFFFFFFu, high);
+    if (lane == 0) ends[0][warp] = low, ends[1][warp] = high;
+    __syncthreads();
+    low = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? ends[0][lane] : 0xFFFFFFFFu);
+    high = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? ends[1][lane] : 0u);
+    // the largest rank that at least `keep` pages reach; of those in the span `want` are to be taken
+    uint32_t lo = low;
+    int bits = high > low ? 32 - __clz(high - low) : 0, want = A.keep - min(n, A.first + A.recent);
+    while (want > 0 && bits > 0) {
+        const int shift = max(0, bits - kSelBits);
+        const uint32_t span = bits >= 32 ? 0xFFFFFFFFu : (1u << bits) - 1u;
         each([&](int, uint32_t r) {
-#pragma unroll
-            for (int x = 0; x < 3; ++x) c[x] += r >= (bar | ((uint32_t)(x + 1) << shift)) ? 1 : 0;
+            if (r - 1u < 0xFFFFFFFEu && r - lo <= span) atomicAdd(&bins[(r - lo) >> shift], 1);
         });
-#pragma unroll
-        for (int x = 0; x < 3; ++x) c[x] = __reduce_add_sync(0xFFFFFFFFu, c[x]);
-        if (lane == 0)
-            for (int x = 0; x < 3; ++x) counts[side][x][warp] = c[x];
         __syncthreads();
-        int step = 0;
+        int c[kEach], sum = 0;  // from the top: the thread's bins, and those above them
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (__reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? counts[side][x][lane] : 0) >= A.keep) step = x + 1;
-        bar |= (uint32_t)step << shift;
+        for (int e = 0; e < kEach; ++e) {
+            const int at = kSelBins - 1 - (tid * kEach + e);
+            c[e] = bins[at];
+            bins[at] = 0;
+            sum += c[e];
+        }
+        int x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += u;
+        }
+        if (lane == 31) scan[0][warp] = x;
+        __syncthreads();
+        const int w = lane < kWarps ? scan[0][lane] : 0;
+        int above = x - sum + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
+        if (above < want && above + sum >= want) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (above < want && above + c[e] >= want) found[0] = kSelBins - 1 - (tid * kEach + e), found[1] = above;
+                above += c[e];
+            }
+        }
+        __syncthreads();
+        lo += (uint32_t)found[0] << shift;
+        want -= found[1];
+        bits = shift;
     }
-    // pages above the bar are all taken, of those at it the first ones
+    // pages above the bar are all taken, of those at it the first ones.  (With nothing up for choice, only those
+    // that have to be; of those, too many, the first.)
+    const uint32_t bar = A.keep > min(n, A.first + A.recent) ? lo : 0xFFFFFFFFu;
     int above = 0, at = 0;
     each([&](int, uint32_t r) { above += r > bar ? 1 : 0, at += r == bar ? 1 : 0; });
     int x = above, y = at;
@@ -296,6 +362,7 @@ __global__ void __launch_bounds__(THREADS) sv_select(const __grid_constant__ Sel
         const int u = __shfl_up_sync(0xFFFFFFFFu, x, o), v = __shfl_up_sync(0xFFFFFFFFu, y, o);
         if (lane >= o) x += u, y += v;
     }
+    __syncthreads();
     if (lane == 31) scan[0][warp] = x, scan[1][warp] = y;
     __syncthreads();
     const int w0 = lane < kWarps ? scan[0][lane] : 0, w1 = lane < kWarps ? scan[1][lane] : 0;
@@ -310,9 +377,19 @@ __global__ void __launch_bounds__(THREADS) sv_select(const __grid_constant__ Sel
     });
 }
 
+// SMs of the current device, 0 if that fails.
+static int sm_count() {
+    static int sms[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms[dev];
+}
+
 template <class K> static spec_status_t launch_bounds(K kernel, const BoundsArgs &A, int B, cudaStream_t s) {
-    const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256;
-    const int want = (16 * 152 + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
+    const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256, sms = sm_count();
+    if (sms == 0) return SPEC_ERR_CUDA;
+    const int want = (16 * sms + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
     return launch_pdl(kernel, dim3((unsigned)runs, (unsigned)B), dim3((unsigned)x, (unsigned)(256 / x)), 0, s, A);
 }
 
@@ -409,8 +486,9 @@ spec_status_t spec_page_scores(const void *q, spec_dtype_t dtype, long long q_st
     A.tiles = (max_pages - 1) / 16 + 1;
     A.status = dev_status;
     const long long ctas = ((long long)B * heads * A.tiles + 7) / 8;
-    if (ctas >= (1ll << 31)) return SPEC_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)ctas), block(256);
+    const int sms = sv::sm_count();
+    if (sms == 0) return SPEC_ERR_CUDA;
+    const dim3 grid((unsigned)(ctas < 2 * sms ? ctas : 2 * sms)), block(256);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = dtype == SPEC_DTYPE_BF16;
     if (head_dim <= 64)
