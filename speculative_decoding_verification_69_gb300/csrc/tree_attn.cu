@@ -67,7 +67,7 @@ template <int DP, int MODE> struct TaShared {
     uint8_t k[C::kStagesK][C::kStage], v[C::kStagesV][C::kStage];
     long long incl[kTaChunks];  // units of the requests up to the end of each chunk, from every 32nd chunk on
     SegSlot seg[kTaSlots];
-    int pages[2][32];           // K's and V's next pages
+    int pages[2][MODE == kTaSplitHeads ? 2 : 1][32];  // K's and V's next pages, of the unit's heads
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots];
     uint64_t k_full[C::kStagesK], k_empty[C::kStagesK], v_full[C::kStagesV], v_empty[C::kStagesV];
     uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [stream][half of a tile]
@@ -283,15 +283,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             give(seg_no);
-            // (lists of their own for the key heads: not with kTaSplitHeads)
-            const int *row = A.table + s.b * A.row_b + s.hk * A.row_h;
+            const int *row = A.table + s.b * A.row_b + s.hk * kPer * A.row_h;
             const int i_end = s.i0 + s.n;
             // first position of this lane's box in tile i, and whether some node sees any of it
             auto box_pos = [&](int i) -> int { return s.g.tile(i) * kTaKeys + box * A.box; };
             auto box_seen = [&](int j) -> bool {
                 return j < s.g.end && (s.g.wlo - j < A.box || j < A.sinks);
             };
-            auto fetch = [&](int i0) -> int {  // page of this lane's box in tile i0 + lane / nb
+            // the second head of a unit has a list of its own (kTaSplitHeads)
+            const bool lists = kPer == 2 && A.row_h != 0;
+            auto fetch = [&](int i0, const int *row) -> int {  // page of this lane's box in tile i0 + lane / nb
                 const int i = i0 + lane / nb;
                 if (i >= i_end) return 0;
                 const int j = box_pos(i);
@@ -306,8 +307,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             // the pages of `ahead` tiles at a time go to shared memory, where the lane that
             // issues the copies reads them in a loop (unrolled over the boxes its code was
             // read anew for every tile, 250 cycles a copy); the next ones are on their way
-            int base = s.i0, at = s.i0, nxt = 0;  // first tile of those in shared memory, next to be fetched
-            int *pages = sh.pages[is_k ? 0 : 1];
+            int base = s.i0, at = s.i0, nxt = 0, nxt2 = 0;  // first tile of those in shared memory, next to be fetched
+            int *pages = sh.pages[is_k ? 0 : 1][0];
             // Q of this segment once the scores of the last one are done: looked for
             // before every load, so that the tiles need not wait for it
             bool q_due = is_k;
@@ -335,15 +336,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             for (int i = s.i0; i < i_end && ok; ++i) {
                 if (i == s.i0 || i == base + ahead) {
                     base = i;
-                    int now;
+                    int now, now2;
 #pragma unroll 1
                     do {  // at first these and the next ones, then one load ahead
-                        now = nxt;
-                        nxt = fetch(at);
+                        now = nxt, now2 = nxt2;
+                        nxt = fetch(at, row);
+                        if (lists) nxt2 = fetch(at, row + A.row_h);
                         at += ahead;
                     } while (at == s.i0 + ahead);
                     __syncwarp();
                     pages[lane] = now;
+                    if (lists) pages[32 + lane] = now2;
                     __syncwarp();
                 }
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, lane < nb && box_seen(box_pos(i)));
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     uint8_t *tile = tiles + stage * C::kStage;
                     if (elect_one()) {
                         mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
-                        const int *page = pages + (i - base) * nb;
+                        const int *page = pages + (i - base) * nb + (lists && head != s.hk * kPer ? 32 : 0);
 #pragma unroll 1
                         for (int x = 0; x < nb; ++x, ++page, tile += A.box * 128) {
                             if (!((seen >> x) & 1u)) continue;
@@ -928,7 +931,7 @@ static spec_status_t ta_call(const void *q, long long q_stride_b, long long q_st
     //   head_dim 128, 4096 tokens, 9 nodes: B = 32 96 / 96, 256 656 / 664
     // With fewer heads a unit of twice the work is cut more coarsely:
     //   head_dim 128, 500 tokens, 1 node:  B = 16 14.5 / 13.3, 1 10.7 / 10.4; 20000 tokens, 2 nodes: B = 1 29.5 / 26.8
-    const bool pairs = H % 2 == 0 && (long long)B * H >= ctas && !per_head;
+    const bool pairs = H % 2 == 0 && (long long)B * H >= ctas;
     const TaRows r = ta_rows(N, Hq / H, pairs);
     const TaLayout L = ta_layout(N, Hq, H, D);
     TaArgs A = {};
