@@ -34,8 +34,6 @@
 
 namespace sv {
 
-// tensor-memory columns: two buffers each of K, V, S and O
-constexpr uint32_t kT4K = 0, kT4V = 128, kT4S = 256, kT4O = 384, kT4Buf = 64;  // (an O for each stream)
 
 struct T4Args {
     TaArgs a;             // a.H: packs of heads
@@ -70,13 +68,20 @@ template <int DP, int PACK, int RP> struct T4Cfg {
     static_assert(kSoft * kRegSoft + 8 * kTurns * kRegUnpack + 4 * kRegHelp <= kWarps * kRegs &&
                       kWarps * kRegs * 32 <= 65536,
                   "more registers than the CTA has: setmaxnreg would wait for ever");
+    // buffers of K, V, S and P: three where the tensor memory has room for them, so that a warpgroup need not
+    // wait for the products of the other's tile
+    static constexpr uint32_t kBufs = kCols == 16 ? 3 : 2;
+    // tensor-memory columns: 64 for each K and V, then S, then an O for each stream
+    static constexpr uint32_t kTK = 0, kTV = kBufs * 64, kTS = 2 * kTV, kSStep = kBufs == 3 ? 16 : 64;
+    static constexpr uint32_t kTO = kTS + (kBufs == 3 ? 64 : 128), kOStep = kBufs == 3 ? 32 : 64;
+    static_assert(kTS + kBufs * kSStep <= kTO && kTO + (kCols > 32 ? kCols : kOStep + kCols) <= 512, "tensor memory");
     static constexpr int kSwizzle = kCols == 64 ? 2 : kCols == 32 ? 4 : 6;  // 128, 64 or 32 bytes
 };
 
 template <int DP, int PACK, int RP> struct T4Shared {
     using C = T4Cfg<DP, PACK, RP>;
     uint8_t q[kTaSlots][C::kQ];
-    uint8_t p[2][kTaKeys * C::kRowP];
+    uint8_t p[C::kBufs][kTaKeys * C::kRowP];
     uint8_t tile[C::kStages][C::kStage];     // per head: K's codes, V's codes, scales
     uint4 scale[4 * C::kTurns][32];                      // of a V warp: V's multipliers and addends for its keys
     float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references, negated, and their last factors
@@ -86,8 +91,8 @@ template <int DP, int PACK, int RP> struct T4Shared {
     SegSlot seg[kTaSlots];
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots], q_full[kTaSlots], q_free[kTaSlots];
     uint64_t full[C::kStages], empty[C::kStages];
-    uint64_t s_ready[2], s_full[2];          // K is there and the scores before are read; scores are there
-    uint64_t pv_ready[2], pv_done[2];        // V and the weights are there; their product is in O
+    uint64_t s_ready[C::kBufs], s_full[C::kBufs];          // K is there and the scores before are read; scores are there
+    uint64_t pv_ready[C::kBufs], pv_done[C::kBufs];        // V and the weights are there; their product is in O
     uint64_t o_free, done;
     uint32_t tmem_base;
     int abort;
@@ -167,12 +172,26 @@ __device__ __forceinline__ uint32_t hfma2(int dt, uint32_t a, uint32_t b, uint32
     else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// The bits of 128 (bfloat16) or 16 (float16) in both halves, kept in a register: as a known constant beside the
+// mask it would take an instruction of its own, since one instruction holds one constant (64 of 1176
+// instructions a tile for each of K and V).
+template <int DT> __device__ __forceinline__ uint32_t code_base() {
+    uint32_t x;
+    asm volatile("mov.b32 %0, %1;" : "=r"(x) : "n"(DT == SPEC_DTYPE_BF16 ? 0x43004300 : 0x4C004C00));
+    return x;
+}
 // Two codes of a word as numbers, times a scale (see the head of the file): pair i of the word
 // lies at bits 4 i and 4 i + 16.
-template <int DT> __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, uint32_t s, uint32_t b) {
-    if (DT == SPEC_DTYPE_BF16) return hfma2(DT, ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, s, b);
-    const uint32_t y = i == 0 ? w << 6 : i == 1 ? w << 2 : i == 2 ? w >> 2 : w >> 6;
-    return hfma2(DT, (y & 0x03C003C0u) | 0x4C004C00u, s, b);
+template <int DT>
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, uint32_t s, uint32_t b, uint32_t base) {
+    uint32_t x;  // (y & mask) | base
+    if (DT == SPEC_DTYPE_BF16) {
+        asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(x) : "r"(w >> (4 * i)), "r"(base));
+    } else {
+        const uint32_t y = i == 0 ? w << 6 : i == 1 ? w << 2 : i == 2 ? w >> 2 : w >> 6;
+        asm("lop3.b32 %0, %1, 0x03C003C0, %2, 0xEA;" : "=r"(x) : "r"(y), "r"(base));
+    }
+    return hfma2(DT, x, s, b);
 }
 // The multiplier and addend of unpack_pair for the scale(s) lo and hi.
 template <int DT> __device__ __forceinline__ uint2 unpack_scale(float lo, float hi) {
@@ -194,6 +213,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     constexpr int kCols = C::kCols, kStages = C::kStages, kW = C::kW, kSoft = C::kSoft, kStreams = C::kStreams,
                   kTurns = C::kTurns;
+    constexpr uint32_t kBufs = C::kBufs;
     constexpr float kLift = 7.f;  // weights up to 2^15: those 2^-29 below the maximum are still normal in float16
 
     if (threadIdx.x == 0) {
@@ -208,7 +228,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             mbar_init(&sh.full[i], 32);
             mbar_init(&sh.empty[i], 8);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < (int)C::kBufs; ++i) {
             mbar_init(&sh.s_ready[i], 4 + kSoft / kStreams);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.pv_ready[i], 4 + kSoft / kStreams);
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
 #pragma unroll 1
         for (uint32_t e = 0; e <= tiles && tiles > 0 && ok; ++e) {
             if (e < tiles) {
-                const uint32_t buf = e & 1u, use = e >> 1;
+                const uint32_t buf = e % kBufs, use = e / kBufs;
                 if (s_left == 0) {
                     if (!take(sh.seg_full, s_seg)) break;
                     s_left = __shfl_sync(0xFFFFFFFFu, sh.seg[s_seg % kTaSlots].s.n, 0);
@@ -390,7 +410,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 if (!wait(&sh.s_ready[buf], use)) break;
                 tc_fence_after();
                 --s_left;
-                const uint32_t d = tmem + kT4S + buf * kT4Buf, a = tmem + kT4K + buf * kT4Buf;
+                const uint32_t d = tmem + C::kTS + buf * C::kSStep, a = tmem + C::kTK + buf * 64;
                 const uint64_t qd = q_desc + (uint64_t)(qb * (C::kQ / 16));
                 if (elect_one()) {
 #pragma unroll
@@ -406,7 +426,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 __syncwarp();
             }
             if (e > 0) {
-                const uint32_t buf = (e - 1) & 1u, use = (e - 1) >> 1, stream = kStreams == 2 ? buf : 0u;
+                const uint32_t buf = (e - 1) % kBufs, use = (e - 1) / kBufs, stream = kStreams == 2 ? (e - 1) & 1u : 0u;
                 if (v_left == 0) {
                     v_left = __shfl_sync(0xFFFFFFFFu, sh.seg[v_seg % kTaSlots].s.n, 0);
                     if (v_seg > 0 && !wait(&sh.o_free, (uint32_t)(v_seg - 1))) break;
@@ -415,7 +435,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 }
                 if (!wait(&sh.pv_ready[buf], use)) break;
                 tc_fence_after();
-                const uint32_t d = tmem + kT4O + stream * kT4Buf, a = tmem + kT4V + buf * kT4Buf;
+                const uint32_t d = tmem + C::kTO + stream * C::kOStep, a = tmem + C::kTV + buf * 64;
                 const uint64_t wd = w_desc + (uint64_t)(buf * (uint32_t)(kTaKeys * C::kRowP / 16));
                 const uint32_t add = (fresh >> stream) & 1u ? 0u : 1u;
                 if (elect_one()) {
@@ -442,10 +462,10 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int head_off = slot * (kTaKeys / 16 * 17) * T.C, word_off = head_off + kTaKeys / 2 * T.C + ch * 4;
         const int scale_off = head_off + kTaKeys * T.C + (t >> T.block_shift) * T.block * T.groups * 2 +
                               (T.groups + (ch >> 5)) * T.block + (t & (T.block - 1));
-        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kT4V;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kTV;
         uint4 *scale = sh.scale[warp - C::kV];
-        for (uint32_t e = turn, stage = turn, fill = 0; e < tiles; e += kTurns) {
-            const uint32_t buf = kTurns == 2 ? turn : e & 1u;
+        const uint32_t zero = code_base<SPEC_DTYPE_F16>();  // code 0
+        for (uint32_t e = turn, stage = turn, fill = 0, buf = turn, use = 0; e < tiles; e += kTurns) {
             if (!wait(&sh.full[stage], fill)) break;
             const uint8_t *tile = sh.tile[stage];
             uint32_t word[16];
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 scale[lane] = make_uint4(a.x, a.y, b.x, b.y);
             }
             arrive(&sh.empty[stage]);
-            if (e >= 2 && !wait(&sh.pv_done[buf], (e >> 1) - 1)) break;
+            if (use > 0 && !wait(&sh.pv_done[buf], use - 1)) break;
             if (works) {
                 tc_fence_after();
 #pragma unroll
@@ -469,28 +489,29 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     for (int i = 0; i < 4; ++i) {
                         const uint4 a = scale[(h * 4 + i) * 2], b = scale[(h * 4 + i) * 2 + 1];
                         const uint32_t x = word[h * 4 + i];
-                        v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, a.x, a.y);
-                        v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, a.z, a.w);
-                        v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, b.x, b.y);
-                        v[4 * i + 3] = unpack_pair<SPEC_DTYPE_F16>(x, 3, b.z, b.w);
+                        v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, a.x, a.y, zero);
+                        v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, a.z, a.w, zero);
+                        v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, b.x, b.y, zero);
+                        v[4 * i + 3] = unpack_pair<SPEC_DTYPE_F16>(x, 3, b.z, b.w, zero);
                     }
-                    tmem_store(to + buf * kT4Buf + (uint32_t)(h * 16), v);
+                    tmem_store(to + buf * 64 + (uint32_t)(h * 16), v);
                 }
                 tmem_wait_store();
                 tc_fence_before();
             }
             arrive(&sh.pv_ready[buf]);
             if ((stage += kTurns) >= (uint32_t)kStages) stage = turn, ++fill;
+            if ((buf += kTurns) >= kBufs) buf -= kBufs, ++use;
         }
     } else if (warp >= kSoft && warp < C::kV) {  // ---------------------------- K
         fewer_registers<C::kRegUnpack>();
         const uint32_t turn = kTurns == 2 ? (uint32_t)(warp - kSoft) >> 2 : 0u;
         const int quad = warp & 3, key = quad * 32 + lane;
-        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + kT4K;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kTK;
+        const uint32_t zero = code_base<DT>();  // code 0
         const int code_off = ((key >> 3) * T.groups * 8 + (key & 7)) * 16;
         const int scale_off = kTaKeys * T.C + (key >> T.block_shift) * T.block * T.groups * 2 + (key & (T.block - 1));
-        for (uint32_t e = turn, stage = turn, fill = 0; e < tiles; e += kTurns) {
-            const uint32_t buf = kTurns == 2 ? turn : e & 1u;
+        for (uint32_t e = turn, stage = turn, fill = 0, buf = turn, use = 0; e < tiles; e += kTurns) {
             if (!wait(&sh.full[stage], fill)) break;
             uint4 code[PACK * DP / 32];
             uint32_t byte[PACK * DP / 32];
@@ -502,7 +523,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 byte[x] = tile[scale_off + g * T.block];
             }
             arrive(&sh.empty[stage]);
-            if (e >= 2 && !wait(&sh.s_full[buf], (e >> 1) - 1)) break;
+            if (use > 0 && !wait(&sh.s_full[buf], use - 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < PACK * DP / 32; ++x) {
@@ -511,13 +532,14 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 const uint32_t word[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
                 uint32_t k[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) k[i] = unpack_pair<DT>(word[i / 4], i % 4, s.x, s.y);
-                tmem_store(to + buf * kT4Buf + (uint32_t)(x * 16), k);
+                for (int i = 0; i < 16; ++i) k[i] = unpack_pair<DT>(word[i / 4], i % 4, s.x, s.y, zero);
+                tmem_store(to + buf * 64 + (uint32_t)(x * 16), k);
             }
             tmem_wait_store();
             tc_fence_before();
             arrive(&sh.s_ready[buf]);
             if ((stage += kTurns) >= (uint32_t)kStages) stage = turn, ++fill;
+            if ((buf += kTurns) >= kBufs) buf -= kBufs, ++use;
         }
     } else if (warp < kSoft) {  // ---------------------------------------------- softmax
         more_registers<C::kRegSoft>();
@@ -526,7 +548,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int key = quad * 32 + lane;              // of a tile; and the channel (of all heads) in O
         const uint32_t col0 = kStreams == 2 ? 0u : (uint32_t)(wg * kW);  // the warp's columns
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t ts = tmem + lanes + kT4S + col0, to = tmem + lanes + kT4O + (uint32_t)stream * kT4Buf + col0;
+        const uint32_t ts = tmem + lanes + C::kTS + col0, to = tmem + lanes + C::kTO + (uint32_t)stream * C::kOStep + col0;
         const int slot = quad * 32 / DP, ch = key % DP;
         const int rows_used = A.np * A.G, rows_cta = PACK * rows_used;
         // a quarter of the keys' scale was multiplied in float16
@@ -535,8 +557,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         float *m = sh.m[warp], *f = sh.f[warp];
         uint32_t base = 0;  // the CTA's tiles before this segment
         bool ok = true;
-        arrive(&sh.s_ready[kStreams == 2 ? stream : 0]);  // no scores to be read yet
-        if (kStreams == 1) arrive(&sh.s_ready[1]);
+        for (int i = stream; i < (int)kBufs; i += kStreams) arrive(&sh.s_ready[i]);  // no scores to be read yet
         // The warps leave together: a wait in vain is told at their next meeting, so that no warp stands
         // at a barrier that another one has left for good.
         for (int seg_no = 0;; ++seg_no) {
@@ -561,7 +582,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
 #pragma unroll 1
             for (int t = t0; t < n; t += kStreams) {
                 const int j0 = g.tile(i0 + t) * kTaKeys;
-                const uint32_t e = base + (uint32_t)t, buf = e & 1u, use = e >> 1;
+                const uint32_t e = base + (uint32_t)t, buf = e % kBufs, use = e / kBufs;
                 const bool all = g.c - j0 >= kTaKeys && (j0 >= whole || sinks - j0 >= kTaKeys);
                 unsigned long long seen = ~0ull;  // the rows of a head that see this key
                 if (!all) {
@@ -585,7 +606,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 tc_fence_after();
                 float2 z[kW / 2];
                 auto scores = [&](uint32_t (&x)[kW]) {  // -inf where they are not seen
-                    tmem_load(ts + buf * kT4Buf, x);
+                    tmem_load(ts + buf * C::kSStep, x);
                     if (!all) {
 #pragma unroll
                         for (int i = 0; i < kW; ++i)
@@ -647,7 +668,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     for (int i = 0; i < kW; ++i) l[i] *= f[i];
                     if (t > t0) {  // O holds the stream's tiles before this one
                         // (through, of two streams, since before these scores: see below)
-                        if (kStreams == 1) ok = wait(&sh.pv_done[buf ^ 1u], (e - 1) >> 1);
+                        if (kStreams == 1) ok = wait(&sh.pv_done[(e - 1) % kBufs], (e - 1) / kBufs);
                         if (ok) {
                             tc_fence_after();
 #pragma unroll
@@ -710,8 +731,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             base += (uint32_t)n;
             // the last tiles' products (of the other stream's last tile too, if the segment has two)
             const uint32_t last = base - 1;
-            ok = ok && wait(&sh.pv_done[last & 1u], last >> 1);
-            if (kStreams == 2 && n > 1) ok = ok && wait(&sh.pv_done[(last - 1) & 1u], (last - 1) >> 1);
+            ok = ok && wait(&sh.pv_done[last % kBufs], last / kBufs);
+            if (kStreams == 2 && n > 1) ok = ok && wait(&sh.pv_done[(last - 1) % kBufs], (last - 1) / kBufs);
             if (meet<256>(3, !ok)) {
                 ok = false;
                 break;
@@ -763,12 +784,12 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             if (slot < PACK && hk < T.heads && ch - lane < A.D && r0 < rows_used) {
                 int local = r0 / A.G, in_group = r0 - local * A.G;
                 uint32_t o[kO];
-                tmem_load(tmem + lanes + kT4O + (uint32_t)((only < 0 ? 0 : only) * (int)kT4Buf + c0), o);
+                tmem_load(tmem + lanes + C::kTO + (only > 0 ? C::kOStep : 0u) + (uint32_t)c0, o);
 #pragma unroll
                 for (int i = 0; i < kO; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.w[0][c0 + i]);
                 if (kStreams == 2 && only < 0) {
                     uint32_t y[kO];
-                    tmem_load(tmem + lanes + kT4O + kT4Buf + (uint32_t)c0, y);
+                    tmem_load(tmem + lanes + C::kTO + C::kOStep + (uint32_t)c0, y);
 #pragma unroll
                     for (int i = 0; i < kO; ++i)
                         o[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), sh.w[1][c0 + i], __uint_as_float(o[i])));
