@@ -87,6 +87,8 @@ template <int DP, int PACK, int RP> struct T4Shared {
     float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references, negated, and their last factors
     float top[C::kSoft][C::kW], sum[C::kSoft][C::kW];
     float w[2][C::kCols];                    // the streams' factors in the result
+    long long row[C::kCols];                 // where a row goes: twice its first element (of out, or of the parts), one
+                                             // more if it sees nothing; -1: nowhere
     long long incl[kTaChunks];
     SegSlot seg[kTaSlots];
     uint64_t seg_full[kTaSlots], path_full[kTaSlots], seg_free[kTaSlots], q_full[kTaSlots], q_free[kTaSlots];
@@ -468,27 +470,24 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         for (uint32_t e = turn, stage = turn, fill = 0, buf = turn, use = 0; e < tiles; e += kTurns) {
             if (!wait(&sh.full[stage], fill)) break;
             const uint8_t *tile = sh.tile[stage];
-            uint32_t word[16];
             if (works) {
                 const uint32_t x = *reinterpret_cast<const uint32_t *>(tile + scale_off);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    word[i] = *reinterpret_cast<const uint32_t *>(tile + word_off + i * T.C * 4);
                 const uint2 a = unpack_scale<SPEC_DTYPE_F16>(scale_of(x & 255u), scale_of((x >> 8) & 255u));
                 const uint2 b = unpack_scale<SPEC_DTYPE_F16>(scale_of((x >> 16) & 255u), scale_of(x >> 24));
                 scale[lane] = make_uint4(a.x, a.y, b.x, b.y);
             }
-            arrive(&sh.empty[stage]);
             if (use > 0 && !wait(&sh.pv_done[buf], use - 1)) break;
             if (works) {
                 tc_fence_after();
-#pragma unroll
+                __syncwarp();
+                // (a loop, as for K: the roles' code passes through one instruction cache)
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     uint32_t v[16];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint4 a = scale[(h * 4 + i) * 2], b = scale[(h * 4 + i) * 2 + 1];
-                        const uint32_t x = word[h * 4 + i];
+                        const uint32_t x = *reinterpret_cast<const uint32_t *>(tile + word_off + (h * 4 + i) * T.C * 4);
                         v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, a.x, a.y, zero);
                         v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, a.z, a.w, zero);
                         v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, b.x, b.y, zero);
@@ -499,6 +498,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 tmem_wait_store();
                 tc_fence_before();
             }
+            arrive(&sh.empty[stage]);
             arrive(&sh.pv_ready[buf]);
             if ((stage += kTurns) >= (uint32_t)kStages) stage = turn, ++fill;
             if ((buf += kTurns) >= kBufs) buf -= kBufs, ++use;
@@ -513,28 +513,22 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int scale_off = kTaKeys * T.C + (key >> T.block_shift) * T.block * T.groups * 2 + (key & (T.block - 1));
         for (uint32_t e = turn, stage = turn, fill = 0, buf = turn, use = 0; e < tiles; e += kTurns) {
             if (!wait(&sh.full[stage], fill)) break;
-            uint4 code[PACK * DP / 32];
-            uint32_t byte[PACK * DP / 32];
-#pragma unroll
+            if (use > 0 && !wait(&sh.s_full[buf], use - 1)) break;
+            tc_fence_after();
+#pragma unroll 1
             for (int x = 0; x < PACK * DP / 32; ++x) {
                 const uint8_t *tile = sh.tile[stage] + x / (DP / 32) * (kTaKeys / 16 * 17) * T.C;
                 const int g = x % (DP / 32) < T.groups ? x % (DP / 32) : 0;  // (past the last group: not multiplied)
-                code[x] = *reinterpret_cast<const uint4 *>(tile + code_off + g * 128);
-                byte[x] = tile[scale_off + g * T.block];
-            }
-            arrive(&sh.empty[stage]);
-            if (use > 0 && !wait(&sh.s_full[buf], use - 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < PACK * DP / 32; ++x) {
-                const float f = scale_of(byte[x]);
+                const uint4 code = *reinterpret_cast<const uint4 *>(tile + code_off + g * 128);
+                const float f = scale_of(tile[scale_off + g * T.block]);
                 const uint2 s = unpack_scale<DT>(f, f);
-                const uint32_t word[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+                const uint32_t word[4] = {code.x, code.y, code.z, code.w};
                 uint32_t k[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) k[i] = unpack_pair<DT>(word[i / 4], i % 4, s.x, s.y, zero);
                 tmem_store(to + buf * 64 + (uint32_t)(x * 16), k);
             }
+            arrive(&sh.empty[stage]);
             tmem_wait_store();
             tc_fence_before();
             arrive(&sh.s_ready[buf]);
@@ -555,6 +549,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const float scale = A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
         const int sinks = A.window ? A.sinks : 0;
         float *m = sh.m[warp], *f = sh.f[warp];
+        // the row of which this thread writes the sum: its head in the pack, node of the tile and head of the group
+        const int c = (int)threadIdx.x, of = c / RP, r = c % RP, local = r / A.G, in_group = r - local * A.G;
         uint32_t base = 0;  // the CTA's tiles before this segment
         bool ok = true;
         for (int i = stream; i < (int)kBufs; i += kStreams) arrive(&sh.s_ready[i]);  // no scores to be read yet
@@ -629,13 +625,13 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     }
                     return fmaxf(mx[0], mx[1]);
                 };
-                float largest;
-                {
+                float largest = 0.f;
+                if (t > t0) {  // (the stream's first tile has its references to find)
                     uint32_t x[kW];
                     scores(x);
                     largest = shift(x);
                 }
-                if (meet<128>(1 + wg, !ok || largest > kLift + kTaGrow)) {
+                if (t == t0 || meet<128>(1 + wg, !ok || largest > kLift + kTaGrow)) {
                     if (meet<128>(1 + wg, !ok)) {
                         ok = false;
                         break;
@@ -741,8 +737,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             const bool whole_item = n == g.nt;
             const long long place = (long long)blockIdx.x * 2 + (i0 == 0 ? 1 : 0);  // a cut item's part
             const int only = kStreams == 2 && n == 1 ? (int)(last & 1u) : -1;      // the one stream with a part
-            if ((int)threadIdx.x < kCols) {  // a thread per row: its sum and lse, and the factors of its parts
-                const int c = (int)threadIdx.x;
+            if (c < kCols) {  // a thread per row: its sum and lse, and the factors of its parts
                 float ref, total;
                 auto part = [&](int w0, int at, float &mm, float &ll) {  // of the warps w0 .. w0 + 3
                     mm = -sh.m[w0][at];
@@ -761,20 +756,17 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     w0 = ex2(ma - ref), w1 = ex2(mb - ref);
                     total = la * w0 + lb * w1;
                 }
-                const int r = c % RP, local = r / A.G, node = s.node0 + local, hk = s.hk * PACK + c / RP;
+                const int node = s.node0 + local, hk = s.hk * PACK + of;
                 const bool exists = r < rows_used && node < A.N && hk < T.heads, valid = exists && node < g.cnt;
                 if (total != total) ref = fmaxf(ref, 0.f);  // the row's part must not pass for empty
                 const float inv = whole_item ? 4.f / total : 4.f;  // (O is a quarter of itself)
                 sh.w[0][c] = w0 * inv, sh.w[1][c] = w1 * inv;
-                if (exists) {
-                    if (whole_item) {
-                        const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + (r - local * A.G);
-                        if (A.lse) A.lse[orow] = ta_lse(valid, ref, total);
-                    } else {
-                        A.part_ml[place * rows_cta + (c / RP) * rows_used + r] =
-                            valid ? make_float2(ref, total) : make_float2(-INFINITY, 0.f);
-                    }
-                }
+                const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + in_group;
+                const long long prow = place * rows_cta + of * rows_used + r;
+                sh.row[c] = whole_item ? (exists ? 2 * orow * A.D + (valid ? 0 : 1) : -1) : (valid ? 2 * prow * A.D : -1);
+                if (exists && whole_item && A.lse) A.lse[orow] = ta_lse(valid, ref, total);
+                if (exists && !whole_item)
+                    A.part_ml[prow] = valid ? make_float2(ref, total) : make_float2(-INFINITY, 0.f);
             }
             meet<256>(3, false);
             // a warpgroup writes half of the columns of every head
@@ -782,7 +774,6 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             constexpr int kO = RP / 2;
             const int r0 = wg * kO, c0 = slot * RP + r0;
             if (slot < PACK && hk < T.heads && ch - lane < A.D && r0 < rows_used) {
-                int local = r0 / A.G, in_group = r0 - local * A.G;
                 uint32_t o[kO];
                 tmem_load(tmem + lanes + C::kTO + (only > 0 ? C::kOStep : 0u) + (uint32_t)c0, o);
 #pragma unroll
@@ -796,18 +787,10 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 }
 #pragma unroll
                 for (int i = 0; i < kO; ++i) {
-                    const int node = s.node0 + local;
-                    if (r0 + i < rows_used && node < A.N && ch < A.D) {
-                        const bool valid = node < g.cnt;
-                        const float y = __uint_as_float(o[i]);
-                        if (whole_item) {
-                            const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + in_group;
-                            A.out[orow * A.D + ch] = valid ? (uint16_t)pack2<DT>(y, 0.f) : (uint16_t)0;
-                        } else if (valid) {
-                            A.part_o[(place * rows_cta + slot * rows_used + r0 + i) * A.D + ch] = y;
-                        }
-                    }
-                    if (++in_group == A.G) in_group = 0, ++local;
+                    const long long row = sh.row[c0 + i], at = (row >> 1) + ch;
+                    if (row < 0 || ch >= A.D) continue;
+                    if (whole_item) A.out[at] = row & 1 ? (uint16_t)0 : (uint16_t)pack2<DT>(__uint_as_float(o[i]), 0.f);
+                    else A.part_o[at] = __uint_as_float(o[i]);
                 }
             }
             tc_fence_before();
