@@ -338,13 +338,17 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 }
                 return T.data + p * T.page_st + head * T.head_st + ((j & (A.page - 1)) >> T.block_shift) * T.bytes;
             };
-            int base = s.i0;
-            const uint8_t *now = fetch(base), *next = fetch(base + ahead);
+            int base = s.i0, at = s.i0;
+            const uint8_t *now = nullptr, *next = nullptr;
             for (int i = s.i0; i < i_end; ++i, ++e) {
-                if (i == base + ahead) {
+                if (i == s.i0 || i == base + ahead) {
                     base = i;
-                    now = next;
-                    next = fetch(base + ahead);
+#pragma unroll 1
+                    do {  // at first these and the next ones, then one load ahead
+                        now = next;
+                        next = fetch(at);
+                        at += ahead;
+                    } while (at == s.i0 + ahead);
                 }
                 if ((e & 1u) != turn) {
                     if (++stage == kStages) stage = 0, ++fill;
@@ -625,21 +629,25 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     }
                     return fmaxf(mx[0], mx[1]);
                 };
-                float largest = 0.f;
-                if (t > t0) {  // (the stream's first tile has its references to find)
+                // The scores less the references; where one has grown, or at the stream's first tile, after new references.
+                // (One copy of each step: the roles' code passes through one instruction cache.)
+                bool gone = false;
+                // 0: whether one has grown, 1: new references, 2: with those.  (Not again however large: scores that
+                // float32 holds to more than 2^3 stay above references as coarse as they.)
+                int step = t == t0 ? 1 : 0;
+#pragma unroll 1
+                for (; step <= 2; ++step) {
                     uint32_t x[kW];
                     scores(x);
-                    largest = shift(x);
-                }
-                if (t == t0 || meet<128>(1 + wg, !ok || largest > kLift + kTaGrow)) {
-                    if (meet<128>(1 + wg, !ok)) {
-                        ok = false;
-                        break;
+                    if (step != 1) {
+                        const float largest = shift(x);
+                        if (step == 2 || !meet<128>(1 + wg, !ok || largest > kLift + kTaGrow)) break;
+                        gone = meet<128>(1 + wg, !ok);
+                        if (gone) break;
+                        continue;
                     }
-                    // new references: the columns' maxima over the four warps' keys
+                    // the columns' maxima over the four warps' keys
                     float mine = -INFINITY;
-                    uint32_t x[kW];
-                    scores(x);
 #pragma unroll
                     for (int i = 0; i < kW; ++i) {
                         // (as integers that order alike; a NaN's column is NaN whatever its reference)
@@ -658,26 +666,26 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         m[lane] = -y;
                     }
                     __syncwarp();
-                    scores(x);
-                    shift(x);
+                    if (t > t0) {  // O and the sums hold the stream's tiles before this one
 #pragma unroll
-                    for (int i = 0; i < kW; ++i) l[i] *= f[i];
-                    if (t > t0) {  // O holds the stream's tiles before this one
-                        // (through, of two streams, since before these scores: see below)
-                        if (kStreams == 1) ok = wait(&sh.pv_done[(e - 1) % kBufs], (e - 1) / kBufs);
-                        if (ok) {
-                            tc_fence_after();
+                        for (int i = 0; i < kW; ++i) l[i] *= f[i];
+                        // (their products are through, of two streams, since before these scores: see below)
+                        if (kStreams == 1) ok = ok && wait(&sh.pv_done[(e - 1) % kBufs], (e - 1) / kBufs);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < kW && ok; d += 16) {
+                            uint32_t o[16];
+                            tmem_load(to + (uint32_t)d, o);
 #pragma unroll
-                            for (int d = 0; d < kW; d += 16) {
-                                uint32_t o[16];
-                                tmem_load(to + (uint32_t)d, o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[d + i]);
-                                tmem_store(to + (uint32_t)d, o);
-                            }
-                            tmem_wait_store();
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[d + i]);
+                            tmem_store(to + (uint32_t)d, o);
                         }
+                        tmem_wait_store();
                     }
+                }
+                if (gone) {
+                    ok = false;
+                    break;
                 }
                 tc_fence_before();
                 arrive(&sh.s_ready[buf]);
