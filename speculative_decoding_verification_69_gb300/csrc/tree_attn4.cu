@@ -42,6 +42,7 @@ struct T4Args {
     int heads;            // key heads
     int C, groups;        // channels kept and groups of 32 of them
     int block, block_shift, bytes;  // tokens of a block, its bytes
+    int value[kTaKeys / 8];         // where a tile's values lie in a head's blocks, 8 tokens at a time
 };
 
 #ifndef T4_TURNS
@@ -82,7 +83,8 @@ template <int DP, int PACK, int RP> struct T4Shared {
     using C = T4Cfg<DP, PACK, RP>;
     uint8_t q[kTaSlots][C::kQ];
     uint8_t p[C::kBufs][kTaKeys * C::kRowP];
-    uint8_t tile[C::kStages][C::kStage];     // per head: K's codes, V's codes, scales
+    uint8_t tile[C::kStages][C::kStage];     // per head: its blocks, as they lie in memory
+    const uint8_t *places[2][32];            // of a loading warp: where the next blocks lie in memory
     uint4 scale[4 * C::kTurns][32];                      // of a V warp: V's multipliers and addends for its keys
     float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references, negated, and their last factors
     float top[C::kSoft][C::kW], sum[C::kSoft][C::kW];
@@ -101,16 +103,6 @@ template <int DP, int PACK, int RP> struct T4Shared {
 };
 
 // ------------------------------------------------------------------ PTX
-
-// 16 bytes from global to shared memory, without waiting; the arrival of this thread's copies so far on
-// `bar`, and the wait for all of them.
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ta_wait in one statement: the compiler's code around its loop doubles the 67 cycles of a look that succeeds at
 // once, and a tile's stages wait for each other half a dozen times.
@@ -227,7 +219,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             mbar_init(&sh.q_free[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 32);
+            mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 8);
         }
         for (int i = 0; i < (int)C::kBufs; ++i) {
@@ -288,21 +280,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int recs = kTaKeys >> T.block_shift;           // blocks of a head's tile
         const int nb = PACK * recs, ahead = 32 / nb;         // blocks of a tile, tiles whose pages are fetched at once
         const int slot = lane % nb / recs, rec = lane % recs;  // of the pages that the lane fetches
-        // 8 tokens of K's or V's codes are 4 C bytes: 16 to a lane, a half-warp to a head of a pack
-        constexpr int kHalf = 32 / PACK;
-        const int to_slot = lane / kHalf, part = lane % kHalf;
-        const bool copies = part * 4 < T.C;
-        const uint32_t codes = (uint32_t)(T.block * T.C / 2), scales = (uint32_t)(T.block * T.groups * 2);
-        const uint32_t to0 = smem_u32(sh.tile[0]) + (uint32_t)(to_slot * (kTaKeys / 16 * 17) * T.C);
-        // the lane's 16-byte pieces of a head's scales: block of tokens, and place in it
-        constexpr int kScaleVecs = DP / 2 / kHalf;
-        int scale_rec[kScaleVecs], scale_off[kScaleVecs];
-#pragma unroll
-        for (int x = 0; x < kScaleVecs; ++x) {
-            const int at = (x * kHalf + part) * 16;
-            scale_rec[x] = at / (int)scales;
-            scale_off[x] = 2 * (int)codes + at - scale_rec[x] * (int)scales;
-        }
+        const uint8_t **places = sh.places[turn];
         uint32_t e = 0, stage = 0, fill = 0;
         int seg_no = 0;
         bool ok = true;
@@ -325,12 +303,12 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             __syncwarp();
             const int head = s.hk * PACK + slot, i_end = s.i0 + s.n;
             const int *row = A.table + s.b * A.row_b + head * A.row_h;
-            // the block's place in memory: of this lane's block in tile i0 + lane / nb, 0 where no node sees any of it
+            // the place in memory of this lane's block of tile i0 + lane / nb; that of any block where no node sees it
             auto fetch = [&](int i0) -> const uint8_t * {
                 const int i = i0 + lane / nb;
-                if (i >= i_end || head >= T.heads) return nullptr;
+                if (i >= i_end || head >= T.heads) return T.data;
                 const int j = s.g.tile(i) * kTaKeys + (rec << T.block_shift);  // its first position
-                if (j >= s.g.end || (s.g.wlo - j >= T.block && j >= A.sinks)) return nullptr;
+                if (j >= s.g.end || (s.g.wlo - j >= T.block && j >= A.sinks)) return T.data;
                 int p = __ldcg(row + (j >> A.page_shift));
                 if ((unsigned)p >= (unsigned)A.num_pages) {
                     flag(A.status, SPEC_DEV_BAD_PAGE);
@@ -338,17 +316,21 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 }
                 return T.data + p * T.page_st + head * T.head_st + ((j & (A.page - 1)) >> T.block_shift) * T.bytes;
             };
-            int base = s.i0, at = s.i0;
-            const uint8_t *now = nullptr, *next = nullptr;
+            int base = s.i0 - ahead;
+            const uint8_t *next = T.data;
             for (int i = s.i0; i < i_end; ++i, ++e) {
-                if (i == s.i0 || i == base + ahead) {
-                    base = i;
+                if (i == base + ahead) {
+                    // at first these blocks' places and then the next ones', one load ahead
 #pragma unroll 1
-                    do {  // at first these and the next ones, then one load ahead
-                        now = next;
+                    for (int at = i == s.i0 ? i : i + ahead; at <= i + ahead; at += ahead) {
+                        if (at > i) {
+                            __syncwarp();
+                            places[lane] = next;
+                            __syncwarp();
+                        }
                         next = fetch(at);
-                        at += ahead;
-                    } while (at == s.i0 + ahead);
+                    }
+                    base = i;
                 }
                 if ((e & 1u) != turn) {
                     if (++stage == kStages) stage = 0, ++fill;
@@ -358,36 +340,24 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     ok = false;
                     break;
                 }
-                const uint32_t to = to0 + stage * C::kStage;
-                const int from_lane = (i - base) * nb + to_slot * recs;
-                auto place = [&](int r) -> const uint8_t * {
-                    return reinterpret_cast<const uint8_t *>(
-                        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(now), from_lane + r));
-                };
-                // (unrolled, so that a copy does not wait for the one before it to have read its addresses)
+                // (One lane issues, in a loop: copies by a lane each are issued one after the other all the same.  A copy
+                // takes the warp 100 cycles and more, so blocks come whole, codes and scales.)
+                if (elect_one()) {
+                    const uint8_t *const *from = places + (i - base) * nb;
+                    uint8_t *to = sh.tile[stage];
+                    mbar_expect_tx(&sh.full[stage], (uint32_t)(nb * T.bytes));
 #pragma unroll 4
-                for (int x = 0; x < kTaKeys / 8; ++x) {
-                    const uint8_t *src = place(x * 8 >> T.block_shift);
-                    const uint32_t off = (uint32_t)((x * 8 & (T.block - 1)) * T.C / 2 + part * 16);
-                    const uint32_t k = to + (uint32_t)(x * T.C * 4 + part * 16);
-                    if (copies && src) {
-                        copy16(k, src + off);
-                        copy16(k + (uint32_t)(kTaKeys / 2 * T.C), src + codes + off);
-                    }
+                    for (int r = 0; r < nb; ++r, to += T.bytes) bulk_g2s(to, from[r], (uint32_t)T.bytes, &sh.full[stage]);
                 }
-#pragma unroll
-                for (int x = 0; x < kScaleVecs; ++x) {
-                    const uint8_t *src = place(scale_rec[x] & (recs - 1));
-                    if (scale_rec[x] < recs && src)
-                        copy16(to + (uint32_t)(kTaKeys * T.C + (x * kHalf + part) * 16), src + scale_off[x]);
-                }
-                copy_arrive(&sh.full[stage]);
                 __syncwarp();
                 if (++stage == kStages) stage = 0, ++fill;
             }
         }
         // every copy has landed before the CTA may exit
-        copy_wait_all();
+        for (uint32_t x = turn; x < (uint32_t)kStages; x += 2) {
+            const uint32_t n = fill + (x < stage ? 1u : 0u);
+            if (n > 0) mbar_wait_bounded(&sh.full[x], (n - 1) & 1u, kTaWaitNs);
+        }
         for (int x = 0; x < kTaSlots && turn == 0; ++x) {
             const int n = (seg_no + kTaSlots - 1 - x) / kTaSlots;
             if (n > 0) mbar_wait_bounded(&sh.q_full[x], (uint32_t)(n - 1) & 1u, kTaWaitNs);
@@ -465,9 +435,9 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int quad = warp & 3, slot = quad * 32 / DP, ch = (quad * 32 + lane) % DP;
         const bool works = slot < PACK && ch - lane < T.C;  // the warp's lanes alike
         const int t = 4 * lane;                             // the keys whose scales the lane unpacks
-        const int head_off = slot * (kTaKeys / 16 * 17) * T.C, word_off = head_off + kTaKeys / 2 * T.C + ch * 4;
-        const int scale_off = head_off + kTaKeys * T.C + (t >> T.block_shift) * T.block * T.groups * 2 +
-                              (T.groups + (ch >> 5)) * T.block + (t & (T.block - 1));
+        const int head_off = slot * (kTaKeys / 16 * 17) * T.C, word_off = head_off + ch * 4;
+        const int scale_off = head_off + (t >> T.block_shift) * T.bytes + T.block * (T.C + T.groups + (ch >> 5)) +
+                              (t & (T.block - 1));
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kTV;
         uint4 *scale = sh.scale[warp - C::kV];
         const uint32_t zero = code_base<SPEC_DTYPE_F16>();  // code 0
@@ -491,7 +461,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint4 a = scale[(h * 4 + i) * 2], b = scale[(h * 4 + i) * 2 + 1];
-                        const uint32_t x = *reinterpret_cast<const uint32_t *>(tile + word_off + (h * 4 + i) * T.C * 4);
+                        const uint32_t x = *reinterpret_cast<const uint32_t *>(tile + word_off + T.value[h * 4 + i]);
                         v[4 * i] = unpack_pair<SPEC_DTYPE_F16>(x, 0, a.x, a.y, zero);
                         v[4 * i + 1] = unpack_pair<SPEC_DTYPE_F16>(x, 1, a.z, a.w, zero);
                         v[4 * i + 2] = unpack_pair<SPEC_DTYPE_F16>(x, 2, b.x, b.y, zero);
@@ -513,8 +483,9 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const int quad = warp & 3, key = quad * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kTK;
         const uint32_t zero = code_base<DT>();  // code 0
-        const int code_off = ((key >> 3) * T.groups * 8 + (key & 7)) * 16;
-        const int scale_off = kTaKeys * T.C + (key >> T.block_shift) * T.block * T.groups * 2 + (key & (T.block - 1));
+        const int in_block = key & (T.block - 1), block_off = (key >> T.block_shift) * T.bytes;
+        const int code_off = block_off + ((in_block >> 3) * T.groups * 8 + (in_block & 7)) * 16;
+        const int scale_off = block_off + T.block * T.C + in_block;
         for (uint32_t e = turn, stage = turn, fill = 0, buf = turn, use = 0; e < tiles; e += kTurns) {
             if (!wait(&sh.full[stage], fill)) break;
             if (use > 0 && !wait(&sh.s_full[buf], use - 1)) break;
@@ -979,6 +950,8 @@ spec_status_t spec_tree_attention4(const void *q, spec_dtype_t dtype, long long 
     T.block = P.block;
     while ((1 << T.block_shift) < P.block) ++T.block_shift;
     T.bytes = P.bytes;
+    for (int i = 0; i < sv::kTaKeys / 8; ++i)
+        T.value[i] = (i * 8 >> T.block_shift) * P.bytes + P.block * P.C / 2 + (i * 8 & (P.block - 1)) / 8 * P.C * 4;
 
     CUtensorMap tq;
     // an extent of one is never stepped over: any valid stride stands for it
