@@ -23,17 +23,24 @@
 // per 32 channels, those of a channel 4 bytes per 8 tokens, each without bank
 // conflicts, and the scales of a warp's 32 channels of V are the same for all lanes.
 //
-// One CTA per SM: four warps unpack K, four V, four (of 64 rows: eight) form the weights, and a warp
-// each loads, issues the products and
-// schedules.  Tiles of keys alternate between two buffers of K, V, S and P, so the
-// stages of consecutive tiles overlap.  Heads of up to 64 are taken in pairs (the
-// lanes of V^T are two heads' channels; the quarter of the product that mixes them is
-// not read).  More than 64 rows are cut into row tiles.
+// One CTA per SM.  Eight warps form the weights, two warpgroups with a tile each in turn (of 64 columns: half of every
+// tile's), four warps unpack K and four V (of 16 columns: eight each, in turn), two load, a bulk copy for each block of
+// the cache, one issues the products and one schedules.  Tiles of keys go round two or three buffers of K, V, S and P, so
+// the stages of consecutive tiles overlap.  Heads of up to 64 are taken in pairs (the lanes of V^T are two heads'
+// channels; the quarter of the product that mixes them is not read).  More rows than a tile has are cut into row tiles.
+//
+// Measured: 64 single tokens of 32 query heads and 8 key heads of 128 after up to 8192 positions, 140 us for their
+// 428 MB, 3.1 TB/s or 45 % of a copy's rate (the same with 16 bits a number: 248 us).  16 nodes after 131071 positions:
+// 77.6 us (99).  Chains of 9 of 32 requests, up to 4096 positions, 8 key heads of 64: 66.4 us.  What bounds it is the
+// issuing of instructions: 4180 warp instructions to a tile of 128 keys, of which a code's pair takes three (a shift, the
+// mask, the multiply-add); 68 % of the issue slots, 50 % of the integer pipe, the rest lost to the barriers between the
+// stages.  The roles run from one instruction cache, so a shorter loop gains more than one unrolled.
 #include "attn_plan.cuh"
 #include "cache4.cuh"
 
-namespace sv {
+#include <climits>
 
+namespace sv {
 
 struct T4Args {
     TaArgs a;             // a.H: packs of heads
@@ -45,9 +52,6 @@ struct T4Args {
     int value[kTaKeys / 8];         // where a tile's values lie in a head's blocks, 8 tokens at a time
 };
 
-#ifndef T4_TURNS
-#define T4_TURNS(c) ((c) == 16 ? 2 : 1)
-#endif
 template <int DP, int PACK, int RP> struct T4Cfg {
     static constexpr int kCols = PACK * RP;              // rows of all heads of a pack
     static constexpr int kRowP = kCols * 2;              // bytes of a key's weights
@@ -57,8 +61,10 @@ template <int DP, int PACK, int RP> struct T4Cfg {
     static constexpr int kW = kCols < 32 ? kCols : 32;   // columns of a softmax warp
     // two warpgroups of softmax: a tile each in turn, or with 64 columns half of every tile's
     static constexpr int kStreams = kCols > 32 ? 1 : 2;
-    // a tile's K and V: a warpgroup each, or two in turn
-    static constexpr int kTurns = T4_TURNS(kCols);
+    // K and V: a warpgroup each, or two in turn with 16 columns, where the softmax leaves most of the issue slots to
+    // them (64 requests of 8192 positions: 152 us so, 182 with one).  With more columns a second one only takes
+    // registers and turns from the softmax (16 nodes after 131071 positions: 122 us against 85 with one).
+    static constexpr int kTurns = kCols == 16 ? 2 : 1;
     static constexpr int kSoft = 8, kV = kSoft + 4 * kTurns;  // softmax warps, then K's, then V's
     static constexpr int kLoad = kV + 4 * kTurns, kMma = kLoad + 2, kPlan = kLoad + 3;  // (two warps load)
     static constexpr int kWarps = kLoad + 4, kThreads = kWarps * 32;
@@ -302,6 +308,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             }
             __syncwarp();
             const int head = s.hk * PACK + slot, i_end = s.i0 + s.n;
+            const int have = min(nb, (T.heads - s.hk * PACK) * recs);  // blocks of heads that there are
             const int *row = A.table + s.b * A.row_b + head * A.row_h;
             // the place in memory of this lane's block of tile i0 + lane / nb; that of any block where no node sees it
             auto fetch = [&](int i0) -> const uint8_t * {
@@ -341,13 +348,14 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     break;
                 }
                 // (One lane issues, in a loop: copies by a lane each are issued one after the other all the same.  A copy
-                // takes the warp 100 cycles and more, so blocks come whole, codes and scales.)
+                // takes the warp 100 cycles and more, so blocks come whole, codes and scales.  What an odd last head's
+                // place in a pair holds is finite whatever its bits are, and meets rows of zeros that nobody reads.)
                 if (elect_one()) {
                     const uint8_t *const *from = places + (i - base) * nb;
                     uint8_t *to = sh.tile[stage];
-                    mbar_expect_tx(&sh.full[stage], (uint32_t)(nb * T.bytes));
+                    mbar_expect_tx(&sh.full[stage], (uint32_t)(have * T.bytes));
 #pragma unroll 4
-                    for (int r = 0; r < nb; ++r, to += T.bytes) bulk_g2s(to, from[r], (uint32_t)T.bytes, &sh.full[stage]);
+                    for (int r = 0; r < have; ++r, to += T.bytes) bulk_g2s(to, from[r], (uint32_t)T.bytes, &sh.full[stage]);
                 }
                 __syncwarp();
                 if (++stage == kStages) stage = 0, ++fill;
@@ -811,11 +819,16 @@ struct T4Rows {
 static T4Rows t4_rows(int N, int G, int heads, int D) {
     T4Rows r;
     r.dp = D <= 64 ? 64 : 128;
-    // two heads to a pack while their rows fit 64 columns, since one head of 64 leaves half of V's lanes empty
-    r.pack = r.dp == 64 && heads > 1 && N * G <= 32 ? 2 : 1;
-    const int most = r.pack == 2 ? 32 : 64, fit = most / G;
-    const int tiles = (N + fit - 1) / fit;
-    r.np = (N + tiles - 1) / tiles;
+    auto tiles = [&](int most) { return most < G ? INT_MAX / 2 : (N + most / G - 1) / (most / G); };
+    // Heads of up to 64 go in pairs of 32 rows each where that makes no more pairs and row tiles than heads alone with
+    // 64 rows, which leave half of V's lanes empty (64 requests of 4096 positions, 8 key heads of 64: 32 rows of a
+    // head 67 us in pairs and 114 alone, 36 rows 113 and 115, 64 rows 116 and 122).
+    r.pack = r.dp == 64 && (long long)tiles(32) * ((heads + 1) / 2) <= (long long)tiles(64) * heads ? 2 : 1;
+    const int count = tiles(r.pack == 2 ? 32 : 64);
+    r.np = (N + count - 1) / count;
+    // The fewest columns that hold the rows (64 requests of 4096 positions, heads of 128: 4 rows of a head 84 us with
+    // 16 columns, 87 with 32, 105 with 64; 20 rows 93 with 32, 113 with 64; pairs of 4 rows at 8192 positions 94 with
+    // 16 for each, 103 with 32).  A head of 64 alone has more than 32 rows.
     const int rows = r.np * G;
     r.rp = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     if (r.dp == 64 && r.pack == 1) r.rp = 64;
