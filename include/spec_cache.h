@@ -328,7 +328,10 @@ spec_status_t spec_tree_attention4(const void *q, spec_dtype_t dtype, long long 
  * (a NaN makes both NaN).  pages->layers = 1; its v is not read.
  *   bounds  [num_pages, heads, 2, head_dim] of the pool's dtype (`dtype` for a
  *           4-bit pool), 16-byte aligned.  Other pages keep theirs.
- * start[b] < 0 counts as 0.  Positions that the table does not reach, and pages outside the pool,
+ * start[b] < 0 counts as 0.  Rows that share a page have to agree on its
+ * committed positions, as forked requests do on all but their last page; the
+ * copied last page of a fork has bounds once a position of it is summarised.
+ * Positions that the table does not reach, and pages outside the pool,
  * are skipped (SPEC_DEV_BAD_LEN, SPEC_DEV_BAD_PAGE).  1 <= B < 2^16.
  * SPEC_DTYPE_BF16 and SPEC_DTYPE_F16.  One launch.
  */
