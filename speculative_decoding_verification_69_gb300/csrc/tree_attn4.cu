@@ -92,7 +92,8 @@ template <int DP, int PACK, int RP> struct T4Shared {
     uint8_t tile[C::kStages][C::kStage];     // per head: its blocks, as they lie in memory
     const uint8_t *places[2][32];            // of a loading warp: where the next blocks lie in memory
     uint4 scale[4 * C::kTurns][32];                      // of a V warp: V's multipliers and addends for its keys
-    float m[C::kSoft][C::kW], f[C::kSoft][C::kW];    // per warp: references, negated, and their last factors
+    // per warp: the largest scores so far as references, what z adds for them, and the factors of the last change
+    float ref[C::kSoft][C::kW], m[C::kSoft][C::kW], f[C::kSoft][C::kW];
     float top[C::kSoft][C::kW], sum[C::kSoft][C::kW];
     float w[2][C::kCols];                    // the streams' factors in the result
     long long row[C::kCols];                 // where a row goes: twice its first element (of out, or of the parts), one
@@ -531,7 +532,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         // a quarter of the keys' scale was multiplied in float16
         const float scale = A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
         const int sinks = A.window ? A.sinks : 0;
-        float *m = sh.m[warp], *f = sh.f[warp];
+        float *m = sh.m[warp], *f = sh.f[warp], *top = sh.ref[warp];
+        auto in_base2 = [&](float y) -> float { return fmaxf(y * scale, -FLT_MAX) - kLift; };  // what a reference is for z
         // the row of which this thread writes the sum: its head in the pack, node of the tile and head of the group
         const int c = (int)threadIdx.x, of = c / RP, r = c % RP, local = r / A.G, in_group = r - local * A.G;
         uint32_t base = 0;  // the CTA's tiles before this segment
@@ -554,7 +556,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             float l[kW];
 #pragma unroll
             for (int i = 0; i < kW; ++i) l[i] = 0.f;
-            if (lane < kW) m[lane] = FLT_MAX;
+            if (lane < kW) top[lane] = -FLT_MAX;
+            bool coarse = false;
             __syncwarp();
             const int t0 = kStreams == 2 ? (int)((base + (uint32_t)stream) & 1u) : 0;
             const int i0 = s.i0;
@@ -611,9 +614,8 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                 // The scores less the references; where one has grown, or at the stream's first tile, after new references.
                 // (One copy of each step: the roles' code passes through one instruction cache.)
                 bool gone = false;
-                // 0: whether one has grown, 1: new references, 2: with those.  (Not again however large: scores that
-                // float32 holds to more than 2^3 stay above references as coarse as they.)
-                int step = t == t0 ? 1 : 0;
+                // 0: whether one has grown, 1: new references, 2: with those, which none exceeds by more than a rounding.
+                int step = t == t0 || coarse ? 1 : 0;
 #pragma unroll 1
                 for (; step <= 2; ++step) {
                     uint32_t x[kW];
@@ -635,15 +637,20 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                     }
                     if (lane < kW) sh.top[warp][lane] = mine;
                     meet<128>(1 + wg, false);
+                    bool large = false;
                     if (lane < kW) {
                         const int w0 = wg * 4;
                         float y = fmaxf(fmaxf(sh.top[w0][lane], sh.top[w0 + 1][lane]),
-                                        fmaxf(sh.top[w0 + 2][lane], sh.top[w0 + 3][lane])) * scale;
-                        const float old = -m[lane];
-                        y = y > old + kLift ? y - kLift : old;
-                        f[lane] = ex2(old - y);
-                        m[lane] = -y;
+                                        fmaxf(sh.top[w0 + 2][lane], sh.top[w0 + 3][lane]));
+                        const float old = top[lane];
+                        f[lane] = 1.f;
+                        if (y > old) f[lane] = ex2((old - y) * scale), top[lane] = y;
+                        else y = old;
+                        m[lane] = -in_base2(y);
+                        large = y > -FLT_MAX && fabsf(y * scale) > 0x1p24f;
                     }
+                    coarse = __any_sync(0xFFFFFFFFu, large) != 0;
+                    if (coarse && lane < kW) m[lane] = kLift;
                     __syncwarp();
                     if (t > t0) {  // O and the sums hold the stream's tiles before this one
 #pragma unroll
@@ -660,6 +667,20 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                             tmem_store(to + (uint32_t)d, o);
                         }
                         tmem_wait_store();
+                    }
+                    // Scores whose scaled form float32 holds to 1 or more: the reference is taken off them first, which is
+                    // exact near it, so that their weights neither overflow nor vanish.  Every tile goes this way then.
+                    if (coarse) {
+#pragma unroll 1
+                        for (int d = 0; d < kW; d += 16) {
+                            uint32_t y[16];
+                            tmem_load(ts + buf * C::kSStep + (uint32_t)d, y);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) - top[d + i]);
+                            tmem_store(ts + buf * C::kSStep + (uint32_t)d, y);
+                        }
+                        tmem_wait_store();
+                        meet<128>(1 + wg, false);  // (the next tile's maxima are written where these were read)
                     }
                 }
                 if (gone) {
@@ -727,7 +748,7 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             if (c < kCols) {  // a thread per row: its sum and lse, and the factors of its parts
                 float ref, total;
                 auto part = [&](int w0, int at, float &mm, float &ll) {  // of the warps w0 .. w0 + 3
-                    mm = -sh.m[w0][at];
+                    mm = in_base2(sh.ref[w0][at]);
                     ll = sh.sum[w0][at] + sh.sum[w0 + 1][at] + sh.sum[w0 + 2][at] + sh.sum[w0 + 3][at];
                 };
                 float w0 = 1.f, w1 = 0.f;

@@ -196,6 +196,40 @@ def test_scores_of_minus_infinity():
     assert (o[0, 0, 1].double() - want).abs().max() <= 2 ** -7 * 11 and abs(float(l[0, 0, 1]) - 1.9459101) < 1e-5
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,hq,hkv,D", [(1, 4, 2, 128), (8, 4, 1, 128), (40, 2, 1, 128), (9, 4, 2, 64)])
+@pytest.mark.parametrize("power", [10, 14, 30, 90])
+def test_scores_as_large_as_float32_holds(power, N, hq, hkv, D, dtype):
+    """One key twice as large as all others, and scores so large that it takes all the weight: the result is its value,
+    which the formats hold, but for the roundings of that weight 2^z to float16 (the sum takes it unrounded, and z is
+    whole only where the scores are less their reference exactly) and of the result, each half a step.  The key lies
+    in the first tile or in a later one."""
+    sv = _sv()
+    if dtype == torch.float16 and power > 14:
+        pytest.skip("beyond float16")
+    page, lens = 16, [5, 130, 700, 2000]
+    c = _case(power + N, lens, N, hq, hkv, D, page, dtype, tree=False)
+    sc = c4.places(page, D, "k")[2].cuda()
+    at, shift, _ = (x.cuda() for x in c4.places(page, D, "k"))
+    c["pool"][..., sc] = 248 if power > 10 else 152                   # 2^12 and 1
+    c["pool"][..., :page * D // 2] = 0xBB                             # all keys 3 scales
+    for b, (n0, j) in enumerate(zip(lens, (3, 129, 0, 1777))):
+        p = int(c["table"][b, j // page])
+        byte = torch.unique(at[j % page])
+        c["pool"][p, :, byte] = 0xEE                                  # and one of 6
+    c["q"].fill_(2.0 ** power)
+    scale = 1.0
+    o, l, st = _run(c, scale=scale)
+    k, v = c4.decode(c["pool"], page, D)
+    for b, j in enumerate((3, 129, 0, 1777)):
+        p = int(c["table"][b, j // page])
+        want = v[p, j % page].to(dtype).repeat_interleave(hq // hkv, 0)
+        score = float(k[p, j % page, 0].sum()) * 2.0 ** power
+        assert ((o[b] - want).double().abs() <= want.double().abs() * (2 ** -11 + torch.finfo(dtype).eps / 2 + 2 ** -18)).all()
+        assert (l[b].double() - score).abs().max() <= score * 2 ** -20
+    assert st == 0
+
+
 def test_bad_inputs_are_reported():
     sv = _sv()
     c = _case(12, [20, 50], 6, 4, 2, 64, 16, torch.bfloat16)
@@ -248,3 +282,40 @@ def test_streams_out_and_graphs():
         for graph, d, res in graphs:
             ref = c4.ref_attention(d["q"], d["pool"], d["page"], d["table"], d["len"], d["parent"])
             ch.check_attention(res[0], res[1], ref, torch.bfloat16, 128)
+
+
+@pytest.mark.parametrize("N,hq,hkv,D", [(1, 8, 2, 128), (9, 8, 2, 64), (8, 8, 2, 128), (64, 16, 2, 128), (40, 4, 1, 64)])
+def test_wait_that_runs_out_is_reported(N, hq, hkv, D):
+    """Every wait between the kernel's roles gives up at once: the call reports it and ends, the next one is right."""
+    sv = _sv()
+    c = _case(N, [900, 300, 5], N, hq, hkv, D, 16, torch.bfloat16)
+    try:
+        sv.force_wait_timeout(True)
+        _, _, st = _run(c)
+    finally:
+        sv.force_wait_timeout(False)
+    assert st == sv.DEV_TIMEOUT
+    _check(c)
+
+
+@pytest.mark.parametrize("N,hq,hkv,D", [(1, 8, 2, 128), (9, 12, 3, 64), (5, 8, 1, 64), (64, 8, 2, 96)])
+def test_exact_workspace_and_two_calls_at_once(N, hq, hkv, D):
+    """The workspace that the library asks for, full of a pattern, suffices; calls on two streams, each with its own,
+    do not disturb each other."""
+    sv = _sv()
+    cs = [_case(N + i, [700, 90, 0, 2000 * i], N, hq, hkv, D, 16, torch.bfloat16) for i in range(2)]
+    want = [_check(c) for c in cs]
+    n = sv.load_library().spec_tree_attention4_workspace_bytes(4, N, hq, hkv, D)
+    guard = [torch.full((n + 4096,), 255, dtype=torch.uint8, device="cuda") for _ in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for c, w, s in zip(cs, guard, streams):
+            got.append(sv.tree_attention4(c["q"], c["pool"], c["table"], c["len"], c["page"], c["parent"],
+                                          return_lse=True, workspace=w[:n], stream=s))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    assert all(bool((w[n:] == 255).all()) for w in guard)
