@@ -489,9 +489,10 @@ static __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_
 }
 
 // A 4D tensor map over 16-bit elements, 64 of them (128 bytes, the swizzle
-// span) wide; elements past an extent read as zero.
+// span) wide; elements past an extent read as zero.  lines: what lies beside a row is of no use, so L2 fetches
+// 128 bytes and not 256.
 static bool ta_tmap(CUtensorMap *tm, int dtype, const void *base, const cuuint64_t (&dims)[4],
-                    const cuuint64_t (&strides)[3], cuuint32_t box1, cuuint32_t box2) {
+                    const cuuint64_t (&strides)[3], cuuint32_t box1, cuuint32_t box2, bool lines = false) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
         void *fn = nullptr;
@@ -505,7 +506,8 @@ static bool ta_tmap(CUtensorMap *tm, int dtype, const void *base, const cuuint64
     const cuuint32_t box[4] = {64, box1, box2, 1}, estr[4] = {1, 1, 1, 1};
     return encode(tm, dtype == SPEC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   4, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_SWIZZLE_128B,
+                  lines ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

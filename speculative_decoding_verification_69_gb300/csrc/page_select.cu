@@ -145,7 +145,8 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
 // The grid is as many CTAs as run at once; a warp's next page numbers come while it
 // multiplies, so that each unit waits for memory once.  14 us for 4 requests of 4096 pages of 8 heads of 128 (67 MB, 4.8
 // TB/s, launch included; 25 with a CTA for every 8 units), 18.4 for 64 requests of up to 512 pages of 8 heads of 64 and
-// 20 rows (50 MB: 20 rows are three products for every page).
+// 20 rows (50 MB in pieces of 256 bytes of a page and head; three CTAs to an SM, or q fetched
+// ahead, change nothing).
 template <int DT, int BLOCKS>  // BLOCKS of 32 channels
 __global__ void __launch_bounds__(256, 2) sv_scores(const __grid_constant__ ScoreArgs A) {
     pdl_trigger();
@@ -256,7 +257,7 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 // which the keep-th largest lies is the next span.  (Parts of the span that occurs, not digits of the whole
 // number: scores of one sign and size share their upper digits, which all threads would count
 // in one place.  Three rounds at most, most often two, instead of sixteen of a search by bits, which
-// took 13 us for 8 heads of 4096 pages and 22 for 256 of 1024; this takes 6.4 for 32 heads of 4096 and 12 for
+// took 13 us for 8 heads of 4096 pages and 22 for 256 of 1024; this takes 6.4 for 32 heads of 4096 and 7 for
 // 256 of 1024, both mostly latency.)  Then a scan gives every page its place.
 constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
 template <int THREADS, int ITEMS>  // ITEMS 0: any number, read anew in every round
@@ -528,7 +529,10 @@ spec_status_t spec_page_select(const float *scores, const int32_t *page_table, c
     A.status = dev_status;
     const dim3 grid((unsigned)heads, (unsigned)B);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // The fewest threads that keep a row in registers, 16 places each at most: 32 requests of 1025 places and 8 heads take
+    // 7 us with 256 threads and 12 with 1024; beyond, every round reads the scores again.
     if (max_pages <= 256 * 4) return sv::launch_pdl(sv::sv_select<256, 4>, grid, dim3(256), 0, s, A);
+    if (max_pages <= 256 * 8) return sv::launch_pdl(sv::sv_select<256, 8>, grid, dim3(256), 0, s, A);
     if (max_pages <= 1024 * 8) return sv::launch_pdl(sv::sv_select<1024, 8>, grid, dim3(1024), 0, s, A);
     if (max_pages <= 1024 * 16) return sv::launch_pdl(sv::sv_select<1024, 16>, grid, dim3(1024), 0, s, A);
     return sv::launch_pdl(sv::sv_select<1024, 0>, grid, dim3(1024), 0, s, A);
