@@ -35,8 +35,8 @@ template <int DT> __device__ __forceinline__ void take_bounds(uint4 &lo, uint4 &
 
 // The smallest and largest of every channel of a page's keys, which any order of the keys gives alike.  Grid (runs of
 // pages, requests), block (vector columns, tokens): the columns' threads take every blockDim.y-th token and join in
-// shared memory.  Bound by reading the keys: 18.7 us for 32768 tokens of 8 heads of 128 (67 MB and 8 MB of bounds, 4 TB/s,
-// launch included); after a step only the pages that grew are read, 5 to 6 us, a launch.
+// shared memory.  Bound by reading the keys: 18.4 us for 32768 tokens of 8 heads of 128 (67 MB and 8 MB of bounds, 4 TB/s,
+// launch included); after a step only the pages that grew are read, 4 to 5 us, a launch.
 template <int DT, bool FOUR>
 __global__ void __launch_bounds__(256) sv_bounds(const __grid_constant__ BoundsArgs A) {
     __shared__ uint4 part[2][256];
@@ -52,8 +52,11 @@ __global__ void __launch_bounds__(256) sv_bounds(const __grid_constant__ BoundsA
     if (from >= end) return;
     const int last = (int)((end - 1) >> A.page_shift);
     const int cols = A.heads * A.vecs;
-    for (int i = (from >> A.page_shift) + blockIdx.x; i <= last; i += gridDim.x) {
-        const int p = A.table[(long long)b * A.max_pages + i];
+    const int *row = A.table + (long long)b * A.max_pages;
+    int i = (from >> A.page_shift) + blockIdx.x, next = i <= last ? row[i] : 0;
+    for (; i <= last; i += gridDim.x) {
+        const int p = next;
+        if (i + (int)gridDim.x <= last) next = row[i + gridDim.x];
         if ((unsigned)p >= (unsigned)A.num_pages) {
             if (threadIdx.x == 0 && threadIdx.y == 0) flag(A.status, SPEC_DEV_BAD_PAGE);
             continue;
@@ -395,7 +398,8 @@ static int sm_count() {
 template <class K> static spec_status_t launch_bounds(K kernel, const BoundsArgs &A, int B, cudaStream_t s) {
     const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256, sms = sm_count();
     if (sms == 0) return SPEC_ERR_CUDA;
-    const int want = (16 * sms + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
+    // as many CTAs as run at once (16 to an SM take 1 us more to start, 3 leave memory idle: 26 us of the 18.4 above)
+    const int want = (5 * sms + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
     return launch_pdl(kernel, dim3((unsigned)runs, (unsigned)B), dim3((unsigned)x, (unsigned)(256 / x)), 0, s, A);
 }
 

@@ -199,7 +199,7 @@ def test_select(keep, first, recent, extra, kind):
     assert torch.equal(got.cpu(), want) and kept.tolist() == want_len and int(st) == 0
 
 
-@pytest.mark.parametrize("places", [1024, 1025, 8192, 8193, 16384, 16390, 40000])
+@pytest.mark.parametrize("places", [1024, 1025, 2048, 2049, 8192, 8193, 16384, 16390, 40000])
 def test_select_from_many(places):
     sv = _sv()
     page, keep = 8, 333
