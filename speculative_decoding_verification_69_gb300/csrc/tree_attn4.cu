@@ -29,9 +29,9 @@
 // the stages of consecutive tiles overlap.  Heads of up to 64 are taken in pairs (the lanes of V^T are two heads'
 // channels; the quarter of the product that mixes them is not read).  More rows than a tile has are cut into row tiles.
 //
-// Measured: 64 single tokens of 32 query heads and 8 key heads of 128 after up to 8192 positions, 140 us for their
+// Measured: 64 single tokens of 32 query heads and 8 key heads of 128 after up to 8192 positions, 141 us for their
 // 428 MB, 3.1 TB/s or 45 % of a copy's rate (the same with 16 bits a number: 248 us).  16 nodes after 131071 positions:
-// 77.6 us (99).  Chains of 9 of 32 requests, up to 4096 positions, 8 key heads of 64: 66.4 us.  What bounds it is the
+// 78.8 us (99).  Chains of 9 of 32 requests, up to 4096 positions, 8 key heads of 64: 65 us.  What bounds it is the
 // issuing of instructions: 4180 warp instructions to a tile of 128 keys, of which a code's pair takes three (a shift, the
 // mask, the multiply-add); 68 % of the issue slots, 50 % of the integer pipe, the rest lost to the barriers between the
 // stages.  The roles run from one instruction cache, so a shorter loop gains more than one unrolled.
