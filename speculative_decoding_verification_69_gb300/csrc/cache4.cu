@@ -30,7 +30,7 @@ struct Block8 {
 __device__ __forceinline__ bool block8(const Move4Args &A, int b, int i, int n0, int m, bool report, Block8 &x) {
     const long long first = ((long long)n0 >> 3) + i;         // the block's number in the sequence
     const long long pos = first << 3, n = pos - n0;
-    if (n >= m) return false;
+    if (n >= m || m <= 0) return false;  // (without tokens a block that begins before n0 has none either)
     x.n = (int)n;
     x.t0 = n < 0 ? (int)-n : 0;
     x.t1 = (int)min(8ll, m - n);

@@ -234,6 +234,19 @@ def test_bad_lengths_and_pages_are_skipped():
     assert (k[:2] == 0).all() and (k[2, :2] == 63.0 / 64.0).all() and (k[2, 2:] == 0).all() and torch.equal(k, v)
 
 
+def test_rows_without_tokens_touch_and_report_nothing():
+    """count 0 in a row whose pages are gone, its length in the middle of a block of 8 tokens."""
+    sv = _sv()
+    page, D = 8, 32
+    pool = c4.make_pool(torch.Generator(device="cuda").manual_seed(1), 4, 1, page, D)
+    before = pool.clone()
+    x = torch.ones((3, 4, 1, D), device="cuda", dtype=torch.bfloat16)
+    table, lens, count, st = _i32([[-1, -1], [0, 99], [2, 3]]), _i32([5, 11, 13]), _i32([0, 0, -2]), _status()
+    sv.cache4_append(pool, table, lens, x, x, page, count=count, dev_status=st)
+    k, v = sv.cache4_read(pool, table, lens, 4, page, D, count=count, dev_status=st)
+    assert int(st) == 0 and torch.equal(pool, before) and (k == 0).all() and (v == 0).all()
+
+
 def test_pools_with_strides():
     """A pool inside a larger tensor, heads and pages in any order."""
     sv = _sv()
