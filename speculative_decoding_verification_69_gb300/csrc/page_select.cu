@@ -148,8 +148,8 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
 // The grid is as many CTAs as run at once; a warp's next page numbers come while it
 // multiplies, so that each unit waits for memory once.  14 us for 4 requests of 4096 pages of 8 heads of 128 (67 MB, 4.8
 // TB/s, launch included; 25 with a CTA for every 8 units), 18.4 for 64 requests of up to 512 pages of 8 heads of 64 and
-// 20 rows (50 MB in pieces of 256 bytes of a page and head; three CTAs to an SM, or q fetched
-// ahead, change nothing).
+// 20 rows (50 MB in pieces of 256 bytes of a page and head; three CTAs to an SM, q fetched
+// ahead or 32 pages to a warp gain nothing).
 template <int DT, int BLOCKS>  // BLOCKS of 32 channels
 __global__ void __launch_bounds__(256, 2) sv_scores(const __grid_constant__ ScoreArgs A) {
     pdl_trigger();
@@ -398,7 +398,7 @@ static int sm_count() {
 template <class K> static spec_status_t launch_bounds(K kernel, const BoundsArgs &A, int B, cudaStream_t s) {
     const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256, sms = sm_count();
     if (sms == 0) return SPEC_ERR_CUDA;
-    // as many CTAs as run at once (16 to an SM take 1 us more to start, 3 leave memory idle: 26 us of the 18.4 above)
+    // as many CTAs as run at once (16 to an SM: 0.5 us more for few pages; 3: 26 us instead of the 18.4 above)
     const int want = (5 * sms + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
     return launch_pdl(kernel, dim3((unsigned)runs, (unsigned)B), dim3((unsigned)x, (unsigned)(256 / x)), 0, s, A);
 }
