@@ -196,21 +196,18 @@ def test_scores_of_minus_infinity():
     assert (o[0, 0, 1].double() - want).abs().max() <= 2 ** -7 * 11 and abs(float(l[0, 0, 1]) - 1.9459101) < 1e-5
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dtype,power", [(torch.bfloat16, 10), (torch.bfloat16, 14), (torch.bfloat16, 30),
+                                         (torch.bfloat16, 90), (torch.float16, 10), (torch.float16, 14)])
 @pytest.mark.parametrize("N,hq,hkv,D", [(1, 4, 2, 128), (8, 4, 1, 128), (40, 2, 1, 128), (9, 4, 2, 64)])
-@pytest.mark.parametrize("power", [10, 14, 30, 90])
 def test_scores_as_large_as_float32_holds(power, N, hq, hkv, D, dtype):
     """One key twice as large as all others, and scores so large that it takes all the weight: the result is its value,
     which the formats hold, but for the roundings of that weight 2^z to float16 (the sum takes it unrounded, and z is
     whole only where the scores are less their reference exactly) and of the result, each half a step.  The key lies
     in the first tile or in a later one."""
-    sv = _sv()
-    if dtype == torch.float16 and power > 14:
-        pytest.skip("beyond float16")
     page, lens = 16, [5, 130, 700, 2000]
     c = _case(power + N, lens, N, hq, hkv, D, page, dtype, tree=False)
     sc = c4.places(page, D, "k")[2].cuda()
-    at, shift, _ = (x.cuda() for x in c4.places(page, D, "k"))
+    at = c4.places(page, D, "k")[0].cuda()
     c["pool"][..., sc] = 248 if power > 10 else 152                   # 2^12 and 1
     c["pool"][..., :page * D // 2] = 0xBB                             # all keys 3 scales
     for b, (n0, j) in enumerate(zip(lens, (3, 129, 0, 1777))):
@@ -218,8 +215,7 @@ def test_scores_as_large_as_float32_holds(power, N, hq, hkv, D, dtype):
         byte = torch.unique(at[j % page])
         c["pool"][p, :, byte] = 0xEE                                  # and one of 6
     c["q"].fill_(2.0 ** power)
-    scale = 1.0
-    o, l, st = _run(c, scale=scale)
+    o, l, st = _run(c, scale=1.0)
     k, v = c4.decode(c["pool"], page, D)
     for b, j in enumerate((3, 129, 0, 1777)):
         p = int(c["table"][b, j // page])
