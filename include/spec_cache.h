@@ -375,7 +375,9 @@ spec_status_t spec_page_scores(const void *q, spec_dtype_t dtype, long long q_st
  *              its end), then -1.
  *   out_len    [B] int32: the committed positions that the selected pages hold.
  * So a position p >= cache_len[b] of the cache is position p - cache_len[b] +
- * out_len[b] of the lists.  cache_len[b] outside [0, max_pages * page_size] is
+ * out_len[b] of the lists.  extra is at least the nodes N of the attention over the lists,
+ * which finds their keys there; what the lists do not reach it reports (SPEC_DEV_BAD_PAGE, SPEC_DEV_BAD_LEN) and
+ * answers as for any such row of a page table.  cache_len[b] outside [0, max_pages * page_size] is
  * cut (SPEC_DEV_BAD_LEN).  1 <= B < 2^16, 1 <= heads <= 1024, first >= 0, recent >= 1,
  * first + recent <= keep, extra >= 0, max_pages <= SPEC_MAX_SELECT.  One launch.
  */

@@ -28,7 +28,7 @@ cheap score picks, of either cache:
 
     bounds = cache.new_bounds()                       # of one layer
     cache.append(layer, k_new, v_new)
-    pages = cache.select(layer, q, bounds, keep=64, extra=N, start=start)
+    pages = cache.select(layer, q, bounds, keep=64, start=start)
     o = cache.attention(layer, q, parent, pages=pages)
 
 `start` int32 [slots]: the lengths up to which the bounds have been formed (None:
@@ -281,7 +281,8 @@ def page_scores(q, bounds, page_table, cache_len, page_size, *, node_count=None,
 def page_select(scores, page_table, cache_len, page_size, keep, *, first=1, recent=1, extra=0, dev_status=None,
                 stream=None):
     """The `keep` pages of each request and key head that rank highest (spec_page_select), the first `first` and
-    last `recent` ones before all others, and behind them the pages of `extra` drafted tokens.  Returns
+    last `recent` ones before all others, and behind them the pages of `extra` drafted tokens: of all nodes of the
+    attention that follows, since it looks them up behind the selected positions.  Returns
     (table, length): int32 [B, kv_heads, keep + ceil(extra / page_size)] and [B], the page_table
     and cache_len of attention over these pages."""
     args = (scores, page_table, cache_len, page_size, keep, first, recent, extra, dev_status, None)
@@ -312,9 +313,12 @@ class _Slots:
         """The pages past every slot's length given back."""
         self.reserve(0, stream=stream)
 
-    def select(self, layer, q, bounds, keep, *, start=None, first=1, recent=1, extra=0, stream=None):
+    def select(self, layer, q, bounds, keep, *, start=None, first=1, recent=1, extra=None, stream=None):
         """Pages for attention(..., pages=): the bounds of the pages written since `start` formed, all pages
-        scored and the best `keep` of each key head taken."""
+        scored and the best `keep` of each key head taken, and behind them the pages of `extra` drafted tokens
+        (None: the nodes of q, which that attention looks up there)."""
+        if extra is None:
+            extra = q.shape[1]
         self.summarise(layer, bounds, start=start, stream=stream)
         scores = page_scores(q, bounds, self.page_table, self.cache_len, self.page_size, dev_status=self.status,
                              stream=stream)

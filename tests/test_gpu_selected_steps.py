@@ -1,0 +1,55 @@
+"""Steps that attend to selected pages, through the caches' own calls."""
+import pytest
+import torch
+
+import cache4_helpers as c4
+import cache_helpers as ch
+
+pytestmark = pytest.mark.gpu
+
+
+def _sv():
+    import speculative_decoding_verification_69_gb300 as sv
+    return sv
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _cache(four, lens, N, seed, hkv=2, D=64, page=16, max_pages=40):
+    """A cache of one layer whose slots hold prompts of these lengths, and have pages for N tokens more."""
+    sv = _sv()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cache = (sv.PagedCache4 if four else sv.PagedCache)(1, 150, page, hkv, D, len(lens), max_pages)
+    want = _i32(lens)
+    sv.cache_resize(cache.page_table, cache.page_count, cache.page_ref, want, page, extra=N, dev_status=cache.status)
+    x = torch.randn((len(lens), max(lens), 2 * hkv, D), generator=g, device="cuda").bfloat16()
+    cache.append(0, x[:, :, :hkv], x[:, :, hkv:], count=want)
+    cache.cache_len.copy_(want)
+    x = torch.randn((len(lens), N, 8 + 2 * hkv, D), generator=g, device="cuda").bfloat16()
+    cache.append(0, x[:, :, 8:8 + hkv], x[:, :, 8 + hkv:])
+    return cache, x[:, :, :8], g
+
+
+def _numbers(cache, four, D=64, page=16):
+    k, v = c4.decode(cache.pool[0], page, D) if four else (cache.k[0], cache.v[0])
+    return k.bfloat16(), v.bfloat16()
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("N", [1, 3, 20])
+def test_the_pages_of_the_nodes_follow_the_selected_ones(N, four):
+    """Lengths at the end of a page, below and above `keep` pages: the nodes see themselves without being asked for."""
+    keep = 4
+    cache, q, g = _cache(four, [0, 16, 30, 64, 96, 320, 333], N, 3 + N)
+    for cls_kw in (dict(), dict(extra=N)):
+        pages = cache.select(0, q, cache.new_bounds(), keep, **cls_kw)
+        assert pages[0].shape[2] == keep + -(-N // 16)
+        parent = ch.random_parents(g, 7, N)
+        o, l = cache.attention(0, q, parent, pages=pages, return_lse=True)
+        assert int(cache.status) == 0
+        k, v = _numbers(cache, four)
+        ch.check_attention(o, l, c4.ref_lists(q, k, v, *pages, parent), torch.bfloat16, 64)
+    none = cache.select(0, q, cache.new_bounds(), keep, extra=0)       # pages for no node, when that is asked for
+    assert none[0].shape[2] == keep and torch.equal(none[1], pages[1])
