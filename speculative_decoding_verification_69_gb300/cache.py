@@ -313,15 +313,17 @@ class _Slots:
         """The pages past every slot's length given back."""
         self.reserve(0, stream=stream)
 
-    def select(self, layer, q, bounds, keep, *, start=None, first=1, recent=1, extra=None, stream=None):
+    def select(self, layer, q, bounds, keep, *, start=None, first=1, recent=1, extra=None, node_count=None,
+               stream=None):
         """Pages for attention(..., pages=): the bounds of the pages written since `start` formed, all pages
         scored and the best `keep` of each key head taken, and behind them the pages of `extra` drafted tokens
-        (None: the nodes of q, which that attention looks up there)."""
+        (None: the nodes of q, which that attention looks up there).  node_count int32 [slots]: the nodes
+        that each slot has; rows of q past them, which that attention leaves out, have no part in the scores."""
         if extra is None:
             extra = q.shape[1]
         self.summarise(layer, bounds, start=start, stream=stream)
-        scores = page_scores(q, bounds, self.page_table, self.cache_len, self.page_size, dev_status=self.status,
-                             stream=stream)
+        scores = page_scores(q, bounds, self.page_table, self.cache_len, self.page_size, node_count=node_count,
+                             dev_status=self.status, stream=stream)
         return page_select(scores, self.page_table, self.cache_len, self.page_size, keep, first=first, recent=recent,
                            extra=extra, dev_status=self.status, stream=stream)
 

@@ -53,3 +53,21 @@ def test_the_pages_of_the_nodes_follow_the_selected_ones(N, four):
         ch.check_attention(o, l, c4.ref_lists(q, k, v, *pages, parent), torch.bfloat16, 64)
     none = cache.select(0, q, cache.new_bounds(), keep, extra=0)       # pages for no node, when that is asked for
     assert none[0].shape[2] == keep and torch.equal(none[1], pages[1])
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_rows_past_the_node_counts_have_no_say(four):
+    """Rows past a request's count hold NaN: its lists are those of the rows before."""
+    N, keep, cnt = 5, 4, _i32([5, 1, 3, 2])
+    cache, q, _ = _cache(four, [200, 320, 333, 100], N, 8)
+    past = torch.arange(N, device="cuda").view(1, N, 1, 1) >= cnt.view(4, 1, 1, 1)
+    alike = torch.where(past, q[:, :1], q)                             # in their place the first row once more
+    want = cache.select(0, alike, cache.new_bounds(), keep)
+    other = cache.select(0, q, cache.new_bounds(), keep)
+    got = cache.select(0, torch.where(past, torch.full_like(q, float("nan")), q), cache.new_bounds(), keep,
+                       node_count=cnt)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not torch.equal(other[0], want[0])                          # (they would have had one)
+    o = cache.attention(0, torch.where(past, torch.full_like(q, float("nan")), q), pages=got, node_count=cnt)
+    ref = cache.attention(0, alike, pages=want, node_count=cnt)
+    assert torch.equal(o, ref) and torch.isfinite(o).all() and int(cache.status) == 0
