@@ -881,7 +881,7 @@ static spec_status_t ta_launch(const TaArgs &A, const CUtensorMap &q, const CUte
     if (st != SPEC_OK) return st;
     constexpr int rows = 256 / kTaJoinLanes;
     return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((r.cta + rows - 1) / rows)), dim3(256), 0, s,
-                      A, r.used, r.cta, MODE);
+                      A, r.used, r.cta, MODE, 1.f, 0.f);
 }
 
 template <int DT, int DP>

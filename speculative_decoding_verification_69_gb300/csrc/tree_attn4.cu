@@ -202,6 +202,13 @@ template <int DT> __device__ __forceinline__ uint2 unpack_scale(float lo, float 
 
 // ------------------------------------------------------------------ the kernel
 
+constexpr float kLift = 7.f;  // weights up to 2^15: those 2^-29 below the maximum are still normal in float16
+
+// The factor of the scores, of which float16 has a quarter (see unpack_scale).
+template <int DT> __host__ __device__ __forceinline__ float t4_scale(const TaArgs &A) {
+    return A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
+}
+
 template <int DT, int DP, int PACK, int RP>
 __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
     tree_attn4(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ T4Args T) {
@@ -215,7 +222,6 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
     constexpr int kCols = C::kCols, kStages = C::kStages, kW = C::kW, kSoft = C::kSoft, kStreams = C::kStreams,
                   kTurns = C::kTurns;
     constexpr uint32_t kBufs = C::kBufs;
-    constexpr float kLift = 7.f;  // weights up to 2^15: those 2^-29 below the maximum are still normal in float16
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTaSlots; ++i) {
@@ -529,11 +535,15 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
         const uint32_t ts = tmem + lanes + C::kTS + col0, to = tmem + lanes + C::kTO + (uint32_t)stream * C::kOStep + col0;
         const int slot = quad * 32 / DP, ch = key % DP;
         const int rows_used = A.np * A.G, rows_cta = PACK * rows_used;
-        // a quarter of the keys' scale was multiplied in float16
-        const float scale = A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
+        const float scale = t4_scale<DT>(A);
         const int sinks = A.window ? A.sinks : 0;
         float *m = sh.m[warp], *f = sh.f[warp], *top = sh.ref[warp];
-        auto in_base2 = [&](float y) -> float { return fmaxf(y * scale, -FLT_MAX) - kLift; };  // what a reference is for z
+        // A column's reference is its largest score so far, `top`.  What its weights 2^z hold of that is the scaled form
+        // as float32 rounds it, z = x scale - in_base2(top); of a top that is `far`, whose scaled form float32 holds
+        // to 1 or more, all of it, z = (x - top) scale + kLift.  Which of the two follows from the top alone, so
+        // sums over other tiles, streams and parts are brought together by what each of them holds.
+        auto in_base2 = [&](float y) -> float { return fmaxf(y * scale, -FLT_MAX) - kLift; };
+        auto far = [&](float y) -> bool { return y > -FLT_MAX && fabsf(y * scale) > 0x1p24f; };
         // the row of which this thread writes the sum: its head in the pack, node of the tile and head of the group
         const int c = (int)threadIdx.x, of = c / RP, r = c % RP, local = r / A.G, in_group = r - local * A.G;
         uint32_t base = 0;  // the CTA's tiles before this segment
@@ -643,14 +653,17 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         float y = fmaxf(fmaxf(sh.top[w0][lane], sh.top[w0 + 1][lane]),
                                         fmaxf(sh.top[w0 + 2][lane], sh.top[w0 + 3][lane]));
                         const float old = top[lane];
-                        f[lane] = 1.f;
-                        if (y > old) f[lane] = ex2((old - y) * scale), top[lane] = y;
-                        else y = old;
-                        m[lane] = -in_base2(y);
-                        large = y > -FLT_MAX && fabsf(y * scale) > 0x1p24f;
+                        y = fmaxf(y, old);
+                        large = far(y);
+                        const bool was = far(old);
+                        const float now = large ? 0.f : in_base2(y), before = was ? 0.f : in_base2(old);
+                        f[lane] = y == old ? 1.f
+                                           : ex2(fmaf((was ? old : 0.f) - (large ? y : 0.f), scale, before - now) +
+                                                 ((large ? kLift : 0.f) - (was ? kLift : 0.f)));
+                        top[lane] = y;
+                        m[lane] = large ? kLift : -now;
                     }
                     coarse = __any_sync(0xFFFFFFFFu, large) != 0;
-                    if (coarse && lane < kW) m[lane] = kLift;
                     __syncwarp();
                     if (t > t0) {  // O and the sums hold the stream's tiles before this one
 #pragma unroll
@@ -668,15 +681,18 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         }
                         tmem_wait_store();
                     }
-                    // Scores whose scaled form float32 holds to 1 or more: the reference is taken off them first, which is
-                    // exact near it, so that their weights neither overflow nor vanish.  Every tile goes this way then.
+                    // A reference that is far is taken off the scores first, which is exact near it, so that their weights
+                    // neither overflow nor vanish.  Every tile goes this way then.
                     if (coarse) {
+                        __syncwarp();
+                        if (lane < kW) f[lane] = far(top[lane]) ? top[lane] : 0.f;
+                        __syncwarp();
 #pragma unroll 1
                         for (int d = 0; d < kW; d += 16) {
                             uint32_t y[16];
                             tmem_load(ts + buf * C::kSStep + (uint32_t)d, y);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) - top[d + i]);
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) - f[d + i]);
                             tmem_store(ts + buf * C::kSStep + (uint32_t)d, y);
                         }
                         tmem_wait_store();
@@ -747,32 +763,33 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
             const int only = kStreams == 2 && n == 1 ? (int)(last & 1u) : -1;      // the one stream with a part
             if (c < kCols) {  // a thread per row: its sum and lse, and the factors of its parts
                 float ref, total;
-                auto part = [&](int w0, int at, float &mm, float &ll) {  // of the warps w0 .. w0 + 3
-                    mm = in_base2(sh.ref[w0][at]);
-                    ll = sh.sum[w0][at] + sh.sum[w0 + 1][at] + sh.sum[w0 + 2][at] + sh.sum[w0 + 3][at];
+                // of the warps wa .. wa + 3: the reference, the sum, and the factor that makes their weights
+                // 2^((x - top) scale + kLift) where the reference was held rounded
+                auto part = [&](int wa, int at, float &mm, float &ll, float &ww) {
+                    mm = sh.ref[wa][at];
+                    ll = sh.sum[wa][at] + sh.sum[wa + 1][at] + sh.sum[wa + 2][at] + sh.sum[wa + 3][at];
+                    ww = mm == -FLT_MAX || far(mm) ? 1.f : ex2(fmaf(-mm, scale, in_base2(mm)) + kLift);
                 };
-                float w0 = 1.f, w1 = 0.f;
-                if (kStreams == 1) {
-                    part(c / kW * 4, c % kW, ref, total);
-                } else if (only >= 0) {
-                    part(only * 4, c, ref, total);
+                float w0, w1 = 0.f;
+                if (kStreams == 1 || only >= 0) {
+                    part(kStreams == 1 ? c / kW * 4 : only * 4, c % kW, ref, total, w0);
+                    total *= w0;
                 } else {
                     float ma, la, mb, lb;
-                    part(0, c, ma, la);
-                    part(4, c, mb, lb);
+                    part(0, c, ma, la, w0);
+                    part(4, c, mb, lb, w1);
                     ref = fmaxf(ma, mb);
-                    w0 = ex2(ma - ref), w1 = ex2(mb - ref);
+                    w0 *= ex2((ma - ref) * scale), w1 *= ex2((mb - ref) * scale);
                     total = la * w0 + lb * w1;
                 }
                 const int node = s.node0 + local, hk = s.hk * PACK + of;
                 const bool exists = r < rows_used && node < A.N && hk < T.heads, valid = exists && node < g.cnt;
-                if (total != total) ref = fmaxf(ref, 0.f);  // the row's part must not pass for empty
                 const float inv = whole_item ? 4.f / total : 4.f;  // (O is a quarter of itself)
                 sh.w[0][c] = w0 * inv, sh.w[1][c] = w1 * inv;
                 const long long orow = ((long long)s.b * A.N + node) * A.Hq + hk * A.G + in_group;
                 const long long prow = place * rows_cta + of * rows_used + r;
                 sh.row[c] = whole_item ? (exists ? 2 * orow * A.D + (valid ? 0 : 1) : -1) : (valid ? 2 * prow * A.D : -1);
-                if (exists && whole_item && A.lse) A.lse[orow] = ta_lse(valid, ref, total);
+                if (exists && whole_item && A.lse) A.lse[orow] = ta_lse(valid, in_base2(ref), total);
                 if (exists && !whole_item)
                     A.part_ml[prow] = valid ? make_float2(ref, total) : make_float2(-INFINITY, 0.f);
             }
@@ -887,7 +904,7 @@ static spec_status_t t4_launch(const T4Args &T, const CUtensorMap &q, int ctas, 
     constexpr int rows = 256 / kTaJoinLanes;
     const int used = T.a.np * T.a.G, cta = PACK * used;
     return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((cta + rows - 1) / rows)), dim3(256), 0, s,
-                      T.a, used, cta, PACK == 2 ? (int)kTaSplitHeads : (int)kTaSplitKeys);
+                      T.a, used, cta, PACK == 2 ? (int)kTaSplitHeads : (int)kTaSplitKeys, t4_scale<DT>(T.a), kLift);
 }
 
 template <int DT>

@@ -97,7 +97,7 @@ def test_weights_beside_a_reference_that_moves(low, N, hq, D, requests, dtype):
     q[..., 32] = 7
     many = {0: 7, 1: 4, 2: 4, 33: 1, 34: 1, 35: 1}
     for j in list(range(127)) + list(range(128, 255)) + [290]:
-        keys.key(j, dict(many, **({32: 1} if j == 290 else {})))
+        keys.key(j, {**many, 32: int(j == 290)})
         keys.value(j, -7 if j == 290 else 2)
     k, v = keys.numbers(n0 + 1)
     score = q[0, 0].double() @ k.T
