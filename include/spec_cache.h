@@ -201,7 +201,7 @@ spec_status_t spec_cache_commit(const spec_pages_t *pages, const int32_t *page_t
  *   the call up (SPEC_DEV_TIMEOUT; outputs undefined).
  *   1 <= B < 2^16, 1 <= N <= SPEC_MAX_TREE, head_dim a multiple of 8 up to
  *   SPEC_MAX_HEAD_DIM, Hq a multiple of heads, heads <= 1024, Hq / heads <= 64,
- *   window >= 0, sinks >= 0.  scale > 0.
+ *   window >= 0, sinks >= 0.  scale > 0, and scale * log2(e) a float32.
  *   workspace: spec_tree_attention_workspace_bytes, 256-byte aligned; nothing
  *   in it is read that the call has not written.  Two launches.
  * Scores, softmax statistics and sums are float32; the softmax weights are
@@ -298,6 +298,8 @@ spec_status_t spec_cache4_fork(const spec_pages4_t *pages, int32_t *page_table, 
  *   per_head   0: page_table [B, max_pages]; 1: [B, heads, max_pages], a list of
  *              pages for every key head, as spec_page_select writes them.
  *   workspace: spec_tree_attention4_workspace_bytes, 256-byte aligned.
+ * In SPEC_DTYPE_F16 four times scale * log2(e) has to be a float32.  The softmax
+ * weights are rounded to float16 for the product with v, in either dtype.
  * All else, rows that are empty or not finite included, is as there.
  */
 size_t spec_tree_attention4_workspace_bytes(int B, int N, int Hq, int heads, int head_dim);

@@ -492,6 +492,10 @@ static __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_
     if (lane == 0 && A.lse) A.lse[orow] = ta_lse(some, fmaxf(m * scale, -FLT_MAX) - lift, l);
 }
 
+constexpr float kTaLog2e = 1.44269504089f;
+// Whether the factor of the scores is a number: an infinite one would make NaN of a score of 0.
+static bool ta_scale_ok(float scale, float times) { return scale > 0.f && scale * kTaLog2e * times <= FLT_MAX; }
+
 // A 4D tensor map over 16-bit elements, 64 of them (128 bytes, the swizzle
 // span) wide; elements past an extent read as zero.  lines: what lies beside a row is of no use, so L2 fetches
 // 128 bytes and not 256.

@@ -907,8 +907,8 @@ static spec_status_t ta_call(const void *q, long long q_stride_b, long long q_st
     const int D = pages->head_dim, H = pages->heads;
     const size_t need = spec_tree_attention_workspace_bytes(B, N, Hq, H, D);
     if (!q || !page_table || !cache_len || !out || need == 0 || pages->layers != 1 || max_pages < 1 ||
-        ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || window < 0 || sinks < 0 || !(scale > 0.f) ||
-        !(scale < 3.0e38f))
+        ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || window < 0 || sinks < 0 ||
+        !ta_scale_ok(scale, 1.f))
         return SPEC_ERR_INVALID_ARG;
     const long long qst[3] = {q_stride_h, q_stride_n, q_stride_b};
     const int qext[3] = {Hq, N, B};
@@ -955,7 +955,7 @@ static spec_status_t ta_call(const void *q, long long q_stride_b, long long q_st
     A.sinks = sinks;
     A.np = r.np;
     A.box = P.page < kTaKeys ? P.page : kTaKeys;
-    A.scale_log2 = scale * 1.44269504089f;
+    A.scale_log2 = scale * kTaLog2e;
     A.out = static_cast<uint16_t *>(out);
     A.lse = lse;
     char *ws = static_cast<char *>(workspace);

@@ -205,8 +205,9 @@ template <int DT> __device__ __forceinline__ uint2 unpack_scale(float lo, float 
 constexpr float kLift = 7.f;  // weights up to 2^15: those 2^-29 below the maximum are still normal in float16
 
 // The factor of the scores, of which float16 has a quarter (see unpack_scale).
+template <int DT> constexpr float kKeyPart = DT == SPEC_DTYPE_F16 ? 4.f : 1.f;
 template <int DT> __host__ __device__ __forceinline__ float t4_scale(const TaArgs &A) {
-    return A.scale_log2 * (DT == SPEC_DTYPE_F16 ? 4.f : 1.f);
+    return A.scale_log2 * kKeyPart<DT>;
 }
 
 template <int DT, int DP, int PACK, int RP>
@@ -945,8 +946,9 @@ spec_status_t spec_tree_attention4(const void *q, spec_dtype_t dtype, long long 
     const int D = P.D, H = P.heads;
     const size_t need = spec_tree_attention4_workspace_bytes(B, N, Hq, H, D);
     if (!q || !page_table || !cache_len || !out || need == 0 || pages->layers != 1 || max_pages < 1 ||
-        ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || window < 0 || sinks < 0 || !(scale > 0.f) ||
-        !(scale < 3.0e38f) || (per_head != 0 && per_head != 1))
+        ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || window < 0 || sinks < 0 ||
+        !sv::ta_scale_ok(scale, dtype == SPEC_DTYPE_F16 ? sv::kKeyPart<SPEC_DTYPE_F16> : 1.f) ||
+        (per_head != 0 && per_head != 1))
         return SPEC_ERR_INVALID_ARG;
     const long long qst[3] = {q_stride_h, q_stride_n, q_stride_b};
     const int qext[3] = {Hq, N, B};
@@ -983,7 +985,7 @@ spec_status_t spec_tree_attention4(const void *q, spec_dtype_t dtype, long long 
     A.window = window;
     A.sinks = sinks;
     A.np = r.np;
-    A.scale_log2 = scale * 1.44269504089f;
+    A.scale_log2 = scale * sv::kTaLog2e;
     A.out = static_cast<uint16_t *>(out);
     A.lse = lse;
     char *ws = static_cast<char *>(workspace);
