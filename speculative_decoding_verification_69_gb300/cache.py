@@ -198,7 +198,8 @@ def cache4_page_bytes(page_size, head_dim):
 def cache4_append(pool, page_table, cache_len, k_new, v_new, page_size, *, count=None, dev_status=None, stream=None):
     """New keys and values of one layer quantised into a 4-bit pool (spec_cache4_append): pool uint8
     [num_pages, kv_heads, cache4_page_bytes(page_size, head_dim)]; the rest as for cache_append,
-    k_new and v_new bfloat16 or float16."""
+    k_new and v_new bfloat16 or float16.  A pool's bytes tell neither its page_size nor its head_dim: every call
+    has to give it the same ones (PagedCache4 sees to that)."""
     _native().append4(pool, page_table, cache_len, k_new, v_new, page_size, count, dev_status, _handle(stream))
 
 
@@ -393,13 +394,20 @@ class PagedCache4(_Slots):
         _, num_pages, heads, _ = self.pool.shape
         return torch.zeros((num_pages, heads, 2, self.head_dim), dtype=self.dtype, device=self.pool.device)
 
+    def _own(self, x, name):
+        """(A pool's bytes do not tell: pages have the same for heads of 72, 80, 88 and 96.)"""
+        if x.shape[-1] != self.head_dim:
+            raise ValueError("%s has heads of %d, the cache of %d" % (name, x.shape[-1], self.head_dim))
+        return x
+
     def summarise(self, layer, bounds, start=None, stream=None):
+        self._own(bounds, "bounds")
         cache4_bounds(self._layers[layer], bounds, self.page_table, self.cache_len, self.page_size, start=start,
                       dev_status=self.status, stream=stream)
 
     def append(self, layer, k_new, v_new, count=None, stream=None):
-        cache4_append(self._layers[layer], self.page_table, self.cache_len, k_new, v_new, self.page_size, count=count,
-                      dev_status=self.status, stream=stream)
+        cache4_append(self._layers[layer], self.page_table, self.cache_len, self._own(k_new, "k_new"), v_new,
+                      self.page_size, count=count, dev_status=self.status, stream=stream)
 
     def read(self, start, n, layer=None, count=None, stream=None):
         """Keys and values of `n` positions from `start` on (int32 [slots]), of one layer or of all."""
@@ -409,8 +417,8 @@ class PagedCache4(_Slots):
 
     def attention(self, layer, q, parent=None, pages=None, **kw):
         table, length = self._lists(pages)
-        return tree_attention4(q, self._layers[layer], table, length, self.page_size, parent, dev_status=self.status,
-                               **kw)
+        return tree_attention4(self._own(q, "q"), self._layers[layer], table, length, self.page_size, parent,
+                               dev_status=self.status, **kw)
 
     def commit(self, out_nodes, accept_len, nodes=None, stream=None):
         cache4_commit(self.pool, self.page_table, self.cache_len, out_nodes, accept_len, self.page_size, self.head_dim,
