@@ -419,14 +419,13 @@ __device__ __forceinline__ void ta_schedule(const TaArgs &A, Walk<MODE> &w, cons
 // The parts of an item that cuts fell into, joined in the order of the keys.
 // joins[j]: the first cut of an item lies at CTA j's first unit; its parts are
 // slot 1 of the CTA before, where it begins, and slot 0 of CTA j and those after.  A part
-// holds sums of weights 2^((x - m) scale + lift), m -inf where the row does not exist.  (Scores
-// in base 2 have a scale of 1; where the scaled form of a large score would lose what m - m' is,
-// it is left to this product.)
+// holds sums of weights 2^(x - m) of scores x in base 2, or (RAW) 2^((x - m) scale + lift) of scores
+// that are not scaled yet, whose differences scaling would round; m is -inf where the row does not exist.
 // 16 lanes per row, two vectors of four columns each: bound by the latency of three
 // dependent loads at few rows (3.4 us of a call of one token at one request) and
 // by instructions at many (10 us at 64 nodes and 64 requests); a warp per row
 // took 16.7 us there, 8 lanes 9.5 but 3 us more with 20 parts of 64 rows.
-template <int DT>
+template <int DT, bool RAW>
 static __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_used, int rows_cta, int mode,
                                                              float scale, float lift) {
     constexpr int L = kTaJoinLanes, kVecs = 32 / L;
@@ -458,7 +457,7 @@ static __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_
         float w = 0.f;
         if (some && i0 + lane < parts) {
             const float2 x = i0 == 0 ? x0 : A.part_ml[slot(i0 + lane)];
-            w = ex2((x.x - m) * scale);
+            w = ex2(RAW ? (x.x - m) * scale : x.x - m);
             l = fmaf(x.y, w, l);
         }
         const int k = min(L, parts - i0);
@@ -489,7 +488,7 @@ static __global__ void __launch_bounds__(256) tree_attn_join(TaArgs A, int rows_
             dst[lane + v * L] = some ? make_uint2(pack2<DT>(o[v].x * inv, o[v].y * inv),
                                                   pack2<DT>(o[v].z * inv, o[v].w * inv))
                                      : make_uint2(0u, 0u);
-    if (lane == 0 && A.lse) A.lse[orow] = ta_lse(some, fmaxf(m * scale, -FLT_MAX) - lift, l);
+    if (lane == 0 && A.lse) A.lse[orow] = ta_lse(some, RAW ? fmaxf(m * scale, -FLT_MAX) - lift : m, l);
 }
 
 constexpr float kTaLog2e = 1.44269504089f;

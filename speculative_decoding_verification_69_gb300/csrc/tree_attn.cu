@@ -181,7 +181,9 @@ __device__ __noinline__ void ta_add_not_finite(const TaArgs &A, Seg s, int hk, u
 
 // ------------------------------------------------------------------ the kernel
 
-template <int DT, int DP, int MODE>
+// LISTS: each of the two heads of a unit (kTaSplitHeads) has a list of pages.  (A kernel of its own: in that of all
+// calls the second list cost 512 requests with a window of 128 1.2 us of 102.)
+template <int DT, int DP, int MODE, bool LISTS>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TaArgs A) {
@@ -283,15 +285,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (!sp || sp->s.n == 0) break;
             const Seg s = sp->s;
             give(seg_no);
-            const int *row = A.table + s.b * A.row_b + s.hk * kPer * A.row_h;
+            const int *row = kPer == 1 || LISTS ? A.table + s.b * A.row_b + s.hk * kPer * A.row_h
+                                                : A.table + (long long)s.b * A.max_pages;
             const int i_end = s.i0 + s.n;
             // first position of this lane's box in tile i, and whether some node sees any of it
             auto box_pos = [&](int i) -> int { return s.g.tile(i) * kTaKeys + box * A.box; };
             auto box_seen = [&](int j) -> bool {
                 return j < s.g.end && (s.g.wlo - j < A.box || j < A.sinks);
             };
-            // the second head of a unit has a list of its own (kTaSplitHeads)
-            const bool lists = kPer == 2 && A.row_h != 0;
             auto fetch = [&](int i0, const int *row) -> int {  // page of this lane's box in tile i0 + lane / nb
                 const int i = i0 + lane / nb;
                 if (i >= i_end) return 0;
@@ -341,12 +342,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     do {  // at first these and the next ones, then one load ahead
                         now = nxt, now2 = nxt2;
                         nxt = fetch(at, row);
-                        if (lists) nxt2 = fetch(at, row + A.row_h);
+                        if (LISTS) nxt2 = fetch(at, row + A.row_h);
                         at += ahead;
                     } while (at == s.i0 + ahead);
                     __syncwarp();
                     pages[lane] = now;
-                    if (lists) pages[32 + lane] = now2;
+                    if (LISTS) pages[32 + lane] = now2;
                     __syncwarp();
                 }
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, lane < nb && box_seen(box_pos(i)));
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                     uint8_t *tile = tiles + stage * C::kStage;
                     if (elect_one()) {
                         mbar_expect_tx(&full[stage], (uint32_t)(__popc(seen) * kHalves * A.box * 128));
-                        const int *page = pages + (i - base) * nb + (lists && head != s.hk * kPer ? 32 : 0);
+                        const int *page = pages + (i - base) * nb + (LISTS && head != s.hk * kPer ? 32 : 0);
 #pragma unroll 1
                         for (int x = 0; x < nb; ++x, ++page, tile += A.box * 128) {
                             if (!((seen >> x) & 1u)) continue;
@@ -864,23 +865,23 @@ static TaLayout ta_layout(int N, int Hq, int heads, int D) {
     return L;
 }
 
-template <int DT, int DP, int MODE>
+template <int DT, int DP, int MODE, bool LISTS>
 static spec_status_t ta_launch(const TaArgs &A, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                const TaRows &r, int ctas, int dev, cudaStream_t s) {
     constexpr size_t smem = sizeof(TaShared<DP, MODE>) + 1024;
     static_assert(smem <= 232448, "shared memory of a CTA");
     static bool ready[64] = {};
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(tree_attn<DT, DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(tree_attn<DT, DP, MODE, LISTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
             return SPEC_ERR_CUDA;
         ready[dev] = true;
     }
     const spec_status_t st =
-        launch_pdl(tree_attn<DT, DP, MODE>, dim3((unsigned)ctas), dim3(kTaThreads), smem, s, q, k, v, A);
+        launch_pdl(tree_attn<DT, DP, MODE, LISTS>, dim3((unsigned)ctas), dim3(kTaThreads), smem, s, q, k, v, A);
     if (st != SPEC_OK) return st;
     constexpr int rows = 256 / kTaJoinLanes;
-    return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((r.cta + rows - 1) / rows)), dim3(256), 0, s,
+    return launch_pdl(tree_attn_join<DT, false>, dim3((unsigned)ctas, (unsigned)((r.cta + rows - 1) / rows)), dim3(256), 0, s,
                       A, r.used, r.cta, MODE, 1.f, 0.f);
 }
 
@@ -888,9 +889,11 @@ template <int DT, int DP>
 static spec_status_t ta_launch_mode(const TaArgs &A, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                     const TaRows &r, int ctas, int dev, cudaStream_t s) {
     switch (r.mode) {
-    case kTaSplitRows: return ta_launch<DT, DP, kTaSplitRows>(A, q, k, v, r, ctas, dev, s);
-    case kTaSplitHeads: return ta_launch<DT, DP, kTaSplitHeads>(A, q, k, v, r, ctas, dev, s);
-    default: return ta_launch<DT, DP, kTaSplitKeys>(A, q, k, v, r, ctas, dev, s);
+    case kTaSplitRows: return ta_launch<DT, DP, kTaSplitRows, false>(A, q, k, v, r, ctas, dev, s);
+    case kTaSplitHeads:
+        return A.row_h ? ta_launch<DT, DP, kTaSplitHeads, true>(A, q, k, v, r, ctas, dev, s)
+                       : ta_launch<DT, DP, kTaSplitHeads, false>(A, q, k, v, r, ctas, dev, s);
+    default: return ta_launch<DT, DP, kTaSplitKeys, false>(A, q, k, v, r, ctas, dev, s);
     }
 }
 

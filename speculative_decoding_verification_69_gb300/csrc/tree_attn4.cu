@@ -904,7 +904,7 @@ static spec_status_t t4_launch(const T4Args &T, const CUtensorMap &q, int ctas, 
     if (st != SPEC_OK) return st;
     constexpr int rows = 256 / kTaJoinLanes;
     const int used = T.a.np * T.a.G, cta = PACK * used;
-    return launch_pdl(tree_attn_join<DT>, dim3((unsigned)ctas, (unsigned)((cta + rows - 1) / rows)), dim3(256), 0, s,
+    return launch_pdl(tree_attn_join<DT, true>, dim3((unsigned)ctas, (unsigned)((cta + rows - 1) / rows)), dim3(256), 0, s,
                       T.a, used, cta, PACK == 2 ? (int)kTaSplitHeads : (int)kTaSplitKeys, t4_scale<DT>(T.a), kLift);
 }
 
