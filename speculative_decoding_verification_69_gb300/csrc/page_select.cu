@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(256, 2) sv_scores(const __grid_constant__ Scor
             float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < BLOCKS; ++k) {
-                const uint4 y = r < rows_now && k * 4 + t < A.vecs ? __ldg(q + k * 4 + t) : none;
+                // (a plain load: one of data declared constant may be moved before the wait for who writes q)
+                const uint4 y = r < rows_now && k * 4 + t < A.vecs ? q[k * 4 + t] : none;
                 mma16<DT>(c, hi[0][k].x, hi[1][k].x, hi[0][k].y, hi[1][k].y, max16<DT>(y.x, 0u), max16<DT>(y.y, 0u));
                 mma16<DT>(c, hi[0][k].z, hi[1][k].z, hi[0][k].w, hi[1][k].w, max16<DT>(y.z, 0u), max16<DT>(y.w, 0u));
                 mma16<DT>(c, lo[0][k].x, lo[1][k].x, lo[0][k].y, lo[1][k].y, min16<DT>(y.x, 0u), min16<DT>(y.y, 0u));
