@@ -535,8 +535,10 @@ spec_status_t spec_cache4_commit(const spec_pages4_t *pages, const int32_t *page
     const bool in_place = new_len == cache_len;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (out_nodes || !in_place) {
+        int dev = 0, sms = 0;
+        if (!sv::current_device(dev, sms)) return SPEC_ERR_CUDA;
         // about four CTAs to an SM: more would find the paths anew
-        const long long shares = ((long long)P.layers * P.heads + sv::kC4Warps - 1) / sv::kC4Warps, fit = 608 / B + 1;
+        const long long shares = ((long long)P.layers * P.heads + sv::kC4Warps - 1) / sv::kC4Warps, fit = 4 * sms / B + 1;
         const unsigned each = out_nodes ? (unsigned)(shares < fit ? shares : fit) : 1u;
         const spec_status_t r = sv::launch_pdl(sv::sv_commit4, dim3((unsigned)B, each),
                                                dim3(sv::kC4Warps * 32), 0, s, P, ids, page_table, cache_len,

@@ -387,18 +387,10 @@ __global__ void __launch_bounds__(THREADS) sv_select(const __grid_constant__ Sel
     });
 }
 
-// SMs of the current device, 0 if that fails.
-static int sm_count() {
-    static int sms[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms[dev];
-}
-
 template <class K> static spec_status_t launch_bounds(K kernel, const BoundsArgs &A, int B, cudaStream_t s) {
-    const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256, sms = sm_count();
-    if (sms == 0) return SPEC_ERR_CUDA;
+    const int cols = A.heads * A.vecs, x = cols < 256 ? cols : 256;
+    int dev = 0, sms = 0;
+    if (!current_device(dev, sms)) return SPEC_ERR_CUDA;
     // as many CTAs as run at once (16 to an SM: 0.5 us more for few pages; 3: 26 us instead of the 18.4 above)
     const int want = (5 * sms + B - 1) / B, runs = want < A.max_pages ? want : A.max_pages;
     return launch_pdl(kernel, dim3((unsigned)runs, (unsigned)B), dim3((unsigned)x, (unsigned)(256 / x)), 0, s, A);
@@ -497,8 +489,8 @@ spec_status_t spec_page_scores(const void *q, spec_dtype_t dtype, long long q_st
     A.tiles = (max_pages - 1) / 16 + 1;
     A.status = dev_status;
     const long long ctas = ((long long)B * heads * A.tiles + 7) / 8;
-    const int sms = sv::sm_count();
-    if (sms == 0) return SPEC_ERR_CUDA;
+    int dev = 0, sms = 0;
+    if (!sv::current_device(dev, sms)) return SPEC_ERR_CUDA;
     const dim3 grid((unsigned)(ctas < 2 * sms ? ctas : 2 * sms)), block(256);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = dtype == SPEC_DTYPE_BF16;

@@ -483,6 +483,15 @@ spec_status_t make_pool(const spec_pages_t *p, Pool &P) {
     return SPEC_OK;
 }
 
+bool current_device(int &dev, int &sms) {
+    static int known[kMaxDevices] = {};
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    if (known[dev] == 0 && cudaDeviceGetAttribute(&known[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return false;
+    sms = known[dev];
+    return true;
+}
+
 // Threads over the vector columns of a token, and over tokens.
 static dim3 column_block(int cols) {
     const int x = cols < 256 ? cols : 256;
@@ -501,9 +510,9 @@ static spec_status_t launch_pages(const PagesArgs &A, cudaStream_t s) {
     constexpr size_t most = (item + (FORK ? sizeof(int) : 0)) * SPEC_MAX_SLOTS;
     static_assert(most + 2048 <= 232448, "shared memory of a CTA");
     const size_t smem = item * A.n + (FORK ? sizeof(int) * (size_t)A.slots : 0);
-    static bool ready[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    static bool ready[kMaxDevices] = {};
+    int dev = 0, sms = 0;
+    if (!current_device(dev, sms)) return SPEC_ERR_CUDA;
     if (!ready[dev]) {
         if (cudaFuncSetAttribute(sv_pages<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)most) != cudaSuccess)

@@ -106,6 +106,10 @@ __device__ __forceinline__ int commit_len(int len, int kept) {
     return (int)min((long long)len + 1 + kept, (long long)INT_MAX);
 }
 
+// The current device, and how many SMs it has; false if that fails or there are more devices than kMaxDevices.
+constexpr int kMaxDevices = 64;
+bool current_device(int &dev, int &sms);
+
 // Launch that may begin while the kernel before it on the stream is still
 // running: every kernel launched this way waits (pdl_wait) before it touches
 // memory, so the order of the stream holds.

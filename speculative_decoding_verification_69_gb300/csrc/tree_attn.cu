@@ -870,7 +870,7 @@ static spec_status_t ta_launch(const TaArgs &A, const CUtensorMap &q, const CUte
                                const TaRows &r, int ctas, int dev, cudaStream_t s) {
     constexpr size_t smem = sizeof(TaShared<DP, MODE>) + 1024;
     static_assert(smem <= 232448, "shared memory of a CTA");
-    static bool ready[64] = {};
+    static bool ready[kMaxDevices] = {};
     if (!ready[dev]) {
         if (cudaFuncSetAttribute(tree_attn<DT, DP, MODE, LISTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
@@ -918,12 +918,9 @@ static spec_status_t ta_call(const void *q, long long q_stride_b, long long q_st
     for (int i = 0; i < 3; ++i)
         if (qst[i] % 8 || qst[i] < (qext[i] > 1 ? D : 0)) return SPEC_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need) return SPEC_ERR_WORKSPACE;
-    int dev = 0;
-    static int sms[64] = {};
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
-    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-    const int ctas = sms[dev] < kTaMaxCtas ? sms[dev] : kTaMaxCtas;
+    int dev = 0, sms = 0;
+    if (!current_device(dev, sms)) return SPEC_ERR_CUDA;
+    const int ctas = sms < kTaMaxCtas ? sms : kTaMaxCtas;
 
     // A key head per stream once there is one for every CTA: the streams then share
     // nothing but the CTA, where streams that divide the keys meet at the end of

@@ -892,7 +892,7 @@ template <int DT, int DP, int PACK, int RP>
 static spec_status_t t4_launch(const T4Args &T, const CUtensorMap &q, int ctas, int dev, cudaStream_t s) {
     constexpr size_t smem = sizeof(T4Shared<DP, PACK, RP>) + 1024;
     static_assert(smem <= 232448, "shared memory of a CTA");
-    static bool ready[64] = {};
+    static bool ready[kMaxDevices] = {};
     if (!ready[dev]) {
         if (cudaFuncSetAttribute(tree_attn4<DT, DP, PACK, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
@@ -955,12 +955,9 @@ spec_status_t spec_tree_attention4(const void *q, spec_dtype_t dtype, long long 
     for (int i = 0; i < 3; ++i)
         if (qst[i] % 8 || qst[i] < (qext[i] > 1 ? D : 0)) return SPEC_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < need) return SPEC_ERR_WORKSPACE;
-    int dev = 0;
-    static int sms[64] = {};
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
-    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-    const int ctas = sms[dev] < sv::kTaMaxCtas ? sms[dev] : sv::kTaMaxCtas;
+    int dev = 0, sms = 0;
+    if (!sv::current_device(dev, sms)) return SPEC_ERR_CUDA;
+    const int ctas = sms < sv::kTaMaxCtas ? sms : sv::kTaMaxCtas;
 
     const sv::T4Rows r = sv::t4_rows(N, Hq / H, H, D);
     const sv::T4Layout L = sv::t4_layout(r, Hq / H, D);
