@@ -894,7 +894,11 @@ static spec_status_t t4_launch(const T4Args &T, const CUtensorMap &q, int ctas, 
     static_assert(smem <= 232448, "shared memory of a CTA");
     static bool ready[kMaxDevices] = {};
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(tree_attn4<DT, DP, PACK, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        // (compiled with fewer registers than are divided between the warps, setmaxnreg would wait for ever)
+        cudaFuncAttributes made = {};
+        if (cudaFuncGetAttributes(&made, tree_attn4<DT, DP, PACK, RP>) != cudaSuccess ||
+            made.numRegs < T4Cfg<DP, PACK, RP>::kRegs ||
+            cudaFuncSetAttribute(tree_attn4<DT, DP, PACK, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
             return SPEC_ERR_CUDA;
         ready[dev] = true;
