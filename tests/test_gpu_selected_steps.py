@@ -71,3 +71,46 @@ def test_rows_past_the_node_counts_have_no_say(four):
     o = cache.attention(0, torch.where(past, torch.full_like(q, float("nan")), q), pages=got, node_count=cnt)
     ref = cache.attention(0, alike, pages=want, node_count=cnt)
     assert torch.equal(o, ref) and torch.isfinite(o).all() and int(cache.status) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,hq,hkv,D,page", [(1, 8, 2, 128, 16), (9, 12, 3, 64, 8), (40, 8, 2, 80, 16), (6, 16, 16, 32, 128)])
+@pytest.mark.parametrize("window,sinks,counts", [(70, 2, False), (0, 0, True), (130, 0, True), (7, 140, True)])
+def test_lists_in_4_bits_with_windows_and_counts(window, sinks, counts, N, hq, hkv, D, page, dtype):
+    """Windows and sinks count the positions of the lists."""
+    sv = _sv()
+    g = torch.Generator(device="cuda").manual_seed(N * 7 + window)
+    lens = [0, 3, 127, 129, 300, 700]
+    P = max(-(-(n + N) // page) for n in lens) + 1
+    pages = sum(-(-(n + N) // page) for n in lens) + 3
+    table = torch.stack([ch.make_table(g, lens, N, page, P, pages)[0] for _ in range(hkv)], 1).contiguous()
+    pool = c4.make_pool(g, pages, hkv, page, D)
+    q = (torch.randn((len(lens), N, hq, D), generator=g, device="cuda") * 2).to(dtype)
+    parent, cl, st = ch.random_parents(g, len(lens), N), _i32(lens), _i32([0])
+    kw = dict(window=window, sinks=sinks, node_count=_i32([N, 1, 0, N, N // 2, N]) if counts else None)
+    o, l = sv.tree_attention4(q, pool, table, cl, page, parent, return_lse=True, dev_status=st, **kw)
+    ch.check_attention(o, l, c4.ref_attention(q, pool, page, table, cl, parent, **kw), dtype, D)
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_a_selection_on_a_stream_that_is_given(four):
+    """Every call of it behind the work that its stream has to do, with the results of the current stream."""
+    sv = _sv()
+    cache, q, _ = _cache(four, [200, 320, 0, 100], 2, 9)
+    bounds = cache.new_bounds()
+    want = cache.select(0, q, bounds, 4)
+    scores = sv.page_scores(q, bounds, cache.page_table, cache.cache_len, 16)
+    s = torch.cuda.Stream()
+    late, x = torch.zeros_like(bounds), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                                  # about 10 ms
+        x.copy_(q)
+    got = cache.select(0, x, late, 4, stream=s)
+    again = sv.page_scores(x, late, cache.page_table, cache.cache_len, 16, stream=s)
+    table, length = sv.page_select(again, cache.page_table, cache.cache_len, 16, 4, extra=2, stream=s)
+    s.synchronize()
+    assert torch.equal(late, bounds) and torch.equal(again, scores)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(table, want[0]) and torch.equal(length, want[1]) and int(cache.status) == 0
