@@ -390,7 +390,9 @@ spec_status_t spec_page_select(const float *scores, const int32_t *page_table, c
 
 /* spec_sparse_attention -- spec_tree_attention with a list of pages for every key
    head: page_table [B, heads, max_pages], cache_len the positions that each
-   list of the request holds. */
+   list of the request holds.  `window` and `sinks` count positions of the list, as do those of
+   spec_tree_attention4 with per_head = 1: neighbours there may lie far apart in the
+   sequence, so a window over a selection is not the window's part of it. */
 spec_status_t spec_sparse_attention(const void *q, long long q_stride_b, long long q_stride_n, long long q_stride_h,
                                     const spec_pages_t *pages, const int32_t *page_table, const int32_t *cache_len,
                                     const int32_t *parent, const int32_t *node_count, int B, int N, int Hq,

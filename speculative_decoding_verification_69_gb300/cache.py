@@ -175,9 +175,9 @@ def tree_attention(q, k, v, page_table, cache_len, parent=None, *, node_count=No
     b sees the positions [0, cache_len[b]), its ancestors and itself, with a
     window only the last `window` of them along its path and the first `sinks`
     tokens.  page_table [B, max_pages], or [B, kv_heads, max_pages] (with cache_len as
-    page_select returns them): a list of pages for every key head.  Returns out
-    [B, N, q_heads, head_dim], with return_lse also the log of the softmax sums,
-    float32 [B, N, q_heads]."""
+    page_select returns them): a list of pages for every key head, in whose positions
+    window and sinks then count, not in the sequence's.  Returns out [B, N, q_heads, head_dim], with
+    return_lse also the log of the softmax sums, float32 [B, N, q_heads]."""
     if stream is None:
         return _native().tree_attention(q, k, v, page_table, cache_len, parent, node_count, scale, window, sinks, out,
                                         return_lse, workspace, dev_status, None)

@@ -119,9 +119,11 @@ __device__ __forceinline__ void exchange(uint32_t (&w)[8], int j, uint32_t lanes
 }
 
 // New keys and values into the pages.  Grid (blocks of 8 tokens, requests), block (columns of
-// 8 channels, token blocks).  Bound by the instructions of the quantising: 55 us for 32752 tokens of 8
-// heads of 128, 3.1 TB/s of the 170 MB (92 us with divisions, and with 4-byte stores of the keys); a step of 9 tokens
-// for 8 requests is a launch, 6.6 us.
+// 8 channels, token blocks).  55 us for 32752 tokens of 8 heads of 128, 3.1 TB/s of the 170 MB (92 us with divisions,
+// and with 4-byte stores of the keys).  A thread loads its 16 vectors, then quantises: its 109 registers leave two CTAs
+// to an SM, too few warps (23 % of those that fit) to load while others compute, so neither HBM (31 %) nor the
+// issue slots (50 %, the integer pipe 45 %) are full, and warps wait for loads and shuffles.  A step of 9 tokens for 8
+// requests is a launch, 6.6 us.
 template <int DT> __global__ void __launch_bounds__(256) sv_append4(const __grid_constant__ Move4Args A) {
     pdl_trigger();
     pdl_wait();
@@ -200,9 +202,10 @@ template <int DT> __global__ void __launch_bounds__(256) sv_append4(const __grid
     }
 }
 
-// The numbers of a 4-bit cache.  Grid (blocks of 8 tokens, requests, layers), block as above.  Bound by its writes:
-// 35 us for the 170 MB of 32752 tokens of 8 heads of 128, 4.8 TB/s; 78 us for 64 requests of 32 tokens in 36 layers, the
-// same rate.
+// The numbers of a 4-bit cache.  Grid (blocks of 8 tokens, requests, layers), block as above.  35 us for the 170 MB of
+// 32752 tokens of 8 heads of 128, 4.8 TB/s; 78 us for 64 requests of 32 tokens in 36 layers, the same rate.  Codes are
+// converted one by one, which takes 62 % of the integer pipe with two CTAs to an SM (94 registers); HBM is busy for 38 to
+// 55 % of the time.
 template <int DT> __global__ void __launch_bounds__(256) sv_read4(const __grid_constant__ Move4Args A) {
     pdl_trigger();
     pdl_wait();
@@ -270,9 +273,9 @@ template <int DT> __global__ void __launch_bounds__(256) sv_read4(const __grid_c
 // All that moves is read before anything is written: the keys' codes and all scales into
 // registers, the values' words (which hold other tokens' codes too) into shared memory, where a
 // lane takes four channels' codes from node to place in the order of the path (place <= node, so no
-// code is overwritten before it is read), and writes the words back that changed.  Bound by
-// instructions, so by how much is found once; a thread per channel took 77 us where this takes 28.7
-// (64 requests of 32 nodes, 36 layers of 8 heads).
+// code is overwritten before it is read), and writes the words back that changed.  28.7 us for 64 requests of 32
+// nodes, 36 layers of 8 heads (a thread per channel took 77), 46 MB from HBM: bound by latency (HBM 20 %, issue slots
+// 16 %), since a warp reads a layer and head only when it has written the one before.
 constexpr int kC4Warps = 8, kC4Blocks = SPEC_MAX_TREE / 8 + 1, kC4Pieces = SPEC_MAX_TREE * 4;
 struct Piece4 {  // 16 bytes of codes of a moved key, and the scales beside them: offsets from a layer's head
     long long src, dst;

@@ -36,7 +36,7 @@
 //   32 requests of up to 4096 tokens, 9 nodes   75 us   5.5 TB/s    HBM
 //   64 requests, 64 nodes each (256 rows)      210 us   4.2 TB/s, 1000 TFLOP/s: a stream's chain of
 //                scores, two halves of weights and values; the tensor cores are 45% busy
-//   512 requests, 9 nodes, window of 128      101 us   2.2 TB/s    64 query heads of 64: short segments,
+//   512 requests, 9 nodes, window of 128      102 us   2.2 TB/s    64 query heads of 64: short segments,
 //                so the softmax warps' latency, half of it in masks, clearing and output
 //   1 request of 1000 tokens, 1 node          11.5 us   latency: lengths, pages, a tile, the join
 // K, V and P go through 128-key tiles because a product of 64 columns takes 48 cycles where

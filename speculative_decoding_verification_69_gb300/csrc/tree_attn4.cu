@@ -3,7 +3,9 @@
 //
 // Mathematics: that of tree_attn.cu (one pass over the keys with a reference near
 // the running maximum, parts over disjoint keys joined), on keys and values (c -
-// 8) s with a 4-bit code c and a scale s per 32 channels.  Both are formed exactly:
+// 8) s with a 4-bit code c and a scale s per 32 channels.  References are kept unscaled, and where
+// float32 holds their scaled form to 1 or more they are taken off the scores before scaling, so that large
+// scores weigh what their exact difference says wherever the keys lie.  Keys and values are formed exactly:
 // a code is put into the low mantissa bits of a 16-bit float of fixed exponent
 // (which then is 128 + c in bfloat16, 16 + c in float16), and one fused
 // multiply-add with s and -136 s, or s/4 and -6 s, gives (c - 8) s or a quarter of
@@ -31,7 +33,10 @@
 //
 // Measured: 64 single tokens of 32 query heads and 8 key heads of 128 after up to 8192 positions, 141 us for their
 // 428 MB, 3.1 TB/s or 45 % of a copy's rate (the same with 16 bits a number: 248 us).  16 nodes after 131071 positions:
-// 78.8 us (99).  Chains of 9 of 32 requests, up to 4096 positions, 8 key heads of 64: 65 us.  What bounds it is the
+// 78.8 us (99).  Chains of 9 of 32 requests, up to 4096 positions, 8 key heads of 64: 65 us (60.5: two row tiles, each
+// of which unpacks every key; chains of 8 fit in one, 42 us against 56).  With more rows, or in short segments, 16 bits
+// are faster: 64 requests of 64 nodes after up to 2000 positions 342 us (130), 512 of 9 with a window of 128 212 (103).
+// What bounds it is the
 // issuing of instructions: 4180 warp instructions to a tile of 128 keys, of which a code's pair takes three (a shift, the
 // mask, the multiply-add); 68 % of the issue slots, 50 % of the integer pipe, the rest lost to the barriers between the
 // stages.  The roles run from one instruction cache, so a shorter loop gains more than one unrolled.
@@ -718,8 +723,9 @@ __global__ void __launch_bounds__((T4Cfg<DP, PACK, RP>::kThreads), 1)
                         const float2 w2 = make_float2(ex2(z[i / 2 + y].x), ex2(z[i / 2 + y].y));
                         const float2 sum = add2(make_float2(l[i + 2 * y], l[i + 2 * y + 1]), w2);
                         l[i + 2 * y] = sum.x, l[i + 2 * y + 1] = sum.y;
-                        // rounded to float16 for the product; the sum takes them unrounded, and the
-                        // errors, 2^-12 each, average out
+                        // rounded to float16 for the product, up to 2^-11 of each; the sum takes them unrounded.
+                        // In a float16 result that is seen: its rms error is 1.25 to 1.3 times that of one rounding
+                        // (2.6e-4 against 2.1e-4 over 2000 keys); in bfloat16 it is not.
                         p[y] = pack2<SPEC_DTYPE_F16>(w2.x, w2.y);
                     }
                     *reinterpret_cast<uint4 *>(p_row + ((((int)col0 / 8 + i / 8) ^ swap) * 16)) =
