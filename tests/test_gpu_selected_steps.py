@@ -114,3 +114,57 @@ def test_a_selection_on_a_stream_that_is_given(four):
     assert torch.equal(late, bounds) and torch.equal(again, scores)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(table, want[0]) and torch.equal(length, want[1]) and int(cache.status) == 0
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("N,hq,hkv,D,page,slots", [
+    (1, 8, 2, 128, 16, 4),       # a stream's keys
+    (5, 16, 8, 64, 8, 24),       # heads in pairs
+    (3, 12, 3, 64, 32, 4),       # an odd one left
+    (40, 16, 2, 96, 64, 3),      # many rows
+    (2, 40, 40, 72, 16, 6),
+])
+def test_lists_of_pages_in_another_order_change_nothing(N, hq, hkv, D, page, slots, four):
+    """Each head's pages moved to other places of the pool and listed there, in 16 bits with values and keys that are
+    not finite at the nodes of a branch: the same bits as with one table for all heads."""
+    sv = _sv()
+    g = torch.Generator(device="cuda").manual_seed(N + D)
+    lens = [(7, 300, 0, 133)[b % 4] + b for b in range(slots)]
+    P = -(-(max(lens) + N) // page)
+    pages = slots * P + 2
+    table, _, _, cl = ch.make_table(g, lens, N, page, P, pages)
+    q = torch.randn((slots, N, hq, D), generator=g, device="cuda").bfloat16()
+    parent = ch.random_parents(g, slots, N)
+    if four:
+        pools = [c4.make_pool(g, pages, hkv, page, D)]
+    else:
+        pools = [torch.randn((pages, page, hkv, D), generator=g, device="cuda").bfloat16() for _ in range(2)]
+        for b in range(0, slots, 2):
+            at = lens[b] + N - 1
+            pools[1][int(table[b, at // page]), at % page, b % hkv, 3] = (float("inf"), float("nan"))[b // 2 % 2]
+            if N > 2:
+                at -= 1
+                pools[0][int(table[b, at // page]), at % page, (b + 1) % hkv, 5] = float("nan")
+    moved = [p.clone() for p in pools]
+    lists = table.unsqueeze(1).repeat(1, hkv, 1)
+    for h in range(hkv):
+        perm = torch.randperm(pages, generator=g, device="cuda")
+        for p, m in zip(pools, moved):
+            if four:
+                m[perm, h] = p[:, h]
+            else:
+                m[perm, :, h] = p[:, :, h]
+        held = lists[:, h] >= 0
+        lists[:, h][held] = perm[lists[:, h][held].long()].int()
+    st = _i32([0])
+    for kw in (dict(), dict(window=100, sinks=3), dict(node_count=_i32([N - b % 2 for b in range(slots)]))):
+        kw.update(return_lse=True, dev_status=st)
+        if four:
+            a = sv.tree_attention4(q, pools[0], table, cl, page, parent, **kw)
+            b = sv.tree_attention4(q, moved[0], lists, cl, page, parent, **kw)
+        else:
+            a = sv.tree_attention(q, *pools, table, cl, parent, **kw)
+            b = sv.tree_attention(q, *moved, lists, cl, parent, **kw)
+        for x, y in zip(a, b):
+            assert torch.equal(x.isnan(), y.isnan()) and torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0))
+    assert int(st) == 0

@@ -109,3 +109,31 @@ def test_weights_beside_a_reference_that_moves(low, N, hq, D, requests, dtype):
     err = (o - want).abs()
     assert (err <= tol).all(), "worst %g of its bound" % float((err / tol).max())
     assert ((l - torch.logsumexp(score, 1)).abs() <= low * 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,hq,hkv,D", [(1, 8, 2, 128), (5, 8, 2, 128), (16, 8, 2, 128), (5, 8, 4, 64), (1, 8, 4, 64)])
+def test_rows_beside_one_of_large_scores(N, hq, hkv, D, dtype):
+    """Every fourth head's scores are 2^14 times as large, or beyond 2^40 (bfloat16): the other rows, which share the
+    kernel's tiles with it, are as ever."""
+    import cache_helpers as ch
+    import speculative_decoding_verification_69_gb300 as sv
+    g = torch.Generator(device="cuda").manual_seed(N + D)
+    lens, page = [40, 1000, 0, 3000], 16
+    P = -(-(max(lens) + N) // page)
+    table, _, _, cl = ch.make_table(g, lens, N, page, P, 4 * P)
+    pool = c4.make_pool(g, 4 * P, hkv, page, D)
+    parent = ch.random_parents(g, 4, N)
+    q = torch.randn((4, N, hq, D), generator=g, device="cuda").to(dtype)
+    q[:, :, ::4] *= 2.0 ** 14 if dtype == torch.float16 else 2.0 ** 40
+    q.clamp_(-6e4 if dtype == torch.float16 else -1e30, 6e4 if dtype == torch.float16 else 1e30)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, l = sv.tree_attention4(q, pool, table, cl, page, parent, return_lse=True, dev_status=st)
+    ref = c4.ref_attention(q, pool, page, table, cl, parent)
+    assert int(st) == 0 and torch.isfinite(o).all() and torch.isfinite(l).all()
+    rest = [h for h in range(hq) if h % 4]
+    ch.check_attention(o[:, :, rest], l[:, :, rest], tuple(x[:, :, rest] for x in ref), dtype, D)
+    # of the large ones at least the sum: the largest score, to float32
+    big = l[:, :, ::4].double().cpu()
+    want, scale = ref[1][:, :, ::4].double().cpu(), ref[3][:, :, ::4].double().cpu()
+    assert ((big - want).abs() <= (D + 4) * 2.0 ** -24 * scale + 2.0 ** -18 + 2.0 ** -22 * want.abs()).all()
