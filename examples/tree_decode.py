@@ -7,11 +7,12 @@ slots greedily, odd ones sampled.  A step drafts a tree of nodes per slot, runs
 the target on all nodes at once (cache_append, tree_attention in every layer),
 verifies the tree (verify_tree) and keeps the accepted path (cache_commit).
 
-    python examples/tree_decode.py [--slots 4] [--steps 24] [--prompt 150]
+    python examples/tree_decode.py [--slots 4] [--steps 24] [--prompt 150] [--bits 4] [--keep 8]
 
 Prints the tokens emitted per step, and the largest difference between the
 logits the steps verified and the ones of the plain model on the finished
-sequences.
+sequences.  With --bits 4 the cache is held in 4 bits, with --keep a step attends
+to that many pages of each key head, chosen by their scores; both move the logits.
 """
 import argparse
 import os
@@ -74,6 +75,7 @@ class Model:
 
 def prefill(model, cache, prompt, chunk=64):
     """The prompt into slot 0.  The chunks are chains: every token sees those before it."""
+    four = isinstance(cache, sv.PagedCache4)
     want = torch.zeros_like(cache.cache_len)
     want[0] = prompt.numel()
     sv.cache_resize(cache.page_table, cache.page_count, cache.page_ref, want, cache.page_size,
@@ -84,12 +86,19 @@ def prefill(model, cache, prompt, chunk=64):
         n = part.shape[1]
 
         def attend(layer, q, k, v):
+            if four:
+                sv.cache4_append(cache.pool[layer], table, length, k, v, cache.page_size, dev_status=cache.status)
+                return sv.tree_attention4(q, cache.pool[layer], table, length, cache.page_size, dev_status=cache.status)
             sv.cache_append(cache.k[layer], cache.v[layer], table, length, k, v, dev_status=cache.status)
             return sv.tree_attention(q, cache.k[layer], cache.v[layer], table, length, dev_status=cache.status)
         model.forward(part, torch.arange(at, at + n, device="cuda")[None], attend)
         # a chain whose every token is kept: the root and n - 1 nodes after it
-        sv.cache_commit(cache.k, cache.v, table, length, None, torch.full_like(length, n - 1), nodes=n,
-                        dev_status=cache.status)
+        kept = torch.full_like(length, n - 1)
+        if four:
+            sv.cache4_commit(cache.pool, table, length, None, kept, cache.page_size, cache.head_dim, nodes=n,
+                             dev_status=cache.status)
+        else:
+            sv.cache_commit(cache.k, cache.v, table, length, None, kept, nodes=n, dev_status=cache.status)
 
 
 def draft_tree(model, root, temperature, g):
@@ -108,20 +117,23 @@ def draft_tree(model, root, temperature, g):
     return torch.stack(tokens, 1), torch.stack(logits[:-1], 1)
 
 
-def run(slots=4, steps=24, prompt_len=150, page_size=16, seed=0, model=None):
+def run(slots=4, steps=24, prompt_len=150, page_size=16, seed=0, model=None, bits=16, keep=None):
     """Decodes, and returns (sequences, tokens emitted per step and slot, the
     largest difference from the plain model's logits)."""
     model = model or Model(seed=seed)
     N = len(PARENT)
     pages = -(-(prompt_len + steps * N + N) // page_size) + 1
-    cache = sv.PagedCache(model.layers, slots * pages, page_size, model.kv_heads, model.head_dim, slots, pages,
-                          dtype=model.dtype)
+    cache = (sv.PagedCache4 if bits == 4 else sv.PagedCache)(
+        model.layers, slots * pages, page_size, model.kv_heads, model.head_dim, slots, pages, dtype=model.dtype)
     g = torch.Generator(device="cuda").manual_seed(seed)
     prompt = torch.randint(model.vocab, (prompt_len,), generator=g, device="cuda", dtype=torch.int32)
     prefill(model, cache, prompt[:-1])  # the last token is the first root
     i32 = dict(dtype=torch.int32, device="cuda")
     if slots > 1:
         cache.fork(torch.zeros(slots - 1, **i32), torch.arange(1, slots, **i32))
+
+    bounds = [cache.new_bounds() for _ in range(model.layers)] if keep else None
+    start = torch.zeros_like(cache.cache_len)  # positions whose pages have their bounds
 
     parent = torch.tensor(PARENT, **i32).repeat(slots, 1)
     depth = [0] * N
@@ -138,8 +150,10 @@ def run(slots=4, steps=24, prompt_len=150, page_size=16, seed=0, model=None):
 
         def attend(layer, q, k, v):
             cache.append(layer, k, v)
-            return cache.attention(layer, q, parent)
+            chosen = cache.select(layer, q, bounds[layer], keep, start=start) if keep else None
+            return cache.attention(layer, q, parent, pages=chosen)
         target = model.forward(tokens, cache.cache_len[:, None] + depth, attend)
+        start.copy_(cache.cache_len)
         out, nodes, accepted = sv.verify_tree(target, draft.contiguous(), parent, tokens, temperature, seed + step)
         cache.commit(nodes, accepted)
         cache.trim()
@@ -164,8 +178,10 @@ def main():
     ap.add_argument("--slots", type=int, default=4)
     ap.add_argument("--steps", type=int, default=24)
     ap.add_argument("--prompt", type=int, default=150)
+    ap.add_argument("--bits", type=int, choices=(4, 16), default=16)
+    ap.add_argument("--keep", type=int)
     a = ap.parse_args()
-    _, emitted, worst = run(a.slots, a.steps, a.prompt)
+    _, emitted, worst = run(a.slots, a.steps, a.prompt, bits=a.bits, keep=a.keep)
     print("%d slots, %d steps: %.2f tokens a step; logits within %.4f of the plain model's"
           % (a.slots, a.steps, emitted, worst))
 
